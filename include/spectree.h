@@ -31,6 +31,10 @@
  *     the root, the last verified token, and parent[t] is the LOCAL index of
  *     the parent (-1 for the root).  Parents come before children:
  *     0 <= parent[i] < i.  n_b <= n_max <= 1024.
+ *   - Calls on prompts and packed rows (spec_prompt_attention,
+ *     spec_token_logprobs, and spec_kv_append when it appends a prompt's rows)
+ *     use the same ragged packing with seq_off in the place of tree_off; their
+ *     requests have no limit of 1024 rows.
  *   - mask rows have W = ceil(n_max / 64) 64-bit words.
  *   - The return value reports errors visible on the host (bad scalar
  *     arguments, NULL pointers, unsupported sizes, launch failures); on such
@@ -70,6 +74,7 @@ typedef int32_t spec_status;
 #define SPEC_DEV_BAD_BLOCK 16 /* a block-table entry outside [0, num_blocks) */
 #define SPEC_DEV_BAD_PATH 32  /* a commit path that is not strictly increasing from node 0 */
 #define SPEC_DEV_BAD_TEMP 64  /* stochastic verify: an inverse temperature that is not finite and positive */
+#define SPEC_DEV_BAD_ROW 128 /* page calls: a block-table row out of range, named twice, or not empty where it must be */
 
 typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 
@@ -285,7 +290,8 @@ spec_status spec_tree_verify_stochastic(const float* p_logits, const float* q_pr
  * slot changes.  This is how the tree K/V reach the slots that
  * spec_tree_attention reads.
  *   k_new, v_new  [T][Hkv][D] dtype, T = tree_off[B]; 16-byte aligned, as are the caches
- *                 (else SPEC_ERR_INVALID_ARG)
+ *                 (else SPEC_ERR_INVALID_ARG).  A prompt's rows are appended the same way
+ *                 (tree_off = its packing, n_max = its longest request, of any length)
  *   k_cache, v_cache, block_table, max_blocks, block_size, num_blocks  as for attention
  *   prefix_len, tree_off  int32 [B], [B+1]
  *   status   int32 [B] in/out, or-ed with SPEC_DEV_BAD_TREE (n_b outside [0, n_max]),
@@ -421,6 +427,156 @@ spec_status spec_tree_expand_level(const float* scores, int B, int F, int V, int
 spec_status spec_tree_merge(const int32_t* seqs, const int32_t* lens, const int32_t* root_tok, int B, int M, int m,
                             int V, int32_t* tree_off, int32_t* parent, int32_t* tokens, int32_t* src,
                             int32_t* node_of, int32_t* status, void* stream);
+
+/*
+ * Prompt attention (the pages have no counterpart: they start from a committed
+ * prefix; this call fills the prefix's hidden states).  Causal attention of
+ * whole prompts, or of the next chunk of prompts, over the paged cache:
+ * request b's new tokens are rows [seq_off[b], seq_off[b+1]) of q and out; row
+ * i of them is the token at slot s = prefix_len[b] + i and sees slots 0 .. s:
+ * out = sum_{k <= s} softmax_k(scale * q . K_k) V_k.  Query head h reads
+ * kv-head h / (Hq / Hkv).  One token per request (n_b = 1) is the plain decode
+ * step.  The rows' own K/V must be in the cache (spec_kv_append before this
+ * call on the stream).  fp32 accumulation and softmax; bf16 inputs give bf16
+ * output.
+ *   q        [T][Hq][D] dtype, T >= seq_off[B]; 16-byte aligned, as are out and the caches
+ *            (else SPEC_ERR_INVALID_ARG)
+ *   k_cache, v_cache, block_table, max_blocks, block_size, num_blocks  paged cache, see
+ *            the conventions above.  Slots [0, prefix_len[b] + n_b) hold finite values; what
+ *            lies in the pages behind them is never used.
+ *   prefix_len int32 [B]    slots already filled before row 0 (0: a fresh prompt; <= max_prefix)
+ *   seq_off  int32 [B+1]    packing; n_b may be 0
+ *   n_max    the largest n_b the call may see (n_max * (Hq / Hkv) < 2^30)
+ *   out      [T][Hq][D] dtype out; rows outside every request are not written
+ *   workspace  16-byte aligned device scratch of spec_prompt_workspace_size() bytes (used when
+ *            the keys of few rows are split over the GPU)
+ *   status   int32 [B] in/out: a request that comes in non-zero is skipped, its rows left as
+ *            they were.  Or-ed with SPEC_DEV_BAD_TREE (n_b outside [0, n_max], or rows outside
+ *            [0, T)), SPEC_DEV_CAPACITY (prefix_len outside [0, max_prefix], or
+ *            prefix_len + n_b beyond the block table): such a request is skipped too;
+ *            SPEC_DEV_BAD_BLOCK (a block id outside [0, num_blocks)) and SPEC_DEV_TIMEOUT: its
+ *            output rows are unspecified.
+ */
+size_t spec_prompt_workspace_size(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int D);
+spec_status spec_prompt_attention(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_table, int max_blocks, int block_size, int num_blocks,
+                                  const int32_t* prefix_len, const int32_t* seq_off, int B, int T, int n_max,
+                                  int max_prefix, int Hq, int Hkv, int D, spec_dtype dtype, float scale, void* out,
+                                  void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * Log probabilities of given tokens, with the entropy of their distribution,
+ * their rank and the top alternatives (what a server answers with beside the
+ * tokens; the pages have no counterpart).  For a row of logits x and an
+ * inverse temperature tau, p = softmax(tau * x):
+ *   logprob = log p(token);  entropy = -sum_i p_i log p_i (nats; 0 log 0 = 0);
+ *   rank = number of tokens that come before the given one, and top_tokens the
+ *   first k, in the order of spec_tree_expand_level: larger logit first, equal
+ *   logits by lower id, NaN after every number, -0 equal to +0;
+ *   top_logprobs = their log p.
+ * Logits of -inf have probability 0.  A row with a NaN, a +inf or nothing
+ * above -inf has no distribution: its logprob, entropy and top_logprobs are
+ * NaN, its rank and top_tokens as ordered above.
+ *
+ * spec_token_logprobs: packed rows; row t of logits is scored for tokens[t].
+ * spec_path_logprobs: the tokens a verification emitted: entry (b, i),
+ *   i < accept_len[b], scores emitted[b][i] with the row of node path[b][i]
+ *   (logits row tree_off[b] + path[b][i]).  path, accept_len and emitted are
+ *   the verifier's outputs; a request that failed there has accept_len 0.
+ *
+ *   logits   [T][V] of dtype, aligned to its element; V <= 131072
+ *   tokens   int32 [T]; -1: no token given (logprob NaN, rank -1; the rest is computed)
+ *   seq_off / tree_off int32 [B+1]
+ *   inv_temperature float [B] (device) or NULL for tau = 1
+ *   k        alternatives per entry, 0 <= k <= min(32, V)
+ *   logprob, entropy float, rank int32: [T], or [B][n_max] for the path call; entropy and rank
+ *            may be NULL
+ *   top_tokens int32, top_logprobs float: [T][k], or [B][n_max][k]; either may be NULL
+ *   status   int32 [B] or-ed (the incoming word is not read): SPEC_DEV_BAD_TOKEN (a token
+ *            outside [0, V)), SPEC_DEV_BAD_TEMP (tau not in [1e-30, inf)), SPEC_DEV_BAD_PATH
+ *            (accept_len above n_max, a path node outside the request's tree, or rows outside
+ *            [0, T)); only the entries concerned are affected
+ * Entries without a result (i >= accept_len[b], rows outside every request,
+ * flagged entries) get NaN, rank -1 and top_tokens -1.  One launch.
+ */
+spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, const int32_t* tokens, const int32_t* seq_off,
+                                const float* inv_temperature, int B, int T, int V, int k, float* logprob,
+                                float* entropy, int32_t* rank, int32_t* top_tokens, float* top_logprobs,
+                                int32_t* status, void* stream);
+spec_status spec_path_logprobs(const void* p_logits, spec_dtype dtype, const int32_t* tree_off, const int32_t* path,
+                               const int32_t* accept_len, const int32_t* emitted, const float* inv_temperature,
+                               int B, int T, int n_max, int V, int k, float* logprob, float* entropy, int32_t* rank,
+                               int32_t* top_tokens, float* top_logprobs, int32_t* status, void* stream);
+
+/*
+ * Page calls ("SpecInfer Guide", "PagedKV Allocation with Zero-Copy Pruning":
+ * pages are handed out and taken back by metadata alone; sharing between rows
+ * and compaction have no counterpart there).  A page is held by every row of
+ * the block table that names it, free when it is among free_pool's first
+ * *free_count entries, and otherwise the caller's own; the table is the only
+ * record, so these calls and spec_kv_commit_layers' release need no counters.
+ * Pages are taken from the pool's end.  Table entries below 0 mean "no page".
+ *
+ * spec_pages_fork: fork i makes row dst[i] hold the first len[i] slots of row
+ *   src[i], with pages for room[i] further slots.  Full pages are shared; the
+ *   slots of a partial last page are copied, in every layer, to a fresh page;
+ *   the pages for room are fresh.  src[i] = -1 with len[i] = 0 is an empty
+ *   row.  src[i] == dst[i] extends a row in place: its missing pages up to
+ *   len[i] + room[i] slots are filled in (nothing is shared or copied).
+ *   Fresh pages are taken in the order of i, then of the page.  When the pool
+ *   has fewer pages than the call's sound forks need, none that needs a page
+ *   is done and each of those gets SPEC_DEV_CAPACITY.
+ *   status int32 [N] WRITTEN per fork: 0; SPEC_DEV_BAD_ROW (src outside
+ *   [-1, B), dst outside [0, B), len or room < 0, src = -1 with len > 0, a row
+ *   that is dst twice, a src that another fork has as dst, or a dst row with
+ *   pages where new ones go); SPEC_DEV_CAPACITY (also len + room beyond the
+ *   table); SPEC_DEV_BAD_BLOCK (a source page, or a pool entry about to be
+ *   taken, outside [0, num_blocks)).  A flagged fork changes nothing.
+ *
+ * spec_pages_free: row rows[i] keeps its first keep_len[i] slots (keep_len
+ *   NULL: none): its entries from page ceil(keep_len / block_size) on become
+ *   -1, and the pages among them that no row names any more are appended to
+ *   the pool in the order of i, then of the page, each once.  When the pool
+ *   cannot take them all, nothing is done and each row that had pages to
+ *   release gets SPEC_DEV_CAPACITY.
+ *   status int32 [N] WRITTEN per row: 0, SPEC_DEV_BAD_ROW (outside [0, B),
+ *   named twice, keep_len < 0), SPEC_DEV_BAD_BLOCK (a dropped entry of
+ *   num_blocks or more) or SPEC_DEV_CAPACITY; a flagged row is left as it was.
+ *
+ * spec_pages_compact: moves held pages to the lowest ids.  Among the pages
+ *   that are held or free, in increasing id, the first n (n = held pages)
+ *   become the held ones: the i-th free page among them receives the i-th held
+ *   page beyond them, in every layer.  The table is renumbered, the pool lists
+ *   the remaining pages by decreasing id (so that the lowest is taken first;
+ *   *free_count is unchanged), and page_map tells callers who keep ids
+ *   elsewhere.  The caller's own pages stay.
+ *   page_map int32 [num_blocks] out: new id of each page; moved int32 [1] out
+ *   status int32 [1] WRITTEN: 0, or SPEC_DEV_BAD_BLOCK (an id out of range in
+ *   the table or the pool, a page twice in the pool, or both held and in the
+ *   pool, or a *free_count outside [0, free_cap]): nothing is changed then.
+ *
+ *   k_caches, v_caches  device arrays of `layers` device pointers, as in spec_kv_commit_layers,
+ *            each cache 16-byte aligned; layers = 0 (pointers NULL): metadata only
+ *   block_table int32 [B][max_blocks] in/out; B * max_blocks and N * max_blocks < 2^31
+ *   free_pool int32 [free_cap], free_count int32 [1]: device memory, in/out
+ *   workspace  16-byte aligned device scratch of spec_pages_workspace_size() bytes (N of the
+ *            call; 0 for compact)
+ */
+size_t spec_pages_workspace_size(int B, int max_blocks, int num_blocks, int N);
+spec_status spec_pages_fork(void* const* k_caches, void* const* v_caches, int layers, int32_t* block_table, int B,
+                            int max_blocks, int block_size, int num_blocks, const int32_t* src, const int32_t* dst,
+                            const int32_t* len, const int32_t* room, int N, int Hkv, int D, spec_dtype dtype,
+                            int32_t* free_pool, int free_cap, int32_t* free_count, void* workspace,
+                            size_t workspace_bytes, int32_t* status, void* stream);
+spec_status spec_pages_free(int32_t* block_table, int B, int max_blocks, int block_size, int num_blocks,
+                            const int32_t* rows, const int32_t* keep_len, int N, int32_t* free_pool, int free_cap,
+                            int32_t* free_count, void* workspace, size_t workspace_bytes, int32_t* status,
+                            void* stream);
+spec_status spec_pages_compact(void* const* k_caches, void* const* v_caches, int layers, int32_t* block_table, int B,
+                               int max_blocks, int block_size, int num_blocks, int Hkv, int D, spec_dtype dtype,
+                               int32_t* free_pool, int free_cap, int32_t* free_count, int32_t* page_map,
+                               int32_t* moved, void* workspace, size_t workspace_bytes, int32_t* status,
+                               void* stream);
 
 /*
  * Dynamic draft length ("Hardware-aware dynamic speculative decoding",

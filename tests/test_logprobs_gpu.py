@@ -1,0 +1,204 @@
+"""Log probabilities, entropy, rank and alternatives through the C ABI against
+64-bit softmax rows."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import tree_speculative_verification_spec_gb300 as S
+from request_life import logprob_reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from tree_speculative_verification_spec_gb300 import build
+    build.build()
+    S.lib()
+
+
+def _outputs(shape, k):
+    f = dict(device="cuda")
+    i = dict(dtype=torch.int32, device="cuda")
+    return (torch.full(shape, 7.0, **f), torch.full(shape, 7.0, **f), torch.full(shape, 7, **i),
+            torch.full(shape + (k,), 7, **i), torch.full(shape + (k,), 7.0, **f))
+
+
+def _tokens_call(x, tokens, off, tau, k, status=None):
+    T, V = x.shape
+    B = len(off) - 1
+    out = _outputs((T,), k)
+    status = torch.zeros(B, dtype=torch.int32, device="cuda") if status is None else status
+    S.spec_token_logprobs(x, torch.tensor(tokens, dtype=torch.int32, device="cuda"),
+                          torch.tensor(off, dtype=torch.int32, device="cuda"),
+                          None if tau is None else torch.tensor(tau, dtype=torch.float32, device="cuda"), B, T, V, k,
+                          *out, status)
+    return out, status.tolist()
+
+
+def _tolerance(x, tau, ref_lp):
+    """A weight e^(tau (x - m)) is off by 2^-22 (the exponential) and by 2^-22
+    of its exponent (three roundings), which weighs at most e^-t t < 1 / e of
+    the largest; a thread adds at most ceil(V / 256) + 64 of them and raises
+    its reference at most once per 16, each raise 2^-21; the logarithm and the
+    difference are off by 2^-23 of their size.  The entropy adds one more
+    product per weight: the same, times the size of its terms."""
+    n = -(-len(x) // 256) + 64
+    rel = 2.0 ** -22 * 2 + n * 2.0 ** -24 + (n / 16) * 2.0 ** -21
+    size = 0.0 if not np.isfinite(ref_lp) else abs(ref_lp)
+    return rel + 2.0 ** -22 * (size + math.log(len(x)) + 1)
+
+
+def _check(row, out, i, token, tau, k):
+    lp, ent, rank, top, top_lp = logprob_reference(row, token, tau, k)
+    got = [o[i].cpu() for o in out]
+    for g, r in ((got[0].item(), lp), (got[1].item(), ent)):
+        if math.isnan(r):
+            assert math.isnan(g)
+        elif math.isinf(r):
+            assert g == r
+        else:
+            assert abs(g - r) <= _tolerance(row, tau, r) * (1 + math.log(len(row))), (g, r)
+    assert got[2].item() == rank
+    assert got[3].tolist() == list(top)
+    for g, r in zip(got[4].tolist(), top_lp):
+        assert (math.isnan(g) and math.isnan(r)) or g == r or abs(g - r) <= _tolerance(row, tau, r), (g, r)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("T,V,k", [(1, 1, 1), (3, 2, 2), (2, 7, 5), (1, 31, 31), (4, 33, 32), (5, 1000, 20), (3, 4099, 32),
+                                   (1, 32000, 5), (9, 32001, 1), (400, 513, 3), (2, 128256, 20), (1, 131072, 32),
+                                   (7, 50257, 0)])
+def test_token_logprobs(T, V, k, dtype):
+    g = torch.Generator().manual_seed(T * V + k)
+    x = (torch.randn((T, V), generator=g) * 2.5).to(dtype)
+    tokens = torch.randint(0, V, (T,), generator=g).tolist()
+    tokens[-1] = int(x[-1].float().argmax())
+    cut = sorted(torch.randint(0, T + 1, (2,), generator=g).tolist())
+    off = [0] + cut + [T]
+    tau = [0.7, 1.0, 2.5]
+    out, status = _tokens_call(x.cuda(), tokens, off, tau, k)
+    assert status == [0, 0, 0]
+    for i in list(range(min(T, 6))) + [T - 1]:
+        b = sum(i >= c for c in cut)
+        _check(x[i].double().numpy(), out, i, tokens[i], float(np.float32(tau[b])), k)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_ties_masks_and_rows_without_a_distribution(dtype):
+    V, k = 5000, 32
+    low = torch.finfo(dtype).min
+    g = torch.Generator().manual_seed(4)
+    rows, tokens = [], []
+
+    def add(row, token):
+        rows.append(row)
+        tokens.append(token)
+    add(torch.zeros(V), 4999)                                            # all equal
+    add(torch.randint(-3, 4, (V,), generator=g).float(), 17)             # many ties
+    x = torch.full((V,), -math.inf)
+    x[[70, 4097, 12]] = torch.tensor([1.0, 2.0, 2.0])
+    add(x, 70)                                                           # three tokens left
+    add(x.clone(), 5)                                                    # a masked token: -inf
+    x = torch.full((V,), low)
+    x[4000] = 0.5
+    add(x, 3)                                                            # masked by the type's lowest value
+    add(torch.full((V,), -math.inf), 9)                                  # nothing left: no distribution
+    add(torch.full((V,), low), 9)                                        # every entry the lowest value: uniform
+    x = torch.randn(V, generator=g)
+    x[[3, 44, 4500]] = math.nan
+    add(x, 44)                                                           # NaN ranks last
+    x = torch.randn(V, generator=g)
+    x[[8, 9]] = math.inf
+    add(x, 9)
+    x = torch.zeros(V)
+    x[100:200] = -0.0
+    add(x, 150)                                                          # -0 equals +0
+    add(torch.arange(V).float(), 0)                                      # ascending: every entry enters the list
+    add(torch.randn(V, generator=g), -1)                                 # no token given
+    xs = torch.stack(rows).to(dtype)
+    out, status = _tokens_call(xs.cuda(), tokens, [0, len(rows)], None, k)
+    assert status == [0]
+    for i in range(len(rows)):
+        _check(xs[i].double().numpy(), out, i, tokens[i], 1.0, k)
+
+
+def test_bad_tokens_and_temperatures():
+    x = torch.randn((6, 300), generator=torch.Generator().manual_seed(1))
+    out, status = _tokens_call(x.cuda(), [1, 300, -2, 4, 5, 6], [0, 3, 4, 5], [1.0, 0.0, math.inf], 3)
+    assert status == [S.SPEC_DEV_BAD_TOKEN, S.SPEC_DEV_BAD_TEMP, S.SPEC_DEV_BAD_TEMP]
+    _check(x[0].double().numpy(), out, 0, 1, 1.0, 3)
+    for i in (1, 2, 3, 4, 5):  # flagged entries, and row 5 that no request owns
+        assert math.isnan(out[0][i].item()) and math.isnan(out[1][i].item()) and out[2][i].item() == -1
+        assert out[3][i].tolist() == [-1] * 3 and all(map(math.isnan, out[4][i].tolist()))
+
+
+def test_optional_outputs_and_alignment():
+    """Rows that start anywhere, and calls that want the log probability alone."""
+    for dtype in (torch.float32, torch.bfloat16):
+        V = 1003
+        base = torch.randn(5 * V + 1, generator=torch.Generator().manual_seed(2)).to(dtype).cuda()
+        x = base[1:].view(5, V)
+        out, status = _tokens_call(x, [0, 1002, 500, 501, 7], [0, 5], None, 4)
+        for i, t in enumerate([0, 1002, 500, 501, 7]):
+            _check(x[i].cpu().double().numpy(), out, i, t, 1.0, 4)
+        lp = torch.zeros(5, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        S.spec_token_logprobs(x, torch.tensor([0, 1002, 500, 501, 7], dtype=torch.int32, device="cuda"),
+                              torch.tensor([0, 5], dtype=torch.int32, device="cuda"), None, 1, 5, V, 0, lp, None, None,
+                              None, None, st)
+        assert torch.equal(lp, out[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_path_logprobs(dtype):
+    g = np.random.default_rng(6)
+    sizes, V, k, n_max = [5, 1, 0, 40, 12, 7], 777, 6, 41
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    B, T = len(sizes), int(off[-1])
+    x = torch.from_numpy(g.standard_normal((T, V)).astype(np.float32)).to(dtype)
+    acc = np.array([3, 1, 0, 9, 12, 2], np.int32)
+    path = np.full((B, n_max), -1, np.int32)
+    emitted = np.full((B, n_max), -1, np.int32)
+    for b in range(B):
+        if acc[b]:
+            rest = g.choice(np.arange(1, max(2, sizes[b])), acc[b] - 1, replace=False)
+            path[b, :acc[b]] = [0] + sorted(rest.tolist())
+        emitted[b, :acc[b]] = g.integers(0, V, acc[b])
+    path[5, 1] = 7       # outside the request's tree
+    emitted[3, 4] = V    # outside the vocabulary
+    out = _outputs((B, n_max), k)
+    status = torch.zeros(B, dtype=torch.int32, device="cuda")
+    c = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    S.spec_path_logprobs(x.cuda(), c(off), c(path), c(acc), c(emitted), None, B, T, n_max, V, k, *out, status)
+    assert status.tolist() == [0, 0, 0, S.SPEC_DEV_BAD_TOKEN, 0, S.SPEC_DEV_BAD_PATH]
+    for b in range(B):
+        for i in range(n_max):
+            if i >= acc[b] or (b, i) in ((5, 1), (3, 4)):
+                assert math.isnan(out[0][b, i].item()) and math.isnan(out[1][b, i].item()) and out[2][b, i].item() == -1
+                assert out[3][b, i].tolist() == [-1] * k and all(map(math.isnan, out[4][b, i].tolist()))
+            else:
+                _check(x[off[b] + path[b, i]].double().numpy(), [o[b] for o in out], i, int(emitted[b, i]), 1.0, k)
+
+
+def test_logprobs_repeat_and_replay():
+    x = torch.randn((64, 32000), device="cuda", generator=torch.Generator("cuda").manual_seed(8))
+    tokens = list(range(64))
+    a, _ = _tokens_call(x, tokens, [0, 64], None, 20)
+    b, _ = _tokens_call(x, tokens, [0, 64], None, 20)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    tok = torch.tensor(tokens, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    out, st = _outputs((64,), 20), torch.zeros(1, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        S.spec_token_logprobs(x, tok, off, None, 1, 64, 32000, 20, *out, st)
+    x.neg_()
+    graph.replay()
+    torch.cuda.synchronize()
+    want, _ = _tokens_call(x, tokens, [0, 64], None, 20)
+    assert all(torch.equal(p, q) for p, q in zip(out, want))

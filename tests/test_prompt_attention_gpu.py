@@ -1,0 +1,188 @@
+"""Prompt attention through the C ABI against 64-bit attention: lengths from
+zero to several tiles, prefixes, group widths that do and do not divide a row
+tile, page sizes, both types, split keys, refusals on the device."""
+import math
+
+import pytest
+import torch
+
+import tree_speculative_verification_spec_gb300 as S
+from request_life import paged_batch, prompt_reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from tree_speculative_verification_spec_gb300 import build
+    build.build()
+    S.lib()
+
+
+def _size(d):
+    return (d["B"], d["T"], d["n_max"], d["max_prefix"], d["Hq"], d["Hkv"], d["D"])
+
+
+def _call(d, out=None, status=None, ws=None, stream=None, table=None):
+    out = torch.full_like(d["q"], 7.0) if out is None else out
+    status = torch.zeros(d["B"], dtype=torch.int32, device="cuda") if status is None else status
+    ws = torch.empty(S.spec_prompt_workspace_size(*_size(d)), dtype=torch.uint8, device="cuda") if ws is None else ws
+    table = d["table"] if table is None else table
+    S.spec_prompt_attention(d["q"], d["k"], d["v"], table, table.shape[1], d["bs"], d["nb"], d["prefix"], d["seq_off"],
+                            *_size(d), d["scale"], out, ws, status, stream=stream)
+    return out, status
+
+
+def _holds(d, out, rows=None):
+    ref, tol = prompt_reference(d)
+    rows = torch.arange(int(d["seq_off"][-1]), device="cuda") if rows is None else rows
+    err = (out.double() - ref).abs()[rows]
+    assert torch.isfinite(out[rows].double()).all()
+    worst = (err / tol[rows]).max().item() if rows.numel() else 0.0
+    assert worst <= 1.0, worst
+
+
+CASES = [
+    # lens, prefix, Hq, Hkv, D, bs
+    ([1], [0], 4, 4, 64, 16),
+    ([128], [0], 4, 4, 64, 16),
+    ([5, 0, 1, 64], [0, 7, 0, 3], 8, 2, 64, 8),
+    ([0, 0, 3], [0, 0, 0], 8, 2, 128, 64),
+    ([129, 127, 1, 255, 257], [0, 1, 128, 129, 500], 8, 2, 128, 16),
+    ([300, 33], [0, 1000], 32, 8, 128, 16),
+    ([64, 65, 63], [0, 64, 63], 64, 8, 128, 256),
+    ([100, 43, 2], [13, 0, 200], 6, 2, 64, 64),       # g = 3: a token's heads straddle row tiles
+    ([90, 17], [5, 300], 20, 4, 128, 32),             # g = 5
+    ([70], [20], 5, 1, 64, 16),
+    ([40, 1, 130], [0, 256, 3], 32, 1, 64, 128),      # one kv head
+    ([600], [0], 16, 2, 128, 512),
+    ([2, 1, 1, 3, 1, 1, 1], [900, 1500, 5, 0, 1, 2047, 2048], 16, 4, 128, 16),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("case", CASES, ids=[f"{len(c[0])}x{max(c[0])}-{c[2]}:{c[3]}-D{c[4]}-p{c[5]}" for c in CASES])
+def test_prompt_attention_holds(case, dtype):
+    lens, prefix, Hq, Hkv, D, bs = case
+    d = paged_batch(sum(lens) + D, lens, prefix, Hq, Hkv, D, bs, dtype, extra_rows=3)
+    out, status = _call(d)
+    assert status.tolist() == [0] * d["B"]
+    _holds(d, out)
+    T = int(d["seq_off"][-1])
+    assert (out[T:] == 7.0).all()  # rows behind the last request stay as they were
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_long_prefixes_split_over_the_gpu(dtype):
+    d = paged_batch(5, [3, 1], [6000, 9000], 8, 2, 128, 64, dtype)
+    assert S.spec_prompt_workspace_size(*_size(d)) > 256
+    out, status = _call(d)
+    assert status.tolist() == [0, 0]
+    _holds(d, out)
+    with pytest.raises(S.SpecError) as e:
+        _call(d, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == S.SPEC_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("spread", [0.0, 40.0, 300.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_scores_far_apart(dtype, spread):
+    """Equal keys, and keys whose scores lie hundreds apart: the reference of
+    the exponentials has to follow the maximum along the keys."""
+    d = paged_batch(9, [200, 70], [0, 333], 8, 2, 128, 16, dtype, spread=spread)
+    out, status = _call(d)
+    assert status.tolist() == [0, 0]
+    _holds(d, out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_keys_that_grow_along_the_sequence(dtype):
+    """Each later block of keys dwarfs the ones before, and the reverse."""
+    for sign in (1.0, -1.0):
+        d = paged_batch(11, [400], [0], 4, 2, 64, 16, dtype)
+        ids = d["table"][0, :25].long()
+        grow = torch.exp2(torch.arange(400, device="cuda") / 40.0 * sign).view(25, 1, 16, 1)
+        d["k"][ids] = (d["k"][ids].float() * grow * (1.0 if sign > 0 else 64.0)).to(dtype)
+        out, status = _call(d)
+        _holds(d, out)
+
+
+def test_many_requests():
+    """More requests than one sorting pass takes, most of a few tokens."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 9, (700,), generator=g).tolist()
+    prefix = torch.randint(0, 90, (700,), generator=g).tolist()
+    d = paged_batch(13, lens, prefix, 8, 2, 64, 16, torch.bfloat16)
+    out, status = _call(d)
+    assert status.tolist() == [0] * 700
+    _holds(d, out)
+
+
+def test_larger_ragged_batch():
+    d = paged_batch(17, [1024, 77, 2000, 513], [0, 1500, 100, 0], 32, 8, 128, 16, torch.bfloat16)
+    out, status = _call(d)
+    assert status.tolist() == [0] * 4
+    _holds(d, out)
+
+
+def test_refused_requests_leave_the_others_alone():
+    d = paged_batch(19, [40, 30, 20, 10, 50], [10, 20, 0, 70, 5], 8, 2, 64, 16, torch.bfloat16)
+    ref_out, _ = _call(d)
+    table = d["table"].clone()
+    table[2, 0] = d["nb"]           # an id past the pool
+    d["prefix"] = d["prefix"].clone()
+    d["prefix"][3] = d["max_prefix"] + 1
+    status = torch.zeros(5, dtype=torch.int32, device="cuda")
+    status[1] = S.SPEC_DEV_BAD_TREE  # failed before this call
+    out, status = _call(d, table=table, status=status)
+    assert status.tolist() == [0, S.SPEC_DEV_BAD_TREE, S.SPEC_DEV_BAD_BLOCK, S.SPEC_DEV_CAPACITY, 0]
+    off = d["seq_off"].tolist()
+    for b in (0, 4):
+        assert torch.equal(out[off[b]:off[b + 1]], ref_out[off[b]:off[b + 1]])
+    for b in (1, 3):
+        assert (out[off[b]:off[b + 1]] == 7.0).all()
+
+
+def test_requests_outside_the_stated_bounds():
+    d = paged_batch(23, [40, 30], [0, 0], 8, 2, 64, 16, torch.bfloat16)
+    good, _ = _call(d)
+    d["n_max"] = 35  # the first request is longer than the call allows
+    out, status = _call(d)
+    assert status.tolist() == [S.SPEC_DEV_BAD_TREE, 0]
+    assert (out[:40] == 7.0).all() and torch.equal(out[40:], good[40:])
+    d["n_max"], d["T"] = 40, 60  # rows beyond T
+    out, status = _call(d)
+    assert status.tolist() == [0, S.SPEC_DEV_BAD_TREE]
+    assert torch.equal(out[:40], good[:40]) and (out[40:] == 7.0).all()
+
+
+def test_runs_on_a_side_stream_and_replays_from_a_graph():
+    d = paged_batch(29, [33, 150, 1], [400, 0, 3000], 8, 2, 128, 16, torch.bfloat16)
+    ref, _ = _call(d)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out, status = torch.full_like(d["q"], 7.0), torch.zeros(3, dtype=torch.int32, device="cuda")
+    ws = torch.empty(S.spec_prompt_workspace_size(*_size(d)), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    _call(d, out, status, ws, stream=side)
+    side.synchronize()
+    assert torch.equal(out, ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _call(d, out, status, ws)
+    for seed in (1, 2):
+        d["q"].copy_(torch.randn(d["q"].shape, device="cuda", generator=torch.Generator("cuda").manual_seed(seed)).to(d["q"].dtype))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        _holds(d, out)
+
+
+def test_workspace_contents_do_not_matter(monkeypatch):
+    d = paged_batch(31, [3], [5000], 8, 2, 128, 64, torch.bfloat16)
+    ref, _ = _call(d)
+    monkeypatch.setenv("SPECTREE_WORKSPACE_CANARY", "1")
+    out, _ = _call(d)
+    assert torch.equal(out, ref) and not math.isnan(out.float().sum().item())

@@ -13,7 +13,7 @@ LIB_PATH = os.path.join(_PKG, "libspectree.so")
 
 SPEC_OK, SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA, SPEC_ERR_WORKSPACE = 0, 1, 2, 3, 4
 SPEC_DEV_BAD_TREE, SPEC_DEV_BAD_TOKEN, SPEC_DEV_CAPACITY, SPEC_DEV_TIMEOUT = 1, 2, 4, 8
-SPEC_DEV_BAD_BLOCK, SPEC_DEV_BAD_PATH, SPEC_DEV_BAD_TEMP = 16, 32, 64
+SPEC_DEV_BAD_BLOCK, SPEC_DEV_BAD_PATH, SPEC_DEV_BAD_TEMP, SPEC_DEV_BAD_ROW = 16, 32, 64, 128
 SPEC_Q_PER_PARENT, SPEC_Q_PER_CHILD = 0, 1  # layouts of the draft rows
 SPEC_F32, SPEC_BF16 = 0, 1
 SPEC_ATTN_AUTO, SPEC_ATTN_CUDA_CORE, SPEC_ATTN_TCGEN05 = 0, 1, 2
@@ -47,6 +47,16 @@ SIGNATURES = {
     "spec_kv_commit_layers": ([_P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P],
                               _I),
     "spec_philox_uniforms": ([_U64, _U32, _P, _I, _I, _P, _P], _I),
+    "spec_prompt_workspace_size": ([_I, _I, _I, _I, _I, _I, _I], _SZ),
+    "spec_prompt_attention": ([_P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _SZ,
+                               _P, _P], _I),
+    "spec_token_logprobs": ([_P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
+    "spec_path_logprobs": ([_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
+    "spec_pages_workspace_size": ([_I, _I, _I, _I], _SZ),
+    "spec_pages_fork": ([_P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _SZ, _P, _P],
+                        _I),
+    "spec_pages_free": ([_P, _I, _I, _I, _I, _P, _P, _I, _P, _I, _P, _P, _SZ, _P, _P], _I),
+    "spec_pages_compact": ([_P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _SZ, _P, _P], _I),
     "spec_selftest_bounded_wait": ([_P, _U32, _P], _I),
     "spec_selftest_exp": ([_U32, ctypes.c_longlong, _P, _P, _P], _I),
     "spec_selftest_fx": ([_P, ctypes.c_longlong, _I, _P, _P, _P, _P], _I),
@@ -273,6 +283,75 @@ def spec_kv_commit_layers(k_ptrs, v_ptrs, layers, block_table, max_blocks, block
 def spec_philox_uniforms(seed, round_, tree_off, B, n_max, out, stream=None):
     _check("spec_philox_uniforms", lib().spec_philox_uniforms(
         ctypes.c_uint64(seed), ctypes.c_uint32(round_), _ptr(tree_off), B, n_max, _ptr(out), _stream(stream)))
+
+
+def _scratch(t):
+    return (None, 0) if t is None else (_ptr(t), t.numel() * t.element_size())
+
+
+def spec_prompt_workspace_size(B, T, n_max, max_prefix, Hq, Hkv, D):
+    return int(lib().spec_prompt_workspace_size(B, T, n_max, max_prefix, Hq, Hkv, D))
+
+
+def spec_prompt_attention(q, k_cache, v_cache, block_table, max_blocks, block_size, num_blocks, prefix_len, seq_off,
+                          B, T, n_max, max_prefix, Hq, Hkv, D, scale, out, workspace, status, stream=None):
+    """q, out: [T][Hq][D] CUDA tensors of the caches' dtype."""
+    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or out.dtype != q.dtype:
+        raise ValueError("q, out and the caches must have one dtype")
+    _check("spec_prompt_attention", lib().spec_prompt_attention(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), max_blocks, block_size, num_blocks,
+        _ptr(prefix_len), _ptr(seq_off), B, T, n_max, max_prefix, Hq, Hkv, D, _dtype_code(q), float(scale), _ptr(out),
+        *_scratch(workspace), _ptr(status), _stream(stream)))
+
+
+def spec_token_logprobs(logits, tokens, seq_off, inv_temp, B, T, V, k, logprob, entropy, rank, top_tokens,
+                        top_logprobs, status, stream=None):
+    """logits: float32 or bfloat16 [T, V]; inv_temp: float32 [B] or None (1);
+    entropy, rank, top_tokens and top_logprobs may be None."""
+    _check("spec_token_logprobs", lib().spec_token_logprobs(
+        _ptr(logits), _dtype_code(logits), _ptr(tokens), _ptr(seq_off), _ptr(inv_temp), B, T, V, k, _ptr(logprob),
+        _ptr(entropy), _ptr(rank), _ptr(top_tokens), _ptr(top_logprobs), _ptr(status), _stream(stream)))
+
+
+def spec_path_logprobs(p_logits, tree_off, path, accept_len, emitted, inv_temp, B, T, n_max, V, k, logprob, entropy,
+                       rank, top_tokens, top_logprobs, status, stream=None):
+    """p_logits: float32 or bfloat16 [T, V]; path, accept_len and emitted as
+    a verifier wrote them; the other arguments as in spec_token_logprobs."""
+    _check("spec_path_logprobs", lib().spec_path_logprobs(
+        _ptr(p_logits), _dtype_code(p_logits), _ptr(tree_off), _ptr(path), _ptr(accept_len), _ptr(emitted),
+        _ptr(inv_temp), B, T, n_max, V, k, _ptr(logprob), _ptr(entropy), _ptr(rank), _ptr(top_tokens),
+        _ptr(top_logprobs), _ptr(status), _stream(stream)))
+
+
+def spec_pages_workspace_size(B, max_blocks, num_blocks, N):
+    return int(lib().spec_pages_workspace_size(B, max_blocks, num_blocks, N))
+
+
+def spec_pages_fork(k_ptrs, v_ptrs, layers, block_table, B, max_blocks, block_size, num_blocks, src, dst, length,
+                    room, N, Hkv, D, dtype, free_pool, free_count, workspace, status, stream=None):
+    """k_ptrs / v_ptrs: int64 device tensors of the layers' cache addresses
+    (None with layers = 0); room: int32 [N] or None (0); dtype: SPEC_F32 or
+    SPEC_BF16."""
+    _check("spec_pages_fork", lib().spec_pages_fork(
+        _ptr(k_ptrs), _ptr(v_ptrs), layers, _ptr(block_table), B, max_blocks, block_size, num_blocks, _ptr(src),
+        _ptr(dst), _ptr(length), _ptr(room), N, Hkv, D, dtype, _ptr(free_pool), free_pool.numel(), _ptr(free_count),
+        *_scratch(workspace), _ptr(status), _stream(stream)))
+
+
+def spec_pages_free(block_table, B, max_blocks, block_size, num_blocks, rows, keep_len, N, free_pool, free_count,
+                    workspace, status, stream=None):
+    """keep_len: int32 [N] or None (rows are dropped whole)."""
+    _check("spec_pages_free", lib().spec_pages_free(
+        _ptr(block_table), B, max_blocks, block_size, num_blocks, _ptr(rows), _ptr(keep_len), N, _ptr(free_pool),
+        free_pool.numel(), _ptr(free_count), *_scratch(workspace), _ptr(status), _stream(stream)))
+
+
+def spec_pages_compact(k_ptrs, v_ptrs, layers, block_table, B, max_blocks, block_size, num_blocks, Hkv, D, dtype,
+                       free_pool, free_count, page_map, moved, workspace, status, stream=None):
+    _check("spec_pages_compact", lib().spec_pages_compact(
+        _ptr(k_ptrs), _ptr(v_ptrs), layers, _ptr(block_table), B, max_blocks, block_size, num_blocks, Hkv, D, dtype,
+        _ptr(free_pool), free_pool.numel(), _ptr(free_count), _ptr(page_map), _ptr(moved), *_scratch(workspace),
+        _ptr(status), _stream(stream)))
 
 
 def spec_selftest_bounded_wait(status, polls, stream=None):

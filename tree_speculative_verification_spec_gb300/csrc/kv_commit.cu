@@ -415,7 +415,7 @@ extern "C" spec_status spec_kv_append(const void* k_new, const void* v_new, void
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return SPEC_ERR_UNSUPPORTED;
   if (block_size < 8 || block_size > 65536 || (block_size & (block_size - 1))) return SPEC_ERR_UNSUPPORTED;
-  if (n_max > SPEC_MAX_NODES || B > 65535 || Hkv > 65535) return SPEC_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > 65535) return SPEC_ERR_UNSUPPORTED;
   if (B == 0 || n_max == 0) return SPEC_OK;
   if (!k_new || !v_new || !k_cache || !v_cache || !block_table || !prefix_len || !tree_off || !status)
     return SPEC_ERR_INVALID_ARG;

@@ -113,6 +113,7 @@ const char* spec_dev_status_string(int32_t bit) {
     case SPEC_DEV_BAD_BLOCK: return "bad block id";
     case SPEC_DEV_BAD_PATH: return "bad commit path";
     case SPEC_DEV_BAD_TEMP: return "bad inverse temperature";
+    case SPEC_DEV_BAD_ROW: return "bad table row";
     default: break;
   }
   return "unknown status bit";

@@ -7,6 +7,7 @@
 #include <cooperative_groups.h>
 
 #include "common.cuh"
+#include "topk.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -18,90 +19,6 @@ namespace spectree {
 
 constexpr int kExpandThreads = 256;
 constexpr int kExpandWarps = kExpandThreads / 32;
-
-// Rank key of a draft score: larger is better.  High word: the float made
-// orderable as an unsigned integer (-0 counted as +0, NaN below -inf); low
-// word: the complement of the token id, so that equal scores rank the lower
-// id first.  Keys of distinct tokens are distinct and all above 0.
-__device__ __forceinline__ unsigned long long score_key(float v, int id) {
-  uint32_t u = __float_as_uint(v);
-  uint32_t k;
-  if (v != v) {
-    k = 0u;
-  } else {
-    if (u == 0x80000000u) u = 0u;
-    k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  }
-  return ((unsigned long long)k << 32) | (unsigned long long)(~(uint32_t)id);
-}
-
-// The score of a key's high word: the bar below which no entry can enter a
-// full list (-inf while the list has room or holds a NaN entry).
-__device__ __forceinline__ float key_score(unsigned long long key) {
-  const uint32_t k = (uint32_t)(key >> 32);
-  if (k == 0u) return -INFINITY;
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
-}
-
-// A warp's running top-k (k <= 32): lane r < k holds the r-th best key
-// (descending), lanes >= k hold 0.  thr = the k-th best key (0 while there is
-// room), bar = its score.
-struct WarpTop {
-  unsigned long long list = 0ull, thr = 0ull;
-  float bar = -INFINITY;
-  float floor = -INFINITY;  // a lower bound of the k-th best score, from a first sample
-
-  // Lower bound for the bar from one sample per lane (its best score of a
-  // first batch; NaN counted as -inf): the k-th largest of these 32 distinct
-  // entries, by a bitonic sort across the warp.  No entry scored below it
-  // can be among the k best.
-  __device__ __forceinline__ void seed(float lane_best, int k, int lane) {
-    float v = lane_best != lane_best ? -INFINITY : lane_best;
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-      for (int stride = size >> 1; stride > 0; stride >>= 1) {
-        const float o = __shfl_xor_sync(0xffffffffu, v, stride);
-        const bool desc = ((lane & size) == 0) == ((lane & stride) == 0);  // keep the larger in the lower lane
-        v = desc ? fmaxf(v, o) : fminf(v, o);
-      }
-    }
-    floor = __shfl_sync(0xffffffffu, v, k - 1);
-    bar = fmaxf(bar, floor);
-  }
-
-  // Inserts `key` (the same value in every lane) if it beats the k-th best.
-  __device__ __forceinline__ void insert(unsigned long long key, int k, int lane) {
-    if (key <= thr) return;  // warp-uniform
-    const int pos = __popc(__ballot_sync(0xffffffffu, list > key));  // the greater keys are lanes 0 .. pos-1
-    const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
-    if (lane > pos) list = up;
-    else if (lane == pos) list = key;
-    if (lane >= k) list = 0ull;
-    thr = __shfl_sync(0xffffffffu, list, k - 1);
-    bar = fmaxf(key_score(thr), floor);
-  }
-
-  // Every lane offers one score (valid lanes only); called by the whole warp.
-  __device__ __forceinline__ void offer(float v, int x, bool valid, int k, int lane) {
-    unsigned m = __ballot_sync(0xffffffffu, valid && !(v < bar));
-    while (m) {
-      const int l = __ffs(m) - 1;
-      m &= m - 1;
-      insert(score_key(__shfl_sync(0xffffffffu, v, l), __shfl_sync(0xffffffffu, x, l)), k, lane);
-    }
-  }
-
-  // Every lane offers one key (0 = nothing).
-  __device__ __forceinline__ void offer_key(unsigned long long key, int k, int lane) {
-    unsigned m = __ballot_sync(0xffffffffu, key > thr);
-    while (m) {
-      const int l = __ffs(m) - 1;
-      m &= m - 1;
-      insert(__shfl_sync(0xffffffffu, key, l), k, lane);
-    }
-  }
-};
 
 // One thread-block cluster per frontier row, each CTA on a contiguous chunk
 // of it (chunk: a multiple of 4 entries).  Each warp keeps a running top-k
