@@ -78,11 +78,15 @@ __device__ __forceinline__ void prompt_flag_requests(const PromptArgs& a) {
   }
 }
 
+constexpr int kPromptCcRows = 64;   // rows per CTA of the CUDA-core kernel
+constexpr int kPromptTcRows = 256;  // rows per work item of the tensor-core kernel
+
 struct PromptPlan {
   int splits, chunk;
   long long tiles;  // row tiles, before heads and splits
 };
 
-cudaError_t launch_prompt_cc(const PromptArgs& a, const PromptPlan& p, spec_dtype dt, cudaStream_t stream);
+cudaError_t launch_prompt_cc(const PromptArgs& a, const PromptPlan& p, cudaStream_t stream);
+cudaError_t launch_prompt_tc(const PromptArgs& a, const PromptPlan& p, cudaStream_t stream);
 
 }  // namespace spectree

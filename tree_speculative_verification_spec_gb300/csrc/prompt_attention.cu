@@ -24,7 +24,7 @@ __device__ __forceinline__ float pr_exp2(float x) {
 // and K a thread reads 8 float4 for 64 multiply-adds, so the FMA pipe and not
 // shared memory bounds it (the tensor cores have no fp32 product).
 constexpr int kPrThreads = 256;
-constexpr int kPrRows = 64;
+constexpr int kPrRows = kPromptCcRows;
 constexpr int kPrKeys = 64;
 
 template <int D> struct PromptCcSmem {
@@ -35,15 +35,9 @@ template <int D> struct PromptCcSmem {
   float v[kPrKeys * D];
 };
 
-template <typename T> __device__ __forceinline__ float4 load4(const T* p);
-template <> __device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
-}
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptArgs a) {
   using S = PromptCcSmem<D>;
   extern __shared__ __align__(16) float dyn[];
@@ -69,9 +63,9 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
   const int k_end = min(rq.P + (r0 + rows - 1) / g + 1, k_begin + a.chunk);
   if (k_begin >= k_end) return;
 
-  const T* __restrict__ q = static_cast<const T*>(a.q);
-  const T* __restrict__ kc = static_cast<const T*>(a.k_cache);
-  const T* __restrict__ vc = static_cast<const T*>(a.v_cache);
+  const float* __restrict__ q = static_cast<const float*>(a.q);
+  const float* __restrict__ kc = static_cast<const float*>(a.k_cache);
+  const float* __restrict__ vc = static_cast<const float*>(a.v_cache);
   const int32_t* bt = a.block_table + (size_t)rq.b * a.max_blocks;
   const int bs = a.block_size;
   if (threadIdx.x == 0) s_badblk = 0;
@@ -203,9 +197,11 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
     const size_t row = (size_t)t * a.Hq + h;
     if (a.splits == 1) {
       const float inv = 1.0f / l[i];
-      T* out = static_cast<T*>(a.out) + row * D;
+      float* out = static_cast<float*>(a.out) + row * D;
 #pragma unroll
-      for (int j = 0; j < DJ * 4; ++j) out[tx * 4 + 64 * (j / 4) + j % 4] = from_f32<T>(o[i][j] * inv);
+      for (int j = 0; j < DJ; ++j)
+        *reinterpret_cast<float4*>(out + tx * 4 + 64 * j) =
+            make_float4(o[i][j * 4] * inv, o[i][j * 4 + 1] * inv, o[i][j * 4 + 2] * inv, o[i][j * 4 + 3] * inv);
     } else {
       float* wo = a.ws_o + ((size_t)split * a.T * a.Hq + row) * D;
 #pragma unroll
@@ -257,18 +253,17 @@ __global__ void __launch_bounds__(256) prompt_combine_kernel(const PromptArgs a)
   for (int j = 0; j < D / 32; ++j) out[lane + 32 * j] = from_f32<T>(acc[j] * inv);
 }
 
-template <typename T, int D>
+template <int D>
 static cudaError_t launch_cc(const PromptArgs& a, const PromptPlan& p, cudaStream_t stream) {
   const int dyn = (int)sizeof(PromptCcSmem<D>);
-  const cudaError_t e = cudaFuncSetAttribute(prompt_cc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+  const cudaError_t e = cudaFuncSetAttribute(prompt_cc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
   if (e != cudaSuccess) return e;
-  prompt_cc_kernel<T, D><<<dim3((unsigned)p.tiles, p.splits, a.Hkv), kPrThreads, dyn, stream>>>(a);
+  prompt_cc_kernel<D><<<dim3((unsigned)p.tiles, p.splits, a.Hkv), kPrThreads, dyn, stream>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_prompt_cc(const PromptArgs& a, const PromptPlan& p, spec_dtype dt, cudaStream_t stream) {
-  if (dt == SPEC_F32) return a.D == 64 ? launch_cc<float, 64>(a, p, stream) : launch_cc<float, 128>(a, p, stream);
-  return a.D == 64 ? launch_cc<__nv_bfloat16, 64>(a, p, stream) : launch_cc<__nv_bfloat16, 128>(a, p, stream);
+cudaError_t launch_prompt_cc(const PromptArgs& a, const PromptPlan& p, cudaStream_t stream) {
+  return a.D == 64 ? launch_cc<64>(a, p, stream) : launch_cc<128>(a, p, stream);
 }
 
 static cudaError_t launch_prompt_combine(const PromptArgs& a, spec_dtype dt, cudaStream_t stream) {
@@ -284,16 +279,28 @@ static cudaError_t launch_prompt_combine(const PromptArgs& a, spec_dtype dt, cud
 }
 
 // Row tiles and key splits of a call.  Keys are split only when the row tiles
-// alone leave SMs idle: then enough splits for about two CTAs an SM, each of
-// at least 256 keys.
+// alone leave SMs idle.  CUDA cores: enough splits for about two CTAs an SM,
+// each of at least 256 keys.  Tensor cores (one CTA an SM): the split count of
+// least waves x (4 us of set-up and epilogue + 1.3 us per 128-key step).
 static PromptPlan prompt_plan(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, bool bf16) {
-  (void)bf16;
   PromptPlan p;
   const int g = Hq / Hkv;
-  p.tiles = (long long)T * g / kPrRows + B;
+  p.tiles = (long long)T * g / (bf16 ? kPromptTcRows : kPromptCcRows) + B;
   const long long units = p.tiles * Hkv, keys = (long long)max_prefix + n_max;
-  long long splits = std::max(1LL, std::min((2 * 152 + units - 1) / units, (keys + 255) / 256));
-  if (units >= 152) splits = 1;
+  long long splits = 1;
+  if (units < 152 && !bf16) splits = std::max(1LL, std::min((2 * 152 + units - 1) / units, (keys + 255) / 256));
+  if (units < 152 && bf16) {
+    double best = 1e300;
+    const long long most = std::max(1LL, std::min(64LL, (keys + 127) / 128));
+    for (long long s = 1; s <= most; ++s) {
+      const long long steps = ((keys + s - 1) / s + 127) / 128;
+      const double cost = (double)((units * s + 151) / 152) * (4.0 + 1.3 * (double)steps);
+      if (cost < best * 0.97) {  // fewer splits on near-ties: less partial traffic
+        best = cost;
+        splits = s;
+      }
+    }
+  }
   const long long chunk = std::max(128LL, ((keys + splits - 1) / splits + 127) / 128 * 128);
   p.chunk = (int)std::min<long long>(chunk, 1LL << 30);
   p.splits = (int)std::max(1LL, (keys + chunk - 1) / chunk);
@@ -382,7 +389,8 @@ spec_status spec_prompt_attention(const void* q, const void* k_cache, const void
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = (cudaStream_t)stream;
   if (need > 0) spec_workspace_canary(workspace, need, st);
-  if (launch_prompt_cc(a, plan, dtype, st) != cudaSuccess) return SPEC_ERR_CUDA;
+  const cudaError_t e = dtype == SPEC_BF16 ? launch_prompt_tc(a, plan, st) : launch_prompt_cc(a, plan, st);
+  if (e != cudaSuccess) return SPEC_ERR_CUDA;
   if (plan.splits > 1 && launch_prompt_combine(a, dtype, st) != cudaSuccess) return SPEC_ERR_CUDA;
   return SPEC_OK;
 }

@@ -1,0 +1,669 @@
+// Prompt attention on the 5th-generation tensor cores (tcgen05), bf16 inputs,
+// fp32 scores and accumulators in tensor memory.
+//
+// Per work item (256 rows of one request's kv-head group, one key range) a CTA
+// holds two 128-row tiles t = 0, 1 and walks the keys 128 at a time:
+//   S_t = Q_t K_j^T          A = Q (shared memory), B = K tile (shared memory)
+//   P_t = 2^(S_t c - m)      softmax warps, row r == TMEM lane r, one thread per
+//                            row; bf16 P over the S columns just read
+//   O_t += P_t V_j           A = P (tensor memory), B = V tile (shared memory)
+// The two tiles share every K and V stage, and while one tile's scores are in
+// the softmax the tensor core works for the other:
+//   ... PV_j(0) QK_{j+1}(0) | PV_j(1) QK_{j+1}(1) | PV_{j+1}(0) ...
+// One thread issues all MMAs; they complete in that order, so S_t may be
+// overwritten right after PV_j(t) without a wait.
+//
+// Reference m of a row: softmax(x) = 2^(xc - m) / sum 2^(xc - m) for ANY m, so
+// m is the maximum of the row's first visible half tile and stays, with no
+// maximum taken per tile, as long as the sum of 64 weights stays below 2^60
+// (fp32 and bf16 have the exponents for it: both hold 2^127).  When it does
+// not, that half is done again against its own maximum, and O and the sum are
+// scaled down.  Underflow is the same as for the usual running maximum, which
+// is never below m.
+#include <algorithm>
+
+#include "prompt.cuh"
+#include "tcgen05.cuh"
+
+namespace spectree {
+
+namespace ptc {
+
+using namespace tc5;
+
+constexpr int BM = 128;              // rows per tile (M of the MMA)
+constexpr int BN = 128;              // keys per step
+constexpr int kRows = kPromptTcRows; // rows per work item
+constexpr int HC = BN / 2;           // keys per softmax half
+constexpr int kThreads = 384;        // warps: 0 K/V loads, 1 MMA, 2 work items, 3 Q loads, 4-7 tile 0, 8-11 tile 1
+constexpr uint32_t kTmemCols = 512;  // S_0, S_1 at 0, 128; O_0, O_1 at 256, 384
+constexpr float kSumLimit = 1152921504606846976.0f;  // 2^60
+constexpr int kOrderMax = 256;       // batches up to this size run longest request first
+static_assert(kRows == 2 * BM, "two row tiles per item");
+
+template <int D> struct Layout {
+  static constexpr int DH = D / 64;            // 128-byte halves of a row
+  static constexpr int NST = D == 128 ? 5 : 8; // stages of the ring that K and V tiles share
+  static constexpr uint32_t kTile = BM * D * 2;   // one Q tile, one K or V stage
+  static constexpr uint32_t kOffKV = 2 * kTile;
+  static constexpr uint32_t kBytes = kOffKV + NST * kTile;
+  static constexpr uint32_t kDyn = kBytes + 1024 < 120 * 1024 ? 120 * 1024 : kBytes + 1024;  // one CTA per SM (all of TMEM)
+  static_assert(kDyn + 2048 <= 227 * 1024, "dynamic and (below 2 KB) static shared memory within 227 KB");
+};
+
+struct Params {
+  PromptArgs a;
+  long long rows_total;  // num_blocks * Hkv * block_size: rows of the 2-D cache view
+  long long items;       // work items the grid numbers (upper bound)
+  int box_rows;          // rows per TMA box: min(block_size, 128)
+  int q_tma;             // Q by TMA (g divides 128), else by cp.async
+};
+
+// One work item; valid = 0 ends every role's loop.
+struct Work {
+  int valid, b, off, n, P, kvh, r0, split, k_begin;
+  int nt[2];  // key steps of the two row tiles (0: the tile has no rows or sees none of the keys)
+};
+
+// The requests in decreasing key count (ties by index), with the number of row
+// tiles before each: the longest items start first.  Only the requests' own
+// arguments count here, so every CTA numbers the items alike.
+struct Order {
+  int first[kOrderMax + 1];
+  uint8_t req[kOrderMax];
+};
+
+__device__ __forceinline__ int row_tiles(const PromptArgs& a, int off, int n, int P) {
+  return prompt_check(a, off, n, P) ? 0 : (int)(((long long)n * a.g + kRows - 1) / kRows);
+}
+
+__device__ __forceinline__ void order_requests(const PromptArgs& a, Order& o, int* len, int* tiles) {
+  const int c = threadIdx.x;
+  if (c < a.B) {
+    const int off = a.seq_off[c], n = a.seq_off[c + 1] - off, P = a.prefix_len[c];
+    tiles[c] = row_tiles(a, off, n, P);
+    len[c] = tiles[c] ? P + n : 0;
+  }
+  __syncthreads();
+  if (c < a.B) {
+    int rank = 0, before = 0;
+    for (int j = 0; j < a.B; ++j) {
+      const bool ahead = len[j] > len[c] || (len[j] == len[c] && j < c);
+      rank += ahead;
+      before += ahead ? tiles[j] : 0;
+    }
+    o.req[rank] = (uint8_t)c;
+    o.first[rank] = before;
+    if (rank == a.B - 1) o.first[a.B] = before + tiles[c];
+  }
+  __syncthreads();
+}
+
+// Work item `idx` (one warp, all lanes get it); valid = 0 when it is empty.
+__device__ __forceinline__ Work find_work(const Params& prm, const Order& o, long long idx, int lane) {
+  const PromptArgs& a = prm.a;
+  Work w = {};
+  w.split = (int)(idx % a.splits);
+  idx /= a.splits;
+  w.kvh = (int)(idx % a.Hkv);
+  const long long tile = idx / a.Hkv;
+  int b, mt;
+  if (a.B <= kOrderMax) {
+    if (tile >= o.first[a.B]) return w;
+    int cnt = 0;  // requests whose first tile is not above this one (empty ones rank last)
+    for (int r = lane; r < a.B; r += 32) cnt += o.first[r] <= tile;
+    cnt = warp_sum_i(cnt);
+    const int r = cnt - 1;
+    b = o.req[r];
+    mt = o.first[r + 1] - 1 - (int)tile;  // the last rows see the most keys: first
+  } else {
+    int lo = 0, hi = a.B;  // first_tile(lo) <= tile < first_tile(hi), 32 probes a round
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int at = lo + lane * step;
+      const bool below = at < hi && prompt_first_tile(a, at, kRows) <= tile;
+      const int last = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // lane 0 is always below
+      const int nlo = lo + max(last, 0) * step;
+      hi = min(hi, nlo + step);
+      lo = nlo;
+    }
+    b = lo;
+    const long long at = tile - prompt_first_tile(a, b, kRows);
+    if (at < 0 || at > (1 << 30)) return w;
+    mt = (int)at;
+  }
+  PromptRequest rq;
+  if (lane == 0) rq = prompt_request(a, b);
+  rq.off = __shfl_sync(0xffffffffu, rq.off, 0);
+  rq.n = __shfl_sync(0xffffffffu, rq.n, 0);
+  rq.P = __shfl_sync(0xffffffffu, rq.P, 0);
+  const bool ok = __shfl_sync(0xffffffffu, (int)rq.ok, 0);
+  const long long R = (long long)rq.n * a.g;
+  if (!ok || (long long)mt * kRows >= R) return w;
+  w.b = b;
+  w.off = rq.off;
+  w.n = rq.n;
+  w.P = rq.P;
+  w.r0 = mt * kRows;
+  w.k_begin = w.split * a.chunk;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const long long first = w.r0 + t * BM;
+    if (first >= R) continue;
+    const int end = min(rq.P + (int)(min(first + BM, R) - 1) / a.g + 1, w.k_begin + a.chunk);
+    if (end > w.k_begin) w.nt[t] = (end - w.k_begin + BN - 1) / BN;
+  }
+  w.valid = w.nt[0] > 0 || w.nt[1] > 0;
+  return w;
+}
+
+// Row of the 2-D cache view where the box starting at key k of the item's
+// kv-head begins; keys past the request, or at a bad block id, read the
+// out-of-range row `rows_total` (zero fill).
+__device__ __forceinline__ int box_row(const Params& prm, const int32_t* bt, int kvh, int k, int Lk, int* bad) {
+  const PromptArgs& a = prm.a;
+  int y = (int)prm.rows_total;
+  if (k < Lk) {
+    const int blk = __ldg(bt + k / a.block_size);
+    if (blk >= 0 && blk < a.num_blocks) y = (int)(((long long)blk * a.Hkv + kvh) * a.block_size + k % a.block_size);
+    else *bad = 1;
+  }
+  return y;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                     const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ Params prm) {
+  using L = Layout<D>;
+  constexpr int NST = L::NST;
+  const PromptArgs& a = prm.a;
+  extern __shared__ uint8_t dyn_raw[];
+  __shared__ uint64_t kv_full[NST], kv_empty[NST], s_full[2], p_full[2][2], o_done[2][2], q_full, q_empty, w_full[2],
+      w_empty[2], drain;
+  __shared__ Work work[2];
+  __shared__ Order order;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  if (blockIdx.x == 0) prompt_flag_requests(a);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t][0], 4);
+      mbar_init(&p_full[t][1], 4);
+      mbar_init(&o_done[t][0], 1);
+      mbar_init(&o_done[t][1], 1);
+      mbar_init(&w_full[t], 1);
+      mbar_init(&w_empty[t], 11);  // K/V, MMA and Q warps, eight softmax warps
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&drain, 1);
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (a.B <= kOrderMax) {
+    // scratch of the ranking: the K/V ring's room, which no copy has reached yet
+    int* scratch = reinterpret_cast<int*>(smem + L::kOffKV);
+    order_requests(a, order, scratch, scratch + kOrderMax);
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  // The next work item of a consumer warp; false at the end (or on a timeout).
+  auto take_work = [&](int it, Work& w) -> bool {
+    const bool ok = mbar_wait(&w_full[it & 1], (it >> 1) & 1, &abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    w = work[it & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&w_empty[it & 1]);
+    return w.valid;
+  };
+
+  if (warp == 2) {
+    // ------------------------------------------------------ work items
+    long long idx = blockIdx.x;
+    for (int it = 0;; ++it) {
+      Work w = {};
+      for (; idx < prm.items; idx += gridDim.x) {
+        w = find_work(prm, order, idx, lane);
+        if (w.valid) break;
+      }
+      idx += gridDim.x;
+      bool ok = true;
+      if (it >= 2 && lane == 0) ok = mbar_wait(&w_empty[it & 1], ((it >> 1) - 1) & 1, &abort_flag);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      if (lane == 0) {
+        work[it & 1] = w;
+        mbar_arrive(&w_full[it & 1]);
+      }
+      if (!w.valid) break;
+    }
+  } else if (warp == 0) {
+    // ------------------------------------------------------ K/V producer
+    // lane i issues the box of page (or 128-row piece) i of each tile; the
+    // order K_0, K_1, V_0, K_2, V_1, ... is the order of use
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
+    }
+    const int br = prm.box_rows, nb = BN / br;
+    int ld = 0;  // loads issued so far
+    bool go = true;
+    auto load = [&](const CUtensorMap* map, int y) {
+      const int st = ld % NST;
+      if (lane == 0 && ld >= NST) go = mbar_wait(&kv_empty[st], (ld / NST - 1) & 1, &abort_flag);
+      go = __shfl_sync(0xffffffffu, go, 0);
+      if (!go) return;
+      if (lane == 0) mbar_expect_tx(&kv_full[st], L::kTile);
+      __syncwarp();
+      if (lane < nb) {
+        const uint32_t dst = sbase + L::kOffKV + st * L::kTile + lane * br * 128;
+#pragma unroll
+        for (int h = 0; h < L::DH; ++h) tma_load_2d(dst + h * (BN * 128), map, h * 64, y, &kv_full[st]);
+      }
+      ++ld;
+    };
+    Work w;
+    for (int it = 0; go && take_work(it, w); ++it) {
+      const int n = max(w.nt[0], w.nt[1]), Lk = w.P + w.n;
+      const int32_t* bt = a.block_table + (size_t)w.b * a.max_blocks;
+      int bad = 0;
+      auto row = [&](int j) { return lane < nb ? box_row(prm, bt, w.kvh, w.k_begin + j * BN + lane * br, Lk, &bad) : 0; };
+      int y = row(0), y1 = n > 1 ? row(1) : 0;
+      load(&tmap_k, y);
+      for (int j = 0; j < n && go; ++j) {
+        const int y2 = j + 2 < n ? row(j + 2) : 0;  // the table is read a tile before its box goes out
+        if (j + 1 < n) load(&tmap_k, y1);
+        if (go) load(&tmap_v, y);
+        y = y1;
+        y1 = y2;
+      }
+      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
+    }
+    // every issued load has landed before the CTA can exit
+    if (lane == 0)
+      for (int i = max(0, ld - NST); i < ld; ++i) mbar_wait(&kv_full[i % NST], (i / NST) & 1, &abort_flag);
+  } else if (warp == 3) {
+    // ------------------------------------------------------ Q tiles
+    // row r = (token r / g, head kvh * g + r % g)
+    if (lane == 0 && prm.q_tma)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
+    Work w;
+    bool go = true;
+    int issued = 0;
+    for (int it = 0; go && take_work(it, w); ++it) {
+      if (lane == 0 && it >= 1) go = mbar_wait(&q_empty, (it - 1) & 1, &abort_flag);
+      go = __shfl_sync(0xffffffffu, go, 0);
+      if (!go) break;
+      const int tiles = w.nt[1] > 0 ? 2 : 1;
+      if (prm.q_tma) {
+        if (lane == 0) {
+          mbar_expect_tx(&q_full, tiles * L::kTile);
+          for (int t = 0; t < tiles; ++t)
+#pragma unroll
+            for (int h = 0; h < L::DH; ++h)
+              tma_load_3d(sbase + t * L::kTile + h * (BM * 128), &tmap_q, h * 64, w.kvh * a.g,
+                          w.off + (w.r0 + t * BM) / a.g, &q_full);
+        }
+      } else {
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+        constexpr int CPR = D / 8;  // 16-byte chunks per row
+        const long long R = (long long)w.n * a.g;
+        for (int c = lane; c < tiles * BM * CPR; c += 32) {
+          const int r = c / CPR, ch = c % CPR, t = r / BM, rr = r % BM;
+          const uint32_t at = t * L::kTile + (ch >> 3) * (BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+          const long long row = (long long)w.r0 + r;
+          if (row < R)
+            cp_async16(sbase + at, q + ((size_t)(w.off + row / a.g) * a.Hq + w.kvh * a.g + row % a.g) * D + ch * 8);
+          else
+            *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
+        }
+        cp_async_wait();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
+      }
+      issued = it + 1;
+    }
+    if (lane == 0 && issued > 0) mbar_wait(&q_full, (issued - 1) & 1, &abort_flag);  // the last copy has landed
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc_qk = idesc_bf16(BN, 0), idesc_pv = idesc_bf16(D, 1);
+    const uint64_t qdesc = smem_desc_sw128(sbase, 16, 1024);
+    const uint64_t kdesc = smem_desc_sw128(sbase + L::kOffKV, 16, 1024);
+    const uint64_t vdesc = smem_desc_sw128(sbase + L::kOffKV, BN * 128, 1024);
+    int ld = 0, hv[2] = {0, 0};  // loads used, P halves used per tile
+    bool ok = true;
+    auto wait_kv = [&](int i) {
+      ok = ok && mbar_wait(&kv_full[i % NST], (i / NST) & 1, &abort_flag);
+      tc_fence_after();
+    };
+    auto qk = [&](int t, int i) {
+      const uint64_t kd = kdesc + (uint64_t)((i % NST) * (L::kTile >> 4)), qd = qdesc + (uint64_t)(t * (L::kTile >> 4));
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+        umma_bf16(tmem + t * BN, qd + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
+      }
+      umma_commit(&s_full[t]);
+    };
+    Work w;
+    for (int it = 0; ok && take_work(it, w); ++it) {
+      if (lane == 0) {
+        const int n = max(w.nt[0], w.nt[1]);
+        // load numbers: K_0 = 0, K_j = 2j - 1, V_j = 2j + 2 (the last V: 2n - 1)
+        ok = mbar_wait(&q_full, it & 1, &abort_flag);
+        if (ok) wait_kv(ld);
+        if (ok) {
+          for (int t = 0; t < 2; ++t)
+            if (w.nt[t] > 0) qk(t, ld);
+          umma_commit(&kv_empty[ld % NST]);
+          if (n == 1) umma_commit(&q_empty);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          const int iv = ld + (j + 1 < n ? 2 * j + 2 : 2 * n - 1), ik = ld + 2 * j + 1;
+          const uint64_t vd = vdesc + (uint64_t)((iv % NST) * (L::kTile >> 4));
+          bool have_v = false, have_k = false;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (j >= w.nt[t]) continue;
+            const uint32_t s = tmem + t * BN, o = tmem + 2 * BN + t * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && mbar_wait(&p_full[t][h], (hv[t] >> 1) & 1, &abort_flag);
+              if (!have_v) {
+                wait_kv(iv);
+                have_v = true;
+              }
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < HC / 16; ++kk)
+                umma_bf16_ts(o, s + h * (HC / 2) + kk * 8, vd + (uint64_t)(((h * (HC / 16) + kk) * 2048) >> 4), idesc_pv,
+                             j > 0 || h > 0 || kk > 0 ? 1u : 0u);
+              umma_commit(&o_done[t][h]);
+              ++hv[t];
+            }
+            if (ok && j + 1 < w.nt[t]) {
+              if (!have_k) {
+                wait_kv(ik);
+                have_k = true;
+              }
+              if (ok) qk(t, ik);
+            }
+          }
+          if (!ok) break;
+          umma_commit(&kv_empty[iv % NST]);
+          if (j + 1 < n) umma_commit(&kv_empty[ik % NST]);
+          if (j + 2 == n) umma_commit(&q_empty);  // the item's last QK is out
+        }
+        ld += 2 * n;
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {  // every MMA has completed before TMEM is freed
+      umma_commit(&drain);
+      mbar_wait(&drain, 0, &abort_flag);
+    }
+  } else {
+    // ------------------------------------------------------ softmax, epilogue
+    const int t = (warp - 4) >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + t * BN + lane_off, tO = tmem + 2 * BN + t * 128 + lane_off;
+    const float c2 = a.scale_log2;
+    const float2 c22 = make_float2(c2, c2);
+    int ld = 0, cs = 0;  // loads so far (as the MMA warp counts them), score tiles of this row tile
+    bool ok = true;
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag));
+    };
+    Work w;
+    for (int it = 0; ok && take_work(it, w); ++it) {
+      const int nt = t == 0 ? w.nt[0] : w.nt[1], n = max(w.nt[0], w.nt[1]), Lk = w.P + w.n;
+      const int row = w.r0 + t * BM + r;
+      const bool valid = row < (long long)w.n * a.g;
+      const int tok = valid ? row / a.g : w.n - 1;
+      const int lim = w.P + tok + 1 - w.k_begin;  // visible keys of this range
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < nt && ok; ++j, ++cs) {
+        ok = wait_warp(&s_full[t], cs & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const int k0 = w.k_begin + j * BN;
+        if (k0 + BN > Lk) {
+          // the tile reaches past the request: its V rows there are zeroed, so
+          // that no stale bits (NaN among them) meet a zero probability
+          const int iv = ld + 2 * n - 1;  // only the range's last tile can
+          ok = wait_warp(&kv_full[iv % NST], (iv / NST) & 1);
+          if (!ok) break;
+          const int zr = Lk - k0;
+          uint8_t* vst = smem + L::kOffKV + (iv % NST) * L::kTile;
+          for (int i = r; i < (BN - zr) * L::DH * 8; i += BM) {
+            const int rr = zr + i / (L::DH * 8), rest = i % (L::DH * 8);
+            *reinterpret_cast<uint4*>(vst + (rest >> 3) * (BN * 128) + rr * 128 + ((rest & 7) << 4)) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int vis = lim - j * BN - h * HC;  // visible columns of this half
+          const bool full = __all_sync(0xffffffffu, vis >= HC);
+          uint32_t pk[HC / 2];
+          float sum = INFINITY;
+          uint32_t v0[32], v1[32];
+          tmem_ld32(tS + h * HC, v0);
+          tmem_ld32(tS + h * HC + 32, v1);
+          tmem_wait_ld(v0);
+          tmem_wait_ld(v1);
+          auto hide = [&]() {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (e >= vis) v0[e] = 0xff800000u;
+              if (32 + e >= vis) v1[e] = 0xff800000u;
+            }
+          };
+          if (!full) hide();
+          auto weights = [&](float ref) {
+            const float2 neg = make_float2(-ref, -ref);
+            float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v0[e]), __uint_as_float(v0[e + 1])), c22, neg);
+              const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              acc0 = __fadd2_rn(acc0, p);
+              __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
+              pk[e >> 1] = *reinterpret_cast<uint32_t*>(&h2);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v1[e]), __uint_as_float(v1[e + 1])), c22, neg);
+              const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              acc1 = __fadd2_rn(acc1, p);
+              __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
+              pk[16 + (e >> 1)] = *reinterpret_cast<uint32_t*>(&h2);
+            }
+            sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+          };
+          if (__all_sync(0xffffffffu, m != -INFINITY)) weights(m);
+          if (__any_sync(0xffffffffu, !(sum < kSumLimit))) {
+            // a first reference, or one that the scores have outgrown: this
+            // half again, from its scores in tensor memory
+            tmem_ld32(tS + h * HC, v0);
+            tmem_ld32(tS + h * HC + 32, v1);
+            tmem_wait_ld(v0);
+            tmem_wait_ld(v1);
+            if (!full) hide();
+            float mx = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx = fmax3(mx, __uint_as_float(v0[e]), __uint_as_float(v1[e]));
+            const float to = fmaxf(m, mx * c2);
+            const float f = m == -INFINITY ? 0.0f : fast_exp2(m - to);
+            l *= f;
+            m = to;
+            weights(to == -INFINITY ? 0.0f : to);
+            if ((j > 0 || h > 0) && __any_sync(0xffffffffu, f != 1.0f)) {
+              // O holds every earlier half once the last of them has
+              // completed: this tile's first, or the previous tile's second
+              // (one barrier for each, so that a wait is never two phases behind)
+              ok = wait_warp(&o_done[t][h ^ 1], (h == 1 ? cs : cs - 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO + c * 32, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(tO + c * 32, o);
+              }
+            }
+          }
+          l += sum;
+          tmem_st32(tS + h * (HC / 2), pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t][h]);
+        }
+      }
+      if (!ok) break;
+      ld += 2 * n;
+      if (nt == 0) continue;
+      // epilogue: this thread's row
+      ok = wait_warp(&o_done[t][1], (cs - 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const size_t orow = (size_t)(w.off + tok) * a.Hq + w.kvh * a.g + (valid ? row % a.g : 0);
+      const float inv = 1.0f / l;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + c * 32, o);
+        tmem_wait_ld(o);
+        if (!valid) continue;
+        if (a.splits == 1) {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv);
+              u[i] = *reinterpret_cast<uint32_t*>(&h2);
+            }
+            out[e / 8] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        } else {
+          uint4* wo = reinterpret_cast<uint4*>(a.ws_o + ((size_t)w.split * a.T * a.Hq + orow) * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) wo[e / 4] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (valid && a.splits > 1)
+        *reinterpret_cast<float2*>(a.ws_ml + ((size_t)w.split * a.T * a.Hq + orow) * 2) = make_float2(m, l);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // which of the CTA's items were lost is not kept: every request is flagged
+  if (abort_flag)
+    for (int b = threadIdx.x; b < a.B; b += kThreads) atomicOr(&a.status[b], SPEC_DEV_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+}  // namespace ptc
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+typedef CUresult (*PromptEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static PromptEncodeFn prompt_encode_fn() {
+  static const PromptEncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PromptEncodeFn>(p);
+  }();
+  return fn;
+}
+
+static bool prompt_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                       const cuuint32_t* box) {
+  const PromptEncodeFn enc = prompt_encode_fn();
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+static cudaError_t launch_d(const PromptArgs& a, const PromptPlan& p, cudaStream_t stream) {
+  ptc::Params prm;
+  prm.a = a;
+  prm.box_rows = std::min(a.block_size, ptc::BN);
+  prm.rows_total = (long long)a.num_blocks * a.Hkv * a.block_size;
+  if (prm.rows_total >= (long long)INT32_MAX) return cudaErrorInvalidValue;
+  prm.items = p.tiles * a.Hkv * p.splits;
+  alignas(64) CUtensorMap mk, mv, mq;
+  {
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)prm.rows_total}, strides[1] = {(cuuint64_t)D * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)prm.box_rows};
+    if (!prompt_map(&mk, a.k_cache, 2, dims, strides, box) || !prompt_map(&mv, a.v_cache, 2, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
+  // Q [T][Hq][D] as (columns, heads, tokens): a (64, g, 128 / g) box is one
+  // 64-column half of a row tile
+  prm.q_tma = ptc::BM % a.g == 0;
+  if (prm.q_tma) {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.Hq * D * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.g, (cuuint32_t)(ptc::BM / a.g)};
+    if (!prompt_map(&mq, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  } else {
+    mq = mk;  // not read
+  }
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int dyn = (int)ptc::Layout<D>::kDyn;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(ptc::prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min<long long>(prm.items, sms);
+  ptc::prompt_tc_kernel<D><<<grid, ptc::kThreads, dyn, stream>>>(mk, mv, mq, prm);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prompt_tc(const PromptArgs& a, const PromptPlan& p, cudaStream_t stream) {
+  return a.D == 64 ? launch_d<64>(a, p, stream) : launch_d<128>(a, p, stream);
+}
+
+}  // namespace spectree
