@@ -346,79 +346,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && issued > 0) mbar_wait(&q_full, (issued - 1) & 1, &abort_flag);  // the last copy has landed
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer
+    // The whole warp runs the loop (so that descriptors stay warp-uniform) and
+    // one elected lane issues.
     constexpr uint32_t idesc_qk = idesc_bf16(BN, 0), idesc_pv = idesc_bf16(D, 1);
     const uint64_t qdesc = smem_desc_sw128(sbase, 16, 1024);
     const uint64_t kdesc = smem_desc_sw128(sbase + L::kOffKV, 16, 1024);
     const uint64_t vdesc = smem_desc_sw128(sbase + L::kOffKV, BN * 128, 1024);
-    int ld = 0, hv[2] = {0, 0};  // loads used, P halves used per tile
+    const bool leader = elect_one();
+    int ld = 0;            // loads used
+    int cs0 = 0, cs1 = 0;  // score tiles used, per row tile
     bool ok = true;
-    auto wait_kv = [&](int i) {
-      ok = ok && mbar_wait(&kv_full[i % NST], (i / NST) & 1, &abort_flag);
-      tc_fence_after();
+    auto wait = [&](uint64_t* bar, int phase) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &abort_flag));
     };
     auto qk = [&](int t, int i) {
       const uint64_t kd = kdesc + (uint64_t)((i % NST) * (L::kTile >> 4)), qd = qdesc + (uint64_t)(t * (L::kTile >> 4));
+      tc_fence_after();
+      if (leader) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t o = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-        umma_bf16(tmem + t * BN, qd + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+          umma_bf16(tmem + t * BN, qd + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[t]);
       }
-      umma_commit(&s_full[t]);
+    };
+    auto pv = [&](int t, int h, uint64_t vd, bool first) {
+      const uint32_t s = tmem + t * BN + h * (HC / 2), o = tmem + 2 * BN + t * 128;
+      tc_fence_after();
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < HC / 16; ++kk)
+          umma_bf16_ts(o, s + kk * 8, vd + (uint64_t)(((h * (HC / 16) + kk) * 2048) >> 4), idesc_pv,
+                       first && kk == 0 ? 0u : 1u);
+        umma_commit(&o_done[t][h]);
+      }
     };
     Work w;
     for (int it = 0; ok && take_work(it, w); ++it) {
-      if (lane == 0) {
-        const int n = max(w.nt[0], w.nt[1]);
-        // load numbers: K_0 = 0, K_j = 2j - 1, V_j = 2j + 2 (the last V: 2n - 1)
-        ok = mbar_wait(&q_full, it & 1, &abort_flag);
-        if (ok) wait_kv(ld);
-        if (ok) {
-          for (int t = 0; t < 2; ++t)
-            if (w.nt[t] > 0) qk(t, ld);
-          umma_commit(&kv_empty[ld % NST]);
-          if (n == 1) umma_commit(&q_empty);
+      const int n = max(w.nt[0], w.nt[1]);
+      // load numbers: K_0 = 0, K_j = 2j - 1, V_j = 2j + 2 (the last V: 2n - 1)
+      wait(&q_full, it);
+      wait(&kv_full[ld % NST], ld / NST);
+      if (!ok) break;
+      if (w.nt[0] > 0) qk(0, ld);
+      if (w.nt[1] > 0) qk(1, ld);
+      if (leader) {
+        umma_commit(&kv_empty[ld % NST]);
+        if (n == 1) umma_commit(&q_empty);
+      }
+      for (int j = 0; j < n; ++j) {
+        const int iv = ld + (j + 1 < n ? 2 * j + 2 : 2 * n - 1), ik = ld + 2 * j + 1;
+        const uint64_t vd = vdesc + (uint64_t)((iv % NST) * (L::kTile >> 4));
+        wait(&kv_full[iv % NST], iv / NST);
+        if (j + 1 < n) wait(&kv_full[ik % NST], ik / NST);
+        if (j < w.nt[0]) {
+          wait(&p_full[0][0], cs0);
+          if (ok) pv(0, 0, vd, j == 0);
+          wait(&p_full[0][1], cs0);
+          if (ok) pv(0, 1, vd, false);
+          ++cs0;
+          if (ok && j + 1 < w.nt[0]) qk(0, ik);
         }
-        for (int j = 0; j < n && ok; ++j) {
-          const int iv = ld + (j + 1 < n ? 2 * j + 2 : 2 * n - 1), ik = ld + 2 * j + 1;
-          const uint64_t vd = vdesc + (uint64_t)((iv % NST) * (L::kTile >> 4));
-          bool have_v = false, have_k = false;
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (j >= w.nt[t]) continue;
-            const uint32_t s = tmem + t * BN, o = tmem + 2 * BN + t * 128;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              ok = ok && mbar_wait(&p_full[t][h], (hv[t] >> 1) & 1, &abort_flag);
-              if (!have_v) {
-                wait_kv(iv);
-                have_v = true;
-              }
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < HC / 16; ++kk)
-                umma_bf16_ts(o, s + h * (HC / 2) + kk * 8, vd + (uint64_t)(((h * (HC / 16) + kk) * 2048) >> 4), idesc_pv,
-                             j > 0 || h > 0 || kk > 0 ? 1u : 0u);
-              umma_commit(&o_done[t][h]);
-              ++hv[t];
-            }
-            if (ok && j + 1 < w.nt[t]) {
-              if (!have_k) {
-                wait_kv(ik);
-                have_k = true;
-              }
-              if (ok) qk(t, ik);
-            }
-          }
-          if (!ok) break;
+        if (j < w.nt[1]) {
+          wait(&p_full[1][0], cs1);
+          if (ok) pv(1, 0, vd, j == 0);
+          wait(&p_full[1][1], cs1);
+          if (ok) pv(1, 1, vd, false);
+          ++cs1;
+          if (ok && j + 1 < w.nt[1]) qk(1, ik);
+        }
+        if (!ok) break;
+        if (leader) {
           umma_commit(&kv_empty[iv % NST]);
           if (j + 1 < n) umma_commit(&kv_empty[ik % NST]);
           if (j + 2 == n) umma_commit(&q_empty);  // the item's last QK is out
         }
-        ld += 2 * n;
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ld += 2 * n;
     }
-    if (lane == 0) {  // every MMA has completed before TMEM is freed
+    if (leader) {  // every MMA has completed before TMEM is freed
       umma_commit(&drain);
       mbar_wait(&drain, 0, &abort_flag);
     }
