@@ -68,10 +68,10 @@ __device__ __forceinline__ int prompt_find(const PromptArgs& a, long long tile, 
   return lo;
 }
 
-// Flags every request whose own arguments are out of range (one CTA of a call
-// does it; the others leave such requests out).
-__device__ __forceinline__ void prompt_flag_requests(const PromptArgs& a) {
-  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+// Flags every request whose own arguments are out of range: `count` threads of
+// one CTA of a call do it; every CTA leaves such requests out.
+__device__ __forceinline__ void prompt_flag_requests(const PromptArgs& a, int thread, int count) {
+  for (int b = thread; b < a.B; b += count) {
     const int off = a.seq_off[b];
     const int bad = prompt_check(a, off, a.seq_off[b + 1] - off, a.prefix_len[b]);
     if (bad) atomicOr(&a.status[b], bad);

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
   S& sm = *reinterpret_cast<S*>(dyn);
   __shared__ int s_badblk;
   const int kvh = blockIdx.z, split = blockIdx.y;
-  if (blockIdx.x == 0 && split == 0 && kvh == 0) prompt_flag_requests(a);
+  if (blockIdx.x == 0 && split == 0 && kvh == 0) prompt_flag_requests(a, threadIdx.x, kPrThreads);
   // the last tiles of a request see the most keys: they start first
   const long long tile = (long long)gridDim.x - 1 - blockIdx.x;
   const int g = a.g;

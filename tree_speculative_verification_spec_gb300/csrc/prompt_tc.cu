@@ -10,8 +10,12 @@
 // The two tiles share every K and V stage, and while one tile's scores are in
 // the softmax the tensor core works for the other:
 //   ... PV_j(0) QK_{j+1}(0) | PV_j(1) QK_{j+1}(1) | PV_{j+1}(0) ...
-// One thread issues all MMAs; they complete in that order, so S_t may be
-// overwritten right after PV_j(t) without a wait.
+// Each tile's MMAs are issued by a warp of its own (a wait behind issued MMAs
+// returns only once the tensor core has taken them, and the other tile's are
+// then already queued).  They complete in the order of issue, so S_t may be
+// overwritten right after PV_j(t) without a wait.  The two warps take turns,
+// PV and QK of a step at a time: left alone they fall in step, both tiles'
+// MMAs at one time and both tiles' softmaxes at another.
 //
 // Reference m of a row: softmax(x) = 2^(xc - m) / sum 2^(xc - m) for ANY m, so
 // m is the maximum of the row's first visible half tile and stays, with no
@@ -35,7 +39,7 @@ constexpr int BM = 128;              // rows per tile (M of the MMA)
 constexpr int BN = 128;              // keys per step
 constexpr int kRows = kPromptTcRows; // rows per work item
 constexpr int HC = BN / 2;           // keys per softmax half
-constexpr int kThreads = 384;        // warps: 0 K/V loads, 1 MMA, 2 work items, 3 Q loads, 4-7 tile 0, 8-11 tile 1
+constexpr int kThreads = 384;        // warps: 0 K/V loads, 1 and 3 MMA of tiles 0 and 1, 2 work items and Q loads, 4-7 softmax of tile 0, 8-11 of tile 1
 constexpr uint32_t kTmemCols = 512;  // S_0, S_1 at 0, 128; O_0, O_1 at 256, 384
 constexpr float kSumLimit = 1152921504606846976.0f;  // 2^60
 constexpr int kOrderMax = 256;       // batches up to this size run longest request first
@@ -54,7 +58,6 @@ template <int D> struct Layout {
 struct Params {
   PromptArgs a;
   long long rows_total;  // num_blocks * Hkv * block_size: rows of the 2-D cache view
-  long long items;       // work items the grid numbers (upper bound)
   int box_rows;          // rows per TMA box: min(block_size, 128)
   int q_tma;             // Q by TMA (g divides 128), else by cp.async
 };
@@ -180,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PromptArgs& a = prm.a;
   extern __shared__ uint8_t dyn_raw[];
   __shared__ uint64_t kv_full[NST], kv_empty[NST], s_full[2], p_full[2][2], o_done[2][2], q_full, q_empty, w_full[2],
-      w_empty[2], drain;
+      w_empty[2], turn[2], drain[2], next_full;
+  __shared__ __align__(16) uint4 next_cta[1];
   __shared__ Work work[2];
   __shared__ Order order;
   __shared__ uint32_t tmem_slot;
@@ -189,11 +193,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
-  if (blockIdx.x == 0) prompt_flag_requests(a);
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 2);  // both MMA warps
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
@@ -202,11 +205,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&o_done[t][0], 1);
       mbar_init(&o_done[t][1], 1);
       mbar_init(&w_full[t], 1);
-      mbar_init(&w_empty[t], 11);  // K/V, MMA and Q warps, eight softmax warps
+      mbar_init(&w_empty[t], 11);  // K/V warp, two MMA warps, eight softmax warps
     }
     mbar_init(&q_full, 1);
-    mbar_init(&q_empty, 1);
-    mbar_init(&drain, 1);
+    mbar_init(&q_empty, 2);
+    mbar_init(&next_full, 1);
+    mbar_init(&turn[0], 1);
+    mbar_init(&turn[1], 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -227,26 +234,89 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
+  // The waits of the MMA and softmax warps.  Every lane polls, and nothing
+  // branches on the outcome: a wait that runs out sets the abort flag, every
+  // later wait then ends after a few polls, and the item runs to its end on
+  // whatever it finds (its request is flagged, its rows are unspecified).
+  // A vote on the outcome of each wait measured 1335 -> 1555 us on one prompt
+  // of 16384 tokens, one polling lane and a shuffle 1998 us.
+  auto wait = [&](uint64_t* bar, int phase) { mbar_wait(bar, phase & 1, &abort_flag); };
   // The next work item of a consumer warp; false at the end (or on a timeout).
   auto take_work = [&](int it, Work& w) -> bool {
     const bool ok = mbar_wait(&w_full[it & 1], (it >> 1) & 1, &abort_flag);
-    if (!__all_sync(0xffffffffu, ok)) return false;
+    if (!__all_sync(0xffffffffu, ok && !*(volatile int*)&abort_flag)) return false;
     w = work[it & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&w_empty[it & 1]);
     return w.valid;
   };
 
+  // The Q tiles of an item (one warp): row r = (token r / g, head kvh * g + r % g).
+  auto load_q = [&](const Work& w) {
+    const int tiles = w.nt[1] > 0 ? 2 : 1;
+    if (prm.q_tma) {
+      if (lane == 0) {
+        mbar_expect_tx(&q_full, tiles * L::kTile);
+        for (int t = 0; t < tiles; ++t)
+#pragma unroll
+          for (int h = 0; h < L::DH; ++h)
+            tma_load_3d(sbase + t * L::kTile + h * (BM * 128), &tmap_q, h * 64, w.kvh * a.g,
+                        w.off + (w.r0 + t * BM) / a.g, &q_full);
+      }
+      return;
+    }
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+    constexpr int CPR = D / 8;  // 16-byte chunks per row
+    const long long R = (long long)w.n * a.g;
+    for (int c = lane; c < tiles * BM * CPR; c += 32) {
+      const int r = c / CPR, ch = c % CPR, t = r / BM, rr = r % BM;
+      const uint32_t at = t * L::kTile + (ch >> 3) * (BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+      const long long row = (long long)w.r0 + r;
+      if (row < R)
+        cp_async16(sbase + at, q + ((size_t)(w.off + row / a.g) * a.Hq + w.kvh * a.g + row % a.g) * D + ch * 8);
+      else
+        *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
+    }
+    cp_async_wait();
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full);
+  };
+
+  // registers: 128 x 80 + 256 x 208 = 63488 of the 384 x 168 the CTA was launched with
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   if (warp == 2) {
-    // ------------------------------------------------------ work items
+    // ------------------------------------------------------ work items, Q tiles
+    // item it + 1 is handed out once item it's Q loads are out
+    if (lane == 0 && prm.q_tma)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
+    // item it + 1 is asked for (the launch of a CTA that has not begun is taken
+    // over, so that items go to whichever SM is free) while item it runs
+    int issued = 0, asked = 0;
+    auto ask = [&]() {
+      if (lane == 0) {
+        mbar_expect_tx(&next_full, 16);
+        launch_try_cancel(next_cta, &next_full);
+      }
+      ++asked;
+    };
+    auto answer = [&]() -> long long {  // the next item, -1 when none is left
+      int id = -1;
+      if (lane == 0 && mbar_wait(&next_full, (asked - 1) & 1, &abort_flag)) id = launch_cancelled(next_cta);
+      if (lane == 0) fence_async_smem();  // read before the next answer is written
+      return __shfl_sync(0xffffffffu, id, 0);
+    };
     long long idx = blockIdx.x;
     for (int it = 0;; ++it) {
       Work w = {};
-      for (; idx < prm.items; idx += gridDim.x) {
+      if (it > 0) idx = answer();
+      while (idx >= 0) {
+        ask();
+        if (idx == 0) prompt_flag_requests(a, lane, 32);
         w = find_work(prm, order, idx, lane);
         if (w.valid) break;
+        idx = answer();
       }
-      idx += gridDim.x;
       bool ok = true;
       if (it >= 2 && lane == 0) ok = mbar_wait(&w_empty[it & 1], ((it >> 1) - 1) & 1, &abort_flag);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
@@ -255,6 +325,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&w_full[it & 1]);
       }
       if (!w.valid) break;
+      if (lane == 0 && it >= 1) ok = mbar_wait(&q_empty, (it - 1) & 1, &abort_flag);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      load_q(w);
+      issued = it + 1;
+    }
+    if (lane == 0) {  // the last copy, and on a timeout the last answer, have landed
+      if (issued > 0) mbar_wait(&q_full, (issued - 1) & 1, &abort_flag);
+      if (asked > 0) mbar_wait(&next_full, (asked - 1) & 1, &abort_flag);
     }
   } else if (warp == 0) {
     // ------------------------------------------------------ K/V producer
@@ -301,97 +379,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every issued load has landed before the CTA can exit
     if (lane == 0)
       for (int i = max(0, ld - NST); i < ld; ++i) mbar_wait(&kv_full[i % NST], (i / NST) & 1, &abort_flag);
-  } else if (warp == 3) {
-    // ------------------------------------------------------ Q tiles
-    // row r = (token r / g, head kvh * g + r % g)
-    if (lane == 0 && prm.q_tma)
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
-    Work w;
-    bool go = true;
-    int issued = 0;
-    for (int it = 0; go && take_work(it, w); ++it) {
-      if (lane == 0 && it >= 1) go = mbar_wait(&q_empty, (it - 1) & 1, &abort_flag);
-      go = __shfl_sync(0xffffffffu, go, 0);
-      if (!go) break;
-      const int tiles = w.nt[1] > 0 ? 2 : 1;
-      if (prm.q_tma) {
-        if (lane == 0) {
-          mbar_expect_tx(&q_full, tiles * L::kTile);
-          for (int t = 0; t < tiles; ++t)
-#pragma unroll
-            for (int h = 0; h < L::DH; ++h)
-              tma_load_3d(sbase + t * L::kTile + h * (BM * 128), &tmap_q, h * 64, w.kvh * a.g,
-                          w.off + (w.r0 + t * BM) / a.g, &q_full);
-        }
-      } else {
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-        constexpr int CPR = D / 8;  // 16-byte chunks per row
-        const long long R = (long long)w.n * a.g;
-        for (int c = lane; c < tiles * BM * CPR; c += 32) {
-          const int r = c / CPR, ch = c % CPR, t = r / BM, rr = r % BM;
-          const uint32_t at = t * L::kTile + (ch >> 3) * (BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
-          const long long row = (long long)w.r0 + r;
-          if (row < R)
-            cp_async16(sbase + at, q + ((size_t)(w.off + row / a.g) * a.Hq + w.kvh * a.g + row % a.g) * D + ch * 8);
-          else
-            *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
-        }
-        cp_async_wait();
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full);
-      }
-      issued = it + 1;
-    }
-    if (lane == 0 && issued > 0) mbar_wait(&q_full, (issued - 1) & 1, &abort_flag);  // the last copy has landed
-  } else if (warp == 1) {
-    // ------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop (so that descriptors stay warp-uniform) and
-    // one elected lane issues.
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------ MMA issuers
+    // warp 1: tile 0, warp 3: tile 1.  The whole warp runs the loop (so that
+    // descriptors stay warp-uniform) and one elected lane issues.  A tile that
+    // has no work in a step still gives the step's stages back.
+    const int t = warp >> 1;
     constexpr uint32_t idesc_qk = idesc_bf16(BN, 0), idesc_pv = idesc_bf16(D, 1);
-    const uint64_t qdesc = smem_desc_sw128(sbase, 16, 1024);
+    const uint64_t qd = smem_desc_sw128(sbase + t * L::kTile, 16, 1024);
     const uint64_t kdesc = smem_desc_sw128(sbase + L::kOffKV, 16, 1024);
     const uint64_t vdesc = smem_desc_sw128(sbase + L::kOffKV, BN * 128, 1024);
+    const uint32_t tS = tmem + t * BN, tO = tmem + 2 * BN + t * 128;
     const bool leader = elect_one();
-    int ld = 0;            // loads used
-    int cs0 = 0, cs1 = 0;  // score tiles used, per row tile
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, int phase) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &abort_flag));
-    };
-    auto qk = [&](int t, int i) {
-      const uint64_t kd = kdesc + (uint64_t)((i % NST) * (L::kTile >> 4)), qd = qdesc + (uint64_t)(t * (L::kTile >> 4));
-      tc_fence_after();
-      if (leader) {
+    int ld = 0, cs = 0, turns = 0;  // loads and score tiles used, turns taken
+    // the elected lane's issues
+    auto qk = [&](int i) {
+      const uint64_t kd = kdesc + (uint64_t)((i % NST) * (L::kTile >> 4));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-          umma_bf16(tmem + t * BN, qd + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
-        }
-        umma_commit(&s_full[t]);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+        umma_bf16(tS, qd + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
       }
+      umma_commit(&s_full[t]);
     };
-    auto pv = [&](int t, int h, uint64_t vd, bool first) {
-      const uint32_t s = tmem + t * BN + h * (HC / 2), o = tmem + 2 * BN + t * 128;
-      tc_fence_after();
-      if (leader) {
+    auto pv = [&](int h, uint64_t vd, bool first) {
 #pragma unroll
-        for (int kk = 0; kk < HC / 16; ++kk)
-          umma_bf16_ts(o, s + kk * 8, vd + (uint64_t)(((h * (HC / 16) + kk) * 2048) >> 4), idesc_pv,
-                       first && kk == 0 ? 0u : 1u);
-        umma_commit(&o_done[t][h]);
-      }
+      for (int kk = 0; kk < HC / 16; ++kk)
+        umma_bf16_ts(tO, tS + h * (HC / 2) + kk * 8, vd + (uint64_t)(((h * (HC / 16) + kk) * 2048) >> 4), idesc_pv,
+                     first && kk == 0 ? 0u : 1u);
+      umma_commit(&o_done[t][h]);
     };
     Work w;
-    for (int it = 0; ok && take_work(it, w); ++it) {
-      const int n = max(w.nt[0], w.nt[1]);
+    for (int it = 0; take_work(it, w); ++it) {
+      const int nt = t == 0 ? w.nt[0] : w.nt[1], n = max(w.nt[0], w.nt[1]);
       // load numbers: K_0 = 0, K_j = 2j - 1, V_j = 2j + 2 (the last V: 2n - 1)
       wait(&q_full, it);
       wait(&kv_full[ld % NST], ld / NST);
-      if (!ok) break;
-      if (w.nt[0] > 0) qk(0, ld);
-      if (w.nt[1] > 0) qk(1, ld);
+      tc_fence_after();
       if (leader) {
+        if (nt > 0) qk(ld);
         umma_commit(&kv_empty[ld % NST]);
         if (n == 1) umma_commit(&q_empty);
       }
@@ -400,23 +426,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vd = vdesc + (uint64_t)((iv % NST) * (L::kTile >> 4));
         wait(&kv_full[iv % NST], iv / NST);
         if (j + 1 < n) wait(&kv_full[ik % NST], ik / NST);
-        if (j < w.nt[0]) {
-          wait(&p_full[0][0], cs0);
-          if (ok) pv(0, 0, vd, j == 0);
-          wait(&p_full[0][1], cs0);
-          if (ok) pv(0, 1, vd, false);
-          ++cs0;
-          if (ok && j + 1 < w.nt[0]) qk(0, ik);
+        if (t == 1 || turns > 0) wait(&turn[t], t == 1 ? turns : turns - 1);
+        ++turns;
+        if (j < nt) {
+          wait(&p_full[t][0], cs);
+          tc_fence_after();
+          if (leader) pv(0, vd, j == 0);
+          wait(&p_full[t][1], cs);
+          ++cs;
+          tc_fence_after();
         }
-        if (j < w.nt[1]) {
-          wait(&p_full[1][0], cs1);
-          if (ok) pv(1, 0, vd, j == 0);
-          wait(&p_full[1][1], cs1);
-          if (ok) pv(1, 1, vd, false);
-          ++cs1;
-          if (ok && j + 1 < w.nt[1]) qk(1, ik);
+        // short branches: one long branch of the elected lane for PV, QK and
+        // the commits measured 1320 -> 1490 us on one prompt of 16384 tokens
+        if (j < nt && leader) pv(1, vd, false);
+        if (j + 1 < nt) {
+          tc_fence_after();
+          if (leader) {
+            qk(ik);
+            mbar_arrive(&turn[t ^ 1]);
+          }
+        } else if (leader) {
+          mbar_arrive(&turn[t ^ 1]);
         }
-        if (!ok) break;
         if (leader) {
           umma_commit(&kv_empty[iv % NST]);
           if (j + 1 < n) umma_commit(&kv_empty[ik % NST]);
@@ -426,11 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ld += 2 * n;
     }
     if (leader) {  // every MMA has completed before TMEM is freed
-      umma_commit(&drain);
-      mbar_wait(&drain, 0, &abort_flag);
+      umma_commit(&drain[t]);
+      mbar_wait(&drain[t], 0, &abort_flag);
     }
   } else {
     // ------------------------------------------------------ softmax, epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = (warp - 4) >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -438,29 +470,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c2 = a.scale_log2;
     const float2 c22 = make_float2(c2, c2);
     int ld = 0, cs = 0;  // loads so far (as the MMA warp counts them), score tiles of this row tile
-    bool ok = true;
-    auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag));
+    float m = 0.0f, l = 0.0f;  // the row's reference (log2 domain) and sum
+    // weights 2^(x c - ref) of 64 columns, `vis` of them visible, packed to bf16; returns their sum
+    auto half_weights = [&](uint32_t (&x0)[32], uint32_t (&x1)[32], int vis, float ref, uint32_t (&pk)[HC / 2]) -> float {
+      if (!__all_sync(0xffffffffu, vis >= HC)) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          if (e >= vis) x0[e] = 0xff800000u;
+          if (32 + e >= vis) x1[e] = 0xff800000u;
+        }
+      }
+      const float2 neg = make_float2(-ref, -ref);
+      float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
+#pragma unroll
+      for (int e = 0; e < HC; e += 2) {
+        const float2 s = e < 32 ? make_float2(__uint_as_float(x0[e & 31]), __uint_as_float(x0[(e & 31) + 1]))
+                                : make_float2(__uint_as_float(x1[e & 31]), __uint_as_float(x1[(e & 31) + 1]));
+        const float2 z = __ffma2_rn(s, c22, neg);
+        const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+        if (e & 2) acc1 = __fadd2_rn(acc1, p);
+        else acc0 = __fadd2_rn(acc0, p);
+        __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
+        pk[e >> 1] = *reinterpret_cast<uint32_t*>(&h2);
+      }
+      return (acc0.x + acc0.y) + (acc1.x + acc1.y);
+    };
+    // Half h again, from its scores in tensor memory, against a reference that
+    // covers it: a row's first visible half, or scores that outgrew the old
+    // one.  The sum and O (when it holds anything) are scaled to the new one.
+    auto redo = [&](int h, int vis, bool have_o, uint32_t (&pk)[HC / 2], float& sum) {
+      uint32_t x0[32], x1[32];
+      tmem_ld32(tS + h * HC, x0);
+      tmem_ld32(tS + h * HC + 32, x1);
+      tmem_wait_ld(x0);
+      tmem_wait_ld(x1);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        mx = fmax3(mx, e < vis ? __uint_as_float(x0[e]) : -INFINITY, 32 + e < vis ? __uint_as_float(x1[e]) : -INFINITY);
+      const float to = fmaxf(m, mx * c2);
+      const float f = m == -INFINITY ? 0.0f : fast_exp2(m - to);
+      l *= f;
+      m = to;
+      sum = half_weights(x0, x1, vis, to == -INFINITY ? 0.0f : to, pk);
+      if (!have_o || !__any_sync(0xffffffffu, f != 1.0f)) return;
+      // O holds every earlier half once the last of them has completed: this
+      // tile's first, or the previous tile's second (one barrier for each, so
+      // that a wait is never two phases behind)
+      wait(&o_done[t][h ^ 1], h == 1 ? cs : cs - 1);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        tmem_ld32(tO + c * 32, x0);
+        tmem_wait_ld(x0);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x0[e] = __float_as_uint(__uint_as_float(x0[e]) * f);
+        tmem_st32(tO + c * 32, x0);
+      }
     };
     Work w;
-    for (int it = 0; ok && take_work(it, w); ++it) {
+    for (int it = 0; take_work(it, w); ++it) {
       const int nt = t == 0 ? w.nt[0] : w.nt[1], n = max(w.nt[0], w.nt[1]), Lk = w.P + w.n;
       const int row = w.r0 + t * BM + r;
       const bool valid = row < (long long)w.n * a.g;
       const int tok = valid ? row / a.g : w.n - 1;
       const int lim = w.P + tok + 1 - w.k_begin;  // visible keys of this range
-      float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < nt && ok; ++j, ++cs) {
-        ok = wait_warp(&s_full[t], cs & 1);
-        if (!ok) break;
+      m = -INFINITY;
+      l = 0.0f;
+      for (int j = 0; j < nt; ++j, ++cs) {
+        wait(&s_full[t], cs);
         tc_fence_after();
         const int k0 = w.k_begin + j * BN;
         if (k0 + BN > Lk) {
           // the tile reaches past the request: its V rows there are zeroed, so
           // that no stale bits (NaN among them) meet a zero probability
           const int iv = ld + 2 * n - 1;  // only the range's last tile can
-          ok = wait_warp(&kv_full[iv % NST], (iv / NST) & 1);
-          if (!ok) break;
+          wait(&kv_full[iv % NST], iv / NST);
           const int zr = Lk - k0;
           uint8_t* vst = smem + L::kOffKV + (iv % NST) * L::kTile;
           for (int i = r; i < (BN - zr) * L::DH * 8; i += BM) {
@@ -470,95 +555,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_async_smem();
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int vis = lim - j * BN - h * HC;  // visible columns of this half
-          const bool full = __all_sync(0xffffffffu, vis >= HC);
-          uint32_t pk[HC / 2];
-          float sum = INFINITY;
-          uint32_t v0[32], v1[32];
-          tmem_ld32(tS + h * HC, v0);
-          tmem_ld32(tS + h * HC + 32, v1);
-          tmem_wait_ld(v0);
-          tmem_wait_ld(v1);
-          auto hide = [&]() {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (e >= vis) v0[e] = 0xff800000u;
-              if (32 + e >= vis) v1[e] = 0xff800000u;
-            }
-          };
-          if (!full) hide();
-          auto weights = [&](float ref) {
-            const float2 neg = make_float2(-ref, -ref);
-            float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v0[e]), __uint_as_float(v0[e + 1])), c22, neg);
-              const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-              acc0 = __fadd2_rn(acc0, p);
-              __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
-              pk[e >> 1] = *reinterpret_cast<uint32_t*>(&h2);
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v1[e]), __uint_as_float(v1[e + 1])), c22, neg);
-              const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-              acc1 = __fadd2_rn(acc1, p);
-              __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
-              pk[16 + (e >> 1)] = *reinterpret_cast<uint32_t*>(&h2);
-            }
-            sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
-          };
-          if (__all_sync(0xffffffffu, m != -INFINITY)) weights(m);
-          if (__any_sync(0xffffffffu, !(sum < kSumLimit))) {
-            // a first reference, or one that the scores have outgrown: this
-            // half again, from its scores in tensor memory
-            tmem_ld32(tS + h * HC, v0);
-            tmem_ld32(tS + h * HC + 32, v1);
-            tmem_wait_ld(v0);
-            tmem_wait_ld(v1);
-            if (!full) hide();
-            float mx = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmax3(mx, __uint_as_float(v0[e]), __uint_as_float(v1[e]));
-            const float to = fmaxf(m, mx * c2);
-            const float f = m == -INFINITY ? 0.0f : fast_exp2(m - to);
-            l *= f;
-            m = to;
-            weights(to == -INFINITY ? 0.0f : to);
-            if ((j > 0 || h > 0) && __any_sync(0xffffffffu, f != 1.0f)) {
-              // O holds every earlier half once the last of them has
-              // completed: this tile's first, or the previous tile's second
-              // (one barrier for each, so that a wait is never two phases behind)
-              ok = wait_warp(&o_done[t][h ^ 1], (h == 1 ? cs : cs - 1) & 1);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tO + c * 32, o);
-                tmem_wait_ld(o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(tO + c * 32, o);
-              }
-            }
-          }
-          l += sum;
-          tmem_st32(tS + h * (HC / 2), pk);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[t][h]);
+        // scores of both halves: the second half's load runs beside the first's weights
+        const int vis = lim - j * BN;  // visible columns of this tile
+        uint32_t x0[32], x1[32], y0[32], y1[32], pk[HC / 2];
+        tmem_ld32(tS, x0);
+        tmem_ld32(tS + 32, x1);
+        tmem_wait_ld(x0);
+        tmem_wait_ld(x1);
+        tmem_ld32(tS + HC, y0);
+        tmem_ld32(tS + HC + 32, y1);
+        float sum = half_weights(x0, x1, vis, m, pk);
+        if (__any_sync(0xffffffffu, !(sum < kSumLimit))) {
+          tmem_wait_ld(y0);
+          tmem_wait_ld(y1);
+          redo(0, vis, j > 0, pk, sum);
+          tmem_ld32(tS + HC, y0);
+          tmem_ld32(tS + HC + 32, y1);
         }
+        l += sum;
+        tmem_wait_ld(y0);
+        tmem_wait_ld(y1);
+        tmem_st32(tS, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t][0]);
+        sum = half_weights(y0, y1, vis - HC, m, pk);
+        if (__any_sync(0xffffffffu, !(sum < kSumLimit))) {
+          redo(1, vis - HC, true, pk, sum);
+        }
+        l += sum;
+        tmem_st32(tS + HC / 2, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t][1]);
       }
-      if (!ok) break;
       ld += 2 * n;
       if (nt == 0) continue;
       // epilogue: this thread's row
-      ok = wait_warp(&o_done[t][1], (cs - 1) & 1);
-      if (!ok) break;
+      wait(&o_done[t][1], cs - 1);
       tc_fence_after();
       const size_t orow = (size_t)(w.off + tok) * a.Hq + w.kvh * a.g + (valid ? row % a.g : 0);
       const float inv = 1.0f / l;
@@ -639,7 +675,8 @@ static cudaError_t launch_d(const PromptArgs& a, const PromptPlan& p, cudaStream
   prm.box_rows = std::min(a.block_size, ptc::BN);
   prm.rows_total = (long long)a.num_blocks * a.Hkv * a.block_size;
   if (prm.rows_total >= (long long)INT32_MAX) return cudaErrorInvalidValue;
-  prm.items = p.tiles * a.Hkv * p.splits;
+  const long long items = p.tiles * a.Hkv * p.splits;
+  if (items > INT32_MAX) return cudaErrorInvalidValue;
   alignas(64) CUtensorMap mk, mv, mq;
   {
     const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)prm.rows_total}, strides[1] = {(cuuint64_t)D * 2};
@@ -658,14 +695,11 @@ static cudaError_t launch_d(const PromptArgs& a, const PromptPlan& p, cudaStream
   } else {
     mq = mk;  // not read
   }
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int dyn = (int)ptc::Layout<D>::kDyn;
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(ptc::prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+  const cudaError_t e = cudaFuncSetAttribute(ptc::prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)std::min<long long>(prm.items, sms);
-  ptc::prompt_tc_kernel<D><<<grid, ptc::kThreads, dyn, stream>>>(mk, mv, mq, prm);
+  // one CTA per item; the CTAs that run take over the launches of the others
+  ptc::prompt_tc_kernel<D><<<(unsigned)items, ptc::kThreads, dyn, stream>>>(mk, mv, mq, prm);
   return cudaGetLastError();
 }
 

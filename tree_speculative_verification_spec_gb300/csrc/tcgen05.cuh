@@ -135,6 +135,17 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One column of this thread's lane; the load is complete on return.
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
+}
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r) : : "memory");
+  return __uint_as_float(r);
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle (layout type 2), sm_100
 // family descriptor version 1.  Addresses and offsets in bytes.
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -166,6 +177,44 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b, float& ra, float
   ra = __low2float(h);
   rb = __high2float(h);
   return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Meeting of the two warps that use named barrier `id`; whether `any` holds in
+// any of their 64 threads.
+__device__ __forceinline__ bool pair_any(int id, bool any) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(out)
+      : "r"(id), "r"((uint32_t)any)
+      : "memory");
+  return out != 0;
+}
+
+// Cluster launch control: ask for the launch of a CTA of this grid that has not
+// begun (16 bytes to `answer`, completing on `bar`), and the index of the CTA
+// whose launch was taken over (-1: none was left).
+__device__ __forceinline__ void launch_try_cancel(uint4* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ int launch_cancelled(const uint4* answer) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, h;\n\t}"
+      : "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return x;
 }
 
 // 16-byte asynchronous copy of this thread, and the wait for all of its copies.
