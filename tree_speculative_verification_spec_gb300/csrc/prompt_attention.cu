@@ -320,7 +320,7 @@ static spec_status prompt_shape_check(int B, int T, int n_max, int max_prefix, i
   if (block_size < 8 || block_size > 65536 || (block_size & (block_size - 1))) return SPEC_ERR_UNSUPPORTED;
   if (B > 65535 || Hkv > 65535 || (long long)n_max * (Hq / Hkv) >= (1LL << 30) || (long long)max_prefix + n_max >= (1LL << 30))
     return SPEC_ERR_UNSUPPORTED;
-  if ((long long)T * (Hq / Hkv) / kPrRows + B >= (1LL << 24) || (long long)T * Hq / 8 >= (1LL << 31) - 1)
+  if ((long long)T * (Hq / Hkv) / kPrRows + B >= (1LL << 24) || (long long)T * Hq >= (1LL << 31))
     return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
 }

@@ -17,13 +17,12 @@
 // PV and QK of a step at a time: left alone they fall in step, both tiles'
 // MMAs at one time and both tiles' softmaxes at another.
 //
-// Reference m of a row: softmax(x) = 2^(xc - m) / sum 2^(xc - m) for ANY m, so
-// m is the maximum of the row's first visible half tile and stays, with no
-// maximum taken per tile, as long as the sum of 64 weights stays below 2^60
-// (fp32 and bf16 have the exponents for it: both hold 2^127).  When it does
-// not, that half is done again against its own maximum, and O and the sum are
-// scaled down.  Underflow is the same as for the usual running maximum, which
-// is never below m.
+// Reference m of a row: softmax(x) = 2^(xc - m) / sum 2^(xc - m) for ANY m, and
+// fp32 and bf16 hold 2^127.  So m starts at 0 and no maximum is taken, as long
+// as the sum of 64 weights stays below 2^60 and the first visible ones reach
+// 2^-60 (smaller weights than 2^-60 of the largest do not show in 24 bits).
+// Otherwise that half tile is done again against its own maximum, and O and the
+// sum are scaled to it.
 #include <algorithm>
 
 #include "prompt.cuh"
@@ -39,7 +38,7 @@ constexpr int BM = 128;              // rows per tile (M of the MMA)
 constexpr int BN = 128;              // keys per step
 constexpr int kRows = kPromptTcRows; // rows per work item
 constexpr int HC = BN / 2;           // keys per softmax half
-constexpr int kThreads = 384;        // warps: 0 K/V loads, 1 and 3 MMA of tiles 0 and 1, 2 work items and Q loads, 4-7 softmax of tile 0, 8-11 of tile 1
+constexpr int kThreads = 384;        // warps: 0 K loads, 1 and 3 MMA of tiles 0 and 1, 2 work items, Q and V loads, 4-7 softmax of tile 0, 8-11 of tile 1
 constexpr uint32_t kTmemCols = 512;  // S_0, S_1 at 0, 128; O_0, O_1 at 256, 384
 constexpr float kSumLimit = 1152921504606846976.0f;  // 2^60
 constexpr int kOrderMax = 256;       // batches up to this size run longest request first
@@ -59,6 +58,7 @@ struct Params {
   PromptArgs a;
   long long rows_total;  // num_blocks * Hkv * block_size: rows of the 2-D cache view
   int box_rows;          // rows per TMA box: min(block_size, 128)
+  int bs_log2;           // block_size = 1 << bs_log2
   int q_tma;             // Q by TMA (g divides 128), else by cp.async
 };
 
@@ -103,13 +103,13 @@ __device__ __forceinline__ void order_requests(const PromptArgs& a, Order& o, in
 }
 
 // Work item `idx` (one warp, all lanes get it); valid = 0 when it is empty.
-__device__ __forceinline__ Work find_work(const Params& prm, const Order& o, long long idx, int lane) {
+__device__ __forceinline__ Work find_work(const Params& prm, const Order& o, uint32_t idx, int lane) {
   const PromptArgs& a = prm.a;
   Work w = {};
-  w.split = (int)(idx % a.splits);
-  idx /= a.splits;
-  w.kvh = (int)(idx % a.Hkv);
-  const long long tile = idx / a.Hkv;
+  w.split = (int)(idx % (uint32_t)a.splits);
+  idx /= (uint32_t)a.splits;
+  w.kvh = (int)(idx % (uint32_t)a.Hkv);
+  const int tile = (int)(idx / (uint32_t)a.Hkv);
   int b, mt;
   if (a.B <= kOrderMax) {
     if (tile >= o.first[a.B]) return w;
@@ -118,7 +118,7 @@ __device__ __forceinline__ Work find_work(const Params& prm, const Order& o, lon
     cnt = warp_sum_i(cnt);
     const int r = cnt - 1;
     b = o.req[r];
-    mt = o.first[r + 1] - 1 - (int)tile;  // the last rows see the most keys: first
+    mt = o.first[r + 1] - 1 - tile;  // the last rows see the most keys: first
   } else {
     int lo = 0, hi = a.B;  // first_tile(lo) <= tile < first_tile(hi), 32 probes a round
     while (hi - lo > 1) {
@@ -141,8 +141,8 @@ __device__ __forceinline__ Work find_work(const Params& prm, const Order& o, lon
   rq.n = __shfl_sync(0xffffffffu, rq.n, 0);
   rq.P = __shfl_sync(0xffffffffu, rq.P, 0);
   const bool ok = __shfl_sync(0xffffffffu, (int)rq.ok, 0);
-  const long long R = (long long)rq.n * a.g;
-  if (!ok || (long long)mt * kRows >= R) return w;
+  const int R = rq.n * a.g;  // < 2^30
+  if (!ok || mt >= (1 << 22) || mt * kRows >= R) return w;
   w.b = b;
   w.off = rq.off;
   w.n = rq.n;
@@ -151,9 +151,9 @@ __device__ __forceinline__ Work find_work(const Params& prm, const Order& o, lon
   w.k_begin = w.split * a.chunk;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const long long first = w.r0 + t * BM;
+    const int first = w.r0 + t * BM;
     if (first >= R) continue;
-    const int end = min(rq.P + (int)(min(first + BM, R) - 1) / a.g + 1, w.k_begin + a.chunk);
+    const int end = min(rq.P + (min(first + BM, R) - 1) / a.g + 1, w.k_begin + a.chunk);
     if (end > w.k_begin) w.nt[t] = (end - w.k_begin + BN - 1) / BN;
   }
   w.valid = w.nt[0] > 0 || w.nt[1] > 0;
@@ -167,11 +167,30 @@ __device__ __forceinline__ int box_row(const Params& prm, const int32_t* bt, int
   const PromptArgs& a = prm.a;
   int y = (int)prm.rows_total;
   if (k < Lk) {
-    const int blk = __ldg(bt + k / a.block_size);
-    if (blk >= 0 && blk < a.num_blocks) y = (int)(((long long)blk * a.Hkv + kvh) * a.block_size + k % a.block_size);
+    const int blk = __ldg(bt + (k >> prm.bs_log2));
+    if (blk >= 0 && blk < a.num_blocks) y = ((blk * a.Hkv + kvh) << prm.bs_log2) + (k & (a.block_size - 1));  // < rows_total
     else *bad = 1;
   }
   return y;
+}
+
+// 4 x 4 transpose among four neighbouring lanes: afterwards u[s] of lane i is
+// what u[i] of lane s was.
+__device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
+  auto swap = [&](uint4& a, uint4& b, int d) {  // lanes with bit d send a, the others b
+    const bool hi = lane & d;
+    uint4 x = hi ? a : b;
+    x.x = __shfl_xor_sync(0xffffffffu, x.x, d);
+    x.y = __shfl_xor_sync(0xffffffffu, x.y, d);
+    x.z = __shfl_xor_sync(0xffffffffu, x.z, d);
+    x.w = __shfl_xor_sync(0xffffffffu, x.w, d);
+    if (hi) a = x;
+    else b = x;
+  };
+  swap(u[0], u[1], 1);
+  swap(u[2], u[3], 1);
+  swap(u[0], u[2], 2);
+  swap(u[1], u[3], 2);
 }
 
 template <int D>
@@ -188,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Work work[2];
   __shared__ Order order;
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, kv_issued[NST], q_issued;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~(uintptr_t)1023);
@@ -196,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&kv_full[i], 1);
+      kv_issued[i] = -1;
       mbar_init(&kv_empty[i], 2);  // both MMA warps
     }
     for (int t = 0; t < 2; ++t) {
@@ -215,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     abort_flag = 0;
+    q_issued = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -265,17 +286,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return;
     }
+    // by 16-byte asynchronous copies: lane's chunk of every (32 / CPR)-th row,
+    // token and head of the row stepped along
+    constexpr int CPR = D / 8;        // 16-byte chunks per row
+    constexpr int STEP = 32 / CPR;    // rows per round
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-    constexpr int CPR = D / 8;  // 16-byte chunks per row
-    const long long R = (long long)w.n * a.g;
-    for (int c = lane; c < tiles * BM * CPR; c += 32) {
-      const int r = c / CPR, ch = c % CPR, t = r / BM, rr = r % BM;
-      const uint32_t at = t * L::kTile + (ch >> 3) * (BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
-      const long long row = (long long)w.r0 + r;
-      if (row < R)
-        cp_async16(sbase + at, q + ((size_t)(w.off + row / a.g) * a.Hq + w.kvh * a.g + row % a.g) * D + ch * 8);
+    const int ch = lane % CPR, rows = min(tiles * BM, w.n * a.g - w.r0);
+    int tok = (w.r0 + lane / CPR) / a.g, head = (w.r0 + lane / CPR) % a.g;
+    for (int r = lane / CPR; r < tiles * BM; r += STEP) {
+      const int rr = r % BM;
+      const uint32_t at = (r / BM) * L::kTile + (ch >> 3) * (BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+      if (r < rows)
+        cp_async16(sbase + at, q + ((size_t)(w.off + tok) * a.Hq + w.kvh * a.g + head) * D + ch * 8);
       else
         *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
+      for (head += STEP; head >= a.g; head -= a.g) ++tok;
     }
     cp_async_wait();
     fence_async_smem();
@@ -283,16 +308,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(&q_full);
   };
 
+  // One item's K or V tiles; false after a timeout.  K and V have a producer warp
+  // each, so that neither's box issue holds up the other (pages of 16 keys are
+  // 16 boxes a tile).  The ring's stages go round in the order of use, K_0, K_1,
+  // V_0, K_2, V_1, ..., and each producer takes its own.  Lane i issues the box
+  // of page (or 128-row piece) i of a tile; the table is read a tile before.
+  auto load_ring = [&](const CUtensorMap* map, const Work& w, int& ld, int is_v) -> bool {
+    const int br = prm.box_rows, nb = BN / br, n = max(w.nt[0], w.nt[1]), Lk = w.P + w.n;
+    const int32_t* bt = a.block_table + (size_t)w.b * a.max_blocks;
+    int bad = 0;
+    auto row = [&](int j) { return lane < nb ? box_row(prm, bt, w.kvh, w.k_begin + j * BN + lane * br, Lk, &bad) : 0; };
+    int y = row(0);
+    for (int j = 0; j < n; ++j) {
+      const int y1 = j + 1 < n ? row(j + 1) : 0;
+      const int i = ld + (is_v ? (j + 1 < n ? 2 * j + 2 : 2 * n - 1) : (j == 0 ? 0 : 2 * j - 1));
+      const int st = i % NST;
+      bool go = true;
+      if (lane == 0 && i >= NST) go = mbar_wait(&kv_empty[st], (i / NST - 1) & 1, &abort_flag);
+      if (!__shfl_sync(0xffffffffu, (int)go, 0)) return false;
+      if (lane == 0) {
+        mbar_expect_tx(&kv_full[st], L::kTile);
+        kv_issued[st] = i;
+      }
+      __syncwarp();
+      if (lane < nb) {
+        const uint32_t dst = sbase + L::kOffKV + st * L::kTile + lane * br * 128;
+#pragma unroll
+        for (int h = 0; h < L::DH; ++h) tma_load_2d(dst + h * (BN * 128), map, h * 64, y, &kv_full[st]);
+      }
+      y = y1;
+    }
+    if (!is_v && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
+    ld += 2 * n;
+    return true;
+  };
+
   // registers: 128 x 80 + 256 x 208 = 63488 of the 384 x 168 the CTA was launched with
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   if (warp == 2) {
-    // ------------------------------------------------------ work items, Q tiles
-    // item it + 1 is handed out once item it's Q loads are out
-    if (lane == 0 && prm.q_tma)
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
+    // ------------------------------------------------------ work items, Q and V tiles
+    // item it + 1 is handed out once item it's loads are out
+    if (lane == 0) {
+      if (prm.q_tma) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
+    }
     // item it + 1 is asked for (the launch of a CTA that has not begun is taken
     // over, so that items go to whichever SM is free) while item it runs
-    int issued = 0, asked = 0;
+    int asked = 0, ld = 0;
     auto ask = [&]() {
       if (lane == 0) {
         mbar_expect_tx(&next_full, 16);
@@ -300,20 +362,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++asked;
     };
-    auto answer = [&]() -> long long {  // the next item, -1 when none is left
+    auto answer = [&]() -> int {  // the next item, -1 when none is left
       int id = -1;
       if (lane == 0 && mbar_wait(&next_full, (asked - 1) & 1, &abort_flag)) id = launch_cancelled(next_cta);
       if (lane == 0) fence_async_smem();  // read before the next answer is written
       return __shfl_sync(0xffffffffu, id, 0);
     };
-    long long idx = blockIdx.x;
+    int idx = (int)blockIdx.x;
     for (int it = 0;; ++it) {
       Work w = {};
       if (it > 0) idx = answer();
       while (idx >= 0) {
         ask();
         if (idx == 0) prompt_flag_requests(a, lane, 32);
-        w = find_work(prm, order, idx, lane);
+        w = find_work(prm, order, (uint32_t)idx, lane);
         if (w.valid) break;
         idx = answer();
       }
@@ -328,57 +390,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && it >= 1) ok = mbar_wait(&q_empty, (it - 1) & 1, &abort_flag);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       load_q(w);
-      issued = it + 1;
+      if (lane == 0) q_issued = it;
+      if (!load_ring(&tmap_v, w, ld, 1)) break;
     }
-    if (lane == 0) {  // the last copy, and on a timeout the last answer, have landed
-      if (issued > 0) mbar_wait(&q_full, (issued - 1) & 1, &abort_flag);
-      if (asked > 0) mbar_wait(&next_full, (asked - 1) & 1, &abort_flag);
-    }
+    if (lane == 0 && asked > 0) mbar_drain(&next_full, (asked - 1) & 1);
   } else if (warp == 0) {
-    // ------------------------------------------------------ K/V producer
-    // lane i issues the box of page (or 128-row piece) i of each tile; the
-    // order K_0, K_1, V_0, K_2, V_1, ... is the order of use
-    if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
-    }
-    const int br = prm.box_rows, nb = BN / br;
-    int ld = 0;  // loads issued so far
-    bool go = true;
-    auto load = [&](const CUtensorMap* map, int y) {
-      const int st = ld % NST;
-      if (lane == 0 && ld >= NST) go = mbar_wait(&kv_empty[st], (ld / NST - 1) & 1, &abort_flag);
-      go = __shfl_sync(0xffffffffu, go, 0);
-      if (!go) return;
-      if (lane == 0) mbar_expect_tx(&kv_full[st], L::kTile);
-      __syncwarp();
-      if (lane < nb) {
-        const uint32_t dst = sbase + L::kOffKV + st * L::kTile + lane * br * 128;
-#pragma unroll
-        for (int h = 0; h < L::DH; ++h) tma_load_2d(dst + h * (BN * 128), map, h * 64, y, &kv_full[st]);
-      }
-      ++ld;
-    };
+    // ------------------------------------------------------ K producer
+    if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
     Work w;
-    for (int it = 0; go && take_work(it, w); ++it) {
-      const int n = max(w.nt[0], w.nt[1]), Lk = w.P + w.n;
-      const int32_t* bt = a.block_table + (size_t)w.b * a.max_blocks;
-      int bad = 0;
-      auto row = [&](int j) { return lane < nb ? box_row(prm, bt, w.kvh, w.k_begin + j * BN + lane * br, Lk, &bad) : 0; };
-      int y = row(0), y1 = n > 1 ? row(1) : 0;
-      load(&tmap_k, y);
-      for (int j = 0; j < n && go; ++j) {
-        const int y2 = j + 2 < n ? row(j + 2) : 0;  // the table is read a tile before its box goes out
-        if (j + 1 < n) load(&tmap_k, y1);
-        if (go) load(&tmap_v, y);
-        y = y1;
-        y1 = y2;
-      }
-      if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
-    }
-    // every issued load has landed before the CTA can exit
-    if (lane == 0)
-      for (int i = max(0, ld - NST); i < ld; ++i) mbar_wait(&kv_full[i % NST], (i / NST) & 1, &abort_flag);
+    int ld = 0;
+    for (int it = 0; take_work(it, w); ++it)
+      if (!load_ring(&tmap_k, w, ld, 0)) break;
   } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------ MMA issuers
     // warp 1: tile 0, warp 3: tile 1.  The whole warp runs the loop (so that
@@ -458,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (leader) {  // every MMA has completed before TMEM is freed
       umma_commit(&drain[t]);
-      mbar_wait(&drain[t], 0, &abort_flag);
+      mbar_drain(&drain[t], 0);
     }
   } else {
     // ------------------------------------------------------ softmax, epilogue
@@ -495,9 +517,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return (acc0.x + acc0.y) + (acc1.x + acc1.y);
     };
+    // Whether half weights that sum to `sum` need another reference.
+    auto unfit = [&](float sum, int vis) -> bool {
+      return __any_sync(0xffffffffu, !(sum < kSumLimit) || (l == 0.0f && vis > 0 && sum < 1.0f / kSumLimit));
+    };
     // Half h again, from its scores in tensor memory, against a reference that
-    // covers it: a row's first visible half, or scores that outgrew the old
-    // one.  The sum and O (when it holds anything) are scaled to the new one.
+    // covers it.  A row with nothing summed yet takes its maximum; a row with a
+    // sum takes it where it is larger, and scales the sum and O.
     auto redo = [&](int h, int vis, bool have_o, uint32_t (&pk)[HC / 2], float& sum) {
       uint32_t x0[32], x1[32];
       tmem_ld32(tS + h * HC, x0);
@@ -508,11 +534,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 32; ++e)
         mx = fmax3(mx, e < vis ? __uint_as_float(x0[e]) : -INFINITY, 32 + e < vis ? __uint_as_float(x1[e]) : -INFINITY);
-      const float to = fmaxf(m, mx * c2);
-      const float f = m == -INFINITY ? 0.0f : fast_exp2(m - to);
-      l *= f;
-      m = to;
-      sum = half_weights(x0, x1, vis, to == -INFINITY ? 0.0f : to, pk);
+      float f = 1.0f;
+      if (l == 0.0f) {
+        if (mx != -INFINITY) m = mx * c2;  // O holds zeros
+      } else if (mx * c2 > m) {
+        f = fast_exp2(m - mx * c2);
+        l *= f;
+        m = mx * c2;
+      }
+      sum = half_weights(x0, x1, vis, m, pk);
       if (!have_o || !__any_sync(0xffffffffu, f != 1.0f)) return;
       // O holds every earlier half once the last of them has completed: this
       // tile's first, or the previous tile's second (one barrier for each, so
@@ -532,10 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = 0; take_work(it, w); ++it) {
       const int nt = t == 0 ? w.nt[0] : w.nt[1], n = max(w.nt[0], w.nt[1]), Lk = w.P + w.n;
       const int row = w.r0 + t * BM + r;
-      const bool valid = row < (long long)w.n * a.g;
+      const bool valid = row < w.n * a.g;
       const int tok = valid ? row / a.g : w.n - 1;
       const int lim = w.P + tok + 1 - w.k_begin;  // visible keys of this range
-      m = -INFINITY;
+      m = 0.0f;
       l = 0.0f;
       for (int j = 0; j < nt; ++j, ++cs) {
         wait(&s_full[t], cs);
@@ -565,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tS + HC, y0);
         tmem_ld32(tS + HC + 32, y1);
         float sum = half_weights(x0, x1, vis, m, pk);
-        if (__any_sync(0xffffffffu, !(sum < kSumLimit))) {
+        if (unfit(sum, vis)) {
           tmem_wait_ld(y0);
           tmem_wait_ld(y1);
           redo(0, vis, j > 0, pk, sum);
@@ -581,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[t][0]);
         sum = half_weights(y0, y1, vis - HC, m, pk);
-        if (__any_sync(0xffffffffu, !(sum < kSumLimit))) {
+        if (unfit(sum, vis - HC)) {
           redo(1, vis - HC, true, pk, sum);
         }
         l += sum;
@@ -598,40 +628,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const size_t orow = (size_t)(w.off + tok) * a.Hq + w.kvh * a.g + (valid ? row % a.g : 0);
       const float inv = 1.0f / l;
+      // 64 bytes of every row of the warp, one 16-byte piece u[i] after another
+      // in each thread: four lanes trade pieces so that each store writes 64
+      // contiguous bytes of 8 rows (16 bytes of 32 rows cost four times the
+      // address passes; item of 4 key steps: 22 -> 17 kcycles with the first
+      // reference of 0).
+      uint32_t rows4[4];  // output rows of the four lanes, 0xffffffff: not written
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        rows4[s] = __shfl_sync(0xffffffffu, valid ? (uint32_t)orow : 0xffffffffu, (lane & 28) + s);
+      auto store_rows = [&](char* base, int row_bytes, uint4 (&u)[4]) {
+        transpose4(u, lane);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          if (rows4[s] != 0xffffffffu)
+            *reinterpret_cast<uint4*>(base + (size_t)rows4[s] * row_bytes + (lane & 3) * 16) = u[s];
+      };
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(tO + c * 32, o);
         tmem_wait_ld(o);
-        if (!valid) continue;
         if (a.splits == 1) {
-          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c * 32);
+          uint4 u[4];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t u[4];
+          for (int i = 0; i < 4; ++i) {
+            uint32_t p[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv);
-              u[i] = *reinterpret_cast<uint32_t*>(&h2);
+            for (int e = 0; e < 4; ++e) {
+              __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                                        __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+              p[e] = *reinterpret_cast<uint32_t*>(&h2);
             }
-            out[e / 8] = make_uint4(u[0], u[1], u[2], u[3]);
+            u[i] = make_uint4(p[0], p[1], p[2], p[3]);
           }
+          store_rows(static_cast<char*>(a.out) + c * 64, 2 * D, u);
         } else {
-          uint4* wo = reinterpret_cast<uint4*>(a.ws_o + ((size_t)w.split * a.T * a.Hq + orow) * D + c * 32);
+          char* ws = reinterpret_cast<char*>(a.ws_o + (size_t)w.split * a.T * a.Hq * D);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) wo[e / 4] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int i = 0; i < 2; ++i) {
+            uint4 u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = 16 * i + 4 * e;
+              u[e] = make_uint4(o[at], o[at + 1], o[at + 2], o[at + 3]);
+            }
+            store_rows(ws + c * 128 + i * 64, 4 * D, u);
+          }
         }
       }
       if (valid && a.splits > 1)
-        *reinterpret_cast<float2*>(a.ws_ml + ((size_t)w.split * a.T * a.Hq + orow) * 2) = make_float2(m, l);
+        *reinterpret_cast<float2*>(a.ws_ml + ((size_t)w.split * a.T * a.Hq + orow) * 2) = make_float2(l > 0.0f ? m : -INFINITY, l);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  // which of the CTA's items were lost is not kept: every request is flagged
-  if (abort_flag)
+  if (abort_flag) {
+    // every copy has landed before the CTA exits (without a timeout the MMA
+    // warps have waited for each); which of the CTA's items were lost is not
+    // kept: every request is flagged
+    if (threadIdx.x == 0) {
+      for (int st = 0; st < NST; ++st)
+        if (kv_issued[st] >= 0) mbar_drain(&kv_full[st], (kv_issued[st] / NST) & 1);
+      if (q_issued >= 0) mbar_drain(&q_full, q_issued & 1);
+    }
     for (int b = threadIdx.x; b < a.B; b += kThreads) atomicOr(&a.status[b], SPEC_DEV_TIMEOUT);
+  }
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -673,6 +736,8 @@ static cudaError_t launch_d(const PromptArgs& a, const PromptPlan& p, cudaStream
   ptc::Params prm;
   prm.a = a;
   prm.box_rows = std::min(a.block_size, ptc::BN);
+  prm.bs_log2 = 0;
+  while ((1 << prm.bs_log2) < a.block_size) ++prm.bs_log2;
   prm.rows_total = (long long)a.num_blocks * a.Hkv * a.block_size;
   if (prm.rows_total >= (long long)INT32_MAX) return cudaErrorInvalidValue;
   const long long items = p.tiles * a.Hkv * p.splits;
