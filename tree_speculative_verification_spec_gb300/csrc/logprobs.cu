@@ -2,34 +2,52 @@
 // the token's rank and the top alternatives.
 //
 // For one row of logits x, inverse temperature tau and given token t, with
-// m = max x and d_i = x_i - m:
+// any reference r and d_i = x_i - r:
 //   S = sum_i e^(tau d_i),  W = sum_i e^(tau d_i) d_i
 //   log p(t) = tau d_t - log S
 //   H = -sum_i p_i log p_i = log S - tau W / S
 //   rank(t) = number of tokens ranked before t (larger logit, equal logits by
 //             lower id, NaN last)
-// Every value comes from one read of the row: each thread keeps (m, S, W)
-// against its own running maximum, rescaled by 2^((m_old - m_new) tau log2 e)
-// once per batch of loads that raises it, and the partials merge by the same
-// rule across the warp, the CTA and the row's cluster.  The row is the only
-// traffic that counts (V entries against a few words of results), so the
-// kernel is bound by HBM for many rows and by launch and one row's latency
-// for few.  One cluster of C CTAs per row: C = 1 when the rows alone fill the
-// GPU, else enough CTAs to spread a row, with at least 2048 entries each.
+// Every value comes from one read of the row: each thread keeps (r, S, W)
+// with r the largest logit it has seen, moves to a larger r once per batch of
+// 32 entries, and the partials merge by the same rule across the warp, the CTA
+// and the row's cluster, always in the same order.
+//
+// The row is the only traffic that counts.  A producer warp brings it by bulk
+// copies through a shared-memory ring, so that what is in flight (three CTAs an
+// SM, 64 KB each) does not hang on registers, and runs ahead into the CTA's next
+// row while this one is summed up.  Measured on 2048 rows of 128256 fp32 logits,
+// 30 % of the tokens unlikely ones: 191 us with k = 0 (5.5 TB/s), 265 us with
+// k = 20; loads into registers ahead of each batch: 250 us with k = 0.  What
+// bounds it is the instruction rate: about 15 an entry with k = 0 and 23 with
+// k = 20, at half of the issue slots (bf16 logits take as long as fp32 ones).
+// The rank looks at a lane's entries only when their maximum reaches the given
+// token's logit, and the alternatives only when it reaches the CTA's bar: the
+// least of the eight warps' m-th best scores, m = ceil(k / 8), which k entries
+// reach.  A bar per warp let eight times as many entries through (314 us), and
+// with the insertion inlined per entry the whole took 924 us.  Eight consumer
+// warps in three CTAs of 72 registers; four in five CTAs measured 353 us.
+//
+// One cluster of C CTAs per row: C = 1 when the rows alone fill the GPU, else
+// enough CTAs to spread a row, with at least 2048 entries each.
 #include <algorithm>
 
 #include <cooperative_groups.h>
 
+#include "tcgen05.cuh"
 #include "topk.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace spectree {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpWarps = 8;                          // consumer warps
+constexpr int kLpThreads = kLpWarps * 32 + 32;       // and the producer warp
+constexpr int kLpBatch = 16;                         // entries per lane and stage
+constexpr int kLpEntries = kLpWarps * 32 * kLpBatch; // entries per stage: 16 KB of fp32, 8 KB of bf16
+constexpr int kLpDyn = 64 * 1024;                    // the ring: 4 stages of fp32, 8 of bf16; three CTAs an SM
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpBatch = 4;  // 16-byte loads per thread issued before any is used
+constexpr int kLpMaxLive = 1024;  // requests whose accepted lengths a CTA sums up for itself
 
 __device__ __forceinline__ float lp_exp2(float x) {
   float y;
@@ -44,38 +62,51 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
-// Softmax statistics against a reference m: s = sum e^(tau (x - m)), w = sum
-// e^(tau (x - m)) (x - m).  m = -inf: nothing (finite) seen yet.  A NaN stays
-// NaN through every merge.
-struct SoftStats {
-  float m = -INFINITY, s = 0.0f, w = 0.0f;
+// max(a, b, c) that keeps NaN
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 
-  // the same sums against a larger reference (c = tau * log2 e)
+// S and W against the reference r; r = -inf: nothing above -inf seen yet.  A
+// NaN stays NaN through every merge.  c = tau log2 e.
+struct SoftStats {
+  float r = -INFINITY, s = 0.0f, w = 0.0f;
+
+  // the same sums against a larger reference
   __device__ __forceinline__ void raise(float to, float c) {
-    if (m == to) return;
-    if (m == -INFINITY) {
+    if (r == to) return;
+    if (r == -INFINITY) {
       s = w = 0.0f;
     } else {
-      const float delta = m - to;  // <= 0; -inf when `to` is +inf
-      const float f = lp_exp2(delta * c);
-      // e^(tau delta) vanishes faster than delta grows: the clamp keeps 0 * inf out
-      w = f * fmaf(s, max_nan(delta, -1e30f), w);
+      const float d = r - to;  // <= 0; -inf when `to` is +inf
+      const float f = lp_exp2(d * c);
+      // e^(tau d) vanishes faster than d grows: the clamp keeps 0 * inf out
+      w = f * fmaf(s, max_nan(d, -1e30f), w);
       s *= f;
     }
-    m = to;
+    r = to;
+  }
+  // the statistics of N neighbouring lanes together: their largest reference,
+  // one rescaling, plain sums
+  template <int N> __device__ __forceinline__ void reduce(float c) {
+    float to = r;
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) to = max_nan(to, __shfl_xor_sync(0xffffffffu, to, o));
+    raise(to, c);
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      w += __shfl_xor_sync(0xffffffffu, w, o);
+    }
   }
   __device__ __forceinline__ void merge(SoftStats o, float c) {
-    const float to = max_nan(m, o.m);
+    const float to = max_nan(r, o.r);
     raise(to, c);
     o.raise(to, c);
     s += o.s;
     w += o.w;
-  }
-  __device__ __forceinline__ void add(float x, float c) {
-    const float d = max_nan(x - m, -3e38f);  // -inf entries weigh nothing: e is 0, and 0 * d stays 0
-    const float e = lp_exp2(d * c);
-    s += e;
-    w = fmaf(e, d, w);
   }
 };
 
@@ -90,6 +121,7 @@ struct LpArgs {
   float *logprob, *entropy, *top_logprobs;
   int32_t *rank, *top_tokens, *status;
   int B, T, n_max, V, k, C;
+  int live;  // path call: clusters go round the accepted entries alone
 };
 
 template <typename T> __device__ __forceinline__ void lp_unpack(uint4 v, float (&x)[16 / sizeof(T)]);
@@ -108,202 +140,383 @@ template <> __device__ __forceinline__ void lp_unpack<__nv_bfloat16>(uint4 v, fl
   }
 }
 
-__device__ __forceinline__ uint32_t rank_word(float v) { return (uint32_t)(score_key(v, 0) >> 32); }
+// A float's order as a signed integer (both ways the same mapping).
+__device__ __forceinline__ int float_order(float v) {
+  const int i = __float_as_int(v);
+  return i >= 0 ? i : i ^ 0x7fffffff;
+}
+__device__ __forceinline__ float order_float(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
+
+// Barrier of the consumer warps.
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kLpWarps * 32) : "memory"); }
+
+// The next float below (finite and infinite alike; -inf stays).
+__device__ __forceinline__ float before_float(float v) {
+  return v == -INFINITY ? v : order_float(float_order(v == 0.0f ? -0.0f : v) - 1);
+}
+
+__device__ __forceinline__ void write_none(const LpArgs& a, long long entry, int thread) {
+  if (thread == 0) {
+    a.logprob[entry] = NAN;
+    if (a.entropy) a.entropy[entry] = NAN;
+    if (a.rank) a.rank[entry] = -1;
+  }
+  if (thread < a.k) {
+    if (a.top_tokens) a.top_tokens[entry * a.k + thread] = -1;
+    if (a.top_logprobs) a.top_logprobs[entry * a.k + thread] = NAN;
+  }
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   tc5::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(tc5::smem_u32(bar))
+               : "memory");
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LpArgs a) {
+__global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a, long long entries) {
   constexpr int VEC = 16 / sizeof(T);
-  __shared__ unsigned long long wres[kLpWarps][32];
+  constexpr int NE = kLpBatch, NV = NE / VEC;     // entries and vectors per lane and stage
+  constexpr int kLpChunk = kLpEntries / VEC;      // vectors per stage
+  constexpr int kLpStages = kLpDyn / (kLpChunk * 16);
+  extern __shared__ __align__(128) uint4 ring[];
+  __shared__ unsigned long long s_keys[kLpWarps * 32];  // the warps' keys that reach the last bar
   __shared__ unsigned long long cres[kLpMaxCluster][32];  // leader: the CTAs' lists
   __shared__ SoftStats wst[kLpWarps], cst[kLpMaxCluster];
   __shared__ int wbef[kLpWarps], cbef[kLpMaxCluster];
+  __shared__ int s_mth[kLpWarps];     // each warp's m-th best score, in float_order
+  __shared__ int s_n;
+  __shared__ int s_live[kLpMaxLive];  // accepted entries before each request
+  __shared__ int s_total, abort_flag;
+  __shared__ uint64_t full[kLpStages], empty[kLpStages];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = a.C, part = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long entry = blockIdx.x / C;  // the same for every CTA of the cluster
+  const long long first = blockIdx.x / C, step = gridDim.x / C;
   const int k = a.k;
 
-  // ---- the entry's row, request and token
-  int b, token, bad = 0;
-  long long row = 0;
-  bool none = false;  // nothing to compute: the outputs say so
-  if (a.path) {
-    b = (int)(entry / a.n_max);
-    const int i = (int)(entry % a.n_max);
-    const int n_acc = a.accept_len[b];
-    const int off = a.off[b], n = a.off[b + 1] - off;
-    token = -1;
-    none = i >= n_acc;
-    if (n_acc > a.n_max) {
-      none = true;
-      bad = SPEC_DEV_BAD_PATH;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kLpStages; ++i) {
+      tc5::mbar_init(&full[i], 1);
+      tc5::mbar_init(&empty[i], kLpWarps);
     }
-    if (!none) {
-      const int p = a.path[entry];
-      token = a.tokens[entry];
-      if (off < 0 || n < 0 || n > a.T - off || p < 0 || p >= n) bad |= SPEC_DEV_BAD_PATH;
-      if (token < 0 || token >= a.V) bad |= SPEC_DEV_BAD_TOKEN;
-      row = (long long)off + p;
-    }
-  } else {
-    int lo = 0, hi = a.B;  // the last request with off[lo] <= entry
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.off[mid] <= entry) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-    row = entry;
-    none = entry < a.off[b] || entry >= a.off[b + 1];  // a row no request owns
-    token = none ? -1 : a.tokens[entry];
-    if (token < -1 || token >= a.V) bad = SPEC_DEV_BAD_TOKEN;
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  float tau = 1.0f;
-  if (!none && a.inv_temp) {
-    tau = a.inv_temp[b];
-    if (!(tau >= 1e-30f && tau < INFINITY)) bad |= SPEC_DEV_BAD_TEMP;
-  }
-  if (none || bad) {
-    if (part == 0) {
-      if (threadIdx.x == 0) {
-        if (a.logprob) a.logprob[entry] = NAN;
-        if (a.entropy) a.entropy[entry] = NAN;
-        if (a.rank) a.rank[entry] = -1;
-        if (bad && a.status) atomicOr(&a.status[b], bad);
+  if (a.live && warp == 0) {
+    // the accepted entries alone are gone through, numbered request by request
+    int at = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane;
+      const int n_acc = b < a.B ? a.accept_len[b] : 0;
+      if (n_acc > a.n_max && blockIdx.x == 0) atomicOr(&a.status[b], SPEC_DEV_BAD_PATH);
+      const int n = n_acc > 0 && n_acc <= a.n_max ? n_acc : 0;
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
       }
-      if (threadIdx.x < k) {
-        if (a.top_tokens) a.top_tokens[entry * k + threadIdx.x] = -1;
-        if (a.top_logprobs) a.top_logprobs[entry * k + threadIdx.x] = NAN;
-      }
+      if (b < a.B) s_live[b] = at + incl - n;
+      at += __shfl_sync(0xffffffffu, incl, 31);
     }
-    return;  // the whole cluster leaves
-  }
-
-  const T* src = static_cast<const T*>(a.logits) + row * a.V;
-  const float c = tau * 1.4426950408889634f;
-  const float xt = token >= 0 ? to_f32(src[token]) : 0.0f;
-  const uint32_t rt = rank_word(xt);
-
-  // the row: a head up to the first 16-byte boundary, 16-byte vectors, a tail
-  const int mis = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
-  const int head = min(a.V, mis ? VEC - mis : 0);
-  const int nvec = (a.V - head) / VEC;
-  const int tail0 = head + nvec * VEC;
-  const uint4* vec = reinterpret_cast<const uint4*>(src + head);
-  const int per = (nvec + C - 1) / C;
-  const int v0 = min(nvec, part * per), v1 = min(nvec, v0 + per);
-
-  SoftStats st;
-  WarpTop top;
-  int before = 0;
-  bool seeded = false;
-  // one batch of N values per lane; value q of the lane has id `id(q)`, lanes beyond the
-  // batch hold -inf at an id that `in(q)` tells apart
-  auto consume = [&](auto& x, auto id, auto in) {
-    constexpr int N = sizeof(x) / sizeof(float);
-    float mx = -INFINITY;
-#pragma unroll
-    for (int q = 0; q < N; ++q) mx = max_nan(mx, x[q]);
-    if (!(mx <= st.m)) st.raise(mx, c);
-    if (st.m != -INFINITY) {
-#pragma unroll
-      for (int q = 0; q < N; ++q) st.add(x[q], c);
-    }
-    if (token >= 0) {
-#pragma unroll
-      for (int q = 0; q < N; ++q) {
-        const uint32_t r = rank_word(x[q]);
-        before += in(q) && (r > rt || (r == rt && id(q) < token));
-      }
-    }
-    if (k > 0) {
-      if (!seeded) {
-        top.seed(mx, k, lane);
-        seeded = true;
-      }
-      if (__any_sync(0xffffffffu, !(mx < top.bar))) {
-#pragma unroll
-        for (int q = 0; q < N; ++q) top.offer(x[q], id(q), in(q), k, lane);
-      }
-    }
-  };
-  for (int j0 = v0 + warp * kLpBatch * 32; j0 < v1; j0 += kLpWarps * kLpBatch * 32) {
-    uint4 raw[kLpBatch];
-#pragma unroll
-    for (int q = 0; q < kLpBatch; ++q) {
-      const int j = j0 + q * 32 + lane;
-      if (j < v1) raw[q] = __ldcs(vec + j);
-    }
-    float x[kLpBatch * VEC];
-#pragma unroll
-    for (int q = 0; q < kLpBatch; ++q) {
-      float y[VEC];
-      lp_unpack<T>(raw[q], y);
-      const bool ok = j0 + q * 32 + lane < v1;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[q * VEC + e] = ok ? y[e] : -INFINITY;
-    }
-    consume(
-        x, [&](int q) { return head + (j0 + (q / VEC) * 32 + lane) * VEC + q % VEC; },
-        [&](int q) { return j0 + (q / VEC) * 32 + lane < v1; });
-  }
-  // head and tail: at most 2 (VEC - 1) < 32 entries, warp 0 of the first CTA
-  if (part == 0 && warp == 0 && (head > 0 || tail0 < a.V)) {
-    const int at = lane < 16 ? lane : tail0 + lane - 16;
-    const bool ok = lane < 16 ? lane < head : at < a.V;
-    float x[1] = {ok ? to_f32(src[at]) : -INFINITY};
-    consume(x, [&](int) { return at; }, [&](int) { return ok; });
-  }
-
-  // ---- warp, CTA and cluster merges
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    SoftStats y;
-    y.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    y.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    y.w = __shfl_xor_sync(0xffffffffu, st.w, o);
-    st.merge(y, c);
-  }
-  before = warp_sum_i(before);
-  wres[warp][lane] = top.list;
-  if (lane == 0) {
-    wst[warp] = st;
-    wbef[warp] = before;
+    if (lane == 0) s_total = at;
   }
   __syncthreads();
-  if (warp == 0) {
-    for (int w = 1; w < kLpWarps; ++w) {
-      if (k > 0) top.offer_key(wres[w][lane], k, lane);
-      st.merge(wst[w], c);
-      before += wbef[w];
+  if (a.live) {
+    for (long long e = blockIdx.x * kLpWarps + warp; warp < kLpWarps && e < entries; e += (long long)gridDim.x * kLpWarps) {
+      const int n = a.accept_len[(int)(e / a.n_max)];
+      if ((int)(e % a.n_max) >= n || n > a.n_max) write_none(a, e, lane);
     }
-    if (C > 1) {
-      *cluster.map_shared_rank(&cres[part][lane], 0) = top.list;
+    entries = s_total;
+  }
+
+  int chunks = 0;  // stages used so far
+  for (long long item = first; item < entries; item += step) {
+    // ---- the item's entry, row and token
+    long long entry = item, row = item;
+    int b = 0, token = -1, bad = 0;
+    bool none = false;  // nothing to compute: the outputs say so
+    if (a.path) {
+      if (a.live) {
+        int lo = 0, hi = a.B;  // the last request with s_live[lo] <= item
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_live[mid] <= item) lo = mid;
+          else hi = mid;
+        }
+        b = lo;
+        entry = (long long)b * a.n_max + (item - s_live[b]);
+      } else {
+        b = (int)(entry / a.n_max);
+        const int n_acc = a.accept_len[b];
+        none = (int)(entry % a.n_max) >= n_acc || n_acc > a.n_max;
+        if (n_acc > a.n_max) bad = SPEC_DEV_BAD_PATH;
+      }
+      if (!none) {
+        const int off = a.off[b], n = a.off[b + 1] - off, p = a.path[entry];
+        token = a.tokens[entry];
+        if (off < 0 || n < 0 || n > a.T - off || p < 0 || p >= n) bad |= SPEC_DEV_BAD_PATH;
+        row = (long long)off + p;
+      }
+    } else if (warp < kLpWarps) {  // the producer needs the row alone
+      int lo = 0, hi = a.B;        // the last request with off[lo] <= entry
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.off[mid] <= entry) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      token = a.tokens[entry];
+      none = entry < a.off[b] || entry >= a.off[b + 1];  // a row no request owns
+    }
+    // a path entry without a row is left out by every warp of the cluster; a
+    // row that is read for nothing is settled at the end
+    const bool skip = a.path && (none || bad);
+
+    // ---- the row: a head up to the first 16-byte boundary, 16-byte vectors, a tail
+    const T* src = static_cast<const T*>(a.logits) + row * a.V;
+    const int mis = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
+    const int head = min(a.V, mis ? VEC - mis : 0);
+    const int nvec = (a.V - head) / VEC;
+    const int tail0 = head + nvec * VEC;
+    const int per = (nvec + C - 1) / C;
+    const int v0 = min(nvec, part * per), v1 = min(nvec, v0 + per);
+    const int n_chunks = skip ? 0 : (v1 - v0 + kLpChunk - 1) / kLpChunk;
+    if (warp == kLpWarps) {  // ---- producer
       if (lane == 0) {
-        *cluster.map_shared_rank(&cst[part], 0) = st;
-        *cluster.map_shared_rank(&cbef[part], 0) = before;
+        for (int i = 0; i < n_chunks; ++i) {
+          const int u = chunks + i, st = u % kLpStages;
+          if (u >= kLpStages && !tc5::mbar_wait(&empty[st], (u / kLpStages - 1) & 1, &abort_flag)) break;
+          const uint32_t bytes = 16u * (uint32_t)min(kLpChunk, v1 - v0 - i * kLpChunk);
+          tc5::mbar_expect_tx(&full[st], bytes);
+          bulk_load(ring + st * kLpChunk, reinterpret_cast<const uint4*>(src + head) + v0 + i * kLpChunk, bytes, &full[st]);
+        }
+      }
+      chunks += n_chunks;
+      if (C > 1) {  // a cluster's barriers take every warp; alone, the producer runs ahead into the next rows
+        if (!skip) cluster.sync();
+        if (item + step < entries) cluster.sync();
+      }
+      continue;
+    }
+    float tau = 1.0f;
+    if (a.inv_temp && !none) {
+      tau = a.inv_temp[b];
+      if (!(tau >= 1e-30f && tau < INFINITY)) bad |= SPEC_DEV_BAD_TEMP;
+    }
+    if (!none && (token < (a.path ? 0 : -1) || token >= a.V)) {
+      bad |= SPEC_DEV_BAD_TOKEN;
+      token = -1;
+    }
+    if (!skip) {
+      const float c = tau * 1.4426950408889634f;
+      const float2 cc = make_float2(c, c);
+      const float xt = token >= 0 ? to_f32(src[token]) : INFINITY;  // no token: no entry is above it
+      SoftStats st;
+      WarpTop top;
+      int before = 0;
+      // Of the nw warps that work on this row, each has m = ceil(k / nw) entries
+      // that reach its m-th best: the least of the nw m-th bests is reached by k
+      // entries of the CTA, and no entry below it is among the k best.
+      const int nw = n_chunks > 0 ? min(kLpWarps, (v1 - v0 + NV * 32 - 1) / (NV * 32)) : 1;
+      const int m = (k + nw - 1) / nw;
+      float mth = -INFINITY;
+      if (threadIdx.x < kLpWarps) s_mth[threadIdx.x] = float_order(threadIdx.x < nw ? -INFINITY : INFINITY);
+      if (threadIdx.x == 0) s_n = 0;
+      consumers_sync();
+      auto cta_bar = [&]() -> float {
+        return order_float(__reduce_min_sync(0xffffffffu, *(volatile int*)&s_mth[lane & (kLpWarps - 1)]));
+      };
+      // A batch of entries, one lane's x[0 .. N - 1]; those that are not there
+      // hold -inf.  The sums:
+      auto sums = [&](auto& x, float mx) {
+        constexpr int N = sizeof(x) / sizeof(float);
+        if (!(mx <= st.r)) st.raise(mx, c);
+        if (st.r == -INFINITY) return;
+        // entries of -inf weigh nothing: e is 0, and 0 times the clamped d stays 0
+        float2 s2 = make_float2(0.0f, 0.0f), w2 = s2;
+        if (N == 1) {
+          const float d = max_nan(x[0] - st.r, -3e38f);
+          s2.x = lp_exp2(d * c);
+          w2.x = s2.x * d;
+        } else {
+          const float2 neg = make_float2(-st.r, -st.r);
+#pragma unroll
+          for (int q = 0; q + 1 < N; q += 2) {
+            float2 d = __fadd2_rn(make_float2(x[q], x[q + 1]), neg);
+            d.x = max_nan(d.x, -3e38f);
+            d.y = max_nan(d.y, -3e38f);
+            const float2 z = __fmul2_rn(d, cc);
+            const float2 e = make_float2(lp_exp2(z.x), lp_exp2(z.y));
+            s2 = __fadd2_rn(s2, e);
+            w2 = __ffma2_rn(e, d, w2);
+          }
+        }
+        st.s += s2.x + s2.y;
+        st.w += w2.x + w2.y;
+      };
+      // The given token's rank: entry q has id `id(q)` and is there if in(q).
+      auto count = [&](auto& x, auto id, auto in) {
+        constexpr int N = sizeof(x) / sizeof(float);
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          const bool equal = x[q] == xt || (x[q] != x[q] && xt != xt);
+          before += in(q) && (x[q] > xt || (xt != xt && x[q] == x[q]) || (equal && id(q) < token));
+        }
+      };
+      // The alternatives: a lane whose maximum reaches the bar offers those of
+      // its entries that do; again(q) is entry q's key, 0 if it is not there.
+      auto pick = [&](auto& x, float mx, auto again) {
+        constexpr int N = sizeof(x) / sizeof(float);
+        top.floor = fmaxf(top.floor, cta_bar());
+        top.bar = fmaxf(top.bar, top.floor);
+        if (!__any_sync(0xffffffffu, !(mx < top.bar))) return;
+        uint32_t hits = 0;
+        if (!(mx < top.bar)) {
+#pragma unroll
+          for (int q = 0; q < N; ++q) hits |= !(x[q] < top.bar) ? 1u << q : 0u;
+        }
+#pragma unroll 1
+        while (__any_sync(0xffffffffu, hits)) {  // one entry of each lane a round
+          top.offer_many(hits ? again(__ffs(hits) - 1) : 0ull, k, lane);
+          hits &= hits - 1;
+        }
+        if (m > 0) {
+          const float now = key_score(__shfl_sync(0xffffffffu, top.list, m - 1));
+          if (now > mth) {
+            mth = now;
+            if (lane == 0) *(volatile int*)&s_mth[warp] = float_order(now);
+          }
+        }
+      };
+      for (int i = 0; i < n_chunks; ++i) {
+        const int u = chunks + i, sg = u % kLpStages;
+        const int n = min(kLpChunk, v1 - v0 - i * kLpChunk);       // vectors of the stage
+        const int x0 = head + (v0 + i * kLpChunk) * VEC;           // its first entry
+        const uint4* sv = ring + sg * kLpChunk;
+        const int j0 = warp * NV * 32 + lane;
+        tc5::mbar_wait(&full[sg], (u / kLpStages) & 1, &abort_flag);
+        float x[NE], mx = -INFINITY;
+        const bool here = warp * NV * 32 < n;
+        auto id = [&](int q) { return x0 + (j0 + (q / VEC) * 32) * VEC + q % VEC; };
+        auto in = [&](int q) { return j0 + (q / VEC) * 32 < n; };
+        if (here) {
+#pragma unroll
+          for (int q = 0; q < NV; ++q) lp_unpack<T>(sv[j0 + q * 32], *reinterpret_cast<float(*)[VEC]>(x + q * VEC));
+          if (n < kLpChunk) {  // past the end: an earlier stage's values, or none
+#pragma unroll
+            for (int q = 0; q < NE; ++q) x[q] = in(q) ? x[q] : -INFINITY;
+          }
+          mx = x[0];
+#pragma unroll
+          for (int q = 1; q + 1 < NE; q += 2) mx = max3_nan(mx, x[q], x[q + 1]);
+          mx = max_nan(mx, x[NE - 1]);
+          sums(x, mx);
+          if (!(mx < xt)) {
+            const bool lower = x0 + n * VEC <= token, higher = x0 > token;  // every id of the stage
+            if (n == kLpChunk && (lower || higher) && xt > -INFINITY) {
+              const float bar = lower ? before_float(xt) : xt;  // equal logits of lower ids count too
+#pragma unroll
+              for (int q = 0; q < NE; ++q) before += x[q] > bar;
+            } else {
+              count(x, id, in);
+            }
+          }
+        }
+        if (k > 0) {
+          if (i == 0) {
+            // before any list is filled, from the lanes' maxima
+            mth = WarpTop::nth_largest(mx, m - 1, lane);
+            if (here && lane == 0) *(volatile int*)&s_mth[warp] = float_order(mth);
+            consumers_sync();
+          }
+          if (here)
+            pick(x, mx, [&](int q) {
+              const int at = (j0 + (q / VEC) * 32) * VEC + q % VEC;
+              return at < n * VEC ? score_key(to_f32(reinterpret_cast<const T*>(sv)[at]), x0 + at) : 0ull;
+            });
+        }
+        __syncwarp();
+        if (lane == 0) tc5::mbar_arrive(&empty[sg]);
+      }
+      // head and tail: at most 2 (VEC - 1) < 32 entries, warp 0 of the first CTA
+      if (part == 0 && warp == 0 && (head > 0 || tail0 < a.V)) {
+        const int at = lane < 16 ? lane : tail0 + lane - 16;
+        const bool ok = lane < 16 ? lane < head : at < a.V;
+        float x[1] = {ok ? to_f32(src[at]) : -INFINITY};
+        sums(x, x[0]);
+        count(x, [&](int) { return at; }, [&](int) { return ok; });
+        if (k > 0)
+          pick(x, x[0], [&](int) { return ok ? score_key(x[0], at) : 0ull; });
+      }
+
+      // ---- warp, CTA and cluster merges
+      st.reduce<32>(c);
+      before = warp_sum_i(before);
+      if (lane == 0) {
+        wst[warp] = st;
+        wbef[warp] = before;
+      }
+      consumers_sync();
+      if (k > 0) {
+        const float bar = cta_bar();
+        if (top.list != 0ull && !(key_score(top.list) < bar)) s_keys[atomicAdd(&s_n, 1)] = top.list;
+        consumers_sync();
+      }
+      if (warp == 0) {
+        if (k > 0) {  // in any order: the keys are distinct
+          top = WarpTop();
+          const int n = *(volatile int*)&s_n;
+#pragma unroll 1
+          for (int i = 0; i < n; i += 32) top.offer_many(i + lane < n ? s_keys[i + lane] : 0ull, k, lane);
+        }
+        st = wst[lane & (kLpWarps - 1)];
+        st.reduce<kLpWarps>(c);
+        for (int w = 1; w < kLpWarps; ++w) before += wbef[w];
+        if (C > 1) {
+          *cluster.map_shared_rank(&cres[part][lane], 0) = top.list;
+          if (lane == 0) {
+            *cluster.map_shared_rank(&cst[part], 0) = st;
+            *cluster.map_shared_rank(&cbef[part], 0) = before;
+          }
+        }
+      }
+      if (C > 1) cluster.sync();  // the partials have landed
+      if (part == 0 && warp == 0 && !none && !bad) {
+        for (int r = 1; r < C; ++r) {
+          if (k > 0) top.merge(cres[r][lane], k, lane);
+          st.merge(cst[r], c);
+          before += cbef[r];
+        }
+        // a row without a finite maximum (every entry -inf) has no distribution
+        const float ls = st.s > 0.0f ? logf(st.s) : NAN;
+        if (lane == 0) {
+          a.logprob[entry] = token >= 0 ? (xt - st.r) * tau - ls : NAN;
+          if (a.entropy) a.entropy[entry] = ls - tau * st.w / st.s;
+          if (a.rank) a.rank[entry] = token >= 0 ? before : -1;
+        }
+        if (lane < k) {
+          const int id = (int)(~(uint32_t)(top.list & 0xffffffffull));
+          if (a.top_tokens) a.top_tokens[entry * k + lane] = id;
+          if (a.top_logprobs) a.top_logprobs[entry * k + lane] = (to_f32(src[id]) - st.r) * tau - ls;
+        }
       }
     }
+    if (part == 0 && warp == 0 && (none || bad)) {
+      write_none(a, entry, lane);
+      if (lane == 0 && bad) atomicOr(&a.status[b], bad);
+    }
+    chunks += n_chunks;
+    if (item + step < entries) {  // the lists and partials are read before the next item writes its own
+      if (C > 1) cluster.sync();
+      else consumers_sync();
+    }
   }
-  if (C > 1) cluster.sync();  // the partials have landed; no CTA touches another's memory after this
-  if (part != 0 || warp != 0) return;
-  for (int r = 1; r < C; ++r) {
-    if (k > 0) top.offer_key(cres[r][lane], k, lane);
-    st.merge(cst[r], c);
-    before += cbef[r];
-  }
-  // a row without a finite maximum (every entry -inf) has no distribution
-  const float ls = st.s > 0.0f ? logf(st.s) : NAN;
-  if (lane == 0) {
-    if (a.logprob) a.logprob[entry] = token >= 0 ? (xt - st.m) * tau - ls : NAN;
-    if (a.entropy) a.entropy[entry] = ls - tau * st.w / st.s;
-    if (a.rank) a.rank[entry] = token >= 0 ? before : -1;
-  }
-  if (lane < k) {
-    const int id = (int)(~(uint32_t)(top.list & 0xffffffffull));
-    if (a.top_tokens) a.top_tokens[entry * k + lane] = id;
-    if (a.top_logprobs) a.top_logprobs[entry * k + lane] = (to_f32(src[id]) - st.m) * tau - ls;
-  }
+  __syncthreads();
+  if (abort_flag && threadIdx.x == 0)  // a wait ran out: every request of the call may be short of a row
+    for (int b = 0; b < a.B; ++b) atomicOr(&a.status[b], SPEC_DEV_TIMEOUT);
 }
 
 static spec_status launch_logprobs(LpArgs a, spec_dtype dtype, long long entries, cudaStream_t stream) {
@@ -311,12 +524,15 @@ static spec_status launch_logprobs(LpArgs a, spec_dtype dtype, long long entries
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return SPEC_ERR_CUDA;
+  // a path call has about two accepted tokens a request to spread the GPU by
+  a.live = a.path != nullptr && a.B <= kLpMaxLive;
+  const long long rows = a.live ? std::min(entries, 2LL * a.B) : entries;
   int C = 1;
-  while (C < kLpMaxCluster && entries * C < 2LL * sms && a.V / (2 * C) >= 2048) C *= 2;
-  if (entries * C >= (1LL << 31)) return SPEC_ERR_UNSUPPORTED;
+  while (C < kLpMaxCluster && rows * C < 2LL * sms && a.V / (2 * C) >= 2048) C *= 2;
+  const long long clusters = std::min<long long>(entries, std::max(1, 3 * sms / C));  // what the GPU holds at once
   a.C = C;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(entries * C), 1, 1);
+  cfg.gridDim = dim3((unsigned)(clusters * C), 1, 1);
   cfg.blockDim = dim3(kLpThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -326,8 +542,10 @@ static spec_status launch_logprobs(LpArgs a, spec_dtype dtype, long long entries
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = dtype == SPEC_F32 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<float>, a)
-                                          : cudaLaunchKernelEx(&cfg, logprobs_kernel<__nv_bfloat16>, a);
+  cfg.dynamicSmemBytes = kLpDyn;
+  auto kern = dtype == SPEC_F32 ? logprobs_kernel<float> : logprobs_kernel<__nv_bfloat16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpDyn);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, a, entries);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
   return SPEC_OK;
 }

@@ -39,12 +39,10 @@ struct WarpTop {
   float bar = -INFINITY;
   float floor = -INFINITY;  // a lower bound of the k-th best score, from a first sample
 
-  // Lower bound for the bar from one sample per lane (its best score of a
-  // first batch; NaN counted as -inf): the k-th largest of these 32 distinct
-  // entries, by a bitonic sort across the warp.  No entry scored below it
-  // can be among the k best.
-  __device__ __forceinline__ void seed(float lane_best, int k, int lane) {
-    float v = lane_best != lane_best ? -INFINITY : lane_best;
+  // The (n + 1)-th largest of one value per lane (NaN counted as -inf), by a
+  // bitonic sort across the warp.
+  static __device__ __forceinline__ float nth_largest(float v, int n, int lane) {
+    if (v != v) v = -INFINITY;
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1) {
 #pragma unroll
@@ -54,7 +52,14 @@ struct WarpTop {
         v = desc ? fmaxf(v, o) : fminf(v, o);
       }
     }
-    floor = __shfl_sync(0xffffffffu, v, k - 1);
+    return __shfl_sync(0xffffffffu, v, n);
+  }
+
+  // Lower bound for the bar from one sample per lane (its best score of a
+  // first batch): the k-th largest of these 32 distinct entries.  No entry
+  // scored below it can be among the k best.
+  __device__ __forceinline__ void seed(float lane_best, int k, int lane) {
+    floor = nth_largest(lane_best, k - 1, lane);
     bar = fmaxf(bar, floor);
   }
 
@@ -77,6 +82,48 @@ struct WarpTop {
       const int l = __ffs(m) - 1;
       m &= m - 1;
       insert(score_key(__shfl_sync(0xffffffffu, v, l), __shfl_sync(0xffffffffu, x, l)), k, lane);
+    }
+  }
+
+  // Takes another list, sorted the same way (lane r the r-th best, 0 = nothing).
+  // The larger of list[i] and other[31 - i] are the 32 best of both and rise
+  // then fall, which five exchange steps sort: some 300 cycles, where an
+  // insertion costs about 100 for each key.
+  __device__ __forceinline__ void merge(unsigned long long other, int k, int lane) {
+    const unsigned long long o = __shfl_sync(0xffffffffu, other, 31 - lane);
+    list = list > o ? list : o;
+#pragma unroll
+    for (int stride = 16; stride > 0; stride >>= 1) {
+      const unsigned long long y = __shfl_xor_sync(0xffffffffu, list, stride);
+      list = ((lane & stride) == 0) == (y > list) ? y : list;
+    }
+    if (lane >= k) list = 0ull;
+    thr = __shfl_sync(0xffffffffu, list, k - 1);
+    bar = fmaxf(key_score(thr), floor);
+  }
+
+  // Every lane offers one key (0 = nothing); few are inserted, many are sorted
+  // and merged.
+  __device__ __forceinline__ void offer_many(unsigned long long key, int k, int lane) {
+    unsigned m = __ballot_sync(0xffffffffu, key > thr);
+    if (__popc(m) > 8) {
+      unsigned long long v = key > thr ? key : 0ull;
+#pragma unroll
+      for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+        for (int stride = size >> 1; stride > 0; stride >>= 1) {
+          const unsigned long long y = __shfl_xor_sync(0xffffffffu, v, stride);
+          const bool desc = ((lane & size) == 0) == ((lane & stride) == 0);  // keep the larger in the lower lane
+          v = desc == (y > v) ? y : v;
+        }
+      }
+      merge(v, k, lane);
+      return;
+    }
+    while (m) {
+      const int l = __ffs(m) - 1;
+      m &= m - 1;
+      insert(__shfl_sync(0xffffffffu, key, l), k, lane);
     }
   }
 
