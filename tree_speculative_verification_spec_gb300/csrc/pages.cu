@@ -278,19 +278,17 @@ struct FreeArgs {
   int B, max_blocks, bs, num_blocks, N, pool_cap;
 };
 
-// Rows' marks, from and entry set to "not named".
-__global__ void __launch_bounds__(kScanThreads) pages_free_clear_kernel(const FreeArgs a) {
-  for (int r = blockIdx.x * kScanThreads + threadIdx.x; r < a.B; r += gridDim.x * kScanThreads) {
-    a.from[r] = a.max_blocks;
-    a.mark[r] = 0;
-  }
-}
-
 // One cluster: which entries are sound, and the pages they would drop.
 __global__ void __launch_bounds__(kPlanThreads) pages_free_check_kernel(const FreeArgs a) {
   cg::cluster_group cl = cg::this_cluster();
   const int G = (int)cl.num_blocks() * kPlanThreads, id = (int)cl.block_rank() * kPlanThreads + threadIdx.x;
   const int lane = threadIdx.x & 31;
+  for (int r = id; r < a.B; r += G) {
+    a.from[r] = a.max_blocks;
+    a.mark[r] = 0;
+  }
+  __threadfence();
+  cl.sync();
   for (int i = id; i < a.N; i += G)
     if (a.rows[i] >= 0 && a.rows[i] < a.B) atomicAdd(&a.mark[a.rows[i]], 1);
   __threadfence();
@@ -302,12 +300,15 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_check_kernel(const Fr
     const int j0 = bad ? 0 : (int)min((long long)a.max_blocks, ((long long)keep + a.bs - 1) / a.bs);
     if (!bad) {
       const int32_t* row = a.table + (size_t)r * a.max_blocks;
+      // a page listed here and dropped by no sound row is never looked up
       int bb = 0;
-      for (int j = j0 + lane; j < a.max_blocks; j += 32) bb |= row[j] >= a.num_blocks;
+#pragma unroll 4
+      for (int j = j0 + lane; j < a.max_blocks; j += 32) {
+        const int p = row[j];
+        bb |= p >= a.num_blocks;
+        if (p >= 0 && p < a.num_blocks) a.first[p] = INT32_MAX;
+      }
       if (__any_sync(0xffffffffu, bb)) bad = SPEC_DEV_BAD_BLOCK;
-      if (!bad)
-        for (int j = j0 + lane; j < a.max_blocks; j += 32)
-          if (row[j] >= 0) a.first[row[j]] = INT32_MAX;
     }
     if (lane == 0) {
       a.status[i] = bad;
@@ -322,12 +323,13 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_check_kernel(const Fr
 // Every entry of the table: a page a row keeps is marked -1, a dropped one
 // with its lowest position (entry, then page).
 __global__ void __launch_bounds__(kScanThreads) pages_free_mark_kernel(const FreeArgs a) {
-  const long long n = (long long)a.B * a.max_blocks;
-  for (long long e = (long long)blockIdx.x * kScanThreads + threadIdx.x; e < n; e += (long long)gridDim.x * kScanThreads) {
-    const int p = a.table[e];
-    if (p < 0 || p >= a.num_blocks) continue;
-    const int r = (int)(e / a.max_blocks), j = (int)(e - (long long)r * a.max_blocks);
-    atomicMin(&a.first[p], j < a.from[r] ? -1 : a.entry[r] * a.max_blocks + j);
+  const int chunks = (a.max_blocks + kScanThreads - 1) / kScanThreads;  // a CTA takes one row's chunk at a time
+  for (int u = blockIdx.x; u < a.B * chunks; u += gridDim.x) {
+    const int r = u / chunks, j = (u - r * chunks) * kScanThreads + threadIdx.x;
+    if (j >= a.max_blocks) continue;
+    const int p = a.table[(size_t)r * a.max_blocks + j];
+    if (p >= 0 && p < a.num_blocks)
+      atomicMin(&a.first[p], j < a.from[r] ? -1 : a.entry[r] * a.max_blocks + j);
   }
 }
 
@@ -337,47 +339,42 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_release_kernel(const 
   __shared__ ClusterScan scan;
   cg::cluster_group cl = cg::this_cluster();
   const int G = (int)cl.num_blocks() * kPlanThreads, id = (int)cl.block_rank() * kPlanThreads + threadIdx.x;
-  const long long n = (long long)a.N * a.max_blocks;
+  const int n = a.N * a.max_blocks;  // below 2^31
   const int count = *(volatile int32_t*)a.count;
-  auto page = [&](long long e, int& i) -> int32_t* {  // the table entry at position e, or NULL
-    i = (int)(e / a.max_blocks);
-    const int j = (int)(e - (long long)i * a.max_blocks);
-    if (a.status[i] & (SPEC_DEV_BAD_ROW | SPEC_DEV_BAD_BLOCK)) return nullptr;
-    const int r = a.rows[i];
-    int32_t* p = a.table + (size_t)r * a.max_blocks + j;
-    return j >= a.from[r] && *p >= 0 ? p : nullptr;
-  };
-  // the call's total
-  long long mine = 0, total = 0;
-  for (long long e = id; e < n; e += G) {
-    int i;
-    const int32_t* p = page(e, i);
-    mine += p && a.first[*p] == e;
-  }
-  cluster_scan(cl, scan, mine, total);
-  const bool fits = total == 0 || (count >= 0 && count + total <= a.pool_cap);
-  if (!fits) {
-    for (long long e = id; e < n; e += G) {
-      int i;
-      const int32_t* p = page(e, i);
-      if (p && a.first[*p] == e) atomicOr(&a.status[i], SPEC_DEV_CAPACITY);
+  // Thread `id` owns a run of positions (one scan for the call); a run is walked
+  // with its entry's row looked up once.
+  const int per = (int)(((long long)n + G - 1) / G);
+  const int e0 = (int)min((long long)n, (long long)id * per), e1 = (int)min((long long)n, (long long)e0 + per);
+  auto walk = [&](auto&& see) {
+    int i = e0 / a.max_blocks, j = e0 - i * a.max_blocks;
+    for (int e = e0; e < e1; ++i, j = 0) {
+      const int stop = min(a.max_blocks, j + (e1 - e));
+      if ((a.status[i] & (SPEC_DEV_BAD_ROW | SPEC_DEV_BAD_BLOCK)) == 0) {
+        const int r = a.rows[i], from = a.from[r];
+        int32_t* row = a.table + (size_t)r * a.max_blocks;
+        for (int q = max(j, from); q < stop; ++q) {
+          const int p = row[q];
+          if (p >= 0) see(i, row + q, p, a.first[p] == i * a.max_blocks + q);
+        }
+      }
+      e += stop - j;
     }
+  };
+  int mine = 0;
+  walk([&](int, int32_t*, int, bool released) { mine += released; });
+  long long total = 0;
+  long long pos = count + cluster_scan(cl, scan, mine, total);
+  if (total > 0 && (count < 0 || count + total > a.pool_cap)) {
+    walk([&](int i, int32_t*, int, bool released) {
+      if (released) atomicOr(&a.status[i], SPEC_DEV_CAPACITY);
+    });
     return;
   }
-  // in position order, G positions at a time
-  long long base = count;
-  for (long long e0 = 0; e0 < n; e0 += G) {
-    int i;
-    int32_t* p = e0 + id < n ? page(e0 + id, i) : nullptr;
-    const int at = p ? *p : -1;
-    const bool released = p && a.first[at] == e0 + id;
-    long long sum = 0;
-    const long long pos = cluster_scan(cl, scan, released, sum);
-    if (released) a.pool[base + pos] = at;
-    if (p) *p = -1;
-    base += sum;
-  }
-  if (id == 0) *a.count = (int)base;
+  walk([&](int, int32_t* at, int p, bool released) {
+    if (released) a.pool[pos++] = p;
+    *at = -1;
+  });
+  if (id == 0) *a.count = count + (int)total;
 }
 
 // ---------------------------------------------------------------------------
@@ -675,8 +672,6 @@ spec_status spec_pages_free(int32_t* block_table, int B, int max_blocks, int blo
   if (!sm_count(&sms)) return SPEC_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
   spec_workspace_canary(workspace, c.used, st);
-  pages_free_clear_kernel<<<scan_grid(B, sms), kScanThreads, 0, st>>>(a);
-  SPEC_LAUNCH_CHECK();
   if (launch_plan(pages_free_check_kernel, a, st) != cudaSuccess) return SPEC_ERR_CUDA;
   pages_free_mark_kernel<<<scan_grid((long long)B * max_blocks, sms), kScanThreads, 0, st>>>(a);
   SPEC_LAUNCH_CHECK();
