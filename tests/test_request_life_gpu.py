@@ -1,0 +1,168 @@
+"""A request's life through the C ABI: rows reserved, prompts appended and
+attended over, one continuation forked, a token tree verified with its log
+probabilities, the path committed and its pages released, the fork freed, the
+pool compacted, and single tokens attended over what is left."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+import tree_speculative_verification_spec_gb300 as S
+from request_life import logprob_reference, prompt_reference
+from tree_speculative_verification_spec_gb300.pipeline import DeviceBatch, PromptPass, VerifyPass
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from tree_speculative_verification_spec_gb300 import build
+    build.build()
+    S.lib()
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+class Pool:
+    """Two layers of caches, a block table and a pool; every slot starts as NaN."""
+
+    def __init__(self, rows, max_blocks, num_blocks, Hkv, bs, D, layers=2):
+        self.shape = (rows, max_blocks, bs, num_blocks)
+        self.caches = [[torch.full((num_blocks, Hkv, bs, D), math.nan, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+                       for _ in range(layers)]
+        self.k, self.v = (torch.tensor([c[i].data_ptr() for c in self.caches], dtype=torch.int64, device="cuda") for i in (0, 1))
+        self.layers, self.Hkv, self.D = layers, Hkv, D
+        self.table = torch.full((rows, max_blocks), -1, dtype=torch.int32, device="cuda")
+        perm = torch.randperm(num_blocks, generator=torch.Generator().manual_seed(1)).to(torch.int32)
+        self.pool, self.count = perm.cuda(), _ints([num_blocks])
+        self.ws = torch.empty(S.spec_pages_workspace_size(rows, max_blocks, num_blocks, rows), dtype=torch.uint8, device="cuda")
+
+    def fork(self, src, dst, length, room):
+        st = _ints([77] * len(src))
+        S.spec_pages_fork(self.k, self.v, self.layers, self.table, *self.shape, _ints(src), _ints(dst), _ints(length), _ints(room),
+                          len(src), self.Hkv, self.D, S.SPEC_BF16, self.pool, self.count, self.ws, st)
+        assert st.tolist() == [0] * len(src)
+
+    def free(self, rows):
+        st = _ints([77] * len(rows))
+        S.spec_pages_free(self.table, *self.shape, _ints(rows), None, len(rows), self.pool, self.count, self.ws, st)
+        assert st.tolist() == [0] * len(rows)
+
+    def compact(self):
+        st, moved, page_map = _ints([77]), _ints([77]), _ints([0] * self.shape[3])
+        S.spec_pages_compact(self.k, self.v, self.layers, self.table, *self.shape, self.Hkv, self.D, S.SPEC_BF16, self.pool, self.count,
+                             page_map, moved, self.ws, st)
+        assert st.tolist() == [0]
+        return moved.item()
+
+    def held(self):
+        return len({p for p in self.table.flatten().tolist() if p >= 0})
+
+
+def _attend(pool, rows, q, lens, prefix, kv=None, layer=0):
+    """PromptPass over the given table rows, held to 64-bit attention over the cache."""
+    k, v = pool.caches[layer]
+    off = _ints(np.concatenate([[0], np.cumsum(lens)]).tolist())
+    table = pool.table[torch.tensor(rows, device="cuda")].contiguous()
+    p = PromptPass(q, k, v, table, off, _ints(prefix), max(lens), max(prefix), 1.0 / math.sqrt(pool.D))
+    p.run(kv)
+    assert p.status.tolist() == [0] * len(rows)
+    d = dict(q=q, k=k, v=v, table=table, seq_off=off, prefix=_ints(prefix), B=len(rows), T=q.shape[0], Hq=q.shape[1], Hkv=pool.Hkv,
+             D=pool.D, bs=pool.shape[2], scale=1.0 / math.sqrt(pool.D))
+    ref, tol = prompt_reference(d)
+    assert ((p.out.double() - ref).abs() <= tol).all()
+    return p.out
+
+
+def test_a_request_from_its_prompt_to_its_answer():
+    g = torch.Generator("cuda").manual_seed(5)
+    Hq, Hkv, D, bs, V = 8, 2, 64, 16, 700
+    rand = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    pool = Pool(rows=4, max_blocks=96, num_blocks=300, Hkv=Hkv, bs=bs, D=D)
+    lens = [1203, 37]
+    # ---- rows for both prompts; the prompts in two chunks, every layer
+    pool.fork([-1, -1], [0, 1], [0, 0], [lens[0], lens[1]])
+    cut = [700, 0]
+    for layer in range(2):
+        for a, n, prefix in ((0, cut, [0, 0]), (1, [lens[0] - cut[0], lens[1]], [cut[0], 0])):
+            T = sum(n)
+            _attend(pool, [0, 1], rand(T, Hq, D), n, prefix, (rand(T, Hkv, D), rand(T, Hkv, D)), layer)
+    before = [[c.clone() for c in pair] for pair in pool.caches]
+    # ---- request 0 goes on in a second row, and every row gets room for its tree
+    pool.fork([0], [2], [lens[0]], [0])
+    shared = lens[0] // bs
+    assert torch.equal(pool.table[0, :shared], pool.table[2, :shared]) and pool.table[0, shared] != pool.table[2, shared]
+    for pair, old in zip(pool.caches, before):
+        for c, o in zip(pair, old):
+            tail = lens[0] % bs
+            assert torch.equal(c[pool.table[2, shared], :, :tail], o[pool.table[0, shared], :, :tail])
+    held = [lens[0], lens[1], lens[0]]
+    trees = [12, 5, 20]
+    pool.fork([0, 1, 2], [0, 1, 2], held, trees)
+    before_pass = pool.count.item()
+    # ---- one verification pass over three trees, with log probabilities
+    rng = np.random.default_rng(9)
+    parent = np.concatenate([[-1] + [int(rng.integers(0, i)) for i in range(1, n)] for n in trees]).astype(np.int32)
+    off = np.concatenate([[0], np.cumsum(trees)]).astype(np.int32)
+    T = int(off[-1])
+    logits = rng.standard_normal((T, V)).astype(np.float32) * 2
+    tokens = rng.permutation(V)[:T].astype(np.int32)
+    for b in range(3):  # the greedy walk goes down some edges
+        for u in range(1, trees[b]):
+            if rng.random() < 0.7:
+                p = int(parent[off[b] + u])
+                logits[off[b] + p, tokens[off[b] + u]] = 9.0 + rng.random()
+    k, v = pool.caches[0]
+    batch = DeviceBatch(B=3, T=T, n_max=max(trees), V=V, Hq=Hq, Hkv=Hkv, D=D, block_size=bs, num_blocks=300, max_prefix=max(held),
+                        parent=_ints(parent.tolist()), tree_off=_ints(off.tolist()), tokens=_ints(tokens.tolist()),
+                        prefix_len=_ints(held), block_table=pool.table[:3].contiguous(), q=rand(T, Hq, D), k_cache=k, v_cache=v,
+                        p_logits=torch.from_numpy(logits).cuda(), q_probs=None, uniforms=None, scale=1.0 / math.sqrt(D))
+    vp = VerifyPass(batch, logprob_top=4)
+    vp.run("greedy", commit=False, tree_kv=(rand(T, Hkv, D), rand(T, Hkv, D)))
+    assert vp.status.tolist() == [0, 0, 0]
+    path, alen, emitted = vp.path.tolist(), vp.accept_len.tolist(), vp.emitted.tolist()
+    assert max(alen) > 1
+    for b in range(3):
+        for i in range(max(trees)):
+            if i >= alen[b]:
+                assert math.isnan(vp.logprob[b, i].item()) and vp.rank[b, i].item() == -1
+                continue
+            lp, ent, rank, top, top_lp = logprob_reference(logits[off[b] + path[b][i]], emitted[b][i], 1.0, 4)
+            assert vp.rank[b, i].item() == rank == 0  # greedy: the most likely token
+            assert abs(vp.logprob[b, i].item() - lp) < 1e-4 and abs(vp.entropy[b, i].item() - ent) < 1e-4
+            assert vp.top_tokens[b, i].tolist() == list(top)
+            assert np.abs(vp.top_logprobs[b, i].cpu().numpy() - top_lp).max() < 1e-4
+    # ---- the path stays, the tree's other pages go back
+    new_len = torch.zeros(3, dtype=torch.int32, device="cuda")
+    table = batch.block_table
+    S.spec_kv_commit_layers(pool.k, pool.v, 2, table, 96, bs, 300, batch.prefix_len, batch.tree_off, vp.path, batch.n_max,
+                            vp.accept_len, 3, Hkv, D, S.SPEC_BF16, new_len, pool.pool, pool.count, vp.status)
+    assert vp.status.tolist() == [0, 0, 0]
+    pool.table[:3] = table
+    assert new_len.tolist() == [h + a for h, a in zip(held, alen)]
+    assert pool.count.item() >= before_pass and pool.count.item() + pool.held() == 300
+    # ---- the fork ends; what is left comes together; single tokens go on over it
+    q1 = rand(2, Hq, D)
+    lens_now = new_len.tolist()
+    # layer 0 holds the accepted tokens' K/V: the last one attends to all before it
+    first = _attend(pool, [0, 1], q1, [1, 1], [n - 1 for n in lens_now[:2]])
+    pool.free([2])
+    assert pool.count.item() + pool.held() == 300
+    moved = pool.compact()
+    assert moved > 0 and max(pool.table.flatten().tolist()) == pool.held() - 1
+    again = _attend(pool, [0, 1], q1, [1, 1], [n - 1 for n in lens_now[:2]])
+    assert torch.equal(first, again)
+    pool.free([0, 1])
+    assert pool.count.item() == 300 and sorted(pool.pool.tolist()) == list(range(300))
+
+
+def test_logprobs_need_their_buffers():
+    w = W.small_random(3, B=1, n_range=(4, 4), V=50)
+    with pytest.raises(ValueError):
+        VerifyPass(DeviceBatch.from_workload(w)).logprobs()

@@ -1,9 +1,13 @@
-"""One verification pass through the C ABI: buffers + the five calls in order.
+"""A request's passes through the C ABI: buffers + the calls in order.
+
+PromptPass owns the outputs and workspace of one batch of prompts (or of their
+next chunks) and enqueues spec_kv_append -> spec_prompt_attention.
 
 VerifyPass owns the device outputs and workspaces of one batch shape and
 enqueues, on one stream and with no host synchronisation:
   spec_tree_mask_build -> [spec_kv_append] -> spec_tree_attention ->
-  spec_tree_verify_{greedy, stochastic} -> spec_kv_commit.
+  spec_tree_verify_{greedy, stochastic} -> [spec_path_logprobs] ->
+  spec_kv_commit.
 Allocation happens once, in the constructor; run() only launches.
 """
 from dataclasses import dataclass
@@ -55,6 +59,35 @@ class DeviceBatch:
                    uniforms=d(w.uniforms), scale=w.scale)
 
 
+class PromptPass:
+    """Causal attention of packed prompts (or chunks) over the paged cache.
+
+    seq_off int32 [B + 1] and prefix_len int32 [B] are device tensors; n_max
+    and max_prefix bound the longest request and the longest prefix."""
+
+    def __init__(self, q, k_cache, v_cache, block_table, seq_off, prefix_len, n_max, max_prefix, scale):
+        self.q, self.k_cache, self.v_cache, self.block_table = q, k_cache, v_cache, block_table
+        self.seq_off, self.prefix_len, self.scale = seq_off, prefix_len, scale
+        self.num_blocks, Hkv, self.block_size, D = k_cache.shape
+        T, Hq, _ = q.shape
+        self.size = (seq_off.numel() - 1, T, n_max, max_prefix, Hq, Hkv, D)
+        self.out = torch.empty_like(q)
+        self.ws = torch.empty(S.spec_prompt_workspace_size(*self.size), dtype=torch.uint8, device=q.device)
+        self.status = torch.zeros(max(self.size[0], 1), dtype=torch.int32, device=q.device)
+
+    def run(self, prompt_kv=None, stream=None):
+        """prompt_kv: (k_new, v_new) rows [T][Hkv][D] put behind the prefix
+        first, or None when they are already in the cache."""
+        B, T, n_max, max_prefix, Hq, Hkv, D = self.size
+        if prompt_kv is not None:
+            S.spec_kv_append(*prompt_kv, self.k_cache, self.v_cache, self.block_table, self.block_table.shape[1],
+                             self.block_size, self.num_blocks, self.prefix_len, self.seq_off, B, n_max, Hkv, D,
+                             self.status, stream)
+        S.spec_prompt_attention(self.q, self.k_cache, self.v_cache, self.block_table, self.block_table.shape[1],
+                                self.block_size, self.num_blocks, self.prefix_len, self.seq_off, *self.size,
+                                self.scale, self.out, self.ws, self.status, stream)
+
+
 class VerifyPass:
     # stochastic verification options used when verify() is not given them:
     # per-request inverse temperatures (float32 device tensor [B], or None for
@@ -62,7 +95,9 @@ class VerifyPass:
     inv_temp = None
     q_layout = S.SPEC_Q_PER_PARENT
 
-    def __init__(self, batch: DeviceBatch):
+    def __init__(self, batch: DeviceBatch, logprob_top=None):
+        """logprob_top: number of alternatives (0 to 32) that logprobs() gives
+        for every emitted token; None: no buffers for them."""
         b = batch
         dev = b.q.device
         i32 = dict(dtype=torch.int32, device=dev)
@@ -80,6 +115,13 @@ class VerifyPass:
         self.emitted = torch.full((max(b.B, 1), b.n_max), -1, **i32)
         self.n_emitted = torch.zeros(max(b.B, 1), **i32)
         self.new_len = torch.zeros(max(b.B, 1), **i32)
+        self.logprob_top = logprob_top
+        if logprob_top is not None:
+            shape, f32 = (max(b.B, 1), b.n_max), dict(dtype=torch.float32, device=dev)
+            self.logprob, self.entropy = torch.empty(shape, **f32), torch.empty(shape, **f32)
+            self.rank = torch.empty(shape, **i32)
+            self.top_tokens = torch.empty(shape + (logprob_top,), **i32)
+            self.top_logprobs = torch.empty(shape + (logprob_top,), **f32)
         self.batch = b
 
     def mask_build(self, stream=None):
@@ -110,6 +152,18 @@ class VerifyPass:
                                           b.n_max, b.V, self.path, self.accept_len, self.emitted, self.n_emitted,
                                           self.verify_ws, self.status, stream, inv_temp=inv_temp, q_layout=q_layout)
 
+    def logprobs(self, stream=None, inv_temp=None):
+        """Log probability, entropy, rank and alternatives of every emitted
+        token, [B][n_max] (after verify(); the target distribution is the
+        verifier's)."""
+        if self.logprob_top is None:
+            raise ValueError("VerifyPass was made without logprob_top")
+        b = self.batch
+        S.spec_path_logprobs(b.p_logits, b.tree_off, self.path, self.accept_len, self.emitted,
+                             self.inv_temp if inv_temp is None else inv_temp, b.B, b.T, b.n_max, b.V,
+                             self.logprob_top, self.logprob, self.entropy, self.rank, self.top_tokens,
+                             self.top_logprobs, self.status, stream)
+
     def commit(self, stream=None):
         b = self.batch
         S.spec_kv_commit(b.k_cache, b.v_cache, b.block_table, b.max_blocks, b.block_size, b.num_blocks,
@@ -124,5 +178,7 @@ class VerifyPass:
             self.append(*tree_kv, stream=stream)
         self.attention(attn_flags, stream)
         self.verify(mode, stream)
+        if self.logprob_top is not None:
+            self.logprobs(stream)
         if commit:
             self.commit(stream)
