@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
       // its entries that do; again(q) is entry q's key, 0 if it is not there.
       auto pick = [&](auto& x, float mx, auto again) {
         constexpr int N = sizeof(x) / sizeof(float);
+        if (!__any_sync(0xffffffffu, !(mx < top.bar))) return;  // the bar as last seen, then as it is now
         top.floor = fmaxf(top.floor, cta_bar());
         top.bar = fmaxf(top.bar, top.floor);
         if (!__any_sync(0xffffffffu, !(mx < top.bar))) return;
