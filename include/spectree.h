@@ -446,7 +446,8 @@ spec_status spec_tree_merge(const int32_t* seqs, const int32_t* lens, const int3
  *            lies in the pages behind them is never used.
  *   prefix_len int32 [B]    slots already filled before row 0 (0: a fresh prompt; <= max_prefix)
  *   seq_off  int32 [B+1]    packing; n_b may be 0
- *   n_max    the largest n_b the call may see (n_max * (Hq / Hkv) < 2^30)
+ *   n_max    the largest n_b the call may see (n_max * (Hq / Hkv) < 2^30; T * Hq < 2^31)
+ *   scale    finite and not negative (else SPEC_ERR_INVALID_ARG)
  *   out      [T][Hq][D] dtype out; rows outside every request are not written
  *   workspace  16-byte aligned device scratch of spec_prompt_workspace_size() bytes (used when
  *            the keys of few rows are split over the GPU)

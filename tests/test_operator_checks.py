@@ -18,9 +18,9 @@ def _lib():
 
 
 def _prompt(q=P, k=P, v=P, table=P, max_blocks=4, bs=16, nb=8, prefix=P, off=P, B=1, T=4, n_max=4, max_prefix=10, Hq=4,
-            Hkv=2, D=64, dtype=S.SPEC_BF16, out=P, ws=None, ws_bytes=0, status=P):
+            Hkv=2, D=64, dtype=S.SPEC_BF16, out=P, ws=None, ws_bytes=0, status=P, scale=0.125):
     return S.lib().spec_prompt_attention(q, k, v, table, max_blocks, bs, nb, prefix, off, B, T, n_max, max_prefix, Hq, Hkv,
-                                         D, dtype, 0.125, out, ws, ws_bytes, status, None)
+                                         D, dtype, scale, out, ws, ws_bytes, status, None)
 
 
 @pytest.mark.parametrize("change,code", [
@@ -34,6 +34,8 @@ def _prompt(q=P, k=P, v=P, table=P, max_blocks=4, bs=16, nb=8, prefix=P, off=P, 
     (dict(B=70000), S.SPEC_ERR_UNSUPPORTED), (dict(max_prefix=100000), S.SPEC_ERR_WORKSPACE),
     (dict(max_prefix=100000, ws=P, ws_bytes=64), S.SPEC_ERR_WORKSPACE),
     (dict(max_prefix=100000, ws=ODD, ws_bytes=1 << 30), S.SPEC_ERR_WORKSPACE),
+    (dict(scale=-1.0), S.SPEC_ERR_INVALID_ARG), (dict(scale=float("nan")), S.SPEC_ERR_INVALID_ARG),
+    (dict(scale=float("inf")), S.SPEC_ERR_INVALID_ARG),
     (dict(B=0, q=None), S.SPEC_OK), (dict(T=0, q=None), S.SPEC_OK), (dict(n_max=0, q=None), S.SPEC_OK)])
 def test_prompt_attention_refusals(change, code):
     assert _prompt(**change) == code

@@ -7,6 +7,7 @@
 // for any reference m.  Keys are walked once with the running maximum as
 // reference (online softmax in the log2 domain).
 #include <algorithm>
+#include <cmath>
 
 #include "prompt.cuh"
 
@@ -346,6 +347,7 @@ spec_status spec_prompt_attention(const void* q, const void* k_cache, const void
                                   size_t workspace_bytes, int32_t* status, void* stream) {
   SPEC_NVTX_RANGE("spec_prompt_attention");
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (!(scale >= 0.0f && scale < INFINITY)) return SPEC_ERR_INVALID_ARG;  // the largest score is the largest product
   const spec_status sc = prompt_shape_check(B, T, n_max, max_prefix, Hq, Hkv, D, block_size);
   if (sc != SPEC_OK) return sc;
   if (B == 0 || T == 0 || n_max == 0) return SPEC_OK;

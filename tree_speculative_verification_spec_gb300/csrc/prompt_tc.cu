@@ -23,6 +23,15 @@
 // 2^-60 (smaller weights than 2^-60 of the largest do not show in 24 bits).
 // Otherwise that half tile is done again against its own maximum, and O and the
 // sum are scaled to it.
+//
+// What bounds it, and what it measured (32/8 heads, D 128, one GB300):
+//   long prompts: the tensor core.  A step of 2 x 128 x 128 takes 2048 cycles of
+//   it, and shared memory is as busy (Q and K of a QK come from it).  One prompt
+//   of 16384 tokens: 1258 us, 1748 TFLOP/s, 0.91 of the measured bf16 burst;
+//   with the exponentials left out 1132 us.
+//   prompts of some 500 tokens: the few steps of an item against its change
+//   (first step, output rows, next Q), about 10 kcycles each way.
+//   single tokens over long prefixes: HBM, 5.6 TB/s on 64 requests.
 #include <algorithm>
 
 #include "prompt.cuh"
@@ -343,8 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  // registers: 128 x 80 + 256 x 208 = 63488 of the 384 x 168 the CTA was launched with
-  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  // 168 registers a thread hold every role without a spill (128 x 152 + 256 x
+  // 168 = 62464 of the 384 x 168 launched); a split of 80 and 208 spilled in the
+  // loading warps
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
   if (warp == 2) {
     // ------------------------------------------------------ work items, Q and V tiles
     // item it + 1 is handed out once item it's loads are out
@@ -484,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------ softmax, epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int t = (warp - 4) >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -493,22 +504,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 c22 = make_float2(c2, c2);
     int ld = 0, cs = 0;  // loads so far (as the MMA warp counts them), score tiles of this row tile
     float m = 0.0f, l = 0.0f;  // the row's reference (log2 domain) and sum
-    // weights 2^(x c - ref) of 64 columns, `vis` of them visible, packed to bf16; returns their sum
-    auto half_weights = [&](uint32_t (&x0)[32], uint32_t (&x1)[32], int vis, float ref, uint32_t (&pk)[HC / 2]) -> float {
-      if (!__all_sync(0xffffffffu, vis >= HC)) {
+    // weights 2^(x c - ref) of 32 columns, `vis` of them visible, packed to bf16
+    // in pk[0 .. 15] (each off by at most half a bf16 step); returns their fp32 sum
+    auto weights = [&](uint32_t (&x)[32], int vis, float ref, uint32_t* pk) -> float {
+      if (!__all_sync(0xffffffffu, vis >= 32)) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          if (e >= vis) x0[e] = 0xff800000u;
-          if (32 + e >= vis) x1[e] = 0xff800000u;
-        }
+        for (int e = 0; e < 32; ++e)
+          if (e >= vis) x[e] = 0xff800000u;
       }
       const float2 neg = make_float2(-ref, -ref);
       float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
 #pragma unroll
-      for (int e = 0; e < HC; e += 2) {
-        const float2 s = e < 32 ? make_float2(__uint_as_float(x0[e & 31]), __uint_as_float(x0[(e & 31) + 1]))
-                                : make_float2(__uint_as_float(x1[e & 31]), __uint_as_float(x1[(e & 31) + 1]));
-        const float2 z = __ffma2_rn(s, c22, neg);
+      for (int e = 0; e < 32; e += 2) {
+        const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c22, neg);
         const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
         if (e & 2) acc1 = __fadd2_rn(acc1, p);
         else acc0 = __fadd2_rn(acc0, p);
@@ -525,15 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // covers it.  A row with nothing summed yet takes its maximum; a row with a
     // sum takes it where it is larger, and scales the sum and O.
     auto redo = [&](int h, int vis, bool have_o, uint32_t (&pk)[HC / 2], float& sum) {
-      uint32_t x0[32], x1[32];
-      tmem_ld32(tS + h * HC, x0);
-      tmem_ld32(tS + h * HC + 32, x1);
-      tmem_wait_ld(x0);
-      tmem_wait_ld(x1);
+      uint32_t x[32];
       float mx = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld32(tS + h * HC + c * 32, x);
+        tmem_wait_ld(x);
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        mx = fmax3(mx, e < vis ? __uint_as_float(x0[e]) : -INFINITY, 32 + e < vis ? __uint_as_float(x1[e]) : -INFINITY);
+        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, c * 32 + e < vis ? __uint_as_float(x[e]) : -INFINITY);
+      }
       float f = 1.0f;
       if (l == 0.0f) {
         if (mx != -INFINITY) m = mx * c2;  // O holds zeros
@@ -542,20 +550,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= f;
         m = mx * c2;
       }
-      sum = half_weights(x0, x1, vis, m, pk);
+      sum = 0.0f;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld32(tS + h * HC + c * 32, x);
+        tmem_wait_ld(x);
+        sum += c == 0 ? weights(x, vis, m, pk) : weights(x, vis - 32, m, pk + 16);
+      }
       if (!have_o || !__any_sync(0xffffffffu, f != 1.0f)) return;
       // O holds every earlier half once the last of them has completed: this
       // tile's first, or the previous tile's second (one barrier for each, so
       // that a wait is never two phases behind)
       wait(&o_done[t][h ^ 1], h == 1 ? cs : cs - 1);
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
-        tmem_ld32(tO + c * 32, x0);
-        tmem_wait_ld(x0);
+        tmem_ld32(tO + c * 32, x);
+        tmem_wait_ld(x);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x0[e] = __float_as_uint(__uint_as_float(x0[e]) * f);
-        tmem_st32(tO + c * 32, x0);
+        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+        tmem_st32(tO + c * 32, x);
       }
     };
     Work w;
@@ -585,41 +599,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_async_smem();
         }
-        // scores of both halves: the second half's load runs beside the first's weights
+        // quarters of 32 columns, each loaded beside the weights of the one
+        // before; P of a half goes back once its weights are known to fit.  The
+        // loop stays rolled: short items run each part of the code once, and
+        // what they wait for is instructions (64 prompts of 512 tokens: 224 us
+        // with the halves unrolled, 199 rolled, 257 with the output's chunks
+        // unrolled as well).
         const int vis = lim - j * BN;  // visible columns of this tile
-        uint32_t x0[32], x1[32], y0[32], y1[32], pk[HC / 2];
-        tmem_ld32(tS, x0);
-        tmem_ld32(tS + 32, x1);
-        tmem_wait_ld(x0);
-        tmem_wait_ld(x1);
-        tmem_ld32(tS + HC, y0);
-        tmem_ld32(tS + HC + 32, y1);
-        float sum = half_weights(x0, x1, vis, m, pk);
-        if (unfit(sum, vis)) {
-          tmem_wait_ld(y0);
-          tmem_wait_ld(y1);
-          redo(0, vis, j > 0, pk, sum);
-          tmem_ld32(tS + HC, y0);
-          tmem_ld32(tS + HC + 32, y1);
+        uint32_t x[32], y[32], pk[HC / 2];
+        tmem_ld32(tS, x);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          tmem_wait_ld(x);
+          tmem_ld32(tS + h * HC + 32, y);
+          float sum = weights(x, vis - h * HC, m, pk);
+          tmem_wait_ld(y);
+          if (h == 0) tmem_ld32(tS + HC, x);
+          sum += weights(y, vis - h * HC - 32, m, pk + 16);
+          if (unfit(sum, vis - h * HC)) redo(h, vis - h * HC, j > 0 || h > 0, pk, sum);
+          l += sum;
+          tmem_st32(tS + h * (HC / 2), pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t][h]);
         }
-        l += sum;
-        tmem_wait_ld(y0);
-        tmem_wait_ld(y1);
-        tmem_st32(tS, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t][0]);
-        sum = half_weights(y0, y1, vis - HC, m, pk);
-        if (unfit(sum, vis - HC)) {
-          redo(1, vis - HC, true, pk, sum);
-        }
-        l += sum;
-        tmem_st32(tS + HC / 2, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t][1]);
       }
       ld += 2 * n;
       if (nt == 0) continue;
@@ -631,8 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 64 bytes of every row of the warp, one 16-byte piece u[i] after another
       // in each thread: four lanes trade pieces so that each store writes 64
       // contiguous bytes of 8 rows (16 bytes of 32 rows cost four times the
-      // address passes; item of 4 key steps: 22 -> 17 kcycles with the first
-      // reference of 0).
+      // address passes).
       uint32_t rows4[4];  // output rows of the four lanes, 0xffffffff: not written
 #pragma unroll
       for (int s = 0; s < 4; ++s)
@@ -644,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rows4[s] != 0xffffffffu)
             *reinterpret_cast<uint4*>(base + (size_t)rows4[s] * row_bytes + (lane & 3) * 16) = u[s];
       };
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(tO + c * 32, o);
