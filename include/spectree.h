@@ -496,7 +496,8 @@ spec_status spec_prompt_attention(const void* q, const void* k_cache, const void
  *   status   int32 [B] or-ed (the incoming word is not read): SPEC_DEV_BAD_TOKEN (a token
  *            outside [0, V)), SPEC_DEV_BAD_TEMP (tau not in [1e-30, inf)), SPEC_DEV_BAD_PATH
  *            (accept_len above n_max, a path node outside the request's tree, or rows outside
- *            [0, T)); only the entries concerned are affected
+ *            [0, T)); only the entries concerned are affected.  SPEC_DEV_TIMEOUT: entries may
+ *            be unspecified
  * Entries without a result (i >= accept_len[b], rows outside every request,
  * flagged entries) get NaN, rank -1 and top_tokens -1.  One launch.
  */

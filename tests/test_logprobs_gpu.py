@@ -202,3 +202,55 @@ def test_logprobs_repeat_and_replay():
     torch.cuda.synchronize()
     want, _ = _tokens_call(x, tokens, [0, 64], None, 20)
     assert all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+@pytest.mark.parametrize("B,V,k", [(1, 40000, 7), (1100, 60, 3), (30, 9000, 32)])
+def test_path_logprobs_in_every_launch_shape(B, V, k):
+    """One request spread over a cluster, more requests than a CTA numbers for
+    itself, and rounds of several entries per CTA; each with entries that are
+    left out in the middle."""
+    g = np.random.default_rng(B)
+    n_max = 6
+    sizes = g.integers(1, n_max + 1, B)
+    sizes[0] = n_max
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    T = int(off[-1])
+    x = torch.from_numpy(g.standard_normal((T, V)).astype(np.float32) * 3)
+    acc = np.array([int(g.integers(0, s + 1)) for s in sizes], np.int32)
+    acc[0] = n_max
+    path = np.full((B, n_max), -1, np.int32)
+    emitted = np.full((B, n_max), -1, np.int32)
+    for b in range(B):
+        path[b, :acc[b]] = np.arange(acc[b])
+        emitted[b, :acc[b]] = g.integers(0, V, acc[b])
+    path[0, 2], emitted[0, 4] = sizes[0], -1   # a node outside the tree, and no token
+    if B > 2:
+        acc[B - 1] = n_max + 1                 # more accepted nodes than there can be
+    tau = g.uniform(0.5, 2.0, B).astype(np.float32)
+    out, status = _outputs((B, n_max), k), torch.zeros(B, dtype=torch.int32, device="cuda")
+    c = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    S.spec_path_logprobs(x.cuda(), c(off), c(path), c(acc), c(emitted), c(tau), B, T, n_max, V, k, *out, status)
+    want = [0] * B
+    want[0] = S.SPEC_DEV_BAD_PATH | S.SPEC_DEV_BAD_TOKEN
+    if B > 2:
+        want[B - 1] = S.SPEC_DEV_BAD_PATH
+    assert status.tolist() == want
+    host = [o.cpu() for o in out]
+    for b in list(range(min(B, 25))) + [B - 1]:
+        for i in range(n_max):
+            if i >= acc[b] or acc[b] > n_max or (b == 0 and i in (2, 4)):
+                assert math.isnan(host[0][b, i].item()) and host[2][b, i].item() == -1 and host[3][b, i].tolist() == [-1] * k
+            else:
+                _check(x[off[b] + path[b, i]].double().numpy(), [o[b] for o in host], i, int(emitted[b, i]), float(tau[b]), k)
+
+
+def test_arguments_of_other_types_are_refused():
+    x = torch.zeros((2, 8), device="cuda")
+    off, st = torch.tensor([0, 2], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    lp = torch.zeros(2, device="cuda")
+    tok = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for bad in (dict(tok=tok.long()), dict(lp=lp.double()), dict(x=x.half())):
+        a = dict(x=x, tok=tok, lp=lp)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            S.spec_token_logprobs(a["x"], a["tok"], off, None, 1, 2, 8, 0, a["lp"], None, None, None, None, st)

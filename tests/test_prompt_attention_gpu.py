@@ -186,3 +186,48 @@ def test_workspace_contents_do_not_matter(monkeypatch):
     monkeypatch.setenv("SPECTREE_WORKSPACE_CANARY", "1")
     out, _ = _call(d)
     assert torch.equal(out, ref) and not math.isnan(out.float().sum().item())
+
+
+def test_a_batch_without_any_token():
+    d = paged_batch(37, [0, 0, 0], [0, 5, 40], 8, 2, 64, 16, torch.bfloat16, extra_rows=4)
+    d["n_max"] = 3
+    for dtype in (torch.bfloat16, torch.float32):
+        for n in ("q", "k", "v"):
+            d[n] = d[n].to(dtype)
+        out, status = _call(d)
+        assert status.tolist() == [0, 0, 0] and (out == 7.0).all()
+
+
+def test_calls_on_two_streams_at_once_and_again():
+    """Two batches on two streams, each with its own workspace, several times
+    over: every call gives the same bits."""
+    ds = [paged_batch(41, [500, 3, 129], [0, 4000, 77], 16, 4, 128, 16, torch.bfloat16),
+          paged_batch(43, [1], [9000], 8, 1, 64, 32, torch.bfloat16)]
+    ref = [_call(d)[0] for d in ds]
+    streams = [torch.cuda.Stream() for _ in ds]
+    ws = [torch.empty(S.spec_prompt_workspace_size(*_size(d)), dtype=torch.uint8, device="cuda") for d in ds]
+    outs = [[torch.full_like(d["q"], 7.0) for _ in range(4)] for d in ds]
+    st = [torch.zeros(d["B"], dtype=torch.int32, device="cuda") for d in ds]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for d, s, w, o, t in zip(ds, streams, ws, outs, st):
+            _call(d, o[i], t, w, stream=s)
+    torch.cuda.synchronize()
+    for r, o in zip(ref, outs):
+        assert all(torch.equal(r, x) for x in o)
+
+
+def test_infinities_and_nan_stay_in_their_own_rows():
+    """A query row of NaN, and one whose scores are infinite, next to sound rows."""
+    d = paged_batch(47, [40, 9], [0, 300], 8, 2, 64, 16, torch.bfloat16)
+    ref, _ = _call(d)
+    d["q"] = d["q"].clone()
+    d["q"][7, 2] = math.nan
+    d["q"][11, 5] = math.inf
+    out, status = _call(d)
+    assert status.tolist() == [0, 0] and torch.isnan(out[7, 2]).all()
+    sound = torch.ones(49, 8, dtype=torch.bool, device="cuda")
+    sound[7, 2] = sound[11, 5] = False
+    d["q"][7, 2], d["q"][11, 5] = 0.0, 0.0  # the reference of the other rows
+    want, tol = prompt_reference(d)
+    assert ((out.double() - want).abs() <= tol)[sound].all()

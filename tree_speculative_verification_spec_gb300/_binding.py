@@ -289,6 +289,28 @@ def _scratch(t):
     return (None, 0) if t is None else (_ptr(t), t.numel() * t.element_size())
 
 
+def _i32(t):
+    """Pointer of an int32 tensor argument (None passes)."""
+    if t is not None and t.dtype != torch.int32:
+        raise ValueError("index, table and status arguments must be int32 tensors")
+    return _ptr(t)
+
+
+def _f32(t):
+    """Pointer of a float32 tensor argument (None passes)."""
+    if t is not None and t.dtype != torch.float32:
+        raise ValueError("temperatures and scores must be float32 tensors")
+    return _ptr(t)
+
+
+def _stream_of(t, stream):
+    """The stream of a call on tensor t's device, which has to be the current
+    one (its kernels are launched there)."""
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError("tensor arguments must be on the current CUDA device")
+    return _stream(stream)
+
+
 def spec_prompt_workspace_size(B, T, n_max, max_prefix, Hq, Hkv, D):
     return int(lib().spec_prompt_workspace_size(B, T, n_max, max_prefix, Hq, Hkv, D))
 
@@ -299,9 +321,9 @@ def spec_prompt_attention(q, k_cache, v_cache, block_table, max_blocks, block_si
     if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or out.dtype != q.dtype:
         raise ValueError("q, out and the caches must have one dtype")
     _check("spec_prompt_attention", lib().spec_prompt_attention(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), max_blocks, block_size, num_blocks,
-        _ptr(prefix_len), _ptr(seq_off), B, T, n_max, max_prefix, Hq, Hkv, D, _dtype_code(q), float(scale), _ptr(out),
-        *_scratch(workspace), _ptr(status), _stream(stream)))
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _i32(block_table), max_blocks, block_size, num_blocks,
+        _i32(prefix_len), _i32(seq_off), B, T, n_max, max_prefix, Hq, Hkv, D, _dtype_code(q), float(scale), _ptr(out),
+        *_scratch(workspace), _i32(status), _stream_of(q, stream)))
 
 
 def spec_token_logprobs(logits, tokens, seq_off, inv_temp, B, T, V, k, logprob, entropy, rank, top_tokens,
@@ -309,8 +331,8 @@ def spec_token_logprobs(logits, tokens, seq_off, inv_temp, B, T, V, k, logprob, 
     """logits: float32 or bfloat16 [T, V]; inv_temp: float32 [B] or None (1);
     entropy, rank, top_tokens and top_logprobs may be None."""
     _check("spec_token_logprobs", lib().spec_token_logprobs(
-        _ptr(logits), _dtype_code(logits), _ptr(tokens), _ptr(seq_off), _ptr(inv_temp), B, T, V, k, _ptr(logprob),
-        _ptr(entropy), _ptr(rank), _ptr(top_tokens), _ptr(top_logprobs), _ptr(status), _stream(stream)))
+        _ptr(logits), _dtype_code(logits), _i32(tokens), _i32(seq_off), _f32(inv_temp), B, T, V, k, _f32(logprob),
+        _f32(entropy), _i32(rank), _i32(top_tokens), _f32(top_logprobs), _i32(status), _stream_of(logits, stream)))
 
 
 def spec_path_logprobs(p_logits, tree_off, path, accept_len, emitted, inv_temp, B, T, n_max, V, k, logprob, entropy,
@@ -318,9 +340,9 @@ def spec_path_logprobs(p_logits, tree_off, path, accept_len, emitted, inv_temp, 
     """p_logits: float32 or bfloat16 [T, V]; path, accept_len and emitted as
     a verifier wrote them; the other arguments as in spec_token_logprobs."""
     _check("spec_path_logprobs", lib().spec_path_logprobs(
-        _ptr(p_logits), _dtype_code(p_logits), _ptr(tree_off), _ptr(path), _ptr(accept_len), _ptr(emitted),
-        _ptr(inv_temp), B, T, n_max, V, k, _ptr(logprob), _ptr(entropy), _ptr(rank), _ptr(top_tokens),
-        _ptr(top_logprobs), _ptr(status), _stream(stream)))
+        _ptr(p_logits), _dtype_code(p_logits), _i32(tree_off), _i32(path), _i32(accept_len), _i32(emitted),
+        _f32(inv_temp), B, T, n_max, V, k, _f32(logprob), _f32(entropy), _i32(rank), _i32(top_tokens),
+        _f32(top_logprobs), _i32(status), _stream_of(p_logits, stream)))
 
 
 def spec_pages_workspace_size(B, max_blocks, num_blocks, N):
@@ -333,25 +355,25 @@ def spec_pages_fork(k_ptrs, v_ptrs, layers, block_table, B, max_blocks, block_si
     (None with layers = 0); room: int32 [N] or None (0); dtype: SPEC_F32 or
     SPEC_BF16."""
     _check("spec_pages_fork", lib().spec_pages_fork(
-        _ptr(k_ptrs), _ptr(v_ptrs), layers, _ptr(block_table), B, max_blocks, block_size, num_blocks, _ptr(src),
-        _ptr(dst), _ptr(length), _ptr(room), N, Hkv, D, dtype, _ptr(free_pool), free_pool.numel(), _ptr(free_count),
-        *_scratch(workspace), _ptr(status), _stream(stream)))
+        _ptr(k_ptrs), _ptr(v_ptrs), layers, _i32(block_table), B, max_blocks, block_size, num_blocks, _i32(src),
+        _i32(dst), _i32(length), _i32(room), N, Hkv, D, dtype, _i32(free_pool), free_pool.numel(), _i32(free_count),
+        *_scratch(workspace), _i32(status), _stream_of(block_table, stream)))
 
 
 def spec_pages_free(block_table, B, max_blocks, block_size, num_blocks, rows, keep_len, N, free_pool, free_count,
                     workspace, status, stream=None):
     """keep_len: int32 [N] or None (rows are dropped whole)."""
     _check("spec_pages_free", lib().spec_pages_free(
-        _ptr(block_table), B, max_blocks, block_size, num_blocks, _ptr(rows), _ptr(keep_len), N, _ptr(free_pool),
-        free_pool.numel(), _ptr(free_count), *_scratch(workspace), _ptr(status), _stream(stream)))
+        _i32(block_table), B, max_blocks, block_size, num_blocks, _i32(rows), _i32(keep_len), N, _i32(free_pool),
+        free_pool.numel(), _i32(free_count), *_scratch(workspace), _i32(status), _stream_of(block_table, stream)))
 
 
 def spec_pages_compact(k_ptrs, v_ptrs, layers, block_table, B, max_blocks, block_size, num_blocks, Hkv, D, dtype,
                        free_pool, free_count, page_map, moved, workspace, status, stream=None):
     _check("spec_pages_compact", lib().spec_pages_compact(
-        _ptr(k_ptrs), _ptr(v_ptrs), layers, _ptr(block_table), B, max_blocks, block_size, num_blocks, Hkv, D, dtype,
-        _ptr(free_pool), free_pool.numel(), _ptr(free_count), _ptr(page_map), _ptr(moved), *_scratch(workspace),
-        _ptr(status), _stream(stream)))
+        _ptr(k_ptrs), _ptr(v_ptrs), layers, _i32(block_table), B, max_blocks, block_size, num_blocks, Hkv, D, dtype,
+        _i32(free_pool), free_pool.numel(), _i32(free_count), _i32(page_map), _i32(moved), *_scratch(workspace),
+        _i32(status), _stream_of(block_table, stream)))
 
 
 def spec_selftest_bounded_wait(status, polls, stream=None):

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
   __shared__ int s_mth[kLpWarps];     // each warp's m-th best score, in float_order
   __shared__ int s_n;
   __shared__ int s_live[kLpMaxLive];  // accepted entries before each request
-  __shared__ int s_total, abort_flag;
+  __shared__ int s_total, abort_flag, s_last[kLpStages];  // s_last: the last copy into each stage
   __shared__ uint64_t full[kLpStages], empty[kLpStages];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = a.C, part = (int)cluster.block_rank();
@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
     for (int i = 0; i < kLpStages; ++i) {
       tc5::mbar_init(&full[i], 1);
       tc5::mbar_init(&empty[i], kLpWarps);
+      s_last[i] = -1;
     }
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -291,6 +292,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
           if (u >= kLpStages && !tc5::mbar_wait(&empty[st], (u / kLpStages - 1) & 1, &abort_flag)) break;
           const uint32_t bytes = 16u * (uint32_t)min(kLpChunk, v1 - v0 - i * kLpChunk);
           tc5::mbar_expect_tx(&full[st], bytes);
+          s_last[st] = u;
           bulk_load(ring + st * kLpChunk, reinterpret_cast<const uint4*>(src + head) + v0 + i * kLpChunk, bytes, &full[st]);
         }
       }
@@ -516,8 +518,13 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
     }
   }
   __syncthreads();
-  if (abort_flag && threadIdx.x == 0)  // a wait ran out: every request of the call may be short of a row
+  if (abort_flag && threadIdx.x == 0) {
+    // a wait ran out: the CTA's own copies land before it exits, and every
+    // request of the call may be short of a row
+    for (int st = 0; st < kLpStages; ++st)
+      if (s_last[st] >= 0) tc5::mbar_drain(&full[st], (s_last[st] / kLpStages) & 1);
     for (int b = 0; b < a.B; ++b) atomicOr(&a.status[b], SPEC_DEV_TIMEOUT);
+  }
 }
 
 static spec_status launch_logprobs(LpArgs a, spec_dtype dtype, long long entries, cudaStream_t stream) {

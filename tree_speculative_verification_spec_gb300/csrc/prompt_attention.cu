@@ -357,7 +357,10 @@ spec_status spec_prompt_attention(const void* q, const void* k_cache, const void
   if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
         reinterpret_cast<uintptr_t>(out)) & 15) != 0)
     return SPEC_ERR_INVALID_ARG;
+  // the tensor-core path names cache rows by 32-bit coordinates, and items by a grid index
+  if (dtype == SPEC_BF16 && (long long)num_blocks * Hkv * block_size >= (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
   const PromptPlan plan = prompt_plan(B, T, n_max, max_prefix, Hq, Hkv, dtype == SPEC_BF16);
+  if (plan.tiles * Hkv * plan.splits > (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
   const size_t need = prompt_ws_bytes(plan, T, Hq, D);
   if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return SPEC_ERR_WORKSPACE;

@@ -742,9 +742,7 @@ static cudaError_t launch_d(const PromptArgs& a, const PromptPlan& p, cudaStream
   prm.bs_log2 = 0;
   while ((1 << prm.bs_log2) < a.block_size) ++prm.bs_log2;
   prm.rows_total = (long long)a.num_blocks * a.Hkv * a.block_size;
-  if (prm.rows_total >= (long long)INT32_MAX) return cudaErrorInvalidValue;
   const long long items = p.tiles * a.Hkv * p.splits;
-  if (items > INT32_MAX) return cudaErrorInvalidValue;
   alignas(64) CUtensorMap mk, mv, mq;
   {
     const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)prm.rows_total}, strides[1] = {(cuuint64_t)D * 2};
