@@ -215,12 +215,16 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
 }
 
 // Split-key combine: out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over
-// the splits that begin at or before the row's last key.  One warp per row.
+// the splits that begin at or before the row's last key.  One warp per row:
+// lane s holds split s's weight (32 splits at a time), and four splits' rows are
+// loaded before any is added, since one row's chain of loads is all there is to
+// wait for.  A programmatic dependent of the attention kernel.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) prompt_combine_kernel(const PromptArgs a) {
   const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const long long rows = (long long)a.T * a.Hq;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial rows and the status are the attention's
   if (row >= rows) return;
   const int t = (int)(row / a.Hq);
   int lo = 0, hi = a.B;  // the last request with seq_off[lo] <= t
@@ -231,24 +235,36 @@ __global__ void __launch_bounds__(256) prompt_combine_kernel(const PromptArgs a)
   }
   const PromptRequest rq = prompt_request(a, lo);
   const int i = t - rq.off;
-  if (!rq.ok || i < 0 || i >= rq.n) return;
+  if (!__shfl_sync(0xffffffffu, (int)rq.ok, 0) || i < 0 || i >= rq.n) return;  // one lane's word for the warp
   const int ns = min(a.splits, (rq.P + i) / a.chunk + 1);
-  const float2* ml = reinterpret_cast<const float2*>(a.ws_ml);
+  const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row;
   float M = -INFINITY;
-  for (int s = 0; s < ns; ++s) M = fmaxf(M, ml[s * rows + row].x);
+  for (int s = lane; s < ns; s += 32) M = fmaxf(M, ml[s * rows].x);
+  M = warp_max_f(M);
+  const float* os = a.ws_o + row * D + lane;
   float sum = 0.0f, acc[D / 32];
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) acc[j] = 0.0f;
-  for (int s = 0; s < ns; ++s) {
-    const float2 x = ml[s * rows + row];
-    if (x.x == -INFINITY) continue;
-    const float w = pr_exp2(x.x - M);
-    sum = fmaf(w, x.y, sum);
-    const float* os = a.ws_o + (s * rows + row) * D;
+  for (int s0 = 0; s0 < ns; s0 += 32) {
+    const float2 x = s0 + lane < ns ? ml[(s0 + lane) * rows] : make_float2(-INFINITY, 0.0f);
+    const float wl = x.x == -INFINITY ? 0.0f : pr_exp2(x.x - M);  // no visible key in the split
+    sum = fmaf(wl, x.y, sum);
+    const int n = min(32, ns - s0);
+    for (int s = 0; s < n; s += 4) {
+      float o[4][D / 32];
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(w, os[lane + 32 * j], acc[j]);
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) o[q][j] = s + q < n ? os[(s0 + s + q) * rows * D + 32 * j] : 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float w = __shfl_sync(0xffffffffu, wl, (s + q) & 31);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) acc[j] = s + q < n ? fmaf(w, o[q][j], acc[j]) : acc[j];
+      }
+    }
   }
-  const float inv = 1.0f / sum;
+  const float inv = 1.0f / warp_sum_f(sum);
   T* out = static_cast<T*>(a.out) + row * D;
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) out[lane + 32 * j] = from_f32<T>(acc[j] * inv);
@@ -268,41 +284,52 @@ cudaError_t launch_prompt_cc(const PromptArgs& a, const PromptPlan& p, cudaStrea
 }
 
 static cudaError_t launch_prompt_combine(const PromptArgs& a, spec_dtype dt, cudaStream_t stream) {
-  const unsigned grid = (unsigned)(((long long)a.T * a.Hq + 7) / 8);
-  if (dt == SPEC_F32) {
-    if (a.D == 64) prompt_combine_kernel<float, 64><<<grid, 256, 0, stream>>>(a);
-    else prompt_combine_kernel<float, 128><<<grid, 256, 0, stream>>>(a);
-  } else {
-    if (a.D == 64) prompt_combine_kernel<__nv_bfloat16, 64><<<grid, 256, 0, stream>>>(a);
-    else prompt_combine_kernel<__nv_bfloat16, 128><<<grid, 256, 0, stream>>>(a);
-  }
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)a.T * a.Hq + 7) / 8), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void (*kern)(const PromptArgs) = dt == SPEC_F32 ? (a.D == 64 ? prompt_combine_kernel<float, 64> : prompt_combine_kernel<float, 128>)
+                                                  : (a.D == 64 ? prompt_combine_kernel<__nv_bfloat16, 64>
+                                                               : prompt_combine_kernel<__nv_bfloat16, 128>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // Row tiles and key splits of a call.  Keys are split only when the row tiles
-// alone leave SMs idle.  CUDA cores: enough splits for about two CTAs an SM,
-// each of at least 256 keys.  Tensor cores (one CTA an SM): the split count of
-// least waves x (4 us of set-up and epilogue + 1.3 us per 128-key step).
+// alone leave SMs idle.
+// CUDA cores: a 64-key step of one CTA takes 4 us and more of the FMA pipe, so
+// splits go down to one step, as far as about two CTAs an SM (one token over 600
+// keys: 78 us whole, 33 us by 128 keys, 25 us by 64; 2 x 500 tokens after 500:
+// 119, 72, 74).
+// Tensor cores (one CTA an SM): the split count of least waves x (4 us of
+// set-up and output + 1.3 us per 128-key step) + 5 us for the combine (512
+// tokens: 21 us whole, 29 us in two; one token over 16384: 33 us in 19).
 static PromptPlan prompt_plan(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, bool bf16) {
   PromptPlan p;
   const int g = Hq / Hkv;
   p.tiles = (long long)T * g / (bf16 ? kPromptTcRows : kPromptCcRows) + B;
   const long long units = p.tiles * Hkv, keys = (long long)max_prefix + n_max;
   long long splits = 1;
-  if (units < 152 && !bf16) splits = std::max(1LL, std::min((2 * 152 + units - 1) / units, (keys + 255) / 256));
+  if (units < 152 && !bf16) splits = std::max(1LL, std::min((2 * 152 + units - 1) / units, keys / kPrKeys));
   if (units < 152 && bf16) {
     double best = 1e300;
     const long long most = std::max(1LL, std::min(64LL, (keys + 127) / 128));
     for (long long s = 1; s <= most; ++s) {
       const long long steps = ((keys + s - 1) / s + 127) / 128;
-      const double cost = (double)((units * s + 151) / 152) * (4.0 + 1.3 * (double)steps);
+      const double cost = (double)((units * s + 151) / 152) * (4.0 + 1.3 * (double)steps) + (s > 1 ? 5.0 : 0.0);
       if (cost < best * 0.97) {  // fewer splits on near-ties: less partial traffic
         best = cost;
         splits = s;
       }
     }
   }
-  const long long chunk = std::max(128LL, ((keys + splits - 1) / splits + 127) / 128 * 128);
+  const long long tile = bf16 ? 128 : kPrKeys;
+  const long long chunk = std::max(tile, ((keys + splits - 1) / splits + tile - 1) / tile * tile);
   p.chunk = (int)std::min<long long>(chunk, 1LL << 30);
   p.splits = (int)std::max(1LL, (keys + chunk - 1) / chunk);
   return p;
