@@ -137,6 +137,27 @@ def test_bad_tokens_and_temperatures():
         assert out[3][i].tolist() == [-1] * 3 and all(map(math.isnan, out[4][i].tolist()))
 
 
+@pytest.mark.parametrize("V", [40, 9000], ids=["one_warp", "many"])
+@pytest.mark.parametrize("tau,low", [(1e-30, -1e31), (1e-30, -1e30), (1e-30, -3e38), (3.4e38, -1e9), (3.4e38, -math.inf)])
+def test_temperatures_at_the_ends_of_their_range(tau, low, V):
+    """Masked logits that still weigh at the smallest inverse temperature, before
+    and behind the unmasked ones, and products that overflow at the largest."""
+    x = torch.full((3, V), low)
+    x[0, :2], x[1, V - 3:], x[2, V // 2] = 1.0, 2.0, -0.5
+    tokens, k = [1, 0, V // 2], 5
+    out, status = _tokens_call(x.cuda(), tokens, [0, 3], [tau], k)
+    assert status == [0]
+    for i, t in enumerate(tokens):
+        row, f = x[i].double().numpy(), float(np.float32(tau))
+        lp, ent, rank, top, top_lp = logprob_reference(row, t, f, k)
+        if tau > 1.0:  # beyond fp32: minus infinity there
+            lp, top_lp = (np.where(v < -3.4e38, -math.inf, v) for v in (lp, top_lp))
+        got = [o[i].cpu() for o in out]
+        for g, r in [(got[0].item(), lp), (got[1].item(), ent)] + list(zip(got[4].tolist(), top_lp)):
+            assert g == r or abs(g - r) <= _tolerance(row, f, r) * (1 + math.log(V)), (g, r)
+        assert got[2].item() == rank and got[3].tolist() == list(top)
+
+
 def test_optional_outputs_and_alignment():
     """Rows that start anywhere, and calls that want the log probability alone."""
     for dtype in (torch.float32, torch.bfloat16):

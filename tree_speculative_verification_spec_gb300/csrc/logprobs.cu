@@ -82,8 +82,8 @@ struct SoftStats {
     } else {
       const float d = r - to;  // <= 0; -inf when `to` is +inf
       const float f = lp_exp2(d * c);
-      // e^(tau d) vanishes faster than d grows: the clamp keeps 0 * inf out
-      w = f * fmaf(s, max_nan(d, -1e30f), w);
+      // f > 0 leaves |d| below 88 / tau, so that s d is finite; a NaN has f NaN
+      w = f == 0.0f ? 0.0f : f * fmaf(s, d, w);
       s *= f;
     }
     r = to;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
       token = -1;
     }
     if (!skip) {
-      const float c = tau * 1.4426950408889634f;
+      const float c = fminf(tau * 1.4426950408889634f, 3.4e38f);  // finite: 0 times it is 0
       const float2 cc = make_float2(c, c);
       const float xt = token >= 0 ? to_f32(src[token]) : INFINITY;  // no token: no entry is above it
       SoftStats st;
@@ -503,7 +503,9 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
         if (lane < k) {
           const int id = (int)(~(uint32_t)(top.list & 0xffffffffull));
           if (a.top_tokens) a.top_tokens[entry * k + lane] = id;
-          if (a.top_logprobs) a.top_logprobs[entry * k + lane] = (to_f32(src[id]) - st.r) * tau - ls;
+          // after a timeout the list may be short
+          if (a.top_logprobs)
+            a.top_logprobs[entry * k + lane] = (unsigned)id < (unsigned)a.V ? (to_f32(src[id]) - st.r) * tau - ls : NAN;
         }
       }
     }
