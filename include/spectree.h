@@ -455,6 +455,8 @@ spec_status spec_tree_merge(const int32_t* seqs, const int32_t* lens, const int3
  *            they were.  Or-ed with SPEC_DEV_BAD_TREE (n_b outside [0, n_max], or rows outside
  *            [0, T)), SPEC_DEV_CAPACITY (prefix_len outside [0, max_prefix], or
  *            prefix_len + n_b beyond the block table): such a request is skipped too;
+ *            (a seq_off that decreases flags a request whose n_b is negative; rows that two
+ *            requests then both own are unspecified);
  *            SPEC_DEV_BAD_BLOCK (a block id outside [0, num_blocks)) and SPEC_DEV_TIMEOUT: its
  *            output rows are unspecified.
  */
@@ -559,7 +561,7 @@ spec_status spec_path_logprobs(const void* p_logits, spec_dtype dtype, const int
  *
  *   k_caches, v_caches  device arrays of `layers` device pointers, as in spec_kv_commit_layers,
  *            each cache 16-byte aligned; layers = 0 (pointers NULL): metadata only
- *   block_table int32 [B][max_blocks] in/out; B * max_blocks and N * max_blocks < 2^31
+ *   block_table int32 [B][max_blocks] in/out; B * max_blocks and N * max_blocks <= 2^30
  *   free_pool int32 [free_cap], free_count int32 [1]: device memory, in/out
  *   workspace  16-byte aligned device scratch of spec_pages_workspace_size() bytes (N of the
  *            call; 0 for compact)

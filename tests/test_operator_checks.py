@@ -123,3 +123,12 @@ def test_append_takes_more_rows_than_a_tree_has():
     a = lambda n_max, B: S.lib().spec_kv_append(None, None, None, None, None, 4, 16, 4, None, None, B, n_max, 2, 64, S.SPEC_BF16, None, None)  # noqa: E731
     assert a(100000, 0) == S.SPEC_OK
     assert a(100000, 1) == S.SPEC_ERR_INVALID_ARG  # past the size checks, at the pointers
+
+
+@pytest.mark.parametrize("B,max_blocks,N,code", [((1 << 30) + 1, 1, 1, S.SPEC_ERR_UNSUPPORTED), (4, 1 << 20, 1025, S.SPEC_ERR_UNSUPPORTED),
+                                                 (4, 1 << 20, 1024, S.SPEC_ERR_WORKSPACE), (1025, 1 << 20, 1, S.SPEC_ERR_UNSUPPORTED),
+                                                 (1 << 30, 1, 1, S.SPEC_ERR_WORKSPACE)])
+def test_page_calls_keep_their_counters_in_32_bits(B, max_blocks, N, code):
+    L = S.lib()
+    assert L.spec_pages_free(P, B, max_blocks, 16, 8, P, None, N, P, 8, P, P, 8, P, None) == code
+    assert L.spec_pages_fork(P, P, 1, P, B, max_blocks, 16, 8, P, P, P, None, N, 2, 64, S.SPEC_BF16, P, 8, P, P, 8, P, None) == code

@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_release_kernel(const 
   __shared__ ClusterScan scan;
   cg::cluster_group cl = cg::this_cluster();
   const int G = (int)cl.num_blocks() * kPlanThreads, id = (int)cl.block_rank() * kPlanThreads + threadIdx.x;
-  const int n = a.N * a.max_blocks;  // below 2^31
+  const int n = a.N * a.max_blocks;  // at most 2^30
   const int count = *(volatile int32_t*)a.count;
   // Thread `id` owns a run of positions (one scan for the call), eight of them
   // looked up at a time, since each is a chain of four loads.
@@ -564,7 +564,8 @@ static void carve_compact(CompactArgs& a, Carve& c) {
 static spec_status pages_check(int B, int max_blocks, int block_size, int num_blocks, int N) {
   if (B < 0 || max_blocks <= 0 || num_blocks <= 0 || N < 0) return SPEC_ERR_INVALID_ARG;
   if (block_size < 8 || block_size > 65536 || (block_size & (block_size - 1))) return SPEC_ERR_UNSUPPORTED;
-  if ((long long)B * max_blocks >= (1LL << 31) || (long long)N * max_blocks >= (1LL << 31) || num_blocks > (1 << 30))
+  // 32-bit counters step past the last entry by up to the threads of a grid
+  if ((long long)B * max_blocks > (1LL << 30) || (long long)N * max_blocks > (1LL << 30) || num_blocks > (1 << 30))
     return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
 }
