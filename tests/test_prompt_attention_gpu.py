@@ -231,3 +231,19 @@ def test_infinities_and_nan_stay_in_their_own_rows():
     d["q"][7, 2], d["q"][11, 5] = 0.0, 0.0  # the reference of the other rows
     want, tol = prompt_reference(d)
     assert ((out.double() - want).abs() <= tol)[sound].all()
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (6, 2)], ids=["tma_q", "copied_q"])
+@pytest.mark.parametrize("fill", [math.nan, math.inf, 3e4], ids=["nan", "inf", "large"])
+def test_rows_beside_a_request_leave_its_bits_alone(fill, Hq, Hkv):
+    """A row tile reaches past its request, into the next one's rows and the rows
+    behind the last: what they hold does not show in a single bit."""
+    d = paged_batch(53, [70, 21], [40, 300], Hq, Hkv, 128, 16, torch.bfloat16, extra_rows=5)
+    d["q"][91:] = 0.0
+    ref, _ = _call(d)
+    d["q"][91:] = fill
+    out, status = _call(d)
+    assert status.tolist() == [0, 0] and torch.equal(out[:91], ref[:91])
+    d["q"][70:91] = fill
+    out, status = _call(d)
+    assert status.tolist() == [0, 0] and torch.equal(out[:70], ref[:70])

@@ -352,9 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  // 168 registers a thread hold every role without a spill (128 x 152 + 256 x
-  // 168 = 62464 of the 384 x 168 launched); a split of 80 and 208 spilled in the
-  // loading warps
+  // 168 registers a thread hold every role with one 4-byte spill (128 x 152 +
+  // 256 x 168 = 62464 of the 384 x 168 launched); a split of 80 and 208 spilled
+  // more, in the loading warps
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
   if (warp == 2) {
     // ------------------------------------------------------ work items, Q and V tiles
@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 c22 = make_float2(c2, c2);
     int ld = 0, cs = 0;  // loads so far (as the MMA warp counts them), score tiles of this row tile
     float m = 0.0f, l = 0.0f;  // the row's reference (log2 domain) and sum
+    float limit = kSumLimit;
     // weights 2^(x c - ref) of 32 columns, `vis` of them visible, packed to bf16
     // in pk[0 .. 15] (each off by at most half a bf16 step); returns their fp32 sum
     auto weights = [&](uint32_t (&x)[32], int vis, float ref, uint32_t* pk) -> float {
@@ -525,9 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return (acc0.x + acc0.y) + (acc1.x + acc1.y);
     };
-    // Whether half weights that sum to `sum` need another reference.
+    // Whether half weights that sum to `sum` need another reference (a NaN stays
+    // one against any).
     auto unfit = [&](float sum, int vis) -> bool {
-      return __any_sync(0xffffffffu, !(sum < kSumLimit) || (l == 0.0f && vis > 0 && sum < 1.0f / kSumLimit));
+      return __any_sync(0xffffffffu, sum >= limit || (l == 0.0f && vis > 0 && sum < 1.0f / kSumLimit));
     };
     // Half h again, from its scores in tensor memory, against a reference that
     // covers it.  A row with nothing summed yet takes its maximum; a row with a
@@ -579,8 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = row < w.n * a.g;
       const int tok = valid ? row / a.g : w.n - 1;
       const int lim = w.P + tok + 1 - w.k_begin;  // visible keys of this range
+      // rows behind the request (the next one's q, or NaN) have no say in a redo
+      limit = valid ? kSumLimit : NAN;
       m = 0.0f;
-      l = 0.0f;
+      l = valid ? 0.0f : 1.0f;
       for (int j = 0; j < nt; ++j, ++cs) {
         wait(&s_full[t], cs);
         tc_fence_after();
