@@ -17,7 +17,7 @@
 // copies through a shared-memory ring, so that what is in flight (three CTAs an
 // SM, 64 KB each) does not hang on registers, and runs ahead into the CTA's next
 // row while this one is summed up.  Measured on 2048 rows of 128256 fp32 logits,
-// 30 % of the tokens unlikely ones: 191 us with k = 0 (5.5 TB/s), 265 us with
+// 30 % of the tokens unlikely ones: 191 us with k = 0 (5.5 TB/s), 259 us with
 // k = 20; loads into registers ahead of each batch: 250 us with k = 0.  What
 // bounds it is the instruction rate: about 15 an entry with k = 0 and 23 with
 // k = 20, at half of the issue slots (bf16 logits take as long as fp32 ones).
@@ -368,24 +368,15 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
           before += in(q) && (x[q] > xt || (xt != xt && x[q] == x[q]) || (equal && id(q) < token));
         }
       };
-      // The alternatives: a lane whose maximum reaches the bar offers those of
-      // its entries that do; again(q) is entry q's key, 0 if it is not there.
-      auto pick = [&](auto& x, float mx, auto again) {
-        constexpr int N = sizeof(x) / sizeof(float);
-        if (!__any_sync(0xffffffffu, !(mx < top.bar))) return;  // the bar as last seen, then as it is now
+      // The alternatives, when a lane's maximum reaches the bar (as last seen, then
+      // as it is now): `offer` takes the lanes that do.
+      auto pick = [&](float mx, auto offer) {
+        if (!__any_sync(0xffffffffu, !(mx < top.bar))) return;
         top.floor = fmaxf(top.floor, cta_bar());
         top.bar = fmaxf(top.bar, top.floor);
-        if (!__any_sync(0xffffffffu, !(mx < top.bar))) return;
-        uint32_t hits = 0;
-        if (!(mx < top.bar)) {
-#pragma unroll
-          for (int q = 0; q < N; ++q) hits |= !(x[q] < top.bar) ? 1u << q : 0u;
-        }
-#pragma unroll 1
-        while (__any_sync(0xffffffffu, hits)) {  // one entry of each lane a round
-          top.offer_many(hits ? again(__ffs(hits) - 1) : 0ull, k, lane);
-          hits &= hits - 1;
-        }
+        const unsigned reach = __ballot_sync(0xffffffffu, !(mx < top.bar));
+        if (!reach) return;
+        offer(reach);
         if (m > 0) {
           const float now = key_score(__shfl_sync(0xffffffffu, top.list, m - 1));
           if (now > mth) {
@@ -436,9 +427,40 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
             consumers_sync();
           }
           if (here)
-            pick(x, mx, [&](int q) {
-              const int at = (j0 + (q / VEC) * 32) * VEC + q % VEC;
-              return at < n * VEC ? score_key(to_f32(reinterpret_cast<const T*>(sv)[at]), x0 + at) : 0ull;
+            pick(mx, [&](unsigned reach) {
+              const T* se = reinterpret_cast<const T*>(sv);
+              if (__popc(reach) > 6) {  // a row's beginning: an entry of each lane a round
+                uint32_t hits = 0;
+                if (!(mx < top.bar)) {
+#pragma unroll
+                  for (int q = 0; q < NE; ++q) hits |= !(x[q] < top.bar) ? 1u << q : 0u;
+                }
+#pragma unroll 1
+                while (__any_sync(0xffffffffu, hits)) {
+                  const int q = __ffs(hits) - 1, at = (j0 + (q / VEC) * 32) * VEC + q % VEC;
+                  top.offer_many(hits && at < n * VEC ? score_key(to_f32(se[at]), x0 + at) : 0ull, k, lane);
+                  hits &= hits - 1;
+                }
+                return;
+              }
+              // later mostly one lane with one entry: the 16 entries of two lanes a
+              // round (4096 bf16 rows of 32000: 193 -> 187 us; alone it took rows of
+              // 1000 from 76 to 95 us)
+              const int q = lane % NE, mine = (warp * NV + q / VEC) * 32;
+#pragma unroll 1
+              while (reach) {
+                const int l0 = __ffs(reach) - 1;
+                reach &= reach - 1;
+                const int l = lane < NE ? l0 : __ffs(reach) - 1;
+                reach &= reach - 1;
+                const int at = (mine + l) * VEC + q % VEC;
+                unsigned long long key = 0ull;
+                if (l >= 0 && at < n * VEC) {
+                  const float v = to_f32(se[at]);
+                  if (!(v < top.bar)) key = score_key(v, x0 + at);
+                }
+                top.offer_many(key, k, lane);
+              }
             });
         }
         __syncwarp();
@@ -452,7 +474,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
         sums(x, x[0]);
         count(x, [&](int) { return at; }, [&](int) { return ok; });
         if (k > 0)
-          pick(x, x[0], [&](int) { return ok ? score_key(x[0], at) : 0ull; });
+          pick(x[0], [&](unsigned) { top.offer_many(ok ? score_key(x[0], at) : 0ull, k, lane); });
       }
 
       // ---- warp, CTA and cluster merges
