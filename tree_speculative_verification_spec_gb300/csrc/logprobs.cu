@@ -31,6 +31,7 @@
 // One cluster of C CTAs per row: C = 1 when the rows alone fill the GPU, else
 // enough CTAs to spread a row, with at least 2048 entries each.
 #include <algorithm>
+#include <climits>
 
 #include <cooperative_groups.h>
 
@@ -41,7 +42,7 @@ namespace cg = cooperative_groups;
 
 namespace spectree {
 
-constexpr int kLpWarps = 8;                          // consumer warps
+constexpr int kLpWarps = 8;                          // consumer warps (cta_bar compares 8 scores)
 constexpr int kLpThreads = kLpWarps * 32 + 32;       // and the producer warp
 constexpr int kLpBatch = 16;                         // entries per lane and stage
 constexpr int kLpEntries = kLpWarps * 32 * kLpBatch; // entries per stage: 16 KB of fp32, 8 KB of bf16
@@ -319,17 +320,22 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
       SoftStats st;
       WarpTop top;
       int before = 0;
-      // Of the nw warps that work on this row, each has m = ceil(k / nw) entries
-      // that reach its m-th best: the least of the nw m-th bests is reached by k
-      // entries of the CTA, and no entry below it is among the k best.
+      // The bar: the w-th largest of the warps' m-th best scores, w m >= k, is
+      // reached by k entries of the CTA, and no entry below it is among the k
+      // best.  w of about five eighths of the nw warps that work on this row.
       const int nw = n_chunks > 0 ? min(kLpWarps, (v1 - v0 + NV * 32 - 1) / (NV * 32)) : 1;
-      const int m = (k + nw - 1) / nw;
+      const int most = (5 * nw + 7) / 8, m = (k + most - 1) / most, w = m > 0 ? (k + m - 1) / m : 0;
       float mth = -INFINITY;
-      if (threadIdx.x < kLpWarps) s_mth[threadIdx.x] = float_order(threadIdx.x < nw ? -INFINITY : INFINITY);
+      if (threadIdx.x < kLpWarps) s_mth[threadIdx.x] = float_order(-INFINITY);
       if (threadIdx.x == 0) s_n = 0;
       consumers_sync();
       auto cta_bar = [&]() -> float {
-        return order_float(__reduce_min_sync(0xffffffffu, *(volatile int*)&s_mth[lane & (kLpWarps - 1)]));
+        // lane 8 j + i: is score j, or j + 4, above score i; lane i then counts
+        const volatile int* s = s_mth;
+        const int mine = s[lane & 7], lo = s[lane >> 3], hi = s[(lane >> 3) + 4];
+        const unsigned col = 0x01010101u << (lane & 7);
+        const int above = __popc(__ballot_sync(0xffffffffu, lo > mine) & col) + __popc(__ballot_sync(0xffffffffu, hi > mine) & col);
+        return order_float(__reduce_min_sync(0xffffffffu, above < w ? mine : INT_MAX));
       };
       // A batch of entries, one lane's x[0 .. N - 1]; those that are not there
       // hold -inf.  The sums:
