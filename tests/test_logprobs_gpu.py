@@ -127,6 +127,34 @@ def test_ties_masks_and_rows_without_a_distribution(dtype):
         _check(xs[i].double().numpy(), out, i, tokens[i], 1.0, k)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_ties_and_what_is_not_finite_far_from_the_token(dtype):
+    """Ranks over whole stages of lower and of higher ids than the token's."""
+    V, k = 20000, 7
+    g = torch.Generator().manual_seed(8)
+    zeros = torch.where(torch.rand(V, generator=g) < 0.5, 0.0, -0.0)
+    mixed = torch.randn(V, generator=g)
+    mixed[torch.randint(0, V, (300,), generator=g)] = math.nan
+    some = torch.randn(V, generator=g)
+    some[torch.randint(0, V, (9000,), generator=g)] = -math.inf
+    some[17000:] = -math.inf
+    tiny = torch.randint(-2, 3, (V,), generator=g).float() * 2.0 ** -149
+    high = torch.randn(V, generator=g)
+    high[[40, 9000, 19000]] = math.inf
+    rows, tokens = [], []
+    for row in (zeros, mixed, some, tiny, high):
+        for t in (3, 12001, 19999):
+            rows.append(row)
+            tokens.append(t)
+    rows.append(high)
+    tokens.append(9000)
+    xs = torch.stack(rows).to(dtype)
+    out, status = _tokens_call(xs.cuda(), tokens, [0, len(rows)], None, k)
+    assert status == [0]
+    for i in range(len(rows)):
+        _check(xs[i].double().numpy(), out, i, tokens[i], 1.0, k)
+
+
 def test_bad_tokens_and_temperatures():
     x = torch.randn((6, 300), generator=torch.Generator().manual_seed(1))
     out, status = _tokens_call(x.cuda(), [1, 300, -2, 4, 5, 6], [0, 3, 4, 5], [1.0, 0.0, math.inf], 3)

@@ -17,7 +17,7 @@
 // copies through a shared-memory ring, so that what is in flight (three CTAs an
 // SM, 64 KB each) does not hang on registers, and runs ahead into the CTA's next
 // row while this one is summed up.  Measured on 2048 rows of 128256 fp32 logits,
-// 30 % of the tokens unlikely ones: 191 us with k = 0 (5.5 TB/s), 259 us with
+// 30 % of the tokens unlikely ones: 189 us with k = 0 (5.6 TB/s), 240 us with
 // k = 20; loads into registers ahead of each batch: 250 us with k = 0.  What
 // bounds it is the instruction rate: about 15 an entry with k = 0 and 23 with
 // k = 20, at half of the issue slots (bf16 logits take as long as fp32 ones).
@@ -342,28 +342,35 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
       auto sums = [&](auto& x, float mx) {
         constexpr int N = sizeof(x) / sizeof(float);
         if (!(mx <= st.r)) st.raise(mx, c);
-        if (st.r == -INFINITY) return;
-        // entries of -inf weigh nothing: e is 0, and 0 times the clamped d stays 0
-        float2 s2 = make_float2(0.0f, 0.0f), w2 = s2;
-        if (N == 1) {
-          const float d = max_nan(x[0] - st.r, -3e38f);
-          s2.x = lp_exp2(d * c);
-          w2.x = s2.x * d;
-        } else {
+        if (mx == -INFINITY) return;  // entries of -inf weigh nothing
+        float s = 0.0f, w = NAN;
+        if constexpr (N > 1) {
           const float2 neg = make_float2(-st.r, -st.r);
+          float2 s2 = make_float2(0.0f, 0.0f), w2 = s2;
 #pragma unroll
-          for (int q = 0; q + 1 < N; q += 2) {
-            float2 d = __fadd2_rn(make_float2(x[q], x[q + 1]), neg);
-            d.x = max_nan(d.x, -3e38f);
-            d.y = max_nan(d.y, -3e38f);
+          for (int q = 0; q < N; q += 2) {
+            const float2 d = __fadd2_rn(make_float2(x[q], x[q + 1]), neg);
             const float2 z = __fmul2_rn(d, cc);
             const float2 e = make_float2(lp_exp2(z.x), lp_exp2(z.y));
             s2 = __fadd2_rn(s2, e);
             w2 = __ffma2_rn(e, d, w2);
           }
+          s = s2.x + s2.y;
+          w = w2.x + w2.y;
         }
-        st.s += s2.x + s2.y;
-        st.w += w2.x + w2.y;
+        if (w != w) {
+          // a weight of 0 at an infinite distance (or a NaN, which stays): again,
+          // with the distance held finite
+          s = w = 0.0f;
+#pragma unroll
+          for (int q = 0; q < N; ++q) {
+            const float d = max_nan(x[q] - st.r, -3e38f), e = lp_exp2(d * c);
+            s += e;
+            w = fmaf(e, d, w);
+          }
+        }
+        st.s += s;
+        st.w += w;
       };
       // The given token's rank: entry q has id `id(q)` and is there if in(q).
       auto count = [&](auto& x, auto id, auto in) {
@@ -417,9 +424,17 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
           if (!(mx < xt)) {
             const bool lower = x0 + n * VEC <= token, higher = x0 > token;  // every id of the stage
             if (n == kLpChunk && (lower || higher) && xt > -INFINITY) {
-              const float bar = lower ? before_float(xt) : xt;  // equal logits of lower ids count too
+              // equal logits of lower ids count too; an entry is above the bar where
+              // bar - x has its sign set (+0 for equal ones, NaN positive)
+              const float bar = lower ? before_float(xt) : xt + 0.0f;
+              unsigned signs = 0;
 #pragma unroll
-              for (int q = 0; q < NE; ++q) before += x[q] > bar;
+              for (int q = 0; q < NE; q += 2) {
+                const float2 d = __ffma2_rn(make_float2(x[q], x[q + 1]), make_float2(-1.0f, -1.0f), make_float2(bar, bar));
+                signs = __funnelshift_l(__float_as_uint(d.x), signs, 1);
+                signs = __funnelshift_l(__float_as_uint(d.y), signs, 1);
+              }
+              before += __popc(signs);
             } else {
               count(x, id, in);
             }
