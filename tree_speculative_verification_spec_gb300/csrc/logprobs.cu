@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
     }
     if (lane == 0) s_total = at;
   }
-  __syncthreads();
+  if (C > 1) cluster.sync();  // its CTAs run: partials may be written to the leader's shared memory
+  else __syncthreads();
   if (a.live) {
     for (long long e = blockIdx.x * kLpWarps + warp; warp < kLpWarps && e < entries; e += (long long)gridDim.x * kLpWarps) {
       const int n = a.accept_len[(int)(e / a.n_max)];

@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_release_kernel(const 
   __shared__ ClusterScan scan;
   cg::cluster_group cl = cg::this_cluster();
   const int G = (int)cl.num_blocks() * kPlanThreads, id = (int)cl.block_rank() * kPlanThreads + threadIdx.x;
+  cl.sync();  // every CTA runs: the scan writes to the others' shared memory
   const int n = a.N * a.max_blocks;  // at most 2^30
   const int count = *(volatile int32_t*)a.count;
   // Thread `id` owns a run of positions (one scan for the call), eight of them
