@@ -10,7 +10,7 @@
 //             lower id, NaN last)
 // Every value comes from one read of the row: each thread keeps (r, S, W)
 // with r the largest logit it has seen, moves to a larger r once per batch of
-// 32 entries, and the partials merge by the same rule across the warp, the CTA
+// 16 entries, and the partials merge by the same rule across the warp, the CTA
 // and the row's cluster, always in the same order.
 //
 // The row is the only traffic that counts.  A producer warp brings it by bulk
@@ -19,17 +19,22 @@
 // row while this one is summed up.  Measured on 2048 rows of 128256 fp32 logits,
 // 30 % of the tokens unlikely ones: 189 us with k = 0 (5.6 TB/s), 240 us with
 // k = 20; loads into registers ahead of each batch: 250 us with k = 0.  What
-// bounds it is the instruction rate: about 15 an entry with k = 0 and 23 with
-// k = 20, at half of the issue slots (bf16 logits take as long as fp32 ones).
+// bounds it is a warp's chain through a batch, some 1400 cycles (a row takes a
+// CTA 33 us with the GPU to itself and 38 us beside 455 others; 2048 rows are
+// five rounds of 456), at half of the issue slots; bf16 logits take as long as
+// fp32 ones.  The rest of the last round, a row to two CTAs: 8 us less on 500
+// rows, 14 us more on 2048.
 // The rank looks at a lane's entries only when their maximum reaches the given
-// token's logit, and the alternatives only when it reaches the CTA's bar: the
-// least of the eight warps' m-th best scores, m = ceil(k / 8), which k entries
-// reach.  A bar per warp let eight times as many entries through (314 us), and
-// with the insertion inlined per entry the whole took 924 us.  Eight consumer
-// warps in three CTAs of 72 registers; four in five CTAs measured 353 us.
+// token's logit, and the alternatives only when it reaches the CTA's bar (below).
+// A bar per warp let eight times as many entries through (314 us), and with the
+// insertion inlined per entry the whole took 924 us.  Eight consumer warps in
+// three CTAs of 72 registers; four in five CTAs measured 353 us.
 //
-// One cluster of C CTAs per row: C = 1 when the rows alone fill the GPU, else
-// enough CTAs to spread a row, with at least 2048 entries each.
+// One cluster of C CTAs per row: the most that leave the call within 8 / 3 CTAs
+// an SM (three fit, but clusters do not fill every SM; one that waits for room
+// doubles the call), with at least 2048 entries each.  V 128256, k = 20, by C =
+// 1, 2, 4, 8: 16 rows 46, 35, 27, 23 us; 100 rows 50, 39, 37, 50; 200 rows 54,
+// 46, 60, 111; 250 rows 56, 70, 91, 144.
 #include <algorithm>
 #include <climits>
 
@@ -584,7 +589,7 @@ static spec_status launch_logprobs(LpArgs a, spec_dtype dtype, long long entries
   a.live = a.path != nullptr && a.B <= kLpMaxLive;
   const long long rows = a.live ? std::min(entries, 5LL * a.B) : entries;
   int C = 1;
-  while (C < kLpMaxCluster && rows * C < 2LL * sms && a.V / (2 * C) >= 2048) C *= 2;
+  while (C < kLpMaxCluster && rows * C * 6 <= 8LL * sms && a.V / (2 * C) >= 2048) C *= 2;
   const long long clusters = std::min<long long>(entries, std::max(1, 3 * sms / C));  // what the GPU holds at once
   a.C = C;
   cudaLaunchConfig_t cfg = {};
