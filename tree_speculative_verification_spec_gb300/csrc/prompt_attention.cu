@@ -22,8 +22,10 @@ __device__ __forceinline__ float pr_exp2(float x) {
 // CUDA-core kernel: a CTA takes 64 rows of one kv-head group and one key
 // range, 64 keys at a time; 256 threads as 16 x 16, each 4 rows x 4 keys of
 // the scores and 4 rows x D / 16 columns of the output.  Per 4 columns of q
-// and K a thread reads 8 float4 for 64 multiply-adds, so the FMA pipe and not
-// shared memory bounds it (the tensor cores have no fp32 product).
+// and K a thread reads 8 float4 for 64 multiply-adds, two to an instruction (the
+// tensor cores have no fp32 product).  Shared memory is as busy as the FMA pipe:
+// 4 x 700 tokens after 2000 (32/8 heads, D 128): 865 us, 31 TFLOP/s; one
+// multiply-add an instruction 942 us.
 constexpr int kPrThreads = 256;
 constexpr int kPrRows = kPromptCcRows;
 constexpr int kPrKeys = 64;
@@ -82,7 +84,8 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
 
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   constexpr int DJ = D / 64;  // float4 columns per thread: tx * 4 + 64 * jj
-  float m[4], l[4], o[4][DJ * 4];
+  float m[4], l[4];
+  float2 o[4][DJ * 2];
   int last[4];  // the last key row i sees
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
     l[i] = 0.0f;
     last[i] = rq.P + min(rq.n - 1, (r0 + ty * 4 + i) / g);
 #pragma unroll
-    for (int j = 0; j < DJ * 4; ++j) o[i][j] = 0.0f;
+    for (int j = 0; j < DJ * 2; ++j) o[i][j] = make_float2(0.0f, 0.0f);
   }
   for (int k0 = k_begin; k0 < k_end; k0 += kPrKeys) {
     __syncthreads();
@@ -111,11 +114,11 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
       *reinterpret_cast<float4*>(sm.v + kk * D + c) = vv;
     }
     __syncthreads();
-    float s[4][4];
+    float2 s2[4][4];  // even and odd pairs of columns
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
       float4 qa[4], kb[4];
@@ -127,21 +130,19 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[i][j] = fmaf(qa[i].x, kb[j].x, s[i][j]);
-          s[i][j] = fmaf(qa[i].y, kb[j].y, s[i][j]);
-          s[i][j] = fmaf(qa[i].z, kb[j].z, s[i][j]);
-          s[i][j] = fmaf(qa[i].w, kb[j].w, s[i][j]);
+          s2[i][j] = __ffma2_rn(make_float2(qa[i].x, qa[i].y), make_float2(kb[j].x, kb[j].y), s2[i][j]);
+          s2[i][j] = __ffma2_rn(make_float2(qa[i].z, qa[i].w), make_float2(kb[j].z, kb[j].w), s2[i][j]);
         }
     }
     __syncthreads();  // the keys are read: their room takes the probabilities
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float mx = -INFINITY;
+      float mx = -INFINITY, s[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int k = k0 + tx + 16 * j;
-        s[i][j] = k <= last[i] && k < k_end ? s[i][j] * a.scale_log2 : -INFINITY;
-        mx = fmaxf(mx, s[i][j]);
+        s[j] = k <= last[i] && k < k_end ? (s2[i][j].x + s2[i][j].y) * a.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, s[j]);
       }
 #pragma unroll
       for (int w = 8; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float p = pr_exp2(s[i][j] - ref);
+        const float p = pr_exp2(s[j] - ref);
         sum += p;
         sm.k[(ty * 4 + i) * S::kPStride + tx + 16 * j] = p;
       }
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
       l[i] = l[i] * alpha + sum;
       m[i] = mnew;
 #pragma unroll
-      for (int j = 0; j < DJ * 4; ++j) o[i][j] *= alpha;
+      for (int j = 0; j < DJ * 2; ++j) o[i][j] = __fmul2_rn(o[i][j], make_float2(alpha, alpha));
     }
     __syncwarp();  // a warp's rows are its own: both halves of it wrote them
 #pragma unroll 2
@@ -179,10 +180,8 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
           const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
 #pragma unroll
           for (int jj = 0; jj < DJ; ++jj) {
-            o[i][jj * 4] = fmaf(w, v[jj].x, o[i][jj * 4]);
-            o[i][jj * 4 + 1] = fmaf(w, v[jj].y, o[i][jj * 4 + 1]);
-            o[i][jj * 4 + 2] = fmaf(w, v[jj].z, o[i][jj * 4 + 2]);
-            o[i][jj * 4 + 3] = fmaf(w, v[jj].w, o[i][jj * 4 + 3]);
+            o[i][jj * 2] = __ffma2_rn(make_float2(w, w), make_float2(v[jj].x, v[jj].y), o[i][jj * 2]);
+            o[i][jj * 2 + 1] = __ffma2_rn(make_float2(w, w), make_float2(v[jj].z, v[jj].w), o[i][jj * 2 + 1]);
           }
         }
       }
@@ -202,13 +201,13 @@ __global__ void __launch_bounds__(kPrThreads, 2) prompt_cc_kernel(const PromptAr
 #pragma unroll
       for (int j = 0; j < DJ; ++j)
         *reinterpret_cast<float4*>(out + tx * 4 + 64 * j) =
-            make_float4(o[i][j * 4] * inv, o[i][j * 4 + 1] * inv, o[i][j * 4 + 2] * inv, o[i][j * 4 + 3] * inv);
+            make_float4(o[i][j * 2].x * inv, o[i][j * 2].y * inv, o[i][j * 2 + 1].x * inv, o[i][j * 2 + 1].y * inv);
     } else {
       float* wo = a.ws_o + ((size_t)split * a.T * a.Hq + row) * D;
 #pragma unroll
       for (int j = 0; j < DJ; ++j)
         *reinterpret_cast<float4*>(wo + tx * 4 + 64 * j) =
-            make_float4(o[i][j * 4], o[i][j * 4 + 1], o[i][j * 4 + 2], o[i][j * 4 + 3]);
+            make_float4(o[i][j * 2].x, o[i][j * 2].y, o[i][j * 2 + 1].x, o[i][j * 2 + 1].y);
       if (tx == 0) *reinterpret_cast<float2*>(a.ws_ml + ((size_t)split * a.T * a.Hq + row) * 2) = make_float2(m[i], l[i]);
     }
   }
