@@ -112,12 +112,16 @@ def _ptr(t):
         raise ValueError("tensor arguments must be CUDA tensors")
     if not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream, device=None):
+    """cudaStream_t of a stream, or of the current one of `device` (None: the
+    current device).  The raw handle costs 0.1 us, a Stream object of the current
+    stream 2.8 us, more than a kernel's launch."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
 
 
 def _check(fn, code):
@@ -306,9 +310,10 @@ def _f32(t):
 def _stream_of(t, stream):
     """The stream of a call on tensor t's device, which has to be the current
     one (its kernels are launched there)."""
-    if t.get_device() != torch.cuda.current_device():
+    device = t.get_device()
+    if device != torch.cuda.current_device():
         raise ValueError("tensor arguments must be on the current CUDA device")
-    return _stream(stream)
+    return _stream(stream, device)
 
 
 def spec_prompt_workspace_size(B, T, n_max, max_prefix, Hq, Hkv, D):
