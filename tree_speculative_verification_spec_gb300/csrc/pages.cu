@@ -29,6 +29,12 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanCluster = 8;
 constexpr int kScanThreads = 256;  // grid-wide passes over the table
 
+// A call's kernels are programmatic dependents of one another: each but the last
+// lets the next one launch as it starts, and each but the first begins by waiting
+// for the one before (its whole grid, results included).
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Move of `rows` slots (all of a page, or its first ones) from page src to
 // page dst.
 struct PageMove {
@@ -88,15 +94,15 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveCtas = 16;                    // per SM; four fit at once: the later ones even out the end
                                                  // (600 pages: 408 us with 4, 404 with 8, 398 with 16)
 
-__global__ void __launch_bounds__(kMoveThreads) page_move_kernel(char* const* __restrict__ k_caches,
-                                                                 char* const* __restrict__ v_caches, int n_caches,
-                                                                 const PageMove* __restrict__ moves,
-                                                                 const int* __restrict__ n_moves, int Hkv,
+// The plan's results come by plain pointers: a read-only load could be moved
+// before the wait.
+__global__ void __launch_bounds__(kMoveThreads) page_move_kernel(char* const* k_caches, char* const* v_caches, int n_caches,
+                                                                 const PageMove* moves, const int* n_moves, int Hkv,
                                                                  long long head_bytes, int row_bytes, int whole,
-                                                                 int32_t* __restrict__ table, long long entries,
-                                                                 const int32_t* __restrict__ page_map,
-                                                                 int num_blocks) {
+                                                                 int32_t* table, long long entries,
+                                                                 const int32_t* page_map, int num_blocks) {
   const int lane = threadIdx.x & 31;
+  wait_for_last();
   // compaction: the table's entries take their pages' new ids
   for (long long e = (long long)blockIdx.x * kMoveThreads + threadIdx.x; e < entries;
        e += (long long)gridDim.x * kMoveThreads) {
@@ -149,6 +155,7 @@ struct ForkArgs {
   PageMove* moves;  // [N]
   int* n_moves;
   int B, max_blocks, bs, num_blocks, N, pool_cap;
+  int copies;  // a copying kernel follows
 };
 
 // One cluster.  Fork i is checked by one warp; fresh pages are numbered by a
@@ -157,6 +164,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const ForkArgs
   __shared__ ClusterScan scan;
   __shared__ int s_badpool;
   cg::cluster_group cl = cg::this_cluster();
+  if (a.copies) let_next_launch();  // else the next kernel is not this call's
   const int G = (int)cl.num_blocks() * kPlanThreads, id = (int)cl.block_rank() * kPlanThreads + threadIdx.x;
   const int lane = threadIdx.x & 31;
   const int warps = G / 32, wid = id / 32;
@@ -287,6 +295,7 @@ struct FreeArgs {
 // One cluster: which entries are sound, and the pages they would drop.
 __global__ void __launch_bounds__(kPlanThreads) pages_free_check_kernel(const FreeArgs a) {
   cg::cluster_group cl = cg::this_cluster();
+  let_next_launch();
   const int G = (int)cl.num_blocks() * kPlanThreads, id = (int)cl.block_rank() * kPlanThreads + threadIdx.x;
   for (int r = id; r < a.B; r += G) {
     a.from[r] = a.max_blocks;
@@ -341,6 +350,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_check_kernel(const Fr
 // Every entry of the table: a page a row keeps is marked -1, a dropped one
 // with its lowest position (entry, then page).
 __global__ void __launch_bounds__(kScanThreads) pages_free_mark_kernel(const FreeArgs a) {
+  let_next_launch();
+  wait_for_last();
   const int chunks = (a.max_blocks + kScanThreads - 1) / kScanThreads;  // a CTA takes one row's chunk at a time
   for (int u = blockIdx.x; u < a.B * chunks; u += gridDim.x) {
     const int r = u / chunks, j = (u - r * chunks) * kScanThreads + threadIdx.x;
@@ -358,6 +369,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_release_kernel(const 
   cg::cluster_group cl = cg::this_cluster();
   const int G = (int)cl.num_blocks() * kPlanThreads, id = (int)cl.block_rank() * kPlanThreads + threadIdx.x;
   cl.sync();  // every CTA runs: the scan writes to the others' shared memory
+  wait_for_last();
   const int n = a.N * a.max_blocks;  // at most 2^30
   const int count = *(volatile int32_t*)a.count;
   // Thread `id` owns a run of positions (one scan for the call), eight of them
@@ -427,6 +439,7 @@ struct CompactArgs {
 constexpr int kLive = 1, kFree = 2;
 
 __global__ void __launch_bounds__(kScanThreads) pages_compact_clear_kernel(const CompactArgs a) {
+  let_next_launch();
   const int t = blockIdx.x * kScanThreads + threadIdx.x;
   for (int p = t; p < a.num_blocks; p += gridDim.x * kScanThreads) a.state[p] = 0;
   if (t == 0) *a.error = 0;
@@ -434,6 +447,8 @@ __global__ void __launch_bounds__(kScanThreads) pages_compact_clear_kernel(const
 
 // Every page that a row names, then (second kernel) every page in the pool.
 __global__ void __launch_bounds__(kScanThreads) pages_compact_live_kernel(const CompactArgs a) {
+  let_next_launch();
+  wait_for_last();
   const long long step = (long long)gridDim.x * kScanThreads;
   for (long long e = (long long)blockIdx.x * kScanThreads + threadIdx.x; e < a.entries; e += step) {
     const int p = a.table[e];
@@ -448,6 +463,8 @@ __global__ void __launch_bounds__(kScanThreads) pages_compact_live_kernel(const 
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const CompactArgs a) {
   __shared__ ClusterScan scan;
   __shared__ int s_bad;
+  let_next_launch();
+  wait_for_last();
   cg::cluster_group cl = cg::this_cluster();
   const int G = (int)cl.num_blocks() * kPlanThreads, id = (int)cl.block_rank() * kPlanThreads + threadIdx.x;
   const int count = *(volatile int32_t*)a.count;
@@ -585,21 +602,24 @@ static bool sm_count(int* sms) {
          cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
 }
 
-// A plan kernel: one cluster of kPlanCluster CTAs.
-template <typename A>
-static cudaError_t launch_plan(void (*kern)(const A), const A& a, cudaStream_t stream) {
+// A kernel of a call, in clusters of `cluster` CTAs; every one but the call's
+// first is a programmatic dependent of the one before.
+template <typename... P, typename... A>
+static cudaError_t launch(void (*kern)(P...), int grid, int threads, int cluster, bool first, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kPlanCluster, 1, 1);
-  cfg.blockDim = dim3(kPlanThreads, 1, 1);
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kPlanCluster;
+  attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  cfg.numAttrs = first ? 1 : 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, P(args)...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -656,6 +676,7 @@ spec_status spec_pages_fork(void* const* k_caches, void* const* v_caches, int la
   a.num_blocks = num_blocks;
   a.N = N;
   a.pool_cap = free_cap;
+  a.copies = layers > 0;
   Carve c{static_cast<char*>(workspace)};
   carve_fork(a, c);
   if (!workspace || workspace_bytes < c.used || (reinterpret_cast<uintptr_t>(workspace) & 15)) return SPEC_ERR_WORKSPACE;
@@ -663,16 +684,15 @@ spec_status spec_pages_fork(void* const* k_caches, void* const* v_caches, int la
   if (!sm_count(&sms)) return SPEC_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
   spec_workspace_canary(workspace, c.used, st);
-  if (launch_plan(pages_fork_kernel, a, st) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (launch(pages_fork_kernel, kPlanCluster, kPlanThreads, kPlanCluster, true, st, a) != cudaSuccess) return SPEC_ERR_CUDA;
   if (layers > 0) {
     const int row_bytes = D * (dtype == SPEC_F32 ? 4 : 2);
     const long long head_bytes = (long long)block_size * row_bytes;
     const long long units = (long long)N * 2 * layers * Hkv * ((head_bytes + kMoveBytes - 1) / kMoveBytes);
     const int grid = (int)std::min<long long>((long long)kMoveCtas * sms, (units + 7) / 8);
-    page_move_kernel<<<grid, kMoveThreads, 0, st>>>((char* const*)k_caches, (char* const*)v_caches, 2 * layers,
-                                                    a.moves, a.n_moves, Hkv, head_bytes, row_bytes, 0, nullptr, 0,
-                                                    nullptr, 0);
-    SPEC_LAUNCH_CHECK();
+    if (launch(page_move_kernel, grid, kMoveThreads, 1, false, st, (char* const*)k_caches, (char* const*)v_caches,
+               2 * layers, a.moves, a.n_moves, Hkv, head_bytes, row_bytes, 0, nullptr, 0, nullptr, 0) != cudaSuccess)
+      return SPEC_ERR_CUDA;
   }
   return SPEC_OK;
 }
@@ -707,10 +727,10 @@ spec_status spec_pages_free(int32_t* block_table, int B, int max_blocks, int blo
   if (!sm_count(&sms)) return SPEC_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
   spec_workspace_canary(workspace, c.used, st);
-  if (launch_plan(pages_free_check_kernel, a, st) != cudaSuccess) return SPEC_ERR_CUDA;
-  pages_free_mark_kernel<<<scan_grid((long long)B * max_blocks, sms), kScanThreads, 0, st>>>(a);
-  SPEC_LAUNCH_CHECK();
-  if (launch_plan(pages_free_release_kernel, a, st) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (launch(pages_free_check_kernel, kPlanCluster, kPlanThreads, kPlanCluster, true, st, a) != cudaSuccess ||
+      launch(pages_free_mark_kernel, scan_grid((long long)B * max_blocks, sms), kScanThreads, 1, false, st, a) != cudaSuccess ||
+      launch(pages_free_release_kernel, kPlanCluster, kPlanThreads, kPlanCluster, false, st, a) != cudaSuccess)
+    return SPEC_ERR_CUDA;
   return SPEC_OK;
 }
 
@@ -744,18 +764,17 @@ spec_status spec_pages_compact(void* const* k_caches, void* const* v_caches, int
   if (!sm_count(&sms)) return SPEC_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
   spec_workspace_canary(workspace, c.used, st);
-  pages_compact_clear_kernel<<<scan_grid(num_blocks, sms), kScanThreads, 0, st>>>(a);
-  SPEC_LAUNCH_CHECK();
-  if (a.entries > 0) {
-    pages_compact_live_kernel<<<scan_grid(a.entries, sms), kScanThreads, 0, st>>>(a);
-    SPEC_LAUNCH_CHECK();
-  }
-  if (launch_plan(pages_compact_plan_kernel, a, st) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (launch(pages_compact_clear_kernel, scan_grid(num_blocks, sms), kScanThreads, 1, true, st, a) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  if (a.entries > 0 &&
+      launch(pages_compact_live_kernel, scan_grid(a.entries, sms), kScanThreads, 1, false, st, a) != cudaSuccess)
+    return SPEC_ERR_CUDA;
   const int row_bytes = D * (dtype == SPEC_F32 ? 4 : 2);
-  page_move_kernel<<<kMoveCtas * sms, kMoveThreads, 0, st>>>((char* const*)k_caches, (char* const*)v_caches, 2 * layers, a.moves,
-                                                     a.n_moves, Hkv, (long long)block_size * row_bytes, row_bytes, 1,
-                                                     block_table, a.entries, page_map, num_blocks);
-  SPEC_LAUNCH_CHECK();
+  if (launch(pages_compact_plan_kernel, kPlanCluster, kPlanThreads, kPlanCluster, false, st, a) != cudaSuccess ||
+      launch(page_move_kernel, kMoveCtas * sms, kMoveThreads, 1, false, st, (char* const*)k_caches,
+             (char* const*)v_caches, 2 * layers, a.moves, a.n_moves, Hkv, (long long)block_size * row_bytes, row_bytes,
+             1, block_table, a.entries, page_map, num_blocks) != cudaSuccess)
+    return SPEC_ERR_CUDA;
   return SPEC_OK;
 }
 
