@@ -228,3 +228,19 @@ def test_page_calls_replay_from_a_graph():
     s.ref.compact()
     torch.cuda.synchronize()
     s.same()
+
+
+@pytest.mark.parametrize("B", [8192, 8193, 20000])
+def test_tables_of_many_rows(B):
+    """Rows named twice, rows at both ends of a long table, and more entries than
+    a cluster has threads."""
+    bs, nb = 8, 12000
+    s = Both(_empty(B, 2), list(range(nb)), nb, nb, bs, 0, 1, 64, torch.bfloat16)
+    n = 9000
+    dst = [(7 * i + 3) % B for i in range(n)]
+    dst[5], dst[6], dst[7] = B - 1, B, -1
+    dst[8] = dst[4000]
+    s.fork([-1] * n, dst, [0] * n, [1 + i % 9 for i in range(n)])
+    first = dst[1]
+    s.fork([first, first, dst[8]], [0, 0, 1], [1, 1, 0], [0, 0, 0])
+    s.free([B - 1, first, 0, 0, B] + [d for d in dst[20:3000]], [0, 1, 0, 0, 0] + [0] * 2980)
