@@ -17,13 +17,13 @@
 // copies through a shared-memory ring, so that what is in flight (three CTAs an
 // SM, 64 KB each) does not hang on registers, and runs ahead into the CTA's next
 // row while this one is summed up.  Measured on 2048 rows of 128256 fp32 logits,
-// 30 % of the tokens unlikely ones: 189 us with k = 0 (5.6 TB/s), 240 us with
+// 30 % of the tokens unlikely ones: 181 us with k = 0 (5.8 TB/s), 236 us with
 // k = 20; loads into registers ahead of each batch: 250 us with k = 0.  What
-// bounds it is a warp's chain through a batch, some 1400 cycles (a row takes a
-// CTA 33 us with the GPU to itself and 38 us beside 455 others; 2048 rows are
-// five rounds of 456), at half of the issue slots; bf16 logits take as long as
-// fp32 ones.  The rest of the last round, a row to two CTAs: 8 us less on 500
-// rows, 14 us more on 2048.
+// bounds it: with k = 0 the memory (half of a stage's 2400 cycles are spent
+// waiting for it); with k = 20 a warp's chain through a batch, some 1100 cycles
+// and the alternatives' on top, at half of the issue slots (bf16 logits take as
+// long as fp32 ones).  2048 rows are five rounds of 456 CTAs; the rest of the last
+// round, a row to two CTAs, took 8 us less on 500 rows and 14 us more on 2048.
 // The rank looks at a lane's entries only when their maximum reaches the given
 // token's logit, and the alternatives only when it reaches the CTA's bar (below).
 // A bar per warp let eight times as many entries through (314 us), and with the
@@ -173,11 +173,16 @@ __device__ __forceinline__ void write_none(const LpArgs& a, long long entry, int
   }
 }
 
+// Rows are read once: their lines are the first to leave L2 (2048 rows of 128256
+// fp32, k = 0: 190 -> 181 us; k = 20: 238 -> 233; rows of 1000: 80 -> 82).
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   tc5::smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(tc5::smem_u32(bar))
-               : "memory");
+  uint64_t once;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          tc5::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(tc5::smem_u32(bar)), "l"(once)
+      : "memory");
 }
 
 template <typename T>
