@@ -303,3 +303,33 @@ def test_arguments_of_other_types_are_refused():
         a.update(bad)
         with pytest.raises(ValueError):
             S.spec_token_logprobs(a["x"], a["tok"], off, None, 1, 2, 8, 0, a["lp"], None, None, None, None, st)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("V,nans,masked", [
+    (7, [2], []), (7, [0], []), (1003, [100], []), (1003, [0], []), (1003, [1002], []), (4300, [5], []), (4300, [4200], []),
+    (12288, [5], [(4096, 8192)]), (12288, [4095], [(4096, 12288)]), (12288, [12287], [(0, 12287)]),
+    (131072, [5], [(4096, 8192)]), (131072, [131071], [(0, 131071)]), (131072, [16390], [(16391, 131072)]), (50, list(range(50)), [])])
+def test_one_nan_among_masked_logits(V, nans, masked, dtype):
+    """A NaN leaves the row without a distribution, whatever stands behind it: the
+    row's tail, the end of a partly filled stage, entries of -inf; rows that
+    start anywhere, and rows alone in their call (spread over a cluster when
+    they are long) or among others."""
+    g = torch.Generator().manual_seed(V + len(nans) + len(masked))
+    rows = torch.randn((3, V), generator=g)
+    for a, b in masked:
+        rows[0, a:b] = rows[2, a:b] = -math.inf
+    rows[0, nans] = rows[2, nans] = math.nan
+    base = torch.zeros(3 * V + 8, dtype=dtype)
+    k = min(V, 9)
+    for shift in (0, 1, 3):
+        base[shift:shift + 3 * V] = rows.to(dtype).flatten()
+        x = base.cuda()[shift:shift + 3 * V].view(3, V)
+        for first, n in ((0, 3), (0, 1), (2, 1)):
+            tokens = [(nans[0] + i) % V for i in range(n)]
+            out, status = _tokens_call(x[first:first + n], tokens, [0, n], None, k)
+            assert status == [0]
+            for i in range(n):
+                row = x[first + i].cpu().double().numpy()
+                _check(row, out, i, tokens[i], 1.0, k)
+                assert math.isnan(out[0][i].item()) == (first + i != 1)

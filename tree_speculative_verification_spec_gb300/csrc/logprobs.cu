@@ -352,8 +352,10 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
       // hold -inf.  The sums:
       auto sums = [&](auto& x, float mx) {
         constexpr int N = sizeof(x) / sizeof(float);
+        // entries of -inf weigh nothing; the reference stays, since one of NaN would
+        // be lost to -inf (nothing seen yet), and the row's NaN with it
+        if (mx == -INFINITY) return;
         if (!(mx <= st.r)) st.raise(mx, c);
-        if (mx == -INFINITY) return;  // entries of -inf weigh nothing
         float s = 0.0f, w = NAN;
         if constexpr (N > 1) {
           const float2 neg = make_float2(-st.r, -st.r);
