@@ -247,3 +247,16 @@ def test_rows_beside_a_request_leave_its_bits_alone(fill, Hq, Hkv):
     d["q"][70:91] = fill
     out, status = _call(d)
     assert status.tolist() == [0, 0] and torch.equal(out[:70], ref[:70])
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-30])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_a_scale_of_zero_averages_what_a_row_sees(dtype, scale):
+    """Every score 0: hidden keys weigh nothing all the same.  The second batch
+    splits its keys."""
+    for lens, prefix in (([200, 1, 70], [0, 333, 5]), ([3, 1], [6000, 9000])):
+        d = paged_batch(59, lens, prefix, 8, 2, 128, 16, dtype)
+        d["scale"] = scale
+        out, status = _call(d)
+        assert status.tolist() == [0] * len(lens)
+        _holds(d, out)

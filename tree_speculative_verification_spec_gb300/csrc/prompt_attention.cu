@@ -417,7 +417,10 @@ spec_status spec_prompt_attention(const void* q, const void* k_cache, const void
   a.g = Hq / Hkv;
   a.splits = plan.splits;
   a.chunk = plan.chunk;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  // The tensor-core kernel hides a key by -inf before the scaling, and -inf * 0 is
+  // NaN: the smallest float stands for a scale of 0 (the largest finite score
+  // times it is 2^-21, a weight of 1 + 3e-7).
+  a.scale_log2 = std::max(scale * 1.4426950408889634f, 0x1p-149f);
   cudaStream_t st = (cudaStream_t)stream;
   if (need > 0) spec_workspace_canary(workspace, need, st);
   const cudaError_t e = dtype == SPEC_BF16 ? launch_prompt_tc(a, plan, st) : launch_prompt_cc(a, plan, st);
