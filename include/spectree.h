@@ -541,8 +541,8 @@ spec_status spec_path_logprobs(const void* p_logits, spec_dtype dtype, const int
  *   NULL: none): its entries from page ceil(keep_len / block_size) on become
  *   -1, and the pages among them that no row names any more are appended to
  *   the pool in the order of i, then of the page, each once.  When the pool
- *   cannot take them all, nothing is done and each row that had pages to
- *   release gets SPEC_DEV_CAPACITY.
+ *   cannot take them all, nothing is done and each sound row that had a page to
+ *   drop gets SPEC_DEV_CAPACITY, whoever else names that page.
  *   status int32 [N] WRITTEN per row: 0, SPEC_DEV_BAD_ROW (outside [0, B),
  *   named twice, keep_len < 0), SPEC_DEV_BAD_BLOCK (a dropped entry of
  *   num_blocks or more) or SPEC_DEV_CAPACITY; a flagged row is left as it was.

@@ -244,3 +244,50 @@ def test_tables_of_many_rows(B):
     first = dst[1]
     s.fork([first, first, dst[8]], [0, 0, 1], [1, 1, 0], [0, 0, 0])
     s.free([B - 1, first, 0, 0, B] + [d for d in dst[20:3000]], [0, 1, 0, 0, 0] + [0] * 2980)
+
+
+class AllOrNothing(Pages):
+    """A free that the pool cannot take flags every row that had a page to drop,
+    not only those whose pages would have been released."""
+
+    def free(self, rows, keep):
+        status = super().free(rows, keep)
+        if any(s & S.SPEC_DEV_CAPACITY for s in status):
+            for i, r in enumerate(rows):
+                if status[i] == 0 and any(p >= 0 for p in self.table[r][-(-keep[i] // self.bs):]):
+                    status[i] = S.SPEC_DEV_CAPACITY
+        return status
+
+
+def _tight(table, pool, count, nb, bs=8):
+    s = Both(table, pool, count, nb, bs)
+    s.ref = AllOrNothing(table, pool, count, nb, bs)
+    return s
+
+
+def test_a_full_pool_flags_every_row_that_keeps_pages_it_should_drop():
+    s = _tight([[0, 1], [0, -1], [-1, -1]], [5, 6], 2, 40)
+    assert s.free([0, 1, 2]) == [4, 4, 0]      # row 1's page would go with row 0's; row 2 has none
+    s = _tight([[0, 1, 2], [0, 1, -1], [3, 0, -1], [3, -1, -1]], [5, 6, -1], 2, 40)
+    assert s.free([0, 1, 2], [0, 8, 8]) == [4, 4, 4]
+    assert s.free([1, 2], [8, 8]) == [0, 0]    # both dropped pages stay with row 0: nothing to release
+    assert s.free([0]) == [4]                  # pages 1 and 2: the pool has room for one
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_random_frees_into_a_tight_pool(seed):
+    g = np.random.default_rng(300 + seed)
+    B, mb, bs = int(g.integers(20, 400)), int(g.integers(3, 60)), 8
+    nb = B * mb
+    ids = g.permutation(nb).reshape(B, mb)
+    table = np.where(g.random((B, mb)) < 0.7, ids, -1)
+    half = B // 2
+    table[half:, :mb // 2] = table[g.integers(0, half, B - half)][:, :mb // 2]
+    held = set(table[table >= 0].tolist())
+    spare = [p for p in g.permutation(nb).tolist() if p not in held]
+    s = _tight(table.tolist(), spare + [-1] * (len(held) // 3), len(spare), nb, bs)
+    flagged = 0
+    for _ in range(12):
+        rows = g.choice(B, int(g.integers(1, B // 2 + 1)), replace=False).tolist()
+        flagged += any(s.free(rows, [int(k) for k in g.integers(0, mb * bs, len(rows))]))
+    assert flagged

@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_release_kernel(const 
 #pragma unroll
     for (int q = 0; q < kAt; ++q) {
       const bool released = out >> q & 1u;
-      if (!fits) {
-        if (released) atomicOr(&a.status[(e + q) / a.max_blocks], SPEC_DEV_CAPACITY);
+      if (!fits) {  // nothing is done: every row that keeps a page it was to drop is told
+        if (page[q] >= 0) atomicOr(&a.status[(e + q) / a.max_blocks], SPEC_DEV_CAPACITY);
       } else if (page[q] >= 0) {
         if (released) a.pool[pos++] = page[q];
         *at[q] = -1;
