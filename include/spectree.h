@@ -449,8 +449,11 @@ spec_status spec_tree_merge(const int32_t* seqs, const int32_t* lens, const int3
  *   n_max    the largest n_b the call may see (n_max * (Hq / Hkv) < 2^30; T * Hq < 2^31)
  *   scale    finite and not negative (else SPEC_ERR_INVALID_ARG)
  *   out      [T][Hq][D] dtype out; rows outside every request are not written
- *   workspace  16-byte aligned device scratch of spec_prompt_workspace_size() bytes (used when
- *            the keys of few rows are split over the GPU)
+ *   workspace  16-byte aligned device scratch, used when the keys of few rows are split over
+ *            the GPU.  spec_prompt_workspace_size() is what the call of these sizes wants
+ *            (smaller batches often want more: fewer rows, more splits).  Any buffer of 256
+ *            bytes or more will do: where it is too small for that the keys are split less
+ *            and the call takes longer (else SPEC_ERR_WORKSPACE)
  *   status   int32 [B] in/out: a request that comes in non-zero is skipped, its rows left as
  *            they were.  Or-ed with SPEC_DEV_BAD_TREE (n_b outside [0, n_max], or rows outside
  *            [0, T)), SPEC_DEV_CAPACITY (prefix_len outside [0, max_prefix], or

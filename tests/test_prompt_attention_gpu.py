@@ -260,3 +260,21 @@ def test_a_scale_of_zero_averages_what_a_row_sees(dtype, scale):
         out, status = _call(d)
         assert status.tolist() == [0] * len(lens)
         _holds(d, out)
+
+
+def test_a_workspace_that_fits_one_batch_serves_smaller_ones():
+    """A server's one buffer, sized for its largest batch: smaller batches, which
+    would split their keys further, run in it too."""
+    for dtype in (torch.bfloat16, torch.float32):
+        for lens, prefix in (([1] * 3, [4000, 16000, 90]), ([200], [3000]), ([1], [9000])):
+            d = paged_batch(71, lens, prefix, 8, 2, 128, 64, dtype)
+            d["max_prefix"] = 16384
+            need = S.spec_prompt_workspace_size(*_size(d))
+            per = -(-4 * d["T"] * 8 * 130 // 256) * 256 + 256
+            for room in sorted({256, 256 + 2 * per, 256 + 3 * per, need - 1, need}):
+                out, status = _call(d, ws=torch.empty(room, dtype=torch.uint8, device="cuda"))
+                assert status.tolist() == [0] * len(lens)
+                _holds(d, out)
+            with pytest.raises(S.SpecError) as e:
+                _call(d, ws=torch.empty(255, dtype=torch.uint8, device="cuda"))
+            assert e.value.code == S.SPEC_ERR_WORKSPACE

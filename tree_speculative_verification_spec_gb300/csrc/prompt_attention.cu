@@ -7,6 +7,7 @@
 // for any reference m.  Keys are walked once with the running maximum as
 // reference (online softmax in the log2 domain).
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "prompt.cuh"
@@ -308,16 +309,18 @@ static cudaError_t launch_prompt_combine(const PromptArgs& a, spec_dtype dt, cud
 // Tensor cores (one CTA an SM): the split count of least waves x (4 us of
 // set-up and output + 1.3 us per 128-key step) + 5 us for the combine (512
 // tokens: 21 us whole, 29 us in two; one token over 16384: 33 us in 19).
-static PromptPlan prompt_plan(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, bool bf16) {
+// max_splits: what the caller's workspace holds.
+static PromptPlan prompt_plan(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, bool bf16, long long max_splits) {
   PromptPlan p;
   const int g = Hq / Hkv;
   p.tiles = (long long)T * g / (bf16 ? kPromptTcRows : kPromptCcRows) + B;
   const long long units = p.tiles * Hkv, keys = (long long)max_prefix + n_max;
   long long splits = 1;
-  if (units < 152 && !bf16) splits = std::max(1LL, std::min((2 * 152 + units - 1) / units, keys / kPrKeys));
+  if (units < 152 && !bf16)
+    splits = std::max(1LL, std::min(max_splits, std::min((2 * 152 + units - 1) / units, keys / kPrKeys)));
   if (units < 152 && bf16) {
     double best = 1e300;
-    const long long most = std::max(1LL, std::min(64LL, (keys + 127) / 128));
+    const long long most = std::max(1LL, std::min({max_splits, 64LL, (keys + 127) / 128}));
     for (long long s = 1; s <= most; ++s) {
       const long long steps = ((keys + s - 1) / s + 127) / 128;
       const double cost = (double)((units * s + 151) / 152) * (4.0 + 1.3 * (double)steps) + (s > 1 ? 5.0 : 0.0);
@@ -334,10 +337,16 @@ static PromptPlan prompt_plan(int B, int T, int n_max, int max_prefix, int Hq, i
   return p;
 }
 
+constexpr size_t kPromptWsMin = 256;
+
 static size_t prompt_ws_bytes(const PromptPlan& p, int T, int Hq, int D) {
   if (p.splits <= 1) return 0;
   const size_t o = (size_t)p.splits * T * Hq * D * sizeof(float);
   return ((o + 255) & ~(size_t)255) + (size_t)p.splits * T * Hq * 2 * sizeof(float);
+}
+// The most splits whose partial rows fit into `bytes` (0 and 1: none do).
+static long long prompt_ws_splits(size_t bytes, int T, int Hq, int D) {
+  return bytes < 256 ? 0 : (long long)((bytes - 255) / ((size_t)T * Hq * (D + 2) * sizeof(float)));
 }
 
 static spec_status prompt_shape_check(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int D,
@@ -359,10 +368,11 @@ using namespace spectree;
 extern "C" {
 
 size_t spec_prompt_workspace_size(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int D) {
-  if (B <= 0 || T <= 0 || n_max <= 0 || prompt_shape_check(B, T, n_max, max_prefix, Hq, Hkv, D, 16) != SPEC_OK) return 256;
-  size_t best = 256;
+  if (B <= 0 || T <= 0 || n_max <= 0 || prompt_shape_check(B, T, n_max, max_prefix, Hq, Hkv, D, 16) != SPEC_OK)
+    return kPromptWsMin;
+  size_t best = kPromptWsMin;
   for (bool bf16 : {false, true})
-    best = std::max(best, prompt_ws_bytes(prompt_plan(B, T, n_max, max_prefix, Hq, Hkv, bf16), T, Hq, D));
+    best = std::max(best, prompt_ws_bytes(prompt_plan(B, T, n_max, max_prefix, Hq, Hkv, bf16, INT_MAX), T, Hq, D));
   return best;
 }
 
@@ -385,11 +395,17 @@ spec_status spec_prompt_attention(const void* q, const void* k_cache, const void
     return SPEC_ERR_INVALID_ARG;
   // the tensor-core path names cache rows by 32-bit coordinates, and items by a grid index
   if (dtype == SPEC_BF16 && (long long)num_blocks * Hkv * block_size >= (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
-  const PromptPlan plan = prompt_plan(B, T, n_max, max_prefix, Hq, Hkv, dtype == SPEC_BF16);
+  PromptPlan plan = prompt_plan(B, T, n_max, max_prefix, Hq, Hkv, dtype == SPEC_BF16, INT_MAX);
   if (plan.tiles * Hkv * plan.splits > (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
-  const size_t need = prompt_ws_bytes(plan, T, Hq, D);
-  if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+  size_t need = prompt_ws_bytes(plan, T, Hq, D);
+  if (need > 0 && (!workspace || workspace_bytes < kPromptWsMin || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return SPEC_ERR_WORKSPACE;
+  if (workspace_bytes < need) {
+    // a buffer that was sized for another batch: the best plan that fits it (with
+    // whole keys in the end, which needs none)
+    plan = prompt_plan(B, T, n_max, max_prefix, Hq, Hkv, dtype == SPEC_BF16, prompt_ws_splits(workspace_bytes, T, Hq, D));
+    need = prompt_ws_bytes(plan, T, Hq, D);
+  }
   PromptArgs a = {};
   a.q = q;
   a.k_cache = k_cache;
