@@ -437,8 +437,10 @@ spec_status spec_tree_merge(const int32_t* seqs, const int32_t* lens, const int3
  * out = sum_{k <= s} softmax_k(scale * q . K_k) V_k.  Query head h reads
  * kv-head h / (Hq / Hkv).  One token per request (n_b = 1) is the plain decode
  * step.  The rows' own K/V must be in the cache (spec_kv_append before this
- * call on the stream).  fp32 accumulation and softmax; bf16 inputs give bf16
- * output.
+ * call on the stream).  fp32 accumulation and softmax.  bf16 inputs give bf16
+ * output, and each softmax weight is rounded to bf16 (by at most 2^-8 of it)
+ * before it meets V; the weights are normalised by the sum of the rounded
+ * ones.
  *   q        [T][Hq][D] dtype, T >= seq_off[B]; 16-byte aligned, as are out and the caches
  *            (else SPEC_ERR_INVALID_ARG)
  *   k_cache, v_cache, block_table, max_blocks, block_size, num_blocks  paged cache, see

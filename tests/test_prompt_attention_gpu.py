@@ -278,3 +278,22 @@ def test_a_workspace_that_fits_one_batch_serves_smaller_ones():
             with pytest.raises(S.SpecError) as e:
                 _call(d, ws=torch.empty(255, dtype=torch.uint8, device="cuda"))
             assert e.value.code == S.SPEC_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_row_that_sees_one_key_returns_its_value(D, dtype):
+    """The first token of a fresh prompt, and rows that one key's score leaves
+    alone (it leads by more than 24 bits): V itself, every bit."""
+    lens = [1] * 40 + [130, 300]
+    d = paged_batch(67, lens, [0] * 42, 8, 2, D, 16, dtype, spread=2.0)
+    lead = d["table"][41, 3].long()             # slots 48 .. 63 of the last request: slot 50 leads
+    d["k"][lead, :, 2] = 400.0
+    d["q"][170 + 51:470] = d["q"][170 + 51:470].abs() + 0.5
+    out, status = _call(d)
+    assert status.tolist() == [0] * 42
+    for b, t in [(b, b) for b in range(40)] + [(40, 40), (41, 170)]:
+        v = d["v"][d["table"][b, 0].long(), :, 0]
+        assert torch.equal(out[t], v.repeat_interleave(4, 0)), b
+    v = d["v"][lead, :, 2].repeat_interleave(4, 0)
+    assert (out[170 + 51:470] == v).all()

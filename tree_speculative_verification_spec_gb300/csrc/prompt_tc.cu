@@ -506,7 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = 0.0f, l = 0.0f;  // the row's reference (log2 domain) and sum
     float limit = kSumLimit;
     // weights 2^(x c - ref) of 32 columns, `vis` of them visible, packed to bf16
-    // in pk[0 .. 15] (each off by at most half a bf16 step); returns their fp32 sum
+    // in pk[0 .. 15] (each off by at most half a bf16 step); returns the fp32 sum
+    // of the packed ones: numerator and denominator hold the same weights, so that
+    // a key that stands alone gives its V.  Summing the weights before they are
+    // rounded takes fewer instructions (one prompt of 16384: 1258 us against 1320).
     auto weights = [&](uint32_t (&x)[32], int vis, float ref, uint32_t* pk) -> float {
       if (!__all_sync(0xffffffffu, vis >= 32)) {
 #pragma unroll
@@ -519,10 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int e = 0; e < 32; e += 2) {
         const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c22, neg);
         const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-        if (e & 2) acc1 = __fadd2_rn(acc1, p);
-        else acc0 = __fadd2_rn(acc0, p);
-        __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
-        pk[e >> 1] = *reinterpret_cast<uint32_t*>(&h2);
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(&h2);
+        pk[e >> 1] = u;
+        if (e & 2) add_bf16x2(acc1, u);
+        else add_bf16x2(acc0, u);
       }
       return (acc0.x + acc0.y) + (acc1.x + acc1.y);
     };

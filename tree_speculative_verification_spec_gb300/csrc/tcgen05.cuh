@@ -172,6 +172,16 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// a += the two bf16 of u, in fp32 (mixed-precision add, sm_100 and later)
+__device__ __forceinline__ void add_bf16x2(float2& a, uint32_t u) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "add.f32.bf16 %0, l, %0;\n\t"
+      "add.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "r"(u));
+}
+
 // max(a, b, c) in one instruction (three-input form of max.f32, sm_100 and later)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
