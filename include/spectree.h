@@ -440,7 +440,8 @@ spec_status spec_tree_merge(const int32_t* seqs, const int32_t* lens, const int3
  * call on the stream).  fp32 accumulation and softmax.  bf16 inputs give bf16
  * output, and each softmax weight is rounded to bf16 (by at most 2^-8 of it)
  * before it meets V; the weights are normalised by the sum of the rounded
- * ones.
+ * ones.  Values of V may have any magnitude in fp32, and 0 or 2^-60 to 2^80 in
+ * bf16 (weights reach 2^30 there before they are normalised).
  *   q        [T][Hq][D] dtype, T >= seq_off[B]; 16-byte aligned, as are out and the caches
  *            (else SPEC_ERR_INVALID_ARG)
  *   k_cache, v_cache, block_table, max_blocks, block_size, num_blocks  paged cache, see

@@ -297,3 +297,19 @@ def test_a_row_that_sees_one_key_returns_its_value(D, dtype):
         assert torch.equal(out[t], v.repeat_interleave(4, 0)), b
     v = d["v"][lead, :, 2].repeat_interleave(4, 0)
     assert (out[170 + 51:470] == v).all()
+
+
+@pytest.mark.parametrize("size", [-90, 90])
+@pytest.mark.parametrize("score", [0.0, 35.0, -35.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_values_of_any_size(dtype, score, size):
+    """Values of 2^-90 and 2^90 under scores about +-50 (log2): no accumulator
+    overflows and no product is lost."""
+    for lens, prefix in (([200, 70], [0, 333]), ([3], [6000])):
+        d = paged_batch(61, lens, prefix, 8, 2, 128, 16, dtype, spread=0.5)
+        d["v"] = (d["v"].float() * 2.0 ** size).to(dtype)
+        d["q"] = (d["q"].float() * 0.5 + 1.0).to(dtype)
+        d["k"] = (d["k"].float() + score / math.sqrt(128)).to(dtype)
+        out, status = _call(d)
+        assert status.tolist() == [0] * len(lens)
+        _holds(d, out)

@@ -19,10 +19,14 @@
 //
 // Reference m of a row: softmax(x) = 2^(xc - m) / sum 2^(xc - m) for ANY m, and
 // fp32 and bf16 hold 2^127.  So m starts at 0 and no maximum is taken, as long
-// as the sum of 64 weights stays below 2^60 and the first visible ones reach
-// 2^-60 (smaller weights than 2^-60 of the largest do not show in 24 bits).
-// Otherwise that half tile is done again against its own maximum, and O and the
-// sum are scaled to it.
+// as the sum of 64 weights stays below 2^30 and the first visible ones reach
+// 2^-30.  Otherwise that half tile is done again against its own maximum, and O
+// and the sum are scaled to it.  What the weights take of fp32's range is lost
+// to V: magnitudes of 2^-60 to 2^80 neither overflow (2^30 of 64 weights, 2^18
+// keys and more) nor lose bits below 2^-126 (2^-36 of the largest weight, 24
+// bits).  Limits of 2^60, 2^30 and 2^20 cost the same where scores have a
+// deviation of 1 (natural units) and nearly so at 3; at 10 one prompt of 16384
+// took 1330, 1410 and 1637 us, a redo for every larger maximum.
 //
 // What bounds it, and what it measured (32/8 heads, D 128, one GB300):
 //   long prompts: the tensor core.  A step of 2 x 128 x 128 takes 2048 cycles of
@@ -49,7 +53,7 @@ constexpr int kRows = kPromptTcRows; // rows per work item
 constexpr int HC = BN / 2;           // keys per softmax half
 constexpr int kThreads = 384;        // warps: 0 K loads, 1 and 3 MMA of tiles 0 and 1, 2 work items, Q and V loads, 4-7 softmax of tile 0, 8-11 of tile 1
 constexpr uint32_t kTmemCols = 512;  // S_0, S_1 at 0, 128; O_0, O_1 at 256, 384
-constexpr float kSumLimit = 1152921504606846976.0f;  // 2^60
+constexpr float kSumLimit = 1073741824.0f;  // 2^30
 constexpr int kOrderMax = 256;       // batches up to this size run longest request first
 static_assert(kRows == 2 * BM, "two row tiles per item");
 
