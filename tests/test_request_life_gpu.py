@@ -166,3 +166,32 @@ def test_logprobs_need_their_buffers():
     w = W.small_random(3, B=1, n_range=(4, 4), V=50)
     with pytest.raises(ValueError):
         VerifyPass(DeviceBatch.from_workload(w)).logprobs()
+
+
+def test_temperatures_that_only_the_log_probabilities_refuse():
+    """The verifiers take what the log probabilities flag (a greedy pass ignores
+    temperatures, a stochastic one takes any above 0): the accepted path is
+    committed all the same, and the flag stands in a word of its own."""
+    for mode, temps, bad in (("greedy", [0.0, 1.0, math.inf], [0, 2]), ("stochastic", [1e-31, 1.0, 2.0], [0])):
+        w = W.small_random(11, B=3, n_range=(6, 9), V=60)
+        plain = VerifyPass(DeviceBatch.from_workload(w))
+        plain.inv_temp = None if mode == "greedy" else torch.tensor(temps, device="cuda")
+        plain.run(mode)
+        b = DeviceBatch.from_workload(w)
+        vp = VerifyPass(b, logprob_top=2)
+        vp.inv_temp = torch.tensor(temps, device="cuda")
+        vp.run(mode)
+        assert plain.status.tolist() == vp.status.tolist() == [0, 0, 0]
+        assert vp.accept_len.tolist() == plain.accept_len.tolist() and vp.new_len.tolist() == plain.new_len.tolist()
+        assert vp.new_len.tolist() == [p + a for p, a in zip(b.prefix_len.tolist(), vp.accept_len.tolist())]
+        for x, y in ((plain.batch.k_cache, b.k_cache), (plain.batch.v_cache, b.v_cache)):
+            assert torch.equal(x.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32),
+                               y.view(torch.int16 if y.dtype == torch.bfloat16 else torch.int32))
+        assert vp.logprob_status.tolist() == [S.SPEC_DEV_BAD_TEMP if r in bad else 0 for r in range(3)]
+        for r in range(3):
+            assert all(math.isnan(v) == (r in bad) for v in vp.logprob[r, :vp.accept_len[r]].tolist())
+        vp.inv_temp = torch.ones(3, device="cuda")   # the word is the last pass's
+        vp.mask_build()
+        vp.verify(mode)
+        vp.logprobs()
+        assert vp.logprob_status.tolist() == [0, 0, 0]

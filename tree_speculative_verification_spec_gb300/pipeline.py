@@ -59,6 +59,11 @@ class DeviceBatch:
                    uniforms=d(w.uniforms), scale=w.scale)
 
 
+def _clear(status, stream):
+    with torch.cuda.stream(stream):  # None: the current one
+        status.zero_()
+
+
 class PromptPass:
     """Causal attention of packed prompts (or chunks) over the paged cache.
 
@@ -122,6 +127,8 @@ class VerifyPass:
             self.rank = torch.empty(shape, **i32)
             self.top_tokens = torch.empty(shape + (logprob_top,), **i32)
             self.top_logprobs = torch.empty(shape + (logprob_top,), **f32)
+            # a word of its own: commit() leaves a request whose status is not 0 as it was
+            self.logprob_status = torch.zeros(max(b.B, 1), **i32)
         self.batch = b
 
     def mask_build(self, stream=None):
@@ -155,14 +162,18 @@ class VerifyPass:
     def logprobs(self, stream=None, inv_temp=None):
         """Log probability, entropy, rank and alternatives of every emitted
         token, [B][n_max] (after verify(); the target distribution is the
-        verifier's)."""
+        stochastic verifier's, softmax(inv_temp * logits), after a greedy walk
+        too).  Flags go to logprob_status, cleared first: what this call
+        refuses (a temperature of 0, say, which a greedy walk ignores) does
+        not stop the commit."""
         if self.logprob_top is None:
             raise ValueError("VerifyPass was made without logprob_top")
         b = self.batch
+        _clear(self.logprob_status, stream)
         S.spec_path_logprobs(b.p_logits, b.tree_off, self.path, self.accept_len, self.emitted,
                              self.inv_temp if inv_temp is None else inv_temp, b.B, b.T, b.n_max, b.V,
                              self.logprob_top, self.logprob, self.entropy, self.rank, self.top_tokens,
-                             self.top_logprobs, self.status, stream)
+                             self.top_logprobs, self.logprob_status, stream)
 
     def commit(self, stream=None):
         b = self.batch
