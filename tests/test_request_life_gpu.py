@@ -195,3 +195,31 @@ def test_temperatures_that_only_the_log_probabilities_refuse():
         vp.verify(mode)
         vp.logprobs()
         assert vp.logprob_status.tolist() == [0, 0, 0]
+
+
+def test_a_prompt_pass_runs_again_after_a_refusal():
+    """A request that one run flagged is computed by the next, on the pass's own
+    stream too."""
+    g = torch.Generator("cuda").manual_seed(21)
+    Hq, Hkv, D, bs, n = 4, 2, 64, 16, 50
+    rand = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    k, v = (torch.zeros((16, Hkv, bs, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.arange(16, dtype=torch.int32, device="cuda").view(2, 8).contiguous()
+    q, kv = rand(2 * n, Hq, D), (rand(2 * n, Hkv, D), rand(2 * n, Hkv, D))
+    for stream in (None, torch.cuda.Stream()):
+        prefix = _ints([10, 41])
+        p = PromptPass(q, k, v, table, _ints([0, n, 2 * n]), prefix, n, 40, 1.0 / math.sqrt(D))
+        p.out.fill_(7.0)
+        torch.cuda.synchronize()
+        p.run(kv, stream=stream)
+        torch.cuda.synchronize()
+        assert p.status.tolist() == [0, S.SPEC_DEV_CAPACITY] and (p.out[n:] == 7.0).all()
+        prefix[1] = 0
+        torch.cuda.synchronize()
+        p.run(kv, stream=stream)
+        torch.cuda.synchronize()
+        assert p.status.tolist() == [0, 0]
+        d = dict(q=q, k=k, v=v, table=table, seq_off=_ints([0, n, 2 * n]), prefix=prefix, B=2, T=2 * n, Hq=Hq, Hkv=Hkv, D=D, bs=bs,
+                 scale=1.0 / math.sqrt(D))
+        ref, tol = prompt_reference(d)
+        assert ((p.out.double() - ref).abs() <= tol).all()

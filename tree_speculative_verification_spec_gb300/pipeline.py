@@ -82,8 +82,10 @@ class PromptPass:
 
     def run(self, prompt_kv=None, stream=None):
         """prompt_kv: (k_new, v_new) rows [T][Hkv][D] put behind the prefix
-        first, or None when they are already in the cache."""
+        first, or None when they are already in the cache.  status is this
+        run's: a request that an earlier one flagged is computed again."""
         B, T, n_max, max_prefix, Hq, Hkv, D = self.size
+        _clear(self.status, stream)
         if prompt_kv is not None:
             S.spec_kv_append(*prompt_kv, self.k_cache, self.v_cache, self.block_table, self.block_table.shape[1],
                              self.block_size, self.num_blocks, self.prefix_len, self.seq_off, B, n_max, Hkv, D,
