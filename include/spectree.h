@@ -300,9 +300,9 @@ spec_status spec_tree_verify_stochastic(const float* p_logits, const float* q_pr
  *            [prefix_len, prefix_len + n_b)); such a request is left untouched.  The
  *            incoming status is not read: an upstream failure does not stop the append.
  * Launched as a programmatic dependent of the previous kernel (the mask build
- * allows it at its start): the copies may overlap that kernel, which must not
- * write k_new, v_new or the tree slots; the status update and the end of the
- * grid wait for it.  One launch, grid (B, parts).
+ * allows it at its start), it waits for that kernel's results before it reads
+ * anything: k_new, v_new, the table, the lengths and the packing may come from
+ * the kernel right before this call.  One launch, grid (B, parts).
  */
 spec_status spec_kv_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
                            const int32_t* block_table, int max_blocks, int block_size, int num_blocks,

@@ -223,3 +223,28 @@ def test_a_prompt_pass_runs_again_after_a_refusal():
                  scale=1.0 / math.sqrt(D))
         ref, tol = prompt_reference(d)
         assert ((p.out.double() - ref).abs() <= tol).all()
+
+
+def test_a_prompt_right_behind_the_kernels_that_make_its_rows():
+    """Rows, pages and lengths written by the kernels just before the pass, a
+    library product among them, as a model's layers do."""
+    g = torch.Generator("cuda").manual_seed(31)
+    Hq, Hkv, D, bs, n, width = 8, 2, 128, 16, 2048, 512
+    rand = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    x, wk, wv, wq = rand(2 * n, width), rand(width, Hkv * D), rand(width, Hkv * D), rand(width, Hq * D)
+    want = None
+    for turn in range(6):
+        pool = Pool(rows=2, max_blocks=n // bs + 1, num_blocks=300, Hkv=Hkv, bs=bs, D=D, layers=1)
+        src, dst, zero, room = _ints([-1, -1]), _ints([0, 1]), _ints([0, 0]), _ints([n, n])
+        off, prefix, st = _ints([0, n, 2 * n]), _ints([0, 0]), _ints([7, 7])
+        p = PromptPass(rand(2 * n, Hq, D), *pool.caches[0], pool.table, off, prefix, n, 0, 0.01)
+        torch.cuda.synchronize()
+        p.q = (x @ wq).view(2 * n, Hq, D)
+        S.spec_pages_fork(None, None, 0, pool.table, *pool.shape, src, dst, zero, room, 2, Hkv, D, S.SPEC_BF16, pool.pool, pool.count, pool.ws, st)
+        k, v = (x @ wk).view(2 * n, Hkv, D), (x @ wv).view(2 * n, Hkv, D)
+        p.run((k, v))
+        assert p.status.tolist() == [0, 0] and st.tolist() == [0, 0]
+        got = [c[pool.table[b, :n // bs].long()].transpose(1, 2).reshape(n, Hkv, D) for c in pool.caches[0] for b in (0, 1)]
+        assert torch.equal(torch.cat(got[:2]), k) and torch.equal(torch.cat(got[2:]), v)
+        want = p.out.clone() if want is None else want
+        assert torch.equal(p.out, want)
