@@ -248,3 +248,38 @@ def test_a_prompt_right_behind_the_kernels_that_make_its_rows():
         assert torch.equal(torch.cat(got[:2]), k) and torch.equal(torch.cat(got[2:]), v)
         want = p.out.clone() if want is None else want
         assert torch.equal(p.out, want)
+
+
+@pytest.mark.parametrize("dtype,D,bs", [(torch.bfloat16, 128, 16), (torch.float32, 64, 256), (torch.bfloat16, 64, 8)])
+def test_append_of_more_rows_than_a_tree_has(dtype, D, bs):
+    """Prompts of thousands of rows beside short, empty and refused ones: the
+    caches byte for byte."""
+    g = torch.Generator().manual_seed(bs)
+    Hkv = 3
+    lens, prefix = [5000, 0, 1, 1025, 300, 40], [37, 9, 4095, 0, 90, 17]
+    used = [-(-(n + p) // bs) for n, p in zip(lens, prefix)]
+    nb, width = sum(used) + 5, max(used)
+    perm = torch.randperm(nb, generator=g).tolist()
+    table = torch.full((len(lens), width), -1, dtype=torch.int32)
+    at = 0
+    for b, u in enumerate(used):
+        table[b, :u] = torch.tensor(perm[at:at + u], dtype=torch.int32)
+        at += u
+    table[4, used[4] - 1] = nb                       # a bad id among the pages to be written
+    prefix[5] = width * bs - 39                      # one slot short
+    off = [0] + np.cumsum(lens).tolist()
+    bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+    make = lambda *s: torch.randint(0, 1 << 14, s, generator=g, dtype=torch.int32).to(bits)  # noqa: E731
+    new = [make(off[-1], Hkv, D) for _ in range(2)]
+    caches = [make(nb, Hkv, bs, D) for _ in range(2)]
+    dev = [c.cuda().view(dtype) for c in caches]
+    status = _ints([0] * len(lens))
+    S.spec_kv_append(*[n.cuda().view(dtype) for n in new], *dev, table.cuda(), width, bs, nb, _ints(prefix), _ints(off), len(lens),
+                     max(lens), Hkv, D, status)
+    assert status.tolist() == [0, 0, 0, 0, S.SPEC_DEV_BAD_BLOCK, S.SPEC_DEV_CAPACITY]
+    for c, n in zip(caches, new):
+        for b in range(4):
+            s = prefix[b] + torch.arange(lens[b])
+            c[table[b][s // bs].long(), :, s % bs] = n[off[b]:off[b + 1]]
+    for c, d in zip(caches, dev):
+        assert torch.equal(c, d.cpu().view(bits))
