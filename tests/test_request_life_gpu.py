@@ -283,3 +283,16 @@ def test_append_of_more_rows_than_a_tree_has(dtype, D, bs):
             c[table[b][s // bs].long(), :, s % bs] = n[off[b]:off[b + 1]]
     for c, d in zip(caches, dev):
         assert torch.equal(c, d.cpu().view(bits))
+
+
+def test_page_calls_take_cache_addresses_of_64_bits_alone():
+    pool = Pool(rows=2, max_blocks=4, num_blocks=8, Hkv=1, bs=8, D=64)
+    one, st = _ints([0]), _ints([77])
+    for k, v in ((pool.k.int(), pool.v), (pool.k, pool.v.float()), (pool.k[:1], pool.v), (None, pool.v)):
+        with pytest.raises((ValueError, S.SpecError)):
+            S.spec_pages_fork(k, v, pool.layers, pool.table, *pool.shape, _ints([-1]), one, one, _ints([5]), 1, 1, 64, S.SPEC_BF16,
+                              pool.pool, pool.count, pool.ws, st)
+        with pytest.raises((ValueError, S.SpecError)):
+            S.spec_pages_compact(k, v, pool.layers, pool.table, *pool.shape, 1, 64, S.SPEC_BF16, pool.pool, pool.count,
+                                 torch.zeros(8, dtype=torch.int32, device="cuda"), one, pool.ws, st)
+    assert st.tolist() == [77] and pool.count.item() == 8

@@ -307,6 +307,13 @@ def _f32(t):
     return _ptr(t)
 
 
+def _addresses(t, layers):
+    """Pointer of a table of the layers' cache addresses (None passes)."""
+    if t is not None and (t.dtype != torch.int64 or t.numel() < layers):
+        raise ValueError("cache addresses must be int64 tensors with an entry for each layer")
+    return _ptr(t)
+
+
 def _stream_of(t, stream):
     """The stream of a call on tensor t's device, which has to be the current
     one (its kernels are launched there)."""
@@ -360,9 +367,9 @@ def spec_pages_fork(k_ptrs, v_ptrs, layers, block_table, B, max_blocks, block_si
     (None with layers = 0); room: int32 [N] or None (0); dtype: SPEC_F32 or
     SPEC_BF16."""
     _check("spec_pages_fork", lib().spec_pages_fork(
-        _ptr(k_ptrs), _ptr(v_ptrs), layers, _i32(block_table), B, max_blocks, block_size, num_blocks, _i32(src),
-        _i32(dst), _i32(length), _i32(room), N, Hkv, D, dtype, _i32(free_pool), free_pool.numel(), _i32(free_count),
-        *_scratch(workspace), _i32(status), _stream_of(block_table, stream)))
+        _addresses(k_ptrs, layers), _addresses(v_ptrs, layers), layers, _i32(block_table), B, max_blocks, block_size,
+        num_blocks, _i32(src), _i32(dst), _i32(length), _i32(room), N, Hkv, D, dtype, _i32(free_pool),
+        free_pool.numel(), _i32(free_count), *_scratch(workspace), _i32(status), _stream_of(block_table, stream)))
 
 
 def spec_pages_free(block_table, B, max_blocks, block_size, num_blocks, rows, keep_len, N, free_pool, free_count,
@@ -376,9 +383,9 @@ def spec_pages_free(block_table, B, max_blocks, block_size, num_blocks, rows, ke
 def spec_pages_compact(k_ptrs, v_ptrs, layers, block_table, B, max_blocks, block_size, num_blocks, Hkv, D, dtype,
                        free_pool, free_count, page_map, moved, workspace, status, stream=None):
     _check("spec_pages_compact", lib().spec_pages_compact(
-        _ptr(k_ptrs), _ptr(v_ptrs), layers, _i32(block_table), B, max_blocks, block_size, num_blocks, Hkv, D, dtype,
-        _i32(free_pool), free_pool.numel(), _i32(free_count), _i32(page_map), _i32(moved), *_scratch(workspace),
-        _i32(status), _stream_of(block_table, stream)))
+        _addresses(k_ptrs, layers), _addresses(v_ptrs, layers), layers, _i32(block_table), B, max_blocks, block_size,
+        num_blocks, Hkv, D, dtype, _i32(free_pool), free_pool.numel(), _i32(free_count), _i32(page_map), _i32(moved),
+        *_scratch(workspace), _i32(status), _stream_of(block_table, stream)))
 
 
 def spec_selftest_bounded_wait(status, polls, stream=None):
