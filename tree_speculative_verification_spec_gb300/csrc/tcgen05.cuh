@@ -1,4 +1,4 @@
-// mbarrier, TMA and tcgen05 primitives of the prompt-attention kernel (inline
+// mbarrier, TMA and tcgen05 primitives of the prompt-attention and log-probability kernels (inline
 // PTX; attention_tc.cu keeps its own, so that the source its recorded traffic
 // belongs to stays as it was measured).
 #pragma once
@@ -142,17 +142,6 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// One column of this thread's lane; the load is complete on return.
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
-}
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r) : : "memory");
-  return __uint_as_float(r);
-}
-
 // Shared-memory matrix descriptor, 128-byte swizzle (layout type 2), sm_100
 // family descriptor version 1.  Addresses and offsets in bytes.
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -180,35 +169,6 @@ __device__ __forceinline__ void add_bf16x2(float2& a, uint32_t u) {
       "add.f32.bf16 %1, h, %1;\n\t}"
       : "+f"(a.x), "+f"(a.y)
       : "r"(u));
-}
-
-// max(a, b, c) in one instruction (three-input form of max.f32, sm_100 and later)
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b, float& ra, float& rb) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  ra = __low2float(h);
-  rb = __high2float(h);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-// Meeting of the two warps that use named barrier `id`; whether `any` holds in
-// any of their 64 threads.
-__device__ __forceinline__ bool pair_any(int id, bool any) {
-  uint32_t out;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(out)
-      : "r"(id), "r"((uint32_t)any)
-      : "memory");
-  return out != 0;
 }
 
 // Cluster launch control: ask for the launch of a CTA of this grid that has not
