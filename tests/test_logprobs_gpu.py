@@ -333,3 +333,54 @@ def test_one_nan_among_masked_logits(V, nans, masked, dtype):
                 row = x[first + i].cpu().double().numpy()
                 _check(row, out, i, tokens[i], 1.0, k)
                 assert math.isnan(out[0][i].item()) == (first + i != 1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_logits_beyond_32_bit_offsets(dtype):
+    """Rows behind the first 2^31 elements, of the packed call and of the path's."""
+    V, k = 131071, 3
+    T = (1 << 31) // V + 7
+    x = torch.zeros((T, V), dtype=dtype, device="cuda")
+    last = torch.randn((6, V), generator=torch.Generator().manual_seed(5)).to(dtype)
+    x[-6:] = last.cuda()
+    tokens = [0] * (T - 6) + [V - 1, 7, 0, 65536, 99, 100]
+    out, status = _tokens_call(x, tokens, [0, 11, T], [1.0, 0.5], k)
+    assert status == [0, 0]
+    for i in range(6):
+        _check(last[i].double().numpy(), out, T - 6 + i, tokens[T - 6 + i], 0.5, k)
+    c = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    out, status = _outputs((2, 4), k), c([0, 0])
+    S.spec_path_logprobs(x, c([0, T - 6, T]), c([[0, 1, -1, -1], [0, 2, 3, 5]]), c([2, 4]), c([[4, 5, -1, -1], [8, 9, 10, V - 1]]), None, 2,
+                         T, 4, V, k, *out, status)
+    assert status.tolist() == [0, 0]
+    for i, (r, t) in enumerate(((0, 8), (2, 9), (3, 10), (5, V - 1))):
+        _check(last[r].double().numpy(), [o[1] for o in out], i, t, 1.0, k)
+    _check(np.zeros(V), [o[0] for o in out], 1, 5, 1.0, k)
+
+
+def test_packing_that_starts_behind_row_zero():
+    x = torch.randn((9, 500), generator=torch.Generator().manual_seed(6))
+    out, status = _tokens_call(x.cuda(), list(range(9)), [3, 3, 8], [9.0, 2.0], 4)
+    assert status == [0, 0]
+    for i in range(9):
+        if 3 <= i < 8:
+            _check(x[i].double().numpy(), out, i, i, 2.0, 4)
+        else:
+            assert math.isnan(out[0][i].item()) and out[2][i].item() == -1 and out[3][i].tolist() == [-1] * 4
+
+
+def test_calls_on_two_streams_at_once():
+    """A spread row and many rows side by side, several times over: the same bits."""
+    xs = [torch.randn(s, device="cuda", generator=torch.Generator("cuda").manual_seed(s[0])) for s in ((1, 131072), (300, 32000))]
+    ref = [_tokens_call(x, list(range(len(x))), [0, len(x)], None, 20)[0] for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    args = [(torch.arange(len(x), dtype=torch.int32, device="cuda"), torch.tensor([0, len(x)], dtype=torch.int32, device="cuda"),
+             torch.zeros(1, dtype=torch.int32, device="cuda")) for x in xs]
+    outs = [[_outputs((len(x),), 20) for _ in range(4)] for x in xs]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for x, s, (tok, off, st), o in zip(xs, streams, args, outs):
+            S.spec_token_logprobs(x, tok, off, None, 1, len(x), x.shape[1], 20, *o[i], st, stream=s)
+    torch.cuda.synchronize()
+    for r, o in zip(ref, outs):
+        assert all(torch.equal(p, q) for one in o for p, q in zip(r, one))

@@ -291,3 +291,50 @@ def test_random_frees_into_a_tight_pool(seed):
         rows = g.choice(B, int(g.integers(1, B // 2 + 1)), replace=False).tolist()
         flagged += any(s.free(rows, [int(k) for k in g.integers(0, mb * bs, len(rows))]))
     assert flagged
+
+
+def test_pages_beyond_32_bit_offsets():
+    """Partial pages copied and whole ones moved at the end of caches of more than
+    2^32 bytes."""
+    Hkv, D, bs, layers = 2, 128, 64, 1
+    nb = (1 << 32) // (Hkv * bs * D * 2) + 5
+    caches = [torch.zeros((nb, Hkv, bs, D), dtype=torch.int16, device="cuda") for _ in range(2)]
+    rows = [torch.randint(0, 30000, (2, Hkv, bs, D), dtype=torch.int16, device="cuda") for _ in range(2)]
+    for c, r in zip(caches, rows):
+        c[nb - 4], c[nb - 3] = r[0], r[1]
+    k, v = (torch.tensor([c.data_ptr()], dtype=torch.int64, device="cuda") for c in caches)
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, pool, count = i([[nb - 4, nb - 3], [-1, -1]]), i([3, nb - 1]), i([2])
+    ws = torch.empty(S.spec_pages_workspace_size(2, 2, nb, 1), dtype=torch.uint8, device="cuda")
+    st, moved, page_map = i([77]), i([77]), torch.empty(nb, dtype=torch.int32, device="cuda")
+    S.spec_pages_fork(k, v, layers, table, 2, 2, bs, nb, i([0]), i([1]), i([bs + 9]), None, 1, Hkv, D, S.SPEC_BF16, pool, count, ws, st)
+    assert st.tolist() == [0] and table.tolist() == [[nb - 4, nb - 3], [nb - 4, nb - 1]] and count.tolist() == [1]
+    for c, r in zip(caches, rows):
+        assert torch.equal(c[nb - 1, :, :9], r[1, :, :9]) and not c[nb - 1, :, 9:].any()
+    S.spec_pages_compact(k, v, layers, table, 2, 2, bs, nb, Hkv, D, S.SPEC_BF16, pool, count, page_map, moved, ws, st)
+    assert st.tolist() == [0] and moved.tolist() == [1] and table.tolist() == [[nb - 4, nb - 3], [nb - 4, 3]] and pool.tolist()[0] == nb - 1
+    for c, r in zip(caches, rows):
+        assert torch.equal(c[3, :, :9], r[1, :, :9]) and torch.equal(c[nb - 4], r[0])
+
+
+def test_calls_on_two_streams_at_once_with_their_own_tables():
+    g = np.random.default_rng(17)
+    ss = [Both(_empty(6, 9), g.permutation(60).tolist(), 60, 60, 8, 2, 2, 64, torch.bfloat16, i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in ss]
+    st = [s.ints([77] * 3) for s in ss]
+    ws = [s.ws(3) for s in ss]
+    a = [[s.ints(x) for x in ([-1, -1, -1], [0, 1, 2], [0, 0, 0], [20, 33, 5])] for s in ss]
+    b = [[s.ints(x) for x in ([0, 1, 1], [3, 4, 5], [17, 33, 8], [9, 0, 30])] for s in ss]
+    gone = [s.ints([0, 4, 5]) for s in ss]
+    torch.cuda.synchronize()
+    for call in (a, b):
+        for s, q, w, t, args in zip(ss, streams, ws, st, call):
+            S.spec_pages_fork(s.k, s.v, s.layers, s.table, s.B, s.mb, s.bs, s.nb, *args, 3, s.Hkv, s.D, s.code, s.pool, s.count, w, t, stream=q)
+    for s, q, w, t, rows in zip(ss, streams, ws, st, gone):
+        S.spec_pages_free(s.table, s.B, s.mb, s.bs, s.nb, rows, None, 3, s.pool, s.count, w, t, stream=q)
+    torch.cuda.synchronize()
+    for s in ss:
+        assert s.ref.fork([-1, -1, -1], [0, 1, 2], [0, 0, 0], [20, 33, 5]) == [0] * 3
+        assert s.ref.fork([0, 1, 1], [3, 4, 5], [17, 33, 8], [9, 0, 30]) == [0] * 3
+        assert s.ref.free([0, 4, 5], [0, 0, 0]) == [0] * 3
+        s.same()

@@ -313,3 +313,53 @@ def test_values_of_any_size(dtype, score, size):
         out, status = _call(d)
         assert status.tolist() == [0] * len(lens)
         _holds(d, out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("Hq,Hkv", [(256, 2), (256, 1), (96, 1)], ids=["128", "256", "96"])
+def test_wide_groups(Hq, Hkv, dtype):
+    """Groups as wide as a row tile, wider, and such as share no factor with it."""
+    d = paged_batch(73, [5, 1, 2], [0, 700, 33], Hq, Hkv, 64, 16, dtype)
+    out, status = _call(d)
+    assert status.tolist() == [0] * 3
+    _holds(d, out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("prefix", [[0, 5, 300], [0, 5, 9000]], ids=["whole", "split"])
+def test_packing_that_starts_behind_row_zero(prefix, dtype):
+    """Rows before the first request belong to nobody: NaN in q, left alone in out."""
+    d = paged_batch(79, [40, 3, 77], prefix, 8, 2, 64, 16, dtype)
+    gap = 37
+    lead = torch.full((gap,) + d["q"].shape[1:], math.nan, device="cuda", dtype=dtype)
+    d["q"], d["seq_off"], d["T"] = torch.cat([lead, d["q"]]), d["seq_off"] + gap, d["T"] + gap
+    out, status = _call(d)
+    assert status.tolist() == [0] * 3 and (out[:gap] == 7.0).all()
+    _holds(d, out, torch.arange(gap, d["T"], device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,bs", [(torch.bfloat16, 16), (torch.bfloat16, 65536), (torch.float32, 256)], ids=["bf16", "one_page", "fp32"])
+def test_caches_beyond_32_bit_offsets(dtype, bs):
+    """Pages at the end of caches of more than 2^31 elements (2^32 bytes and more)."""
+    Hkv, D = 2, 128
+    nb = (1 << 31) // (Hkv * bs * D) + 3
+    d = paged_batch(83, [70, 1], [30, 600], 4, Hkv, D, bs, dtype)
+    for n in ("k", "v"):
+        big = torch.empty((nb, Hkv, bs, D), dtype=dtype, device="cuda")
+        big[-d["nb"]:] = d[n]
+        d[n] = big
+    d["table"] = torch.where(d["table"] >= 0, d["table"] + (nb - d["nb"]), -1).to(torch.int32)
+    d["nb"] = nb
+    out, status = _call(d)
+    assert status.tolist() == [0, 0]
+    _holds(d, out)
+    # the append reaches them too
+    new = [torch.randn((71, Hkv, D), device="cuda").to(dtype) for _ in range(2)]
+    S.spec_kv_append(*new, d["k"], d["v"], d["table"], d["table"].shape[1], bs, nb, d["prefix"], d["seq_off"], 2, 70, Hkv, D, status)
+    assert status.tolist() == [0, 0]
+    for c, x in zip((d["k"], d["v"]), new):
+        for b, (o, n, p) in enumerate(((0, 70, 30), (70, 1, 600))):
+            s = p + torch.arange(n, device="cuda")
+            assert torch.equal(c[d["table"][b][s // bs].long(), :, s % bs], x[o:o + n])
+    out, status = _call(d)
+    _holds(d, out)

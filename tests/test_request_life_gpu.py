@@ -296,3 +296,32 @@ def test_page_calls_take_cache_addresses_of_64_bits_alone():
             S.spec_pages_compact(k, v, pool.layers, pool.table, *pool.shape, 1, 64, S.SPEC_BF16, pool.pool, pool.count,
                                  torch.zeros(8, dtype=torch.int32, device="cuda"), one, pool.ws, st)
     assert st.tolist() == [77] and pool.count.item() == 8
+
+
+def test_a_captured_prompt_pass():
+    """A pass replayed from a graph: the status it clears, the rows it appends and
+    the lengths as they are at each replay."""
+    g = torch.Generator("cuda").manual_seed(41)
+    Hq, Hkv, D, bs, n = 4, 2, 64, 16, 60
+    rand = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    k, v = (torch.zeros((24, Hkv, bs, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.arange(24, dtype=torch.int32, device="cuda").view(2, 12).contiguous()
+    q, kv = rand(2 * n, Hq, D), (rand(2 * n, Hkv, D), rand(2 * n, Hkv, D))
+    prefix = _ints([0, 90])
+    p = PromptPass(q, k, v, table, _ints([0, n, 2 * n]), prefix, n, 90, 1.0 / math.sqrt(D))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        p.run(kv)
+    for length, flag in ((90, 0), (91, S.SPEC_DEV_CAPACITY), (64, 0)):
+        prefix[1] = length
+        for t in (q, *kv):
+            t.copy_(rand(*t.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert p.status.tolist() == [0, flag]
+        sound = 2 if flag == 0 else 1
+        d = dict(q=q, k=k, v=v, table=table, seq_off=_ints([0, n, 2 * n]), prefix=prefix, B=sound, T=2 * n, Hq=Hq, Hkv=Hkv, D=D, bs=bs,
+                 scale=1.0 / math.sqrt(D))
+        ref, tol = prompt_reference(d)
+        assert ((p.out.double() - ref).abs() <= tol)[:sound * n].all()
