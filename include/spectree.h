@@ -526,6 +526,11 @@ spec_status spec_path_logprobs(const void* p_logits, spec_dtype dtype, const int
  * *free_count entries, and otherwise the caller's own; the table is the only
  * record, so these calls and spec_kv_commit_layers' release need no counters.
  * Pages are taken from the pool's end.  Table entries below 0 mean "no page".
+ * Slots are written (spec_kv_append, the commits) in pages that one row alone
+ * names: a row that was cut back to a length inside a shared page
+ * (spec_pages_free) goes on in an empty row forked from it, which gets a copy
+ * of that page.  The release of spec_kv_commit_layers likewise returns the
+ * pages behind a tree's new length without looking for them in other rows.
  *
  * spec_pages_fork: fork i makes row dst[i] hold the first len[i] slots of row
  *   src[i], with pages for room[i] further slots.  Full pages are shared; the

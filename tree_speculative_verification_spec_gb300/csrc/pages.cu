@@ -12,8 +12,8 @@
 // atomics below are integer minima and counts, and positions come from scans.
 // The plans are bound by the latency of their few dependent passes (a free of
 // 64 rows of a 256 x 1024 table: 16 + 4 + 15 us for check, mark and release),
-// the copies by HBM: 600 pages of 2 MB move at 6.05 TB/s, the partial pages of
-// 64 forks (32 layers, pages of 256 slots) at 6.1 TB/s.
+// the copies by HBM: 600 pages of 2 MB move at 6.4 TB/s, the partial pages of
+// 64 forks (32 layers, pages of 256 slots) at 6.5 TB/s.
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -92,7 +92,7 @@ constexpr int kMoveVec = 8;                      // 16-byte vectors per lane
 constexpr int kMoveBytes = kMoveVec * 32 * 16;   // 4 KB
 constexpr int kMoveThreads = 256;
 constexpr int kMoveCtas = 16;                    // per SM; four fit at once: the later ones even out the end
-                                                 // (600 pages: 408 us with 4, 404 with 8, 398 with 16)
+                                                 // (600 pages: 408 us with 4, 404 with 8, 398 with 16 on a cold GPU)
 
 // The plan's results come by plain pointers: a read-only load could be moved
 // before the wait.

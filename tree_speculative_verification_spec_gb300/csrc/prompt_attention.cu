@@ -310,20 +310,21 @@ static cudaError_t launch_prompt_combine(const PromptArgs& a, spec_dtype dt, cud
 // set-up and output + 1.3 us per 128-key step) + 5 us for the combine (512
 // tokens: 21 us whole, 29 us in two; one token over 16384: 33 us in 19).
 // max_splits: what the caller's workspace holds.
+constexpr long long kPlanSms = 152;  // a GB300's; the size query is a host call that needs no device
 static PromptPlan prompt_plan(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, bool bf16, long long max_splits) {
   PromptPlan p;
   const int g = Hq / Hkv;
   p.tiles = (long long)T * g / (bf16 ? kPromptTcRows : kPromptCcRows) + B;
   const long long units = p.tiles * Hkv, keys = (long long)max_prefix + n_max;
   long long splits = 1;
-  if (units < 152 && !bf16)
-    splits = std::max(1LL, std::min(max_splits, std::min((2 * 152 + units - 1) / units, keys / kPrKeys)));
-  if (units < 152 && bf16) {
+  if (units < kPlanSms && !bf16)
+    splits = std::max(1LL, std::min({max_splits, (2 * kPlanSms + units - 1) / units, keys / kPrKeys}));
+  if (units < kPlanSms && bf16) {
     double best = 1e300;
     const long long most = std::max(1LL, std::min({max_splits, 64LL, (keys + 127) / 128}));
     for (long long s = 1; s <= most; ++s) {
       const long long steps = ((keys + s - 1) / s + 127) / 128;
-      const double cost = (double)((units * s + 151) / 152) * (4.0 + 1.3 * (double)steps) + (s > 1 ? 5.0 : 0.0);
+      const double cost = (double)((units * s + kPlanSms - 1) / kPlanSms) * (4.0 + 1.3 * (double)steps) + (s > 1 ? 5.0 : 0.0);
       if (cost < best * 0.97) {  // fewer splits on near-ties: less partial traffic
         best = cost;
         splits = s;

@@ -31,11 +31,14 @@
 // What bounds it, and what it measured (32/8 heads, D 128, one GB300):
 //   long prompts: the tensor core.  A step of 2 x 128 x 128 takes 2048 cycles of
 //   it, and shared memory is as busy (Q and K of a QK come from it).  One prompt
-//   of 16384 tokens: 1258 us, 1748 TFLOP/s, 0.91 of the measured bf16 burst;
-//   with the exponentials left out 1132 us.
+//   of 16384 tokens: 1320 us on a cold GPU (1666 TFLOP/s, 0.87 of the measured
+//   bf16 burst), 1435 us one after another at the power cap (0.90 of the
+//   sustained rate).  With sums of unrounded weights 1258 us, and of these 126
+//   for the exponentials.
 //   prompts of some 500 tokens: the few steps of an item against its change
 //   (first step, output rows, next Q), about 10 kcycles each way.
-//   single tokens over long prefixes: HBM, 5.6 TB/s on 64 requests.
+//   single tokens over long prefixes: HBM, 5.6 TB/s on 64 requests cold, 5.8 one
+//   after another.
 #include <algorithm>
 
 #include "prompt.cuh"
