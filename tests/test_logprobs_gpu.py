@@ -384,3 +384,23 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for r, o in zip(ref, outs):
         assert all(torch.equal(p, q) for one in o for p, q in zip(r, one))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("V,k,T", [(9013, 2, 300), (9013, 3, 450), (4096, 2, 400), (30000, 2, 150), (9013, 5, 222), (70000, 20, 60)])
+def test_alternatives_while_every_warp_finds_better_ones(V, k, T, dtype):
+    """Rows that rise towards their end, so that the bars move with every entry
+    while other warps read them: the same list in each of many calls."""
+    g = torch.Generator().manual_seed(V + k)
+    ramp = torch.linspace(0, 8, V)[None] + torch.randn((T, V), generator=g) * torch.rand((T, 1), generator=g) * 4
+    ramp[::5] = torch.linspace(0, 8, V)[None]
+    x = ramp.to(dtype).cuda()
+    order = torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :k].to(torch.int32)  # equal ones by lower id
+    tok, off = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    st, out = torch.zeros(1, dtype=torch.int32, device="cuda"), _outputs((T,), k)
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        out[3].fill_(-7)
+        S.spec_token_logprobs(x, tok, off, None, 1, T, V, k, *out, st)
+        wrong += (out[3] != order).any(1).sum()
+    assert st.tolist() == [0] and wrong.item() == 0

@@ -341,9 +341,13 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a,
       if (threadIdx.x == 0) s_n = 0;
       consumers_sync();
       auto cta_bar = [&]() -> float {
-        // lane 8 j + i: is score j, or j + 4, above score i; lane i then counts
-        const volatile int* s = s_mth;
-        const int mine = s[lane & 7], lo = s[lane >> 3], hi = s[(lane >> 3) + 4];
+        // lane 8 j + i: is score j, or j + 4, above score i; lane i then counts.
+        // The other warps raise their scores meanwhile: each is read once (read
+        // again, a score could be above its own earlier value, which then looked
+        // like one rank more and left the bar too high).
+        const int v = *(const volatile int*)&s_mth[lane & 7];
+        const int mine = __shfl_sync(0xffffffffu, v, lane & 7);
+        const int lo = __shfl_sync(0xffffffffu, v, lane >> 3), hi = __shfl_sync(0xffffffffu, v, (lane >> 3) + 4);
         const unsigned col = 0x01010101u << (lane & 7);
         const int above = __popc(__ballot_sync(0xffffffffu, lo > mine) & col) + __popc(__ballot_sync(0xffffffffu, hi > mine) & col);
         return order_float(__reduce_min_sync(0xffffffffu, above < w ? mine : INT_MAX));
