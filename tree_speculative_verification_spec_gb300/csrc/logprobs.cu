@@ -17,7 +17,7 @@
 // copies through a shared-memory ring, so that what is in flight (three CTAs an
 // SM, 64 KB each) does not hang on registers, and runs ahead into the CTA's next
 // row while this one is summed up.  Measured on 2048 rows of 128256 fp32 logits,
-// 30 % of the tokens unlikely ones: 181 us with k = 0 (5.8 TB/s), 231 us with
+// 30 % of the tokens unlikely ones: 181 us with k = 0 (5.8 TB/s), 235 us with
 // k = 20; loads into registers ahead of each batch: 250 us with k = 0.  What
 // bounds it: with k = 0 the memory (half of a stage's 2400 cycles are spent
 // waiting for it); with k = 20 a warp's chain through a batch, some 1100 cycles
