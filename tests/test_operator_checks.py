@@ -132,3 +132,12 @@ def test_page_calls_keep_their_counters_in_32_bits(B, max_blocks, N, code):
     L = S.lib()
     assert L.spec_pages_free(P, B, max_blocks, 16, 8, P, None, N, P, 8, P, P, 8, P, None) == code
     assert L.spec_pages_fork(P, P, 1, P, B, max_blocks, 16, 8, P, P, P, None, N, 2, 64, S.SPEC_BF16, P, 8, P, P, 8, P, None) == code
+
+
+def test_tables_of_cache_addresses_are_checked_before_a_call():
+    import torch
+    from tree_speculative_verification_spec_gb300 import _binding
+    for table, layers in ((torch.zeros(2, dtype=torch.int32), 2), (torch.zeros(2), 2), (torch.zeros(1, dtype=torch.int64), 2)):
+        with pytest.raises(ValueError, match="int64"):
+            _binding._addresses(table, layers)
+    assert _binding._addresses(None, 0) is None
