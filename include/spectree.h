@@ -75,6 +75,7 @@ typedef int32_t spec_status;
 #define SPEC_DEV_BAD_PATH 32  /* a commit path that is not strictly increasing from node 0 */
 #define SPEC_DEV_BAD_TEMP 64  /* stochastic verify: an inverse temperature that is not finite and positive */
 #define SPEC_DEV_BAD_ROW 128 /* page calls: a block-table row out of range, named twice, or not empty where it must be */
+#define SPEC_DEV_BAD_POSITION 256 /* spec_rope_append: a position outside [0, 2^24), or a pair's axis outside [0, axes) */
 
 typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 
@@ -592,6 +593,122 @@ spec_status spec_pages_compact(void* const* k_caches, void* const* v_caches, int
                                int32_t* free_pool, int free_cap, int32_t* free_count, int32_t* page_map,
                                int32_t* moved, void* workspace, size_t workspace_bytes, int32_t* status,
                                void* stream);
+
+/*
+ * Head norms, rotary positions and the append in one pass (the pages take
+ * queries and cache rows as given; this call makes them from a projection's
+ * output).  Row t of qkv holds Hq query, Hkv key and Hkv value heads of D
+ * elements.  Query and key heads are normalised, x w / sqrt(mean(x^2) + eps),
+ * then the first rot_dim elements of a head are turned by pairs:
+ *   (x, y) -> (x cos a - y sin a, y cos a + x sin a),  a = position * inv_freq[i]
+ * for pair i < rot_dim / 2: elements i and i + rot_dim / 2 (SPEC_ROPE_HALVES) or
+ * 2 i and 2 i + 1 (SPEC_ROPE_NEIGHBOURS).  Queries go to q_out, keys and values
+ * to slot prefix_len[b] + u of row u of request b, as spec_kv_append puts them.
+ * fp32 arithmetic, the angle in 64 bits; results are rounded once to dtype,
+ * values are copied bit for bit.
+ * Positions are not slots: a request that lost slots (spec_kv_evict) goes on at
+ * the positions of its text.  Row u of request b has position
+ *   pos_base[b] + (pos ? pos[axis * T + tree_off[b] + u] : u)
+ * on each of `axes` axes (time, height and width of an image, say).  A tree's
+ * nodes: pos = the depth of spec_tree_mask_build, axes = 1.
+ *   qkv      [T] rows of dtype, row_stride elements apart (>= (Hq + 2 Hkv) D), 16-byte
+ *            aligned, as are row_stride in bytes, q_out, the caches and the norms' weights
+ *   q_norm, k_norm  [D] dtype, either may be NULL: those heads are not normalised; eps >= 0
+ *   inv_freq float [rot_dim / 2], finite (radians per position); NULL with rot_dim = 0
+ *   axis     int32 [rot_dim / 2]: the axis of each pair; NULL: axis 0 (axes = 1)
+ *   rot_dim  even, 0 <= rot_dim <= D (0: no rotation, no position is read)
+ *   pos_base int32 [B] or NULL for prefix_len;  pos int32 [axes][T] or NULL (axes = 1)
+ *   axes     1 to 4
+ *   q_out    [T][Hq][D] dtype out; rows outside every request are not written
+ *   k_cache, v_cache, block_table, max_blocks, block_size, num_blocks, prefix_len, tree_off,
+ *   n_max    as for spec_kv_append (packed prompts have no limit of 1024 rows).  The rows of
+ *            requests behind a tree_off that decreases are unspecified
+ *   status   int32 [B] in/out, not read, or-ed with SPEC_DEV_BAD_TREE (n_b outside [0, n_max],
+ *            or rows outside [0, T)), SPEC_DEV_CAPACITY or SPEC_DEV_BAD_BLOCK as for
+ *            spec_kv_append: such a request is left untouched.  SPEC_DEV_BAD_POSITION: the
+ *            rows with such a position are left untouched
+ * Launched as a programmatic dependent of the previous kernel; it waits for that
+ * kernel's results before it reads anything.  One launch.
+ */
+#define SPEC_ROPE_HALVES 0
+#define SPEC_ROPE_NEIGHBOURS 1
+spec_status spec_rope_append(const void* qkv, long long row_stride, const void* q_norm, const void* k_norm, float eps,
+                             const float* inv_freq, const int32_t* axis, int rot_dim, int pairing,
+                             const int32_t* pos_base, const int32_t* pos, int axes, void* q_out, void* k_cache,
+                             void* v_cache, const int32_t* block_table, int max_blocks, int block_size, int num_blocks,
+                             const int32_t* prefix_len, const int32_t* tree_off, int B, int T, int n_max, int Hq,
+                             int Hkv, int D, spec_dtype dtype, int32_t* status, void* stream);
+
+/*
+ * Attention weight gathered by cached slots (no counterpart on the pages): how
+ * much the attention of a layer looked at every slot, per kv-head, the measure
+ * that spec_kv_evict keeps slots by.  For slot s of request b and kv-head h
+ *   weight[b][h][s] = decay * before[b][h][s] + sum softmax_s(scale * q . K)
+ * over the query heads of the group and the counted rows, each row over the
+ * slots it sees.  Slots of the request's own new rows (s >= prefix_len[b]) have
+ * no `before`.  The rows are those of spec_prompt_attention: row i of request b
+ * is the token at slot prefix_len[b] + i and sees slots 0 .. prefix_len[b] + i;
+ * or, with `path` and `accept_len`, the accepted path of a verification AFTER its
+ * commit: token i < accept_len[b] has its queries in row tree_off[b] + path[b][i]
+ * of q and its key in slot prefix_len[b] + i (seq_off = tree_off, prefix_len as
+ * before the commit).  Sums, maxima and weights are fp32; each slot's weight is
+ * summed in a fixed order.
+ *   q        [T][Hq][D] dtype, as the attention call had it; 16-byte aligned, as is k_cache
+ *   k_cache, block_table, max_blocks, block_size, num_blocks, prefix_len, seq_off, B, T, n_max,
+ *   max_prefix  as for spec_prompt_attention
+ *   path     int32 [B][path_stride] and accept_len int32 [B], or both NULL: every row
+ *   window   > 0: only the last `window` rows of a request count; 0: all
+ *   scale, decay  finite and not negative (else SPEC_ERR_INVALID_ARG)
+ *   before   float [B][Hkv][weight_stride], or NULL for zeros;  weight  the same shape, out;
+ *            they may be one buffer.  Only slots [0, prefix_len[b] + rows) are read and
+ *            written.  A request without rows has its weights decayed
+ *   workspace  16-byte aligned device scratch of spec_weight_workspace_size() bytes
+ *   status   int32 [B] in/out: a request that comes in non-zero is left as it was.  Or-ed with
+ *            SPEC_DEV_BAD_TREE, SPEC_DEV_CAPACITY (also prefix_len + rows beyond
+ *            weight_stride), SPEC_DEV_BAD_PATH (accept_len outside [0, min(path_stride, n_b)],
+ *            or a counted path node outside the tree): left as it was;
+ *            SPEC_DEV_BAD_BLOCK and SPEC_DEV_TIMEOUT: its weights are unspecified
+ */
+size_t spec_weight_workspace_size(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int D);
+spec_status spec_attention_weight(const void* q, const void* k_cache, const int32_t* block_table, int max_blocks,
+                                  int block_size, int num_blocks, const int32_t* prefix_len, const int32_t* seq_off,
+                                  const int32_t* path, int path_stride, const int32_t* accept_len, int window, int B,
+                                  int T, int n_max, int max_prefix, int Hq, int Hkv, int D, spec_dtype dtype,
+                                  float scale, float decay, const float* before, float* weight,
+                                  long long weight_stride, void* workspace, size_t workspace_bytes, int32_t* status,
+                                  void* stream);
+
+/*
+ * Eviction by weight (no counterpart on the pages): eviction i copies what row
+ * src[i] of the block table keeps of its len[i] slots to row dst[i], in every
+ * layer.  Each layer and kv-head keeps kept = min(keep[i], len[i]) slots: the
+ * first min(first, kept), the last min(last, kept - first), and, of the slots
+ * between, those of the largest weight (equal weights by lower slot, NaN after
+ * every number, -0 equal to +0).  They keep their order: the j-th kept slot
+ * becomes slot j of dst[i], K, V and weight.  Keys keep the positions they were
+ * rotated by.  Row src[i] stays as it was: shared pages may be evicted from;
+ * spec_pages_free gives the row's pages back.
+ *   k_caches, v_caches, layers  as in spec_pages_fork (layers >= 1)
+ *   block_table int32 [B][max_blocks], read: dst rows have pages of their own for kept slots
+ *            (spec_pages_fork of an empty row with room), which no source row names
+ *   src, dst, len int32 [N];  keep int32 [N] or NULL for keep_max in every row
+ *   keep_max the most slots a row may keep
+ *   weight   float [layers][B][Hkv][weight_stride] by table row, in/out, or NULL: all equal
+ *            (first and last alone then say what stays, as in a sliding window)
+ *   slots    int32 [layers][N][Hkv][keep_max] out: the kept slots of src[i], increasing, then -1
+ *   new_len  int32 [N] out: kept, the length of row dst[i] (0 for a flagged one)
+ *   status   int32 [N] WRITTEN: 0; SPEC_DEV_BAD_ROW (src or dst outside [0, B), src = dst, a dst
+ *            named twice or a src of the call, len < 0, keep outside [0, keep_max]);
+ *            SPEC_DEV_CAPACITY (len beyond the table, weight_stride or 2^30);
+ *            SPEC_DEV_BAD_BLOCK (a page of either row outside [0, num_blocks)).  A flagged
+ *            eviction copies nothing
+ * Two launches, no workspace.
+ */
+spec_status spec_kv_evict(void* const* k_caches, void* const* v_caches, int layers, const int32_t* block_table, int B,
+                          int max_blocks, int block_size, int num_blocks, const int32_t* src, const int32_t* dst,
+                          const int32_t* len, const int32_t* keep, int N, int keep_max, int first, int last,
+                          float* weight, long long weight_stride, int Hkv, int D, spec_dtype dtype, int32_t* slots,
+                          int32_t* new_len, int32_t* status, void* stream);
 
 /*
  * Dynamic draft length ("Hardware-aware dynamic speculative decoding",

@@ -13,8 +13,9 @@ LIB_PATH = os.path.join(_PKG, "libspectree.so")
 
 SPEC_OK, SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA, SPEC_ERR_WORKSPACE = 0, 1, 2, 3, 4
 SPEC_DEV_BAD_TREE, SPEC_DEV_BAD_TOKEN, SPEC_DEV_CAPACITY, SPEC_DEV_TIMEOUT = 1, 2, 4, 8
-SPEC_DEV_BAD_BLOCK, SPEC_DEV_BAD_PATH, SPEC_DEV_BAD_TEMP, SPEC_DEV_BAD_ROW = 16, 32, 64, 128
+SPEC_DEV_BAD_BLOCK, SPEC_DEV_BAD_PATH, SPEC_DEV_BAD_TEMP, SPEC_DEV_BAD_ROW, SPEC_DEV_BAD_POSITION = 16, 32, 64, 128, 256
 SPEC_Q_PER_PARENT, SPEC_Q_PER_CHILD = 0, 1  # layouts of the draft rows
+SPEC_ROPE_HALVES, SPEC_ROPE_NEIGHBOURS = 0, 1  # which elements of a head turn together
 SPEC_F32, SPEC_BF16 = 0, 1
 SPEC_ATTN_AUTO, SPEC_ATTN_CUDA_CORE, SPEC_ATTN_TCGEN05 = 0, 1, 2
 SPEC_ATTN_NOALLOC_BYTES = 16 << 20  # scratch of spec_tree_attention_noalloc
@@ -22,6 +23,7 @@ SPEC_ATTN_NOALLOC_BYTES = 16 << 20  # scratch of spec_tree_attention_noalloc
 # C signatures (argument ctypes, return ctype) of every exported entry point
 _P, _I, _U32, _U64, _SZ, _F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_size_t,
                                ctypes.c_float)
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "spec_version": ([], _I),
     "spec_status_string": ([_I], ctypes.c_char_p),
@@ -57,6 +59,13 @@ SIGNATURES = {
                         _I),
     "spec_pages_free": ([_P, _I, _I, _I, _I, _P, _P, _I, _P, _I, _P, _P, _SZ, _P, _P], _I),
     "spec_pages_compact": ([_P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _SZ, _P, _P], _I),
+    "spec_rope_append": ([_P, _LL, _P, _P, _F, _P, _P, _I, _I, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I,
+                          _I, _I, _I, _I, _P, _P], _I),
+    "spec_weight_workspace_size": ([_I, _I, _I, _I, _I, _I, _I], _SZ),
+    "spec_attention_weight": ([_P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _F, _P,
+                               _P, _LL, _P, _SZ, _P, _P], _I),
+    "spec_kv_evict": ([_P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _LL, _I, _I, _I, _P, _P, _P,
+                       _P], _I),
     "spec_selftest_bounded_wait": ([_P, _U32, _P], _I),
     "spec_selftest_exp": ([_U32, ctypes.c_longlong, _P, _P, _P], _I),
     "spec_selftest_fx": ([_P, ctypes.c_longlong, _I, _P, _P, _P, _P], _I),
@@ -386,6 +395,53 @@ def spec_pages_compact(k_ptrs, v_ptrs, layers, block_table, B, max_blocks, block
         _addresses(k_ptrs, layers), _addresses(v_ptrs, layers), layers, _i32(block_table), B, max_blocks, block_size,
         num_blocks, Hkv, D, dtype, _i32(free_pool), free_pool.numel(), _i32(free_count), _i32(page_map), _i32(moved),
         *_scratch(workspace), _i32(status), _stream_of(block_table, stream)))
+
+
+def spec_rope_append(qkv, q_norm, k_norm, eps, inv_freq, axis, rot_dim, pairing, pos_base, pos, axes, q_out, k_cache,
+                     v_cache, block_table, max_blocks, block_size, num_blocks, prefix_len, tree_off, B, T, n_max, Hq,
+                     Hkv, D, status, stream=None):
+    """qkv: [T][...] CUDA tensor of the caches' dtype whose rows hold Hq + 2 Hkv
+    heads and may lie apart (a slice of a wider projection); q_norm and k_norm:
+    [D] of that dtype or None; inv_freq: float32; axis, pos_base and pos may be
+    None."""
+    if any(t is not None and t.dtype != qkv.dtype for t in (q_norm, k_norm, q_out, k_cache, v_cache)):
+        raise ValueError("qkv, q_out, the norms and the caches must have one dtype")
+    if not qkv.is_cuda or (T > 0 and not qkv[0].is_contiguous()):
+        raise ValueError("qkv must be a CUDA tensor with contiguous rows")
+    _check("spec_rope_append", lib().spec_rope_append(
+        qkv.data_ptr(), qkv.stride(0) if T > 1 else (Hq + 2 * Hkv) * D, _ptr(q_norm), _ptr(k_norm), float(eps), _f32(inv_freq), _i32(axis),
+        rot_dim, pairing, _i32(pos_base), _i32(pos), axes, _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
+        _i32(block_table), max_blocks, block_size, num_blocks, _i32(prefix_len), _i32(tree_off), B, T, n_max, Hq, Hkv,
+        D, _dtype_code(qkv), _i32(status), _stream_of(qkv, stream)))
+
+
+def spec_weight_workspace_size(B, T, n_max, max_prefix, Hq, Hkv, D):
+    return int(lib().spec_weight_workspace_size(B, T, n_max, max_prefix, Hq, Hkv, D))
+
+
+def spec_attention_weight(q, k_cache, block_table, max_blocks, block_size, num_blocks, prefix_len, seq_off, path,
+                          accept_len, window, B, T, n_max, max_prefix, Hq, Hkv, D, scale, decay, before, weight,
+                          weight_stride, workspace, status, stream=None):
+    """path int32 [B][n] and accept_len int32 [B] as a verifier wrote them, or
+    None for every row; before may be None (zeros) or weight itself."""
+    if k_cache.dtype != q.dtype:
+        raise ValueError("q and the cache must have one dtype")
+    _check("spec_attention_weight", lib().spec_attention_weight(
+        _ptr(q), _ptr(k_cache), _i32(block_table), max_blocks, block_size, num_blocks, _i32(prefix_len),
+        _i32(seq_off), _i32(path), 0 if path is None else path.shape[1], _i32(accept_len), window, B, T, n_max,
+        max_prefix, Hq, Hkv, D, _dtype_code(q), float(scale), float(decay), _f32(before), _f32(weight), weight_stride,
+        *_scratch(workspace), _i32(status), _stream_of(q, stream)))
+
+
+def spec_kv_evict(k_ptrs, v_ptrs, layers, block_table, B, max_blocks, block_size, num_blocks, src, dst, length, keep, N,
+                  keep_max, first, last, weight, weight_stride, Hkv, D, dtype, slots, new_len, status, stream=None):
+    """k_ptrs / v_ptrs: int64 device tensors of the layers' cache addresses;
+    keep: int32 [N] or None (keep_max in every row); weight: float32 or None;
+    dtype: SPEC_F32 or SPEC_BF16."""
+    _check("spec_kv_evict", lib().spec_kv_evict(
+        _addresses(k_ptrs, layers), _addresses(v_ptrs, layers), layers, _i32(block_table), B, max_blocks, block_size,
+        num_blocks, _i32(src), _i32(dst), _i32(length), _i32(keep), N, keep_max, first, last, _f32(weight),
+        weight_stride, Hkv, D, dtype, _i32(slots), _i32(new_len), _i32(status), _stream_of(block_table, stream)))
 
 
 def spec_selftest_bounded_wait(status, polls, stream=None):

@@ -1,0 +1,327 @@
+// The attention weight that cached slots gather: host dispatch, and the
+// CUDA-core kernels (fp32; the tensor cores take bf16 alone).
+//
+//   weight[b][h][s] = decay before[b][h][s] + sum over rows softmax(scale q K^T)[row][s]
+//
+// A column sum of a softmax needs every row's maximum and sum first, so there
+// are two passes over the scores: statistics (row tiles against all keys, split
+// over the keys when there are few rows) and sums (key tiles against the rows
+// that see them).  Each slot's weight is one thread's sum in a fixed order: no
+// atomics, the same bits every time.
+#include <algorithm>
+#include <climits>
+
+#include "weight.cuh"
+
+namespace spectree {
+
+constexpr int kWtRows = 64, kWtKeys = 64, kWtThreads = 256, kWtPad = 4;
+
+// Loads a tile of 64 vectors transposed into shared memory as fp32, [D][64 + pad];
+// `row(i)` gives the address of vector i, or NULL for zeros.
+template <typename T, int D, typename F>
+__device__ __forceinline__ void load_tile(float* dst, F row) {
+  constexpr int V = 16 / sizeof(T), C = D / V;
+  for (int j = threadIdx.x; j < 64 * C; j += kWtThreads) {
+    const int i = j / C, c = j % C;
+    const T* p = row(i);
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (p) u = *reinterpret_cast<const uint4*>(p + c * V);
+    const T* x = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int e = 0; e < V; ++e) dst[(c * V + e) * (64 + kWtPad) + i] = to_f32(x[e]);
+  }
+}
+
+// 4 x 4 scores of this thread: rows 4 ty .., keys 4 tx ..
+template <int D>
+__device__ __forceinline__ void scores(const float* q, const float* k, int ty, int tx, float (&s)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+#pragma unroll 4
+  for (int d = 0; d < D; ++d) {
+    const float4 x = *reinterpret_cast<const float4*>(q + d * (64 + kWtPad) + 4 * ty);
+    const float4 y = *reinterpret_cast<const float4*>(k + d * (64 + kWtPad) + 4 * tx);
+    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = fmaf(xs[i], ys[j], s[i][j]);
+  }
+}
+
+// Whether request b counts (the same answer in every thread of the CTA).
+__device__ __forceinline__ bool weight_request_cta(const WeightArgs& a, int b, WeightRequest& r, bool flag) {
+  __shared__ int s_status;
+  const int bad = weight_check(a, b, r);
+  if (threadIdx.x == 0) s_status = *(const volatile int32_t*)&a.status[b];
+  __syncthreads();
+  r.ok = bad == 0 && s_status == 0;
+  int pb = 0;
+  if (r.ok && a.path)
+    for (int i = r.m - r.cnt + threadIdx.x; i < r.m; i += kWtThreads) pb |= weight_path_bad(a, r, i);
+  pb = __syncthreads_or(pb);
+  if (pb) r.ok = false;
+  if (flag && threadIdx.x == 0 && (bad || pb)) atomicOr(&a.status[b], bad ? bad : SPEC_DEV_BAD_PATH);
+  return r.ok;
+}
+
+template <typename T>
+__device__ __forceinline__ const T* key_row(const WeightArgs& a, const int32_t* bt, int kvh, int s, int* bad) {
+  const int blk = bt[s / a.block_size];
+  if (blk < 0 || blk >= a.num_blocks) {
+    *bad = 1;
+    return nullptr;
+  }
+  return static_cast<const T*>(a.k_cache) + (((size_t)blk * a.Hkv + kvh) * a.block_size + s % a.block_size) * a.D;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWtThreads) weight_stats_cc_kernel(const WeightArgs a) {
+  extern __shared__ float sm[];
+  float *sq = sm, *sk = sm + D * (64 + kWtPad);
+  const int kvh = blockIdx.x % a.Hkv, split = blockIdx.x / a.Hkv % a.splits;
+  const long long tile = blockIdx.x / a.Hkv / a.splits;
+  const int b = weight_find(a, tile, kWtRows);
+  WeightRequest r;
+  if (!weight_request_cta(a, b, r, false)) return;
+  const long long at = tile - weight_first_tile(a, b, kWtRows);
+  const int R = r.cnt * a.g;
+  if (at < 0 || at * kWtRows >= R) return;
+  const int r0 = (int)at * kWtRows, first = r.m - r.cnt;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  load_tile<T, D>(sq, [&](int i) -> const T* {
+    if (r0 + i >= R) return nullptr;
+    return static_cast<const T*>(a.q) + ((size_t)weight_q_row(a, r, first + (r0 + i) / a.g) * a.Hq + kvh * a.g + (r0 + i) % a.g) * D;
+  });
+  const int last = first + (min(r0 + kWtRows, R) - 1) / a.g;  // the tile's last token
+  const int begin = split * a.chunk, end = min(begin + a.chunk, r.P + last + 1);
+  const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
+  float m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.0f;
+  int bad = 0;
+  for (int k0 = begin; k0 < end; k0 += kWtKeys) {
+    __syncthreads();
+    load_tile<T, D>(sk, [&](int i) -> const T* { return k0 + i < end ? key_row<T>(a, bt, kvh, k0 + i, &bad) : nullptr; });
+    __syncthreads();
+    float s[4][4];
+    scores<D>(sq, sk, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int seen = r.P + first + (r0 + 4 * ty + i) / a.g;  // the last slot this row sees
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + 4 * tx + j;
+        s[i][j] = k < end && k <= seen ? s[i][j] * a.scale_log2 : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = fmaxf(top, m[i]);
+      if (top == -INFINITY) continue;  // the 16 lanes of a row agree
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum += exp2f(s[i][j] - top);
+      l[i] = l[i] * exp2f(m[i] - top) + sum;
+      m[i] = top;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int o = 8; o; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+    const int row = r0 + 4 * ty + i;
+    if (tx == 0 && row < R)
+      a.ws_ml[(size_t)split * a.T * a.Hq + (size_t)(r.off + first + row / a.g) * a.Hq + kvh * a.g + row % a.g] = make_float2(m[i], l[i]);
+  }
+  if (bad) atomicOr(&a.status[b], SPEC_DEV_BAD_BLOCK);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWtThreads) weight_sums_cc_kernel(const WeightArgs a, int key_tiles) {
+  extern __shared__ float sm[];
+  float *sq = sm, *sk = sm + D * (64 + kWtPad);
+  __shared__ float s_lse[kWtRows], s_part[16][kWtKeys];
+  const int kvh = blockIdx.x % a.Hkv;
+  const int kt = (int)(blockIdx.x / a.Hkv % key_tiles), b = (int)(blockIdx.x / a.Hkv / key_tiles);
+  WeightRequest r;
+  if (!weight_request_cta(a, b, r, kt == 0 && kvh == 0)) return;
+  const int k0 = kt * kWtKeys, total = r.P + r.m;
+  if (k0 >= total) return;
+  const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int first = r.m - r.cnt, R = r.cnt * a.g;
+  // the first counted token that sees the tile's first slot
+  const int tok0 = max(0, k0 - r.P - first);
+  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  int bad = 0;
+  if (tok0 < r.cnt) {
+    load_tile<T, D>(sk, [&](int i) -> const T* { return k0 + i < total ? key_row<T>(a, bt, kvh, k0 + i, &bad) : nullptr; });
+    for (int r0 = tok0 * a.g / kWtRows * kWtRows; r0 < R; r0 += kWtRows) {
+      __syncthreads();
+      load_tile<T, D>(sq, [&](int i) -> const T* {
+        if (r0 + i >= R) return nullptr;
+        return static_cast<const T*>(a.q) + ((size_t)weight_q_row(a, r, first + (r0 + i) / a.g) * a.Hq + kvh * a.g + (r0 + i) % a.g) * D;
+      });
+      for (int i = threadIdx.x; i < kWtRows && r0 + i < R; i += kWtThreads)
+        s_lse[i] = weight_lse(a, (size_t)(r.off + first + (r0 + i) / a.g) * a.Hq + kvh * a.g + (r0 + i) % a.g);
+      __syncthreads();
+      float s[4][4];
+      scores<D>(sq, sk, ty, tx, s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = r0 + 4 * ty + i;
+        if (row >= R) continue;
+        const int seen = r.P + first + row / a.g;
+        const float lse = s_lse[4 * ty + i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k0 + 4 * tx + j <= seen) w[j] += exp2f(s[i][j] * a.scale_log2 - lse);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s_part[ty][4 * tx + j] = w[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kWtKeys; i += kWtThreads) {
+    const int s = k0 + i;
+    if (s >= total) continue;
+    float sum = 0.0f;
+#pragma unroll
+    for (int y = 0; y < 16; ++y) sum += s_part[y][i];
+    const size_t at = ((size_t)b * a.Hkv + kvh) * a.stride + s;
+    a.weight[at] = (a.before && s < r.P ? a.decay * a.before[at] : 0.0f) + sum;
+  }
+  if (bad) atomicOr(&a.status[b], SPEC_DEV_BAD_BLOCK);
+}
+
+template <typename T, int D>
+static cudaError_t launch_cc(const WeightArgs& a, const WeightPlan& p, cudaStream_t stream) {
+  const int dyn = 2 * D * (64 + kWtPad) * (int)sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(weight_stats_cc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(weight_sums_cc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+  if (e != cudaSuccess) return e;
+  if (p.tiles > 0) {
+    weight_stats_cc_kernel<T, D><<<(unsigned)(p.tiles * a.Hkv * p.splits), kWtThreads, dyn, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  const int key_tiles = (a.max_prefix + a.n_max + kWtKeys - 1) / kWtKeys;
+  weight_sums_cc_kernel<T, D><<<(unsigned)((long long)a.B * key_tiles * a.Hkv), kWtThreads, dyn, stream>>>(a, key_tiles);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_weight_cc(const WeightArgs& a, const WeightPlan& p, spec_dtype dtype, cudaStream_t stream) {
+  if (dtype == SPEC_F32) return a.D == 64 ? launch_cc<float, 64>(a, p, stream) : launch_cc<float, 128>(a, p, stream);
+  return a.D == 64 ? launch_cc<__nv_bfloat16, 64>(a, p, stream) : launch_cc<__nv_bfloat16, 128>(a, p, stream);
+}
+
+// Row tiles of M rows, and key splits while they do not fill the GPU.
+static WeightPlan weight_plan(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int window, int M, int* per_req) {
+  const int g = Hq / Hkv;
+  const long long packed = (long long)T * g / M + B;
+  const long long each = ((long long)(window > 0 ? std::min(window, n_max) : n_max) * g + M - 1) / M;
+  WeightPlan p = {};
+  *per_req = each * B < packed ? (int)each : 0;
+  p.tiles = std::min(each * B, packed);
+  const long long keys = (long long)max_prefix + n_max, work = p.tiles * Hkv;
+  const long long want = std::max(1LL, std::min(4LL * 152 / std::max(work, 1LL), (keys + 511) / 512));
+  const long long chunk = ((keys + want - 1) / want + 127) / 128 * 128;
+  p.chunk = (int)std::max(chunk, 128LL);
+  p.splits = (int)std::max(1LL, (keys + p.chunk - 1) / p.chunk);
+  return p;
+}
+
+static spec_status weight_shape_check(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int D, int block_size) {
+  if (B < 0 || T < 0 || n_max < 0 || max_prefix < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return SPEC_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return SPEC_ERR_UNSUPPORTED;
+  if (block_size < 8 || block_size > 65536 || (block_size & (block_size - 1))) return SPEC_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > 65535 || (long long)n_max * (Hq / Hkv) >= (1LL << 30) || (long long)max_prefix + n_max >= (1LL << 30) ||
+      (long long)T * Hq >= (1LL << 31))
+    return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+}  // namespace spectree
+
+using namespace spectree;
+
+extern "C" {
+
+// One (maximum, sum) per row of q and split; a window only lowers the number of
+// splits that are wanted without one, or raises it to what one row tile wants.
+size_t spec_weight_workspace_size(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int D) {
+  if (B <= 0 || T <= 0 || n_max <= 0 || weight_shape_check(B, T, n_max, max_prefix, Hq, Hkv, D, 16) != SPEC_OK) return 256;
+  int per_req = 0;
+  int splits = 1;
+  for (int window : {0, 1})
+    splits = std::max(splits, weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, kWtRows, &per_req).splits);
+  return std::max<size_t>(256, (size_t)splits * T * Hq * sizeof(float2));
+}
+
+spec_status spec_attention_weight(const void* q, const void* k_cache, const int32_t* block_table, int max_blocks,
+                                  int block_size, int num_blocks, const int32_t* prefix_len, const int32_t* seq_off,
+                                  const int32_t* path, int path_stride, const int32_t* accept_len, int window, int B,
+                                  int T, int n_max, int max_prefix, int Hq, int Hkv, int D, spec_dtype dtype,
+                                  float scale, float decay, const float* before, float* weight,
+                                  long long weight_stride, void* workspace, size_t workspace_bytes, int32_t* status,
+                                  void* stream) {
+  SPEC_NVTX_RANGE("spec_attention_weight");
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (!(scale >= 0.0f && scale < INFINITY) || !(decay >= 0.0f && decay < INFINITY)) return SPEC_ERR_INVALID_ARG;
+  if (window < 0 || weight_stride < 0 || (path && path_stride <= 0) || (path == nullptr) != (accept_len == nullptr))
+    return SPEC_ERR_INVALID_ARG;
+  const spec_status sc = weight_shape_check(B, T, n_max, max_prefix, Hq, Hkv, D, block_size);
+  if (sc != SPEC_OK) return sc;
+  if (weight_stride > (1LL << 31)) return SPEC_ERR_UNSUPPORTED;
+  if (B == 0) return SPEC_OK;
+  if (!k_cache || !block_table || !prefix_len || !seq_off || !weight || !status || max_blocks <= 0 || num_blocks <= 0 ||
+      (!q && T > 0))
+    return SPEC_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache)) & 15) != 0) return SPEC_ERR_INVALID_ARG;
+  WeightArgs a = {};
+  const WeightPlan plan = weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, kWtRows, &a.per_req);
+  const long long key_tiles = ((long long)max_prefix + n_max + kWtKeys - 1) / kWtKeys;
+  if (plan.tiles * Hkv * plan.splits > (long long)INT32_MAX || key_tiles * B * Hkv > (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
+  if (key_tiles == 0) return SPEC_OK;
+  const size_t need = (size_t)plan.splits * T * Hq * sizeof(float2);
+  if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15))) return SPEC_ERR_WORKSPACE;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.block_table = block_table;
+  a.prefix_len = prefix_len;
+  a.seq_off = seq_off;
+  a.path = path;
+  a.accept_len = accept_len;
+  a.before = before;
+  a.weight = weight;
+  a.status = status;
+  a.ws_ml = static_cast<float2*>(workspace);
+  a.stride = weight_stride;
+  a.path_stride = path_stride;
+  a.window = window;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.B = B;
+  a.T = T;
+  a.n_max = n_max;
+  a.max_prefix = max_prefix;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.g = Hq / Hkv;
+  a.splits = plan.splits;
+  a.chunk = plan.chunk;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.decay = decay;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (need > 0) spec_workspace_canary(workspace, need, st);
+  return launch_weight_cc(a, plan, dtype, st) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,296 @@
+// Eviction from the paged K/V cache by weight: each layer and kv-head of a row
+// keeps its first slots, its last ones and, of the others, the heaviest, and
+// what is kept is copied in slot order to another row of the block table.
+//
+// Out of place: the row's pages may be shared (a fork's full pages are), and a
+// copy needs no order among the moves.  The old row's pages go back by
+// spec_pages_free, or stay (the whole cache for the target, the short one for a
+// draft).
+//
+// Two kernels.  The selection (a CTA for each layer, row and kv-head) finds the
+// border weight digit by digit, 11, 11 and 10 bits of an order-preserving key
+// with a histogram in shared memory each, then lists the kept slots in one
+// ordered pass; equal weights at the border are taken from the lowest slot.
+// It is bound by the latency of its four passes over the weights (from L2 but
+// for the first).  The copy moves the listed rows of every layer, 16 bytes a
+// lane: HBM.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace spectree {
+
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 2048;
+constexpr int kGatherThreads = 256;
+constexpr int kGatherCtas = 8;      // per SM
+constexpr int kGatherVec = 4;       // 16-byte vectors of K and V per thread and step
+
+struct EvictArgs {
+  char* const* k_caches;
+  char* const* v_caches;
+  const int32_t* table;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* len;
+  const int32_t* keep;
+  float* weight;
+  int32_t* slots;
+  int32_t* new_len;
+  int32_t* status;
+  long long stride;                 // weights of one (layer, row, kv-head)
+  int layers, B, max_blocks, bs_log2, num_blocks, N, keep_max, first, last, Hkv, vec;  // vec: 16-byte vectors of a row
+};
+
+// A key whose order as a whole number is the weights': NaN lowest, -0 as +0.
+__device__ __forceinline__ uint32_t weight_key(float x) {
+  if (x != x) return 0;
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// What row i of the call keeps, or the SPEC_DEV_* bits that stop it (the same in
+// every CTA).
+struct EvictRow {
+  int src, dst, len, kept, first, last, bad;
+};
+__device__ __forceinline__ EvictRow evict_row(const EvictArgs& a, int i) {
+  EvictRow r = {a.src[i], a.dst[i], a.len[i], 0, 0, 0, 0};
+  const int keep = a.keep ? a.keep[i] : a.keep_max;
+  if (r.src < 0 || r.src >= a.B || r.dst < 0 || r.dst >= a.B || r.src == r.dst || r.len < 0 || keep < 0 || keep > a.keep_max)
+    r.bad = SPEC_DEV_BAD_ROW;
+  int other = 0;
+  for (int j = threadIdx.x; j < a.N; j += kSelThreads) other |= (j != i && a.dst[j] == r.dst) || a.src[j] == r.dst;
+  if (__syncthreads_or(other)) r.bad |= SPEC_DEV_BAD_ROW;
+  if (r.bad) return r;
+  r.kept = min(keep, r.len);
+  r.first = min(a.first, r.kept);
+  r.last = min(a.last, r.kept - r.first);
+  if (r.len > (1 << 30) || r.len > (long long)a.max_blocks << a.bs_log2 || (a.weight && r.len > a.stride)) {
+    r.bad = SPEC_DEV_CAPACITY;
+    return r;
+  }
+  int bb = 0;
+  const int32_t *from = a.table + (size_t)r.src * a.max_blocks, *to = a.table + (size_t)r.dst * a.max_blocks;
+  const long long bs = 1LL << a.bs_log2;
+  const int held = (int)((r.len + bs - 1) >> a.bs_log2), need = (int)((r.kept + bs - 1) >> a.bs_log2);
+  for (int j = threadIdx.x; j < held; j += kSelThreads) bb |= from[j] < 0 || from[j] >= a.num_blocks;
+  for (int j = threadIdx.x; j < need; j += kSelThreads) bb |= to[j] < 0 || to[j] >= a.num_blocks;
+  if (__syncthreads_or(bb)) r.bad = SPEC_DEV_BAD_BLOCK;
+  return r;
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+  __shared__ uint32_t hist[kSelBins];
+  __shared__ uint32_t s_warp[kSelWarps];
+  __shared__ uint32_t s_bin, s_left;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int h = blockIdx.x % a.Hkv, i = blockIdx.x / a.Hkv % a.N, layer = blockIdx.x / a.Hkv / a.N;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const EvictRow r = evict_row(a, i);
+  int32_t* out = a.slots + (((size_t)layer * a.N + i) * a.Hkv + h) * a.keep_max;
+  if (layer == 0 && h == 0 && t == 0) {
+    a.status[i] = r.bad;
+    a.new_len[i] = r.bad ? 0 : r.kept;
+  }
+  const int kept = r.bad ? 0 : r.kept;
+  for (int j = kept + t; j < a.keep_max; j += kSelThreads) out[j] = -1;
+  if (kept == 0) return;
+  const float* w = a.weight ? a.weight + (((size_t)layer * a.B + r.src) * a.Hkv + h) * a.stride : nullptr;
+  float* to = a.weight ? a.weight + (((size_t)layer * a.B + r.dst) * a.Hkv + h) * a.stride : nullptr;
+  const int begin = r.first, end = r.len - r.last;  // the slots that compete
+  uint32_t want = kept - r.first - r.last;          // how many of them stay
+  auto key_at = [&](int s) -> uint32_t { return w ? weight_key(w[s]) : 0u; };
+
+  // border: every key above it stays, and `want` of those equal to it
+  uint32_t border = 0, above_all = want >= (uint32_t)(end - begin) ? 1u : 0u;
+  if (!above_all && want > 0) {
+    uint32_t mask = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+      for (int j = t; j < kSelBins; j += kSelThreads) hist[j] = 0;
+      __syncthreads();
+      for (int s = begin + t; s < end; s += kSelThreads) {
+        const uint32_t k = key_at(s);
+        if ((k & mask) == border) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+      }
+      __syncthreads();
+      // the bin where the count from the top reaches `want`: thread t holds bins
+      // 4 t .. 4 t + 3 counted from the top
+      uint32_t c[4], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[e] = hist[kSelBins - 1 - (4 * t + e)];
+        sum += c[e];
+      }
+      uint32_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s_warp[warp] = incl;
+      __syncthreads();
+      uint32_t before = incl - sum;
+      for (int k = 0; k < warp; ++k) before += s_warp[k];
+      if (before < want && want <= before + sum) {
+        uint32_t at = before;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (at < want && want <= at + c[e]) {
+            s_bin = kSelBins - 1 - (4 * t + e);
+            s_left = want - at;
+          }
+          at += c[e];
+        }
+      }
+      __syncthreads();
+      border |= s_bin << shift;
+      want = s_left;
+      mask |= (uint32_t)(bins - 1) << shift;
+    }
+  }
+
+  // the kept slots in order: counts of larger and of equal keys (the equal ones
+  // stay while there is want) go through one scan
+  uint32_t big = 0, equal = 0;  // of the slots before this round
+  for (int s0 = 0; s0 < r.len; s0 += kSelThreads) {
+    const int s = s0 + t;
+    uint32_t g = 0, q = 0;
+    if (s < r.len) {
+      if (s < begin || s >= end || above_all) g = 1;
+      else if (want > 0) {
+        const uint32_t k = key_at(s);
+        g = k > border;
+        q = k == border;
+      }
+    }
+    const uint32_t mg = __ballot_sync(0xffffffffu, g), mq = __ballot_sync(0xffffffffu, q);
+    __syncthreads();  // s_warp of the round before has been read
+    if (lane == 0) s_warp[warp] = __popc(mg) | (uint32_t)__popc(mq) << 16;
+    __syncthreads();
+    uint32_t bg = big, bq = equal;
+    for (int k = 0; k < kSelWarps; ++k) {
+      const uint32_t x = s_warp[k];
+      if (k < warp) bg += x & 0xffffu, bq += x >> 16;
+      big += x & 0xffffu;
+      equal += x >> 16;
+    }
+    const uint32_t lower = (1u << lane) - 1;
+    bg += __popc(mg & lower);
+    bq += __popc(mq & lower);
+    if (g || (q && bq < want)) {
+      const uint32_t at = bg + min(bq, want);
+      out[at] = s;
+      if (to) to[at] = w[s];
+    }
+  }
+}
+
+// Kept row j of (layer, row i, kv-head h), K and V: a unit is a run of rows whose
+// vectors fill the CTA's threads kGatherVec times.
+__global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictArgs a, long long units, int per_head) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int rows = kGatherThreads * kGatherVec / a.vec;  // of a unit
+  for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int part = (int)(unit % per_head);
+    const long long head = unit / per_head;
+    const int h = (int)(head % a.Hkv), i = (int)(head / a.Hkv % a.N), layer = (int)(head / a.Hkv / a.N);
+    const int kept = a.new_len[i], j0 = part * rows;
+    if (j0 >= kept) continue;
+    const int32_t* slots = a.slots + (size_t)head * a.keep_max;
+    const int32_t *from = a.table + (size_t)a.src[i] * a.max_blocks, *to = a.table + (size_t)a.dst[i] * a.max_blocks;
+    uint4 *kc = reinterpret_cast<uint4*>(a.k_caches[layer]), *vc = reinterpret_cast<uint4*>(a.v_caches[layer]);
+    const int within = (1 << a.bs_log2) - 1;
+    uint4 k[kGatherVec], v[kGatherVec];
+    long long put[kGatherVec];
+#pragma unroll
+    for (int e = 0; e < kGatherVec; ++e) {
+      const int x = threadIdx.x + e * kGatherThreads, j = j0 + x / a.vec, c = x % a.vec;
+      put[e] = -1;
+      if (j < kept) {
+        const int s = slots[j];
+        const long long get = ((((long long)from[s >> a.bs_log2] * a.Hkv + h) << a.bs_log2) + (s & within)) * a.vec + c;
+        put[e] = ((((long long)to[j >> a.bs_log2] * a.Hkv + h) << a.bs_log2) + (j & within)) * a.vec + c;
+        k[e] = kc[get];
+        v[e] = vc[get];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kGatherVec; ++e)
+      if (put[e] >= 0) {
+        kc[put[e]] = k[e];
+        vc[put[e]] = v[e];
+      }
+  }
+}
+
+}  // namespace spectree
+
+using namespace spectree;
+
+extern "C" spec_status spec_kv_evict(void* const* k_caches, void* const* v_caches, int layers, const int32_t* block_table,
+                                     int B, int max_blocks, int block_size, int num_blocks, const int32_t* src,
+                                     const int32_t* dst, const int32_t* len, const int32_t* keep, int N, int keep_max,
+                                     int first, int last, float* weight, long long weight_stride, int Hkv, int D,
+                                     spec_dtype dtype, int32_t* slots, int32_t* new_len, int32_t* status, void* stream) {
+  SPEC_NVTX_RANGE("spec_kv_evict");
+  if (layers <= 0 || B < 0 || max_blocks <= 0 || num_blocks <= 0 || N < 0 || keep_max < 0 || first < 0 || last < 0 ||
+      Hkv <= 0 || weight_stride < 0)
+    return SPEC_ERR_INVALID_ARG;
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return SPEC_ERR_UNSUPPORTED;
+  if (block_size < 8 || block_size > 65536 || (block_size & (block_size - 1))) return SPEC_ERR_UNSUPPORTED;
+  const long long heads = (long long)layers * N * Hkv;
+  if (Hkv > 65535 || layers > 32767 || N > 65535 || heads > INT32_MAX || keep_max > (1 << 30) ||
+      weight_stride > (1LL << 31) || (long long)B * max_blocks > (1LL << 40))
+    return SPEC_ERR_UNSUPPORTED;
+  if (N == 0) return SPEC_OK;
+  if (!k_caches || !v_caches || !block_table || !src || !dst || !len || !new_len || !status || (keep_max > 0 && !slots))
+    return SPEC_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  EvictArgs a = {};
+  a.k_caches = (char* const*)k_caches;
+  a.v_caches = (char* const*)v_caches;
+  a.table = block_table;
+  a.src = src;
+  a.dst = dst;
+  a.len = len;
+  a.keep = keep;
+  a.weight = weight;
+  a.slots = slots;
+  a.new_len = new_len;
+  a.status = status;
+  a.stride = weight_stride;
+  a.layers = layers;
+  a.B = B;
+  a.max_blocks = max_blocks;
+  while ((1 << a.bs_log2) < block_size) ++a.bs_log2;
+  a.num_blocks = num_blocks;
+  a.N = N;
+  a.keep_max = keep_max;
+  a.first = first;
+  a.last = last;
+  a.Hkv = Hkv;
+  a.vec = D * (dtype == SPEC_F32 ? 4 : 2) / 16;
+  cudaStream_t st = (cudaStream_t)stream;
+  evict_select_kernel<<<(unsigned)heads, kSelThreads, 0, st>>>(a);
+  SPEC_LAUNCH_CHECK();
+  if (keep_max == 0) return SPEC_OK;
+  const int rows = kGatherThreads * kGatherVec / a.vec, per_head = (keep_max + rows - 1) / rows;
+  const long long units = heads * per_head;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(units, (long long)kGatherCtas * sms), 1, 1);
+  cfg.blockDim = dim3(kGatherThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_gather_kernel, a, units, per_head);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}

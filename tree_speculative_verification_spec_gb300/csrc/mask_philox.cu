@@ -114,6 +114,7 @@ const char* spec_dev_status_string(int32_t bit) {
     case SPEC_DEV_BAD_PATH: return "bad commit path";
     case SPEC_DEV_BAD_TEMP: return "bad inverse temperature";
     case SPEC_DEV_BAD_ROW: return "bad table row";
+    case SPEC_DEV_BAD_POSITION: return "bad position";
     default: break;
   }
   return "unknown status bit";
