@@ -16,6 +16,7 @@
 namespace spectree {
 
 constexpr int kWtRows = 64, kWtKeys = 64, kWtThreads = 256, kWtPad = 4;
+constexpr int kWtTcRows = 256;  // rows per item of the tensor-core kernel
 
 // Loads a tile of 64 vectors transposed into shared memory as fp32, [D][64 + pad];
 // `row(i)` gives the address of vector i, or NULL for zeros.
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kWtThreads) weight_sums_cc_kernel(const Weight
         return static_cast<const T*>(a.q) + ((size_t)weight_q_row(a, r, first + (r0 + i) / a.g) * a.Hq + kvh * a.g + (r0 + i) % a.g) * D;
       });
       for (int i = threadIdx.x; i < kWtRows && r0 + i < R; i += kWtThreads)
-        s_lse[i] = weight_lse(a, (size_t)(r.off + first + (r0 + i) / a.g) * a.Hq + kvh * a.g + (r0 + i) % a.g);
+        s_lse[i] = weight_lse(a, (size_t)(r.off + first + (r0 + i) / a.g) * a.Hq + kvh * a.g + (r0 + i) % a.g, r.P + first + (r0 + i) / a.g + 1);
       __syncthreads();
       float s[4][4];
       scores<D>(sq, sk, ty, tx, s);
@@ -215,12 +216,14 @@ static cudaError_t launch_cc(const WeightArgs& a, const WeightPlan& p, cudaStrea
   return cudaGetLastError();
 }
 
-cudaError_t launch_weight_cc(const WeightArgs& a, const WeightPlan& p, spec_dtype dtype, cudaStream_t stream) {
-  if (dtype == SPEC_F32) return a.D == 64 ? launch_cc<float, 64>(a, p, stream) : launch_cc<float, 128>(a, p, stream);
-  return a.D == 64 ? launch_cc<__nv_bfloat16, 64>(a, p, stream) : launch_cc<__nv_bfloat16, 128>(a, p, stream);
+cudaError_t launch_weight_cc(const WeightArgs& a, const WeightPlan& p, cudaStream_t stream) {
+  return a.D == 64 ? launch_cc<float, 64>(a, p, stream) : launch_cc<float, 128>(a, p, stream);
 }
 
-// Row tiles of M rows, and key splits while they do not fill the GPU.
+constexpr int kWtSms = 152;  // the plan's SM count (part of the workspace query)
+
+// Row tiles of M rows, and key splits for some twelve items per SM, of 512 keys at
+// least.
 static WeightPlan weight_plan(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int window, int M, int* per_req) {
   const int g = Hq / Hkv;
   const long long packed = (long long)T * g / M + B;
@@ -228,10 +231,9 @@ static WeightPlan weight_plan(int B, int T, int n_max, int max_prefix, int Hq, i
   WeightPlan p = {};
   *per_req = each * B < packed ? (int)each : 0;
   p.tiles = std::min(each * B, packed);
-  const long long keys = (long long)max_prefix + n_max, work = p.tiles * Hkv;
-  const long long want = std::max(1LL, std::min(4LL * 152 / std::max(work, 1LL), (keys + 511) / 512));
-  const long long chunk = ((keys + want - 1) / want + 127) / 128 * 128;
-  p.chunk = (int)std::max(chunk, 128LL);
+  const long long keys = (long long)max_prefix + n_max, work = std::max(1LL, p.tiles * Hkv);
+  const long long want = std::max(1LL, std::min(12LL * kWtSms / work, (keys + 511) / 512));
+  p.chunk = (int)std::max(128LL, ((keys + want - 1) / want + 127) / 128 * 128);
   p.splits = (int)std::max(1LL, (keys + p.chunk - 1) / p.chunk);
   return p;
 }
@@ -258,8 +260,8 @@ size_t spec_weight_workspace_size(int B, int T, int n_max, int max_prefix, int H
   if (B <= 0 || T <= 0 || n_max <= 0 || weight_shape_check(B, T, n_max, max_prefix, Hq, Hkv, D, 16) != SPEC_OK) return 256;
   int per_req = 0;
   int splits = 1;
-  for (int window : {0, 1})
-    splits = std::max(splits, weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, kWtRows, &per_req).splits);
+  for (int rows : {kWtRows, kWtTcRows})
+    for (int window : {0, 1}) splits = std::max(splits, weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, rows, &per_req).splits);
   return std::max<size_t>(256, (size_t)splits * T * Hq * sizeof(float2));
 }
 
@@ -284,7 +286,10 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
     return SPEC_ERR_INVALID_ARG;
   if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache)) & 15) != 0) return SPEC_ERR_INVALID_ARG;
   WeightArgs a = {};
-  const WeightPlan plan = weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, kWtRows, &a.per_req);
+  const bool tc = dtype == SPEC_BF16;
+  // the tensor-core path names cache rows by 32-bit coordinates
+  if (tc && (long long)num_blocks * Hkv * block_size >= (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
+  const WeightPlan plan = weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, tc ? kWtTcRows : kWtRows, &a.per_req);
   const long long key_tiles = ((long long)max_prefix + n_max + kWtKeys - 1) / kWtKeys;
   if (plan.tiles * Hkv * plan.splits > (long long)INT32_MAX || key_tiles * B * Hkv > (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
   if (key_tiles == 0) return SPEC_OK;
@@ -321,7 +326,7 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
   a.decay = decay;
   cudaStream_t st = (cudaStream_t)stream;
   if (need > 0) spec_workspace_canary(workspace, need, st);
-  return launch_weight_cc(a, plan, dtype, st) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return (tc ? launch_weight_tc(a, st) : launch_weight_cc(a, plan, st)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // extern "C"

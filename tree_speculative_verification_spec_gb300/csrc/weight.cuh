@@ -21,7 +21,7 @@ struct WeightArgs {
   const float* before;        // NULL: zeros
   float* weight;
   int32_t* status;
-  float2* ws_ml;              // [splits][T * Hq] partial (maximum, sum) in the log2 domain, at q row off + i of token i
+  float2* ws_ml;              // [splits][T * Hq] partial (reference, sum) in the log2 domain, at q row off + i of token i
   long long stride;           // floats of one (request, kv-head) of before and weight
   int path_stride, window;
   int max_blocks, block_size, num_blocks;
@@ -80,11 +80,13 @@ __device__ __forceinline__ int weight_find(const WeightArgs& a, long long tile, 
   return lo;
 }
 
-// (maximum, sum) of a row over every split, as log2 of the whole sum.
-__device__ __forceinline__ float weight_lse(const WeightArgs& a, size_t row) {
+// log2 of a row's whole sum, from (reference, sum) of every split that holds some
+// of the `seen` keys it sees.
+__device__ __forceinline__ float weight_lse(const WeightArgs& a, size_t row, int seen) {
   const size_t rows = (size_t)a.T * a.Hq;
+  const int splits = min(a.splits, (seen - 1) / a.chunk + 1);
   float m = -INFINITY, l = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
+  for (int s = 0; s < splits; ++s) {
     const float2 x = a.ws_ml[s * rows + row];
     if (x.y > 0.0f) {
       const float top = fmaxf(m, x.x);
@@ -100,6 +102,7 @@ struct WeightPlan {
   long long tiles;  // row tiles, before heads and splits
 };
 
-cudaError_t launch_weight_cc(const WeightArgs& a, const WeightPlan& p, spec_dtype dtype, cudaStream_t stream);
+cudaError_t launch_weight_tc(const WeightArgs& a, cudaStream_t stream);
+cudaError_t launch_weight_cc(const WeightArgs& a, const WeightPlan& p, cudaStream_t stream);
 
 }  // namespace spectree

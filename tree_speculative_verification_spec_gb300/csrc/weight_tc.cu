@@ -1,0 +1,674 @@
+// Attention weight of cached slots on the 5th-generation tensor cores (tcgen05),
+// bf16 inputs, fp32 scores in tensor memory, never in global memory.
+//
+// Three forms of one kernel.  A CTA keeps up to two 128-row tiles in shared
+// memory (resident) and walks a stream of 128-row tiles; each tcgen05.mma gives
+// 128 x 128 scores, a thread of the epilogue owns one TMEM lane and reduces over
+// its columns alone, so no reduction crosses lanes:
+//   statistics      lanes = rows: resident Q (256 rows), stream K.  A row's
+//                   reference and sum of 2^(x - reference).
+//   sums, few rows  lanes = keys: resident Q (all rows, at most 256), stream K.
+//                   A key's weight is done after its tile: sum over the columns
+//                   (rows) of 2^(x - log2 of the row's sum).
+//   sums, many      lanes = keys: resident K (256 keys), stream Q.  The weight
+//                   stays in a register over every row tile that sees the keys.
+// Each of the two epilogue warpgroups has two score buffers of its own, so the
+// tensor core works on the next scores while it reduces.
+//
+// The reference of a row starts at 0 and is not a maximum: 2^(x - m) and its
+// fp32 sum hold any m within 2^60 of the scores; a chunk whose sum leaves that
+// range is done again against its own maximum, and the sum is scaled to it.
+//
+// Items (row tiles or key tiles of one request and kv-head) are numbered over
+// the batch by a prefix sum that each CTA takes of its own, 256 requests at a
+// time, and dealt out round-robin, the longest of a request first.
+#include <algorithm>
+
+#include "tcgen05.cuh"
+#include "weight.cuh"
+
+namespace spectree {
+
+namespace wtc {
+
+using namespace tc5;
+
+constexpr int BM = 128;
+constexpr int kThreads = 384;        // warps: 0 stream, 1 MMA, 2 resident tiles, 3 spare, 4-7 and 8-11 epilogue
+constexpr uint32_t kTmemCols = 512;  // score buffers: 2 per warpgroup, 128 columns each
+constexpr int kGroup = 256;          // requests numbered at a time
+constexpr float kSumTop = 0x1p60f;
+enum Mode { kStats = 0, kSumsFew = 1, kSumsMany = 2 };
+
+template <int D> struct Layout {
+  static constexpr int DH = D / 64;             // 128-byte halves of a row
+  static constexpr int NST = D == 128 ? 4 : 6;  // stages of the stream
+  static constexpr uint32_t kTile = BM * D * 2;
+  static constexpr uint32_t kOffRing = 2 * kTile;
+  static constexpr uint32_t kBytes = kOffRing + NST * kTile;
+  static constexpr uint32_t kDyn = kBytes + 1024 < 120 * 1024 ? 120 * 1024 : kBytes + 1024;  // one CTA per SM (all of TMEM)
+  static_assert(kDyn + 16384 <= 227 * 1024, "dynamic and static shared memory within 227 KB");
+};
+
+struct Params {
+  WeightArgs a;
+  long long rows_total;  // num_blocks * Hkv * block_size: rows of the 2-D cache view
+  int box_rows;          // rows per TMA box: min(block_size, 128)
+  int bs_log2;
+  int q_tma;             // Q by TMA (packed rows, g divides 128), else by cp.async
+  int key_chunk;         // keys per item of the sums over few rows
+};
+
+struct Request {
+  int off, first, cnt, P, m;  // first counted token, counted tokens, prefix, tokens in all
+};
+struct Table {
+  Request r[kGroup];
+  int first[kGroup + 1];      // item tiles before each request
+};
+
+struct Item {
+  Request q;
+  int b, kvh, r0, k0, steps, split;
+  int lo[2], hi[2];  // steps in which tile t has a job (statistics, sums over many rows)
+  int rt;            // row tiles (sums over few rows)
+};
+
+// Tiles of request r in this form of the kernel.
+template <int MODE>
+__device__ __forceinline__ int request_tiles(const Params& prm, const Request& r) {
+  const WeightArgs& a = prm.a;
+  const int R = r.cnt * a.g, total = r.P + r.m;
+  if (MODE == kStats) return (R + 2 * BM - 1) / (2 * BM);
+  const bool few = R <= 2 * BM;
+  if (MODE == kSumsFew) return few ? (total + prm.key_chunk - 1) / prm.key_chunk : 0;
+  return few ? 0 : (total + 2 * BM - 1) / (2 * BM);
+}
+
+// Requests b0 .. of the group with their tiles, by every thread of the CTA.
+// Returns the group's tiles.
+template <int MODE>
+__device__ __forceinline__ int build_table(const Params& prm, Table& tab, int b0, int* scan) {
+  const WeightArgs& a = prm.a;
+  const int c = threadIdx.x, b = b0 + c;
+  int tiles = 0;
+  if (c < kGroup) {
+    Request q = {};
+    if (b < a.B) {
+      WeightRequest r;
+      int bad = weight_check(a, b, r);
+      const int came = *(const volatile int32_t*)&a.status[b];
+      if (!bad && !came && a.path)
+        for (int i = r.m - r.cnt; i < r.m; ++i) bad |= weight_path_bad(a, r, i) ? SPEC_DEV_BAD_PATH : 0;
+      if (bad && blockIdx.x == 0) atomicOr(&a.status[b], bad);
+      q = {r.off, r.m - r.cnt, r.cnt, r.P, r.m};
+      if (!bad && !came) tiles = request_tiles<MODE>(prm, q);
+    }
+    tab.r[c] = q;
+  }
+  // inclusive scan over the group
+  const int lane = c & 31, w = c >> 5;
+  int incl = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scan[w] = incl;
+  __syncthreads();
+  int before = 0;
+  for (int k = 0; k < w; ++k) before += scan[k];
+  if (c < kGroup) tab.first[c + 1] = before + incl;
+  if (c == 0) tab.first[0] = 0;
+  __syncthreads();
+  return tab.first[kGroup];
+}
+
+// Item `idx` of the group (a whole warp).
+template <int MODE>
+__device__ __forceinline__ Item find_item(const Params& prm, const Table& tab, int b0, int idx, int lane) {
+  const WeightArgs& a = prm.a;
+  Item w = {};
+  if (MODE == kStats) {
+    w.split = idx % a.splits;
+    idx /= a.splits;
+  }
+  w.kvh = idx % a.Hkv;
+  const int tile = idx / a.Hkv;
+  int cnt = 0;  // requests whose first tile is not above this one
+#pragma unroll
+  for (int r = lane; r < kGroup; r += 32) cnt += tab.first[r] <= tile;
+  const int r = warp_sum_i(cnt) - 1;
+  w.b = b0 + r;
+  w.q = tab.r[r];
+  const int at = tile - tab.first[r], R = w.q.cnt * a.g, total = w.q.P + w.q.m;
+  if (MODE == kStats) {
+    w.r0 = (tab.first[r + 1] - 1 - tile) * (2 * BM);  // the last rows see the most keys: first
+    w.k0 = w.split * a.chunk;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int row = w.r0 + t * BM;
+      if (row >= R) continue;
+      const int end = min(w.q.P + w.q.first + (min(row + BM, R) - 1) / a.g + 1, w.k0 + a.chunk);
+      if (end > w.k0) w.hi[t] = (end - w.k0 + BM - 1) / BM;
+    }
+    w.steps = max(w.hi[0], w.hi[1]);
+  } else if (MODE == kSumsFew) {
+    w.k0 = at * prm.key_chunk;
+    w.steps = (min(prm.key_chunk, total - w.k0) + BM - 1) / BM;
+    w.rt = (R + BM - 1) / BM;
+  } else {
+    w.k0 = at * (2 * BM);
+    const int tok = max(0, w.k0 - w.q.P - w.q.first);  // the first counted token that sees the first key
+    w.r0 = tok * a.g / BM * BM;
+    w.steps = tok < w.q.cnt ? (R - w.r0 + BM - 1) / BM : 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int need = max(0, w.k0 + t * BM - w.q.P - w.q.first);
+      if (w.k0 + t * BM < total && need < w.q.cnt) {
+        w.lo[t] = (need * a.g - w.r0) / BM;
+        w.hi[t] = w.steps;
+      }
+    }
+  }
+  return w;
+}
+
+// Row of the 2-D cache view of the box that starts at key k; keys behind the
+// request, or at a bad block id, read the out-of-range row `rows_total` (zeros).
+__device__ __forceinline__ int box_row(const Params& prm, const int32_t* bt, int kvh, int k, int end, int* bad) {
+  const WeightArgs& a = prm.a;
+  int y = (int)prm.rows_total;
+  if (k < end) {
+    const int blk = __ldg(bt + (k >> prm.bs_log2));
+    if (blk >= 0 && blk < a.num_blocks) y = ((blk * a.Hkv + kvh) << prm.bs_log2) + (k & (a.block_size - 1));
+    else *bad = 1;
+  }
+  return y;
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    weight_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_q,
+                     const __grid_constant__ Params prm) {
+  using L = Layout<D>;
+  constexpr int NST = L::NST;
+  const WeightArgs& a = prm.a;
+  extern __shared__ uint8_t dyn_raw[];
+  __shared__ uint64_t full[NST], empty[NST], res_full, res_empty, s_full[2][2], s_empty[2][2], drain;
+  __shared__ Table tab;
+  __shared__ __align__(16) float s_lse[2][2 * BM];  // minus log2 of the rows' sums
+  __shared__ __align__(16) int s_lim[2][2 * BM];    // the last slot that each row sees, -1: no row
+  __shared__ int scan[kThreads / 32], abort_flag, issued[NST], res_issued;
+  __shared__ uint32_t tmem_slot;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+      issued[i] = -1;
+    }
+    mbar_init(&res_full, 1);
+    mbar_init(&res_empty, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i >> 1][i & 1], 1);
+      mbar_init(&s_empty[i >> 1][i & 1], 4);
+    }
+    mbar_init(&drain, 1);
+    abort_flag = 0;
+    res_issued = -1;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  // A wait that runs out sets the abort flag; every later wait then ends after a
+  // few polls, and the items run to their ends on whatever they find (every
+  // request is flagged, its weights are unspecified).
+  auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, &abort_flag); };
+
+  // 128 keys from k of an item's kv-head into a tile, by boxes of up to a page.
+  auto load_keys = [&](const Item& w, int k, uint32_t dst, uint64_t* bar, int* bad) {
+    const int br = prm.box_rows, nb = BM / br;
+    const int32_t* bt = a.block_table + (size_t)w.b * a.max_blocks;
+    if (lane < nb) {
+      const int y = box_row(prm, bt, w.kvh, k + lane * br, w.q.P + w.q.m, bad);
+#pragma unroll
+      for (int h = 0; h < L::DH; ++h) tma_load_2d(dst + h * (BM * 128) + lane * br * 128, &tmap_k, h * 64, y, bar);
+    }
+  };
+  // Rows r .. r + 127 of an item (row = (counted token, head of the group)); rows
+  // behind its last are whatever lies there, or zeros.  True: `bar` still has to
+  // be arrived on.
+  auto load_rows = [&](const Item& w, int r, uint32_t dst, uint64_t* bar) -> bool {
+    if (prm.q_tma) {
+      if (lane == 0)
+#pragma unroll
+        for (int h = 0; h < L::DH; ++h)
+          tma_load_3d(dst + h * (BM * 128), &tmap_q, h * 64, w.kvh * a.g, w.q.off + w.q.first + r / a.g, bar);
+      return false;
+    }
+    constexpr int CPR = D / 8;      // 16-byte chunks per row
+    constexpr int STEP = 32 / CPR;  // rows per round
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+    const int ch = lane % CPR, R = w.q.cnt * a.g;
+    const int32_t* path = a.path ? a.path + (size_t)w.b * a.path_stride + w.q.first : nullptr;
+    for (int i = lane / CPR; i < BM; i += STEP) {
+      const uint32_t at = dst + (ch >> 3) * (BM * 128) + i * 128 + (((ch & 7) ^ (i & 7)) << 4);
+      if (r + i < R) {
+        const int tok = (r + i) / a.g, head = (r + i) % a.g;
+        const size_t row = w.q.off + (path ? path[tok] : w.q.first + tok);
+        cp_async16(at, q + (row * a.Hq + w.kvh * a.g + head) * D + ch * 8);
+      } else {
+        *reinterpret_cast<uint4*>(smem + (at - sbase)) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    return true;
+  };
+  auto copies_done = [&](uint64_t* bar) {
+    cp_async_wait();
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+
+  int items = 0;                        // with steps, of this CTA so far
+  int ld = 0;                           // stream tiles so far
+  int jobs[2] = {0, 0};                 // score tiles of each warpgroup so far (MMA warp)
+  int c = 0;                            // score tiles of this warpgroup so far (epilogue)
+  bool dead = false;                    // a producer that gave up
+  for (int b0 = 0; b0 < a.B; b0 += kGroup) {
+    const int tiles = build_table<MODE>(prm, tab, b0, scan);
+    const int n_items = tiles * a.Hkv * (MODE == kStats ? a.splits : 1);
+    if (warp == 0) {
+      // ---------------------------------------------------------- stream
+      for (int idx = blockIdx.x; idx < n_items && !dead; idx += gridDim.x) {
+        const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
+        if (MODE == kSumsFew && w.rt == 0) continue;
+        int bad = 0;
+        for (int j = 0; j < w.steps; ++j, ++ld) {
+          const int st = ld % NST;
+          bool go = true;
+          if (lane == 0 && ld >= NST) go = wait(&empty[st], ld / NST - 1);
+          dead = !__shfl_sync(0xffffffffu, (int)go, 0);
+          if (dead) break;
+          const uint32_t dst = sbase + L::kOffRing + st * L::kTile;
+          if (lane == 0) issued[st] = ld;
+          if (MODE == kSumsMany) {
+            if (lane == 0 && prm.q_tma) mbar_expect_tx(&full[st], L::kTile);
+            __syncwarp();
+            if (load_rows(w, w.r0 + j * BM, dst, &full[st])) copies_done(&full[st]);
+          } else {
+            if (lane == 0) mbar_expect_tx(&full[st], L::kTile);
+            __syncwarp();
+            load_keys(w, w.k0 + j * BM, dst, &full[st], &bad);
+          }
+        }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
+      }
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- resident tiles
+      for (int idx = blockIdx.x; idx < n_items && !dead; idx += gridDim.x) {
+        const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
+        if (w.steps == 0 || (MODE == kSumsFew && w.rt == 0)) continue;
+        bool go = true;
+        if (lane == 0 && items > 0) go = wait(&res_empty, items - 1);
+        dead = !__shfl_sync(0xffffffffu, (int)go, 0);
+        if (dead) break;
+        if (lane == 0) res_issued = items;
+        ++items;
+        const int n = MODE == kSumsFew ? w.rt : w.hi[1] > 0 ? 2 : 1;
+        if (MODE == kSumsMany) {
+          int bad = 0;
+          if (lane == 0) mbar_expect_tx(&res_full, n * L::kTile);
+          __syncwarp();
+          for (int t = 0; t < n; ++t) load_keys(w, w.k0 + t * BM, sbase + t * L::kTile, &res_full, &bad);
+          if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
+        } else {
+          if (lane == 0 && prm.q_tma) mbar_expect_tx(&res_full, n * L::kTile);
+          __syncwarp();
+          bool arrive = false;
+          for (int t = 0; t < n; ++t) arrive = load_rows(w, w.r0 + t * BM, sbase + t * L::kTile, &res_full);
+          if (arrive) copies_done(&res_full);
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA
+      const uint64_t res = smem_desc_sw128(sbase, 16, 1024), ring = smem_desc_sw128(sbase + L::kOffRing, 16, 1024);
+      const bool leader = elect_one();
+      for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
+        const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
+        if (w.steps == 0 || (MODE == kSumsFew && w.rt == 0)) continue;
+        const int R = w.q.cnt * a.g;
+        wait(&res_full, items);
+        ++items;
+        for (int j = 0; j < w.steps; ++j, ++ld) {
+          const int st = ld % NST;
+          wait(&full[st], ld / NST);
+          const uint64_t sd = ring + (uint64_t)(st * (L::kTile >> 4));
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (MODE == kSumsFew ? t >= w.rt : j < w.lo[t] || j >= w.hi[t]) continue;
+            const int g = MODE == kSumsFew ? j & 1 : t;
+            const int c = g ? jobs[1]++ : jobs[0]++;  // this warpgroup's
+            if (c >= 2) wait(&s_empty[g][c & 1], (c >> 1) - 1);
+            tc_fence_after();
+            const uint64_t rd = res + (uint64_t)(t * (L::kTile >> 4));
+            const uint32_t d = tmem + (g * 2 + (c & 1)) * BM;
+            // few rows: only the columns that hold some, 32 at a time
+            const uint32_t n = MODE == kSumsFew ? min(BM, (R - t * BM + 31) / 32 * 32) : BM;
+            const uint32_t idesc = idesc_bf16(BM, 0) & ~(0x3fu << 17) | (n >> 3) << 17;
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+                umma_bf16(d, (MODE == kSumsFew ? sd : rd) + o, (MODE == kSumsFew ? rd : sd) + o, idesc, kk > 0 ? 1u : 0u);
+              }
+              umma_commit(&s_full[g][c & 1]);
+            }
+            __syncwarp();
+          }
+          if (leader) umma_commit(&empty[st]);
+          __syncwarp();
+        }
+        if (leader) umma_commit(&res_empty);
+        __syncwarp();
+      }
+    } else if (warp >= 4) {
+      // ---------------------------------------------------------- epilogue
+      const int g = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;  // warpgroup, TMEM lane
+      const uint32_t tS = tmem + g * 2 * BM + ((uint32_t)(quad * 32) << 16);
+      const float c2 = a.scale_log2;
+      const float2 c22 = make_float2(c2, c2);
+      auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory"); };
+      auto release = [&]() {  // this warp has read the score buffer
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[g][c & 1]);
+      };
+      // row's entry of s_lse and s_lim
+      auto row_entry = [&](const Item& w, int row, float& nl, int& lim) {
+        nl = -INFINITY;
+        lim = -1;
+        if (row < w.q.cnt * a.g) {
+          const int tok = w.q.first + row / a.g;
+          lim = w.q.P + tok;
+          nl = -weight_lse(a, (size_t)(w.q.off + tok) * a.Hq + w.kvh * a.g + row % a.g, lim + 1);
+        }
+      };
+      // sum over 32 columns of 2^(x c + nl), the columns that see `key` alone where
+      // `masked`
+      auto column_sum = [&](const uint32_t (&x)[32], const float* nl, const int* lim, bool masked, int key, float2& acc) {
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float p0 = fast_exp2(fmaf(__uint_as_float(x[e]), c2, nl[e])), p1 = fast_exp2(fmaf(__uint_as_float(x[e + 1]), c2, nl[e + 1]));
+            acc.x += key <= lim[e] ? p0 : 0.0f;
+            acc.y += key <= lim[e + 1] ? p1 : 0.0f;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 n4 = *reinterpret_cast<const float4*>(nl + e);
+            const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c22, make_float2(n4.x, n4.y));
+            const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), c22, make_float2(n4.z, n4.w));
+            acc = __fadd2_rn(acc, make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
+            acc = __fadd2_rn(acc, make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
+          }
+        }
+      };
+      auto put = [&](const Item& w, int key, float sum) {
+        if (key >= w.q.P + w.q.m) return;
+        const size_t at = ((size_t)w.b * a.Hkv + w.kvh) * a.stride + key;
+        a.weight[at] = (a.before && key < w.q.P ? a.decay * a.before[at] : 0.0f) + sum;
+      };
+
+      for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
+        const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
+        const int R = w.q.cnt * a.g, lo = g ? w.lo[1] : w.lo[0], hi = g ? w.hi[1] : w.hi[0];
+        if (MODE == kStats) {
+          if (hi == 0) continue;
+          const int row = w.r0 + g * BM + r;
+          const bool valid = row < R;
+          const int tok = w.q.first + (valid ? row / a.g : w.q.cnt - 1);
+          const int lim = w.q.P + tok + 1 - w.k0;  // visible keys of this range
+          float m = 0.0f, l = 0.0f;
+          auto weights = [&](uint32_t (&x)[32], int vis) -> float {
+            if (!__all_sync(0xffffffffu, vis >= 32)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e >= vis) x[e] = 0xff800000u;
+            }
+            const float2 neg = make_float2(-m, -m);
+            float2 a0 = make_float2(0.0f, 0.0f), a1 = a0;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c22, neg);
+              const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), c22, neg);
+              a0 = __fadd2_rn(a0, make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
+              a1 = __fadd2_rn(a1, make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
+            }
+            return (a0.x + a0.y) + (a1.x + a1.y);
+          };
+          auto chunk = [&](uint32_t (&x)[32], int vis) {
+            float sum = weights(x, vis);
+            const bool unfit = valid && (sum >= kSumTop || (l == 0.0f && vis > 0 && sum < 1.0f / kSumTop));
+            if (__any_sync(0xffffffffu, unfit)) {  // against the chunk's maximum
+              float mx = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));  // hidden ones are -inf
+              mx *= c2;
+              if (l == 0.0f) {
+                if (mx > -INFINITY) m = mx;
+              } else if (mx > m) {
+                l *= fast_exp2(m - mx);
+                m = mx;
+              }
+              sum = weights(x, vis);
+            }
+            l += sum;
+          };
+          const bool idle = !__any_sync(0xffffffffu, valid);  // a warp without rows only passes the buffers on
+          for (int j = 0; j < hi; ++j, ++c) {
+            wait(&s_full[g][c & 1], c >> 1);
+            tc_fence_after();
+            if (!idle) {
+              const int vis = lim - j * BM;
+              const uint32_t t0 = tS + (c & 1) * BM;
+              uint32_t x[32], y[32];
+              tmem_ld32(t0, x);
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                tmem_wait_ld(x);
+                tmem_ld32(t0 + h * 64 + 32, y);
+                chunk(x, vis - h * 64);
+                tmem_wait_ld(y);
+                if (h == 0) tmem_ld32(t0 + 64, x);
+                chunk(y, vis - h * 64 - 32);
+              }
+            }
+            release();
+          }
+          if (valid)
+            a.ws_ml[(size_t)w.split * a.T * a.Hq + (size_t)(w.q.off + tok) * a.Hq + w.kvh * a.g + row % a.g] = make_float2(m, l);
+        } else if (MODE == kSumsFew) {
+          if (w.rt == 0) {  // no rows: the old weights alone
+            for (int j = g; j < w.steps; j += 2) put(w, w.k0 + j * BM + r, 0.0f);
+            continue;
+          }
+          float nl[2];
+          int lim[2];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) row_entry(w, t * BM + r, nl[t], lim[t]);
+          group_sync();  // the item before has been read
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            s_lse[g][t * BM + r] = nl[t];
+            s_lim[g][t * BM + r] = lim[t];
+          }
+          group_sync();
+          for (int j = g; j < w.steps; j += 2) {
+            const int k0 = w.k0 + j * BM, key = k0 + r;
+            float2 acc = make_float2(0.0f, 0.0f);
+            for (int t = 0; t < w.rt; ++t, ++c) {
+              wait(&s_full[g][c & 1], c >> 1);
+              tc_fence_after();
+              const int cols = min(BM, R - t * BM);
+              // rows that do not see the tile's last key, or columns without a row
+              const bool masked = k0 + BM - 1 > w.q.P + w.q.first || (cols & 31) != 0;
+              const uint32_t t0 = tS + (c & 1) * BM;
+#pragma unroll 1
+              for (int e = 0; e < cols; e += 32) {
+                uint32_t x[32];
+                tmem_ld32(t0 + e, x);
+                tmem_wait_ld(x);
+                column_sum(x, &s_lse[g][t * BM + e], &s_lim[g][t * BM + e], masked, key, acc);
+              }
+              release();
+            }
+            put(w, key, acc.x + acc.y);
+          }
+        } else {
+          const int k0 = w.k0 + g * BM, key = k0 + r;
+          float2 acc = make_float2(0.0f, 0.0f);
+          float nl;
+          int lim;
+          if (lo < hi) row_entry(w, w.r0 + lo * BM + r, nl, lim);
+          for (int j = lo; j < hi; ++j, ++c) {
+            const int row0 = w.r0 + j * BM, half = (c & 1) * BM;
+            s_lse[g][half + r] = nl;  // its last reader was two jobs ago, behind a group_sync
+            s_lim[g][half + r] = lim;
+            group_sync();
+            if (j + 1 < hi) row_entry(w, row0 + BM + r, nl, lim);
+            wait(&s_full[g][c & 1], c >> 1);
+            tc_fence_after();
+            const bool masked = k0 + BM - 1 > w.q.P + w.q.first + row0 / a.g || row0 + BM > R;
+            const uint32_t t0 = tS + (c & 1) * BM;
+            uint32_t x[32], y[32];
+            tmem_ld32(t0, x);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              tmem_wait_ld(x);
+              tmem_ld32(t0 + h * 64 + 32, y);
+              column_sum(x, &s_lse[g][half + h * 64], &s_lim[g][half + h * 64], masked, key, acc);
+              tmem_wait_ld(y);
+              if (h == 0) tmem_ld32(t0 + 64, x);
+              column_sum(y, &s_lse[g][half + h * 64 + 32], &s_lim[g][half + h * 64 + 32], masked, key, acc);
+            }
+            release();
+          }
+          put(w, key, acc.x + acc.y);
+        }
+      }
+    }
+    __syncthreads();  // the table has been read
+  }
+
+  if (warp == 1 && elect_one()) {  // every MMA has completed before TMEM is freed
+    umma_commit(&drain);
+    mbar_drain(&drain, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (abort_flag) {
+    if (threadIdx.x == 0) {  // copies in flight land before the CTA exits
+      for (int st = 0; st < NST; ++st)
+        if (issued[st] >= 0) mbar_drain(&full[st], (issued[st] / NST) & 1);
+      if (res_issued >= 0) mbar_drain(&res_full, res_issued & 1);
+    }
+    for (int b = threadIdx.x; b < a.B; b += kThreads) atomicOr(&a.status[b], SPEC_DEV_TIMEOUT);
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+static bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                     const cuuint32_t* box) {
+  const EncodeFn enc = encode_fn();
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int MODE>
+static cudaError_t launch_mode(const CUtensorMap& mk, const CUtensorMap& mq, const Params& prm, int sms, cudaStream_t stream) {
+  const int dyn = (int)Layout<D>::kDyn;
+  const cudaError_t e = cudaFuncSetAttribute(weight_tc_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+  if (e != cudaSuccess) return e;
+  weight_tc_kernel<D, MODE><<<sms, kThreads, dyn, stream>>>(mk, mq, prm);
+  return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  Params prm = {};
+  prm.a = a;
+  prm.box_rows = std::min(a.block_size, BM);
+  while ((1 << prm.bs_log2) < a.block_size) ++prm.bs_log2;
+  prm.rows_total = (long long)a.num_blocks * a.Hkv * a.block_size;
+  prm.q_tma = !a.path && BM % a.g == 0 && a.T > 0;
+  // sums over few rows: some eight items for every CTA, of 256 keys at least
+  const long long keys = ((long long)a.max_prefix + a.n_max) * a.B * a.Hkv / (8LL * sms);
+  prm.key_chunk = (int)std::min(4096LL, std::max(256LL, (keys + 255) / 256 * 256));
+  alignas(64) CUtensorMap mk, mq;
+  {
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)prm.rows_total}, strides[1] = {(cuuint64_t)D * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)prm.box_rows};
+    if (!make_map(&mk, a.k_cache, 2, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  if (prm.q_tma) {  // Q [T][Hq][D] as (columns, heads, tokens)
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.Hq * D * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.g, (cuuint32_t)(BM / a.g)};
+    if (!make_map(&mq, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  } else {
+    mq = mk;  // not read
+  }
+  const long long rows = (long long)(a.window > 0 ? std::min(a.window, a.n_max) : a.n_max) * a.g;  // the most that a request has
+  if (rows > 0) e = launch_mode<D, kStats>(mk, mq, prm, sms, stream);
+  if (e == cudaSuccess) e = launch_mode<D, kSumsFew>(mk, mq, prm, sms, stream);
+  if (e == cudaSuccess && rows > 2 * BM) e = launch_mode<D, kSumsMany>(mk, mq, prm, sms, stream);
+  return e;
+}
+
+}  // namespace wtc
+
+cudaError_t launch_weight_tc(const WeightArgs& a, cudaStream_t stream) {
+  return a.D == 64 ? wtc::launch_d<64>(a, stream) : wtc::launch_d<128>(a, stream);
+}
+
+}  // namespace spectree
