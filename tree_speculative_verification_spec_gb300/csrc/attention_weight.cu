@@ -17,6 +17,7 @@ namespace spectree {
 
 constexpr int kWtRows = 64, kWtKeys = 64, kWtThreads = 256, kWtPad = 4;
 constexpr int kWtTcRows = 256;  // rows per item of the tensor-core kernel
+constexpr int kWtParts = 2;     // partial sums it leaves of a row and split
 
 // Loads a tile of 64 vectors transposed into shared memory as fp32, [D][64 + pad];
 // `row(i)` gives the address of vector i, or NULL for zeros.
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kWtThreads) weight_stats_cc_kernel(const Weigh
     for (int o = 8; o; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
     const int row = r0 + 4 * ty + i;
     if (tx == 0 && row < R)
-      a.ws_ml[(size_t)split * a.T * a.Hq + (size_t)(r.off + first + row / a.g) * a.Hq + kvh * a.g + row % a.g] = make_float2(m[i], l[i]);
+      a.ws_ml[(size_t)split * a.T * a.Hq + weight_ws_row(a, kvh, r.off, first) + row] = make_float2(m[i], l[i]);
   }
   if (bad) atomicOr(&a.status[b], SPEC_DEV_BAD_BLOCK);
 }
@@ -168,8 +169,14 @@ __global__ void __launch_bounds__(kWtThreads) weight_sums_cc_kernel(const Weight
         if (r0 + i >= R) return nullptr;
         return static_cast<const T*>(a.q) + ((size_t)weight_q_row(a, r, first + (r0 + i) / a.g) * a.Hq + kvh * a.g + (r0 + i) % a.g) * D;
       });
-      for (int i = threadIdx.x; i < kWtRows && r0 + i < R; i += kWtThreads)
-        s_lse[i] = weight_lse(a, (size_t)(r.off + first + (r0 + i) / a.g) * a.Hq + kvh * a.g + (r0 + i) % a.g, r.P + first + (r0 + i) / a.g + 1);
+      for (int i = threadIdx.x; i < kWtRows && r0 + i < R; i += kWtThreads) {
+        // the splits that hold some of the keys this row sees
+        const int splits = min(a.splits, (r.P + first + (r0 + i) / a.g) / a.chunk + 1);
+        const float2* ml = a.ws_ml + weight_ws_row(a, kvh, r.off, first) + r0 + i;
+        float2 x = ml[0];
+        for (int k = 1; k < splits; ++k) x = weight_join(x, ml[(size_t)k * a.T * a.Hq]);
+        s_lse[i] = x.x + log2f(x.y);
+      }
       __syncthreads();
       float s[4][4];
       scores<D>(sq, sk, ty, tx, s);
@@ -222,8 +229,10 @@ cudaError_t launch_weight_cc(const WeightArgs& a, const WeightPlan& p, cudaStrea
 
 constexpr int kWtSms = 152;  // the plan's SM count (part of the workspace query)
 
-// Row tiles of M rows, and key splits for some twelve items per SM, of 512 keys at
-// least.
+// Row tiles of M rows, and key splits, of 512 keys at least, while the tiles alone
+// are fewer than four items per SM.  Where most requests fill no tile (single
+// tokens, paths) an item is at most 2048 keys: their lengths differ, and whole
+// ones leave SMs idle at the end.
 static WeightPlan weight_plan(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int window, int M, int* per_req) {
   const int g = Hq / Hkv;
   const long long packed = (long long)T * g / M + B;
@@ -232,8 +241,10 @@ static WeightPlan weight_plan(int B, int T, int n_max, int max_prefix, int Hq, i
   *per_req = each * B < packed ? (int)each : 0;
   p.tiles = std::min(each * B, packed);
   const long long keys = (long long)max_prefix + n_max, work = std::max(1LL, p.tiles * Hkv);
-  const long long want = std::max(1LL, std::min(12LL * kWtSms / work, (keys + 511) / 512));
-  p.chunk = (int)std::max(128LL, ((keys + want - 1) / want + 127) / 128 * 128);
+  const bool few = p.tiles < 2LL * B;
+  long long chunk = work >= 4LL * kWtSms ? keys : std::max(512LL, keys * work / (4LL * kWtSms));
+  if (few) chunk = std::min(chunk, 2048LL);
+  p.chunk = (int)std::max(128LL, (chunk + 127) / 128 * 128);
   p.splits = (int)std::max(1LL, (keys + p.chunk - 1) / p.chunk);
   return p;
 }
@@ -248,21 +259,26 @@ static spec_status weight_shape_check(int B, int T, int n_max, int max_prefix, i
   return SPEC_OK;
 }
 
+static size_t weight_ws_bytes(int splits, int T, int Hq, bool tc) {
+  return (size_t)T * Hq * ((size_t)splits * (tc ? kWtParts : 1) * sizeof(float2) + (tc ? sizeof(float) : 0));
+}
+
 }  // namespace spectree
 
 using namespace spectree;
 
 extern "C" {
 
-// One (maximum, sum) per row of q and split; a window only lowers the number of
-// splits that are wanted without one, or raises it to what one row tile wants.
+// (reference, sum) for every row of q and split, and for the tensor cores two of
+// them and the row's whole; a window only lowers the number of splits that are
+// wanted without one, or raises it to what one row tile wants.
 size_t spec_weight_workspace_size(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int D) {
   if (B <= 0 || T <= 0 || n_max <= 0 || weight_shape_check(B, T, n_max, max_prefix, Hq, Hkv, D, 16) != SPEC_OK) return 256;
   int per_req = 0;
   int splits = 1;
   for (int rows : {kWtRows, kWtTcRows})
     for (int window : {0, 1}) splits = std::max(splits, weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, rows, &per_req).splits);
-  return std::max<size_t>(256, (size_t)splits * T * Hq * sizeof(float2));
+  return std::max<size_t>(256, weight_ws_bytes(splits, T, Hq, true));
 }
 
 spec_status spec_attention_weight(const void* q, const void* k_cache, const int32_t* block_table, int max_blocks,
@@ -291,9 +307,9 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
   if (tc && (long long)num_blocks * Hkv * block_size >= (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
   const WeightPlan plan = weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, tc ? kWtTcRows : kWtRows, &a.per_req);
   const long long key_tiles = ((long long)max_prefix + n_max + kWtKeys - 1) / kWtKeys;
-  if (plan.tiles * Hkv * plan.splits > (long long)INT32_MAX || key_tiles * B * Hkv > (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
+  if (plan.tiles * Hkv * plan.splits > (long long)INT32_MAX / 2 || key_tiles * B * Hkv > (long long)INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
   if (key_tiles == 0) return SPEC_OK;
-  const size_t need = (size_t)plan.splits * T * Hq * sizeof(float2);
+  const size_t need = weight_ws_bytes(plan.splits, T, Hq, tc);
   if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15))) return SPEC_ERR_WORKSPACE;
   a.q = q;
   a.k_cache = k_cache;
@@ -306,6 +322,7 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
   a.weight = weight;
   a.status = status;
   a.ws_ml = static_cast<float2*>(workspace);
+  if (tc) a.ws_lse = static_cast<float*>(workspace) + (size_t)plan.splits * T * Hq * kWtParts * 2;
   a.stride = weight_stride;
   a.path_stride = path_stride;
   a.window = window;

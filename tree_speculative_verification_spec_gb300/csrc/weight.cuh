@@ -21,7 +21,8 @@ struct WeightArgs {
   const float* before;        // NULL: zeros
   float* weight;
   int32_t* status;
-  float2* ws_ml;              // [splits][T * Hq] partial (reference, sum) in the log2 domain, at q row off + i of token i
+  float2* ws_ml;              // [splits][Hkv][T * g][parts] partial (reference, sum) in the log2 domain, at (off + i) g + head of token i
+  float* ws_lse;              // [Hkv][T * g] minus log2 of the whole sum (tensor cores)
   long long stride;           // floats of one (request, kv-head) of before and weight
   int path_stride, window;
   int max_blocks, block_size, num_blocks;
@@ -80,21 +81,17 @@ __device__ __forceinline__ int weight_find(const WeightArgs& a, long long tile, 
   return lo;
 }
 
-// log2 of a row's whole sum, from (reference, sum) of every split that holds some
-// of the `seen` keys it sees.
-__device__ __forceinline__ float weight_lse(const WeightArgs& a, size_t row, int seen) {
-  const size_t rows = (size_t)a.T * a.Hq;
-  const int splits = min(a.splits, (seen - 1) / a.chunk + 1);
-  float m = -INFINITY, l = 0.0f;
-  for (int s = 0; s < splits; ++s) {
-    const float2 x = a.ws_ml[s * rows + row];
-    if (x.y > 0.0f) {
-      const float top = fmaxf(m, x.x);
-      l = l * exp2f(m - top) + x.y * exp2f(x.x - top);
-      m = top;
-    }
-  }
-  return m + log2f(l);
+// Where the partial sums of counted token 0's first head lie, less the split's part.
+__device__ __forceinline__ size_t weight_ws_row(const WeightArgs& a, int kvh, int off, int first) {
+  return (size_t)kvh * a.T * a.g + (size_t)(off + first) * a.g;
+}
+
+// Two partial sums, (reference, sum) each, as one.
+__device__ __forceinline__ float2 weight_join(float2 x, float2 y) {
+  if (!(x.y > 0.0f)) return y;
+  if (!(y.y > 0.0f)) return x;
+  const float top = fmaxf(x.x, y.x);
+  return make_float2(top, x.y * exp2f(x.x - top) + y.y * exp2f(y.x - top));
 }
 
 struct WeightPlan {

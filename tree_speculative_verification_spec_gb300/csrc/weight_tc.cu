@@ -12,8 +12,12 @@
 //                   (rows) of 2^(x - log2 of the row's sum).
 //   sums, many      lanes = keys: resident K (256 keys), stream Q.  The weight
 //                   stays in a register over every row tile that sees the keys.
-// Each of the two epilogue warpgroups has two score buffers of its own, so the
-// tensor core works on the next scores while it reduces.
+// Four epilogue warpgroups, four score buffers.  Statistics and sums over many
+// rows: each resident tile has two buffers in turn and two warpgroups, one for
+// each half of the columns.  Sums over few rows: a warpgroup and a buffer take
+// every fourth key tile.  (Two warpgroups, a whole buffer each, left the
+// exponentials at 44 % and the tensor core at 44 % of a prompt's statistics: two
+// warps a scheduler do not cover a score buffer's hand-over.)
 //
 // The reference of a row starts at 0 and is not a maximum: 2^(x - m) and its
 // fp32 sum hold any m within 2^60 of the scores; a chunk whose sum leaves that
@@ -23,6 +27,7 @@
 // the batch by a prefix sum that each CTA takes of its own, 256 requests at a
 // time, and dealt out round-robin, the longest of a request first.
 #include <algorithm>
+#include <climits>
 
 #include "tcgen05.cuh"
 #include "weight.cuh"
@@ -34,8 +39,9 @@ namespace wtc {
 using namespace tc5;
 
 constexpr int BM = 128;
-constexpr int kThreads = 384;        // warps: 0 stream, 1 MMA, 2 resident tiles, 3 spare, 4-7 and 8-11 epilogue
-constexpr uint32_t kTmemCols = 512;  // score buffers: 2 per warpgroup, 128 columns each
+constexpr int kThreads = 640;        // warps: 0 stream, 1 MMA, 2 resident tiles, 3 sums of the rows, 4-19 epilogue (four warpgroups)
+constexpr uint32_t kTmemCols = 512;  // four score buffers of 128 columns
+constexpr int kLse = 4;              // row tiles whose sums are held for the epilogue
 constexpr int kGroup = 256;          // requests numbered at a time
 constexpr float kSumTop = 0x1p60f;
 enum Mode { kStats = 0, kSumsFew = 1, kSumsMany = 2 };
@@ -195,10 +201,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NST = L::NST;
   const WeightArgs& a = prm.a;
   extern __shared__ uint8_t dyn_raw[];
-  __shared__ uint64_t full[NST], empty[NST], res_full, res_empty, s_full[2][2], s_empty[2][2], drain;
+  __shared__ uint64_t full[NST], empty[NST], res_full, res_empty, s_full[4], s_empty[4], drain;
   __shared__ Table tab;
-  __shared__ __align__(16) float s_lse[2][2 * BM];  // minus log2 of the rows' sums
-  __shared__ __align__(16) int s_lim[2][2 * BM];    // the last slot that each row sees, -1: no row
+  __shared__ uint64_t lse_full[kLse], lse_empty[kLse];
+  __shared__ __align__(16) float s_lse[kLse][BM];  // minus log2 of the sums of a row tile's rows
+  __shared__ __align__(16) int s_lim[kLse][BM];    // the last slot that each of them sees, -1: no row
+  __shared__ float s_part[2][2][BM];
   __shared__ int scan[kThreads / 32], abort_flag, issued[NST], res_issued;
   __shared__ uint32_t tmem_slot;
 
@@ -214,8 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&res_full, 1);
     mbar_init(&res_empty, 1);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_full[i >> 1][i & 1], 1);
-      mbar_init(&s_empty[i >> 1][i & 1], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], MODE == kSumsFew ? 4 : 8);
+    }
+    for (int i = 0; i < kLse; ++i) {
+      mbar_init(&lse_full[i], 1);
+      mbar_init(&lse_empty[i], 16);
     }
     mbar_init(&drain, 1);
     abort_flag = 0;
@@ -232,18 +244,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  // Each kernel of a call but the first waits for the one before; each lets the
+  // next one launch as it starts.
+  if (MODE != kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // A wait that runs out sets the abort flag; every later wait then ends after a
   // few polls, and the items run to their ends on whatever they find (every
   // request is flagged, its weights are unspecified).
   auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, &abort_flag); };
 
-  // 128 keys from k of an item's kv-head into a tile, by boxes of up to a page.
-  auto load_keys = [&](const Item& w, int k, uint32_t dst, uint64_t* bar, int* bad) {
-    const int br = prm.box_rows, nb = BM / br;
-    const int32_t* bt = a.block_table + (size_t)w.b * a.max_blocks;
-    if (lane < nb) {
-      const int y = box_row(prm, bt, w.kvh, k + lane * br, w.q.P + w.q.m, bad);
+  // 128 keys from k of an item's kv-head into a tile, by boxes of up to a page:
+  // lane i's box (looked up ahead) and its copy.
+  auto key_box = [&](const Item& w, int k, int* bad) -> int {
+    return lane < BM / prm.box_rows ? box_row(prm, a.block_table + (size_t)w.b * a.max_blocks, w.kvh, k + lane * prm.box_rows, w.q.P + w.q.m, bad) : 0;
+  };
+  auto load_keys = [&](int y, uint32_t dst, uint64_t* bar) {
+    const int br = prm.box_rows;
+    if (lane < BM / br) {
 #pragma unroll
       for (int h = 0; h < L::DH; ++h) tma_load_2d(dst + h * (BM * 128) + lane * br * 128, &tmap_k, h * 64, y, bar);
     }
@@ -283,22 +301,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(bar);
   };
 
+  // Round k deals items k grid .. (k + 1) grid - 1 to the CTAs, every other round
+  // backwards: costs fall along a request, so a CTA's sums come out alike.
+  const int grid = (int)gridDim.x, me = (int)blockIdx.x;
+  auto dealt = [&](int round) { return round * grid + (round & 1 ? grid - 1 - me : me); };
+  auto rounds_end = [&](int n) { return (n + grid - 1) / grid * grid; };
+
   int items = 0;                        // with steps, of this CTA so far
   int ld = 0;                           // stream tiles so far
-  int jobs[2] = {0, 0};                 // score tiles of each warpgroup so far (MMA warp)
-  int c = 0;                            // score tiles of this warpgroup so far (epilogue)
+  int jobs[4] = {0, 0, 0, 0};           // score tiles so far: of each resident tile, or of each buffer (MMA warp)
+  int c = 0;                            // the same of this warpgroup's (epilogue)
+  int lt = 0;                           // row tiles of sums so far
   bool dead = false;                    // a producer that gave up
   for (int b0 = 0; b0 < a.B; b0 += kGroup) {
     const int tiles = build_table<MODE>(prm, tab, b0, scan);
     const int n_items = tiles * a.Hkv * (MODE == kStats ? a.splits : 1);
     if (warp == 0) {
       // ---------------------------------------------------------- stream
-      for (int idx = blockIdx.x; idx < n_items && !dead; idx += gridDim.x) {
+      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items) && !dead; ++round) {
+        if (idx >= n_items) continue;
         const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
         if (MODE == kSumsFew && w.rt == 0) continue;
-        int bad = 0;
+        int bad = 0, y = MODE == kSumsMany ? 0 : key_box(w, w.k0, &bad);
         for (int j = 0; j < w.steps; ++j, ++ld) {
-          const int st = ld % NST;
+          const int st = ld % NST, next = MODE != kSumsMany && j + 1 < w.steps ? key_box(w, w.k0 + (j + 1) * BM, &bad) : 0;
           bool go = true;
           if (lane == 0 && ld >= NST) go = wait(&empty[st], ld / NST - 1);
           dead = !__shfl_sync(0xffffffffu, (int)go, 0);
@@ -312,14 +338,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             if (lane == 0) mbar_expect_tx(&full[st], L::kTile);
             __syncwarp();
-            load_keys(w, w.k0 + j * BM, dst, &full[st], &bad);
+            load_keys(y, dst, &full[st]);
           }
+          y = next;
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
       }
     } else if (warp == 2) {
       // ---------------------------------------------------------- resident tiles
-      for (int idx = blockIdx.x; idx < n_items && !dead; idx += gridDim.x) {
+      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items) && !dead; ++round) {
+        if (idx >= n_items) continue;
         const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
         if (w.steps == 0 || (MODE == kSumsFew && w.rt == 0)) continue;
         bool go = true;
@@ -333,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int bad = 0;
           if (lane == 0) mbar_expect_tx(&res_full, n * L::kTile);
           __syncwarp();
-          for (int t = 0; t < n; ++t) load_keys(w, w.k0 + t * BM, sbase + t * L::kTile, &res_full, &bad);
+          for (int t = 0; t < n; ++t) load_keys(key_box(w, w.k0 + t * BM, &bad), sbase + t * L::kTile, &res_full);
           if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
         } else {
           if (lane == 0 && prm.q_tma) mbar_expect_tx(&res_full, n * L::kTile);
@@ -347,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- MMA
       const uint64_t res = smem_desc_sw128(sbase, 16, 1024), ring = smem_desc_sw128(sbase + L::kOffRing, 16, 1024);
       const bool leader = elect_one();
-      for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
+      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items); ++round) {
+        if (idx >= n_items) continue;
         const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
         if (w.steps == 0 || (MODE == kSumsFew && w.rt == 0)) continue;
         const int R = w.q.cnt * a.g;
@@ -360,12 +389,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (MODE == kSumsFew ? t >= w.rt : j < w.lo[t] || j >= w.hi[t]) continue;
-            const int g = MODE == kSumsFew ? j & 1 : t;
-            const int c = g ? jobs[1]++ : jobs[0]++;  // this warpgroup's
-            if (c >= 2) wait(&s_empty[g][c & 1], (c >> 1) - 1);
+            // buffer, and the number of its jobs before this one
+            int buf, before;
+            if (MODE == kSumsFew) {
+              buf = w.rt == 2 ? (j & 1) * 2 + t : j & 3;
+              before = buf == 0 ? jobs[0]++ : buf == 1 ? jobs[1]++ : buf == 2 ? jobs[2]++ : jobs[3]++;
+            } else {
+              const int c = jobs[t]++;
+              buf = t * 2 + (c & 1);
+              before = c >> 1;
+            }
+            if (before > 0) wait(&s_empty[buf], before - 1);
             tc_fence_after();
             const uint64_t rd = res + (uint64_t)(t * (L::kTile >> 4));
-            const uint32_t d = tmem + (g * 2 + (c & 1)) * BM;
+            const uint32_t d = tmem + buf * BM;
             // few rows: only the columns that hold some, 32 at a time
             const uint32_t n = MODE == kSumsFew ? min(BM, (R - t * BM + 31) / 32 * 32) : BM;
             const uint32_t idesc = idesc_bf16(BM, 0) & ~(0x3fu << 17) | (n >> 3) << 17;
@@ -375,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t o = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
                 umma_bf16(d, (MODE == kSumsFew ? sd : rd) + o, (MODE == kSumsFew ? rd : sd) + o, idesc, kk > 0 ? 1u : 0u);
               }
-              umma_commit(&s_full[g][c & 1]);
+              umma_commit(&s_full[buf]);
             }
             __syncwarp();
           }
@@ -385,27 +422,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) umma_commit(&res_empty);
         __syncwarp();
       }
+    } else if (warp == 3 && MODE != kStats) {
+      // ---------------------------------------------------------- sums of the rows
+      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items) && !dead; ++round) {
+        if (idx >= n_items) continue;
+        const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
+        const int n = MODE == kSumsFew ? w.rt : w.steps, R = w.q.cnt * a.g;
+        for (int t = 0; t < n; ++t, ++lt) {
+          const int at = lt % kLse;
+          float nl[BM / 32];
+          int lim[BM / 32];
+          const int row0 = w.r0 + t * BM + lane;
+          const float* lse = a.ws_lse + weight_ws_row(a, w.kvh, w.q.off, w.q.first) + row0;
+#pragma unroll
+          for (int e = 0; e < BM / 32; ++e) {
+            const bool there = row0 + e * 32 < R;
+            lim[e] = there ? w.q.P + w.q.first + (row0 + e * 32) / a.g : -1;
+            nl[e] = there ? lse[e * 32] : -INFINITY;
+          }
+          bool go = true;
+          if (lane == 0 && lt >= kLse) go = wait(&lse_empty[at], lt / kLse - 1);
+          dead = !__shfl_sync(0xffffffffu, (int)go, 0);
+          if (dead) break;
+#pragma unroll
+          for (int e = 0; e < BM / 32; ++e) {
+            s_lse[at][e * 32 + lane] = nl[e];
+            s_lim[at][e * 32 + lane] = lim[e];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&lse_full[at]);
+        }
+      }
     } else if (warp >= 4) {
       // ---------------------------------------------------------- epilogue
-      const int g = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;  // warpgroup, TMEM lane
-      const uint32_t tS = tmem + g * 2 * BM + ((uint32_t)(quad * 32) << 16);
+      const int wg = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;  // warpgroup, TMEM lane
+      const int g = wg & 1, half = wg >> 1;  // resident tile and half of its columns
+      const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
       const float c2 = a.scale_log2;
       const float2 c22 = make_float2(c2, c2);
-      auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory"); };
-      auto release = [&]() {  // this warp has read the score buffer
+      // the next score buffer of this warpgroup: its TMEM columns, and its return
+      auto take = [&]() -> uint32_t {
+        const int buf = MODE == kSumsFew ? wg : g * 2 + (c & 1);
+        wait(&s_full[buf], MODE == kSumsFew ? c : c >> 1);
+        tc_fence_after();
+        return tmem + buf * BM + lane_off;
+      };
+      auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[g][c & 1]);
+        if (lane == 0) mbar_arrive(&s_empty[MODE == kSumsFew ? wg : g * 2 + (c & 1)]);
+        ++c;
       };
-      // row's entry of s_lse and s_lim
-      auto row_entry = [&](const Item& w, int row, float& nl, int& lim) {
-        nl = -INFINITY;
-        lim = -1;
-        if (row < w.q.cnt * a.g) {
-          const int tok = w.q.first + row / a.g;
-          lim = w.q.P + tok;
-          nl = -weight_lse(a, (size_t)(w.q.off + tok) * a.Hq + w.kvh * a.g + row % a.g, lim + 1);
-        }
+      auto lse_done = [&](int i) {  // this warp has read row tile i's sums
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&lse_empty[i % kLse]);
       };
       // sum over 32 columns of 2^(x c + nl), the columns that see `key` alone where
       // `masked`
@@ -428,13 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
+      auto slot_at = [&](const Item& w, int key) { return ((size_t)w.b * a.Hkv + w.kvh) * a.stride + key; };
+      auto old_weight = [&](const Item& w, int key) -> float {
+        return a.before && key < w.q.P ? a.decay * a.before[slot_at(w, key)] : 0.0f;
+      };
       auto put = [&](const Item& w, int key, float sum) {
-        if (key >= w.q.P + w.q.m) return;
-        const size_t at = ((size_t)w.b * a.Hkv + w.kvh) * a.stride + key;
-        a.weight[at] = (a.before && key < w.q.P ? a.decay * a.before[at] : 0.0f) + sum;
+        if (key < w.q.P + w.q.m) a.weight[slot_at(w, key)] = sum;
       };
 
-      for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
+      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items); ++round) {
+        if (idx >= n_items) continue;
         const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
         const int R = w.q.cnt * a.g, lo = g ? w.lo[1] : w.lo[0], hi = g ? w.hi[1] : w.hi[0];
         if (MODE == kStats) {
@@ -480,95 +553,88 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += sum;
           };
           const bool idle = !__any_sync(0xffffffffu, valid);  // a warp without rows only passes the buffers on
-          for (int j = 0; j < hi; ++j, ++c) {
-            wait(&s_full[g][c & 1], c >> 1);
-            tc_fence_after();
+          for (int j = 0; j < hi; ++j) {
+            const uint32_t t0 = take() + half * 64;
             if (!idle) {
-              const int vis = lim - j * BM;
-              const uint32_t t0 = tS + (c & 1) * BM;
-              uint32_t x[32], y[32];
-              tmem_ld32(t0, x);
+              const int vis = lim - j * BM - half * 64;
+              uint32_t x[32];
 #pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
+              for (int e = 0; e < 64; e += 32) {
+                tmem_ld32(t0 + e, x);
                 tmem_wait_ld(x);
-                tmem_ld32(t0 + h * 64 + 32, y);
-                chunk(x, vis - h * 64);
-                tmem_wait_ld(y);
-                if (h == 0) tmem_ld32(t0 + 64, x);
-                chunk(y, vis - h * 64 - 32);
+                chunk(x, vis - e);
               }
             }
             release();
           }
           if (valid)
-            a.ws_ml[(size_t)w.split * a.T * a.Hq + (size_t)(w.q.off + tok) * a.Hq + w.kvh * a.g + row % a.g] = make_float2(m, l);
+            a.ws_ml[((size_t)w.split * a.T * a.Hq + weight_ws_row(a, w.kvh, w.q.off, w.q.first) + row) * 2 + half] = make_float2(m, l);
         } else if (MODE == kSumsFew) {
           if (w.rt == 0) {  // no rows: the old weights alone
-            for (int j = g; j < w.steps; j += 2) put(w, w.k0 + j * BM + r, 0.0f);
+            for (int j = wg; j < w.steps; j += 4) put(w, w.k0 + j * BM + r, old_weight(w, w.k0 + j * BM + r));
             continue;
           }
-          float nl[2];
-          int lim[2];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) row_entry(w, t * BM + r, nl[t], lim[t]);
-          group_sync();  // the item before has been read
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            s_lse[g][t * BM + r] = nl[t];
-            s_lim[g][t * BM + r] = lim[t];
-          }
-          group_sync();
-          for (int j = g; j < w.steps; j += 2) {
+          // one row tile: every fourth key tile; two: one of them for every other
+          const bool two = w.rt == 2;
+          const int j0 = two ? wg >> 1 : wg, dj = two ? 2 : 4, t = two ? wg & 1 : 0, at = (lt + t) % kLse;
+          float old = t == 0 ? old_weight(w, w.k0 + j0 * BM + r) : 0.0f;
+          wait(&lse_full[at], (lt + t) / kLse);
+          const int cols = min(BM, R - t * BM);
+          for (int j = j0; j < w.steps; j += dj) {
             const int k0 = w.k0 + j * BM, key = k0 + r;
+            const float next = t == 0 && j + dj < w.steps ? old_weight(w, key + dj * BM) : 0.0f;
             float2 acc = make_float2(0.0f, 0.0f);
-            for (int t = 0; t < w.rt; ++t, ++c) {
-              wait(&s_full[g][c & 1], c >> 1);
-              tc_fence_after();
-              const int cols = min(BM, R - t * BM);
-              // rows that do not see the tile's last key, or columns without a row
-              const bool masked = k0 + BM - 1 > w.q.P + w.q.first || (cols & 31) != 0;
-              const uint32_t t0 = tS + (c & 1) * BM;
+            const uint32_t t0 = take();
+            // rows that do not see the tile's last key, or columns without a row
+            const bool masked = k0 + BM - 1 > w.q.P + w.q.first || (cols & 31) != 0;
 #pragma unroll 1
-              for (int e = 0; e < cols; e += 32) {
+            for (int e = 0; e < cols; e += 32) {
+              uint32_t x[32];
+              tmem_ld32(t0 + e, x);
+              tmem_wait_ld(x);
+              column_sum(x, &s_lse[at][e], &s_lim[at][e], masked, key, acc);
+            }
+            release();
+            float sum = acc.x + acc.y;
+            if (two) {  // the other row tile's share; the buffer is read before the barrier of the pair's next tile
+              float* part = s_part[wg >> 1][(j >> 1) & 1];
+              if (t == 1) part[r] = sum;
+              asm volatile("bar.sync %0, 256;" ::"r"(1 + (wg >> 1)) : "memory");
+              if (t == 0) sum += part[r];
+            }
+            if (t == 0) put(w, key, old + sum);
+            old = next;
+          }
+          // both row tiles' sums go back, read here or not
+          if (two) wait(&lse_full[(lt + 1 - t) % kLse], (lt + 1 - t) / kLse);
+          for (int t = 0; t < w.rt; ++t, ++lt) lse_done(lt);
+        } else {
+          const int k0 = w.k0 + g * BM, key = k0 + r;
+          const float old = half == 0 ? old_weight(w, key) : 0.0f;
+          float2 acc = make_float2(0.0f, 0.0f);
+          for (int j = 0; j < w.steps; ++j, ++lt) {
+            const int at = lt % kLse;
+            wait(&lse_full[at], lt / kLse);
+            if (j >= lo && j < hi) {
+              const int row0 = w.r0 + j * BM;
+              const uint32_t t0 = take();
+              const bool masked = k0 + BM - 1 > w.q.P + w.q.first + row0 / a.g || row0 + BM > R;
+#pragma unroll 1
+              for (int e = half * 64; e < half * 64 + 64; e += 32) {
                 uint32_t x[32];
                 tmem_ld32(t0 + e, x);
                 tmem_wait_ld(x);
-                column_sum(x, &s_lse[g][t * BM + e], &s_lim[g][t * BM + e], masked, key, acc);
+                column_sum(x, &s_lse[at][e], &s_lim[at][e], masked, key, acc);
               }
               release();
             }
-            put(w, key, acc.x + acc.y);
+            lse_done(lt);
           }
-        } else {
-          const int k0 = w.k0 + g * BM, key = k0 + r;
-          float2 acc = make_float2(0.0f, 0.0f);
-          float nl;
-          int lim;
-          if (lo < hi) row_entry(w, w.r0 + lo * BM + r, nl, lim);
-          for (int j = lo; j < hi; ++j, ++c) {
-            const int row0 = w.r0 + j * BM, half = (c & 1) * BM;
-            s_lse[g][half + r] = nl;  // its last reader was two jobs ago, behind a group_sync
-            s_lim[g][half + r] = lim;
-            group_sync();
-            if (j + 1 < hi) row_entry(w, row0 + BM + r, nl, lim);
-            wait(&s_full[g][c & 1], c >> 1);
-            tc_fence_after();
-            const bool masked = k0 + BM - 1 > w.q.P + w.q.first + row0 / a.g || row0 + BM > R;
-            const uint32_t t0 = tS + (c & 1) * BM;
-            uint32_t x[32], y[32];
-            tmem_ld32(t0, x);
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              tmem_wait_ld(x);
-              tmem_ld32(t0 + h * 64 + 32, y);
-              column_sum(x, &s_lse[g][half + h * 64], &s_lim[g][half + h * 64], masked, key, acc);
-              tmem_wait_ld(y);
-              if (h == 0) tmem_ld32(t0 + 64, x);
-              column_sum(y, &s_lse[g][half + h * 64 + 32], &s_lim[g][half + h * 64 + 32], masked, key, acc);
-            }
-            release();
-          }
-          put(w, key, acc.x + acc.y);
+          // the two halves of the columns, through shared memory
+          if (half == 1) s_part[g][0][r] = acc.x + acc.y;
+          asm volatile("bar.sync %0, 256;" ::"r"(1 + g) : "memory");
+          if (half == 0) put(w, key, old + (acc.x + acc.y) + s_part[g][0][r]);
+          asm volatile("bar.sync %0, 256;" ::"r"(1 + g) : "memory");
         }
       }
     }
@@ -593,6 +659,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
+}
+
+// Minus log2 of every counted row's sum, from the parts that the splits with some
+// of its keys left: 8 lanes a row, 32 rows a CTA.
+constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 8;
+__global__ void __launch_bounds__(kJoinThreads) weight_join_kernel(const WeightArgs a, int tiles) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tile = blockIdx.x % tiles, kvh = blockIdx.x / tiles % a.Hkv, b = blockIdx.x / tiles / a.Hkv;
+  WeightRequest r;
+  const bool bad = weight_check(a, b, r) != 0;
+  const int row = tile * kJoinRows + threadIdx.x / 8, part = threadIdx.x % 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (bad || tile * kJoinRows >= r.cnt * a.g) return;
+  const bool there = row < r.cnt * a.g;
+  const int first = r.m - r.cnt;
+  const int splits = there ? min(a.splits, (r.P + first + row / a.g) / a.chunk + 1) : 0;
+  const size_t at = weight_ws_row(a, kvh, r.off, first) + row, step = (size_t)a.T * a.Hq;
+  const float4* ml = reinterpret_cast<const float4*>(a.ws_ml) + at;
+  float2 x = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = part; s < splits; s += 8) {
+    const float4 y = ml[s * step];
+    x = weight_join(x, weight_join(make_float2(y.x, y.y), make_float2(y.z, y.w)));
+  }
+#pragma unroll
+  for (int o = 4; o; o >>= 1) {
+    const float2 y = make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o));
+    x = weight_join(x, y);
+  }
+  if (there && part == 0) a.ws_lse[at] = -(x.x + log2f(x.y));
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -620,13 +716,26 @@ static bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int MODE>
-static cudaError_t launch_mode(const CUtensorMap& mk, const CUtensorMap& mq, const Params& prm, int sms, cudaStream_t stream) {
-  const int dyn = (int)Layout<D>::kDyn;
-  const cudaError_t e = cudaFuncSetAttribute(weight_tc_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
-  if (e != cudaSuccess) return e;
-  weight_tc_kernel<D, MODE><<<sms, kThreads, dyn, stream>>>(mk, mq, prm);
-  return cudaGetLastError();
+// A kernel of a call; every one but the first is a programmatic dependent of the
+// one before.
+template <typename... P, typename... A>
+static cudaError_t launch(void (*kern)(P...), long long grid, int threads, int dyn, bool first, cudaStream_t stream, const A&... args) {
+  if (dyn > 0) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = dyn;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = first ? 0 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D>
@@ -641,9 +750,9 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
   while ((1 << prm.bs_log2) < a.block_size) ++prm.bs_log2;
   prm.rows_total = (long long)a.num_blocks * a.Hkv * a.block_size;
   prm.q_tma = !a.path && BM % a.g == 0 && a.T > 0;
-  // sums over few rows: some eight items for every CTA, of 256 keys at least
-  const long long keys = ((long long)a.max_prefix + a.n_max) * a.B * a.Hkv / (8LL * sms);
-  prm.key_chunk = (int)std::min(4096LL, std::max(256LL, (keys + 255) / 256 * 256));
+  // sums over few rows: some four items for every CTA, of 256 to 2048 keys
+  const long long keys = ((long long)a.max_prefix + a.n_max) * a.B * a.Hkv / (4LL * sms);
+  prm.key_chunk = (int)std::min(2048LL, std::max(256LL, (keys + 255) / 256 * 256));
   alignas(64) CUtensorMap mk, mq;
   {
     const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)prm.rows_total}, strides[1] = {(cuuint64_t)D * 2};
@@ -659,9 +768,15 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
     mq = mk;  // not read
   }
   const long long rows = (long long)(a.window > 0 ? std::min(a.window, a.n_max) : a.n_max) * a.g;  // the most that a request has
-  if (rows > 0) e = launch_mode<D, kStats>(mk, mq, prm, sms, stream);
-  if (e == cudaSuccess) e = launch_mode<D, kSumsFew>(mk, mq, prm, sms, stream);
-  if (e == cudaSuccess && rows > 2 * BM) e = launch_mode<D, kSumsMany>(mk, mq, prm, sms, stream);
+  const int dyn = (int)Layout<D>::kDyn;
+  if (rows > 0) {
+    const int tiles = (int)((rows + kJoinRows - 1) / kJoinRows);
+    if ((long long)tiles * a.Hkv * a.B > INT32_MAX) return cudaErrorInvalidValue;
+    e = launch(weight_tc_kernel<D, kStats>, sms, kThreads, dyn, true, stream, mk, mq, prm);
+    if (e == cudaSuccess) e = launch(weight_join_kernel, (long long)tiles * a.Hkv * a.B, kJoinThreads, 0, false, stream, a, tiles);
+  }
+  if (e == cudaSuccess) e = launch(weight_tc_kernel<D, kSumsFew>, sms, kThreads, dyn, rows == 0, stream, mk, mq, prm);
+  if (e == cudaSuccess && rows > 2 * BM) e = launch(weight_tc_kernel<D, kSumsMany>, sms, kThreads, dyn, false, stream, mk, mq, prm);
   return e;
 }
 
