@@ -180,19 +180,6 @@ __device__ __forceinline__ Item find_item(const Params& prm, const Table& tab, i
   return w;
 }
 
-// Row of the 2-D cache view of the box that starts at key k; keys behind the
-// request, or at a bad block id, read the out-of-range row `rows_total` (zeros).
-__device__ __forceinline__ int box_row(const Params& prm, const int32_t* bt, int kvh, int k, int end, int* bad) {
-  const WeightArgs& a = prm.a;
-  int y = (int)prm.rows_total;
-  if (k < end) {
-    const int blk = __ldg(bt + (k >> prm.bs_log2));
-    if (blk >= 0 && blk < a.num_blocks) y = ((blk * a.Hkv + kvh) << prm.bs_log2) + (k & (a.block_size - 1));
-    else *bad = 1;
-  }
-  return y;
-}
-
 template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_q,
@@ -201,13 +188,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NST = L::NST;
   const WeightArgs& a = prm.a;
   extern __shared__ uint8_t dyn_raw[];
-  __shared__ uint64_t full[NST], empty[NST], res_full, res_empty, s_full[4], s_empty[4], drain;
+  __shared__ uint64_t full[NST], empty[NST], res_full[2], res_empty[2], s_full[4], s_empty[4], drain;
   __shared__ Table tab;
   __shared__ uint64_t lse_full[kLse], lse_empty[kLse];
   __shared__ __align__(16) float s_lse[kLse][BM];  // minus log2 of the sums of a row tile's rows
   __shared__ __align__(16) int s_lim[kLse][BM];    // the last slot that each of them sees, -1: no row
   __shared__ float s_part[2][2][BM];
-  __shared__ int scan[kThreads / 32], abort_flag, issued[NST], res_issued;
+  __shared__ int scan[kThreads / 32], abort_flag, issued[NST], res_issued[2];
   __shared__ uint32_t tmem_slot;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -219,8 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[i], 1);
       issued[i] = -1;
     }
-    mbar_init(&res_full, 1);
-    mbar_init(&res_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&res_full[i], 1);
+      mbar_init(&res_empty[i], 1);
+      res_issued[i] = -1;
+    }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], MODE == kSumsFew ? 4 : 8);
@@ -231,7 +221,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&drain, 1);
     abort_flag = 0;
-    res_issued = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -254,20 +243,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   // request is flagged, its weights are unspecified).
   auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, &abort_flag); };
 
-  // 128 keys from k of an item's kv-head into a tile, by boxes of up to a page:
-  // lane i's box (looked up ahead) and its copy.
-  auto key_box = [&](const Item& w, int k, int* bad) -> int {
-    return lane < BM / prm.box_rows ? box_row(prm, a.block_table + (size_t)w.b * a.max_blocks, w.kvh, k + lane * prm.box_rows, w.q.P + w.q.m, bad) : 0;
+  // Keys come by boxes of up to a page.  The page of an item's box x (boxes count
+  // from slot 0 of the request), -1 behind its keys or at a bad id.
+  const int nb = BM / prm.box_rows;
+  auto box_page = [&](const Item& w, int x, int* bad) -> int {
+    const int k = x * prm.box_rows;
+    if (k >= w.q.P + w.q.m) return -1;
+    const int page = __ldg(a.block_table + (size_t)w.b * a.max_blocks + (k >> prm.bs_log2));
+    if (page >= 0 && page < a.num_blocks) return page;
+    *bad = 1;
+    return -1;
   };
-  auto load_keys = [&](int y, uint32_t dst, uint64_t* bar) {
-    const int br = prm.box_rows;
-    if (lane < BM / br) {
+  // Key tile j of an item: lane i < nb copies box i from its page; without one it
+  // reads behind the cache (zeros).
+  auto load_keys = [&](const Item& w, int j, int page, uint32_t dst, uint64_t* bar) {
+    if (lane < nb) {
+      const int k = w.k0 + j * BM + lane * prm.box_rows;
+      const int y = page < 0 ? (int)prm.rows_total : ((page * a.Hkv + w.kvh) << prm.bs_log2) + (k & (a.block_size - 1));
 #pragma unroll
-      for (int h = 0; h < L::DH; ++h) tma_load_2d(dst + h * (BM * 128) + lane * br * 128, &tmap_k, h * 64, y, bar);
+      for (int h = 0; h < L::DH; ++h) tma_load_2d(dst + h * (BM * 128) + lane * prm.box_rows * 128, &tmap_k, h * 64, y, bar);
     }
   };
   // Rows r .. r + 127 of an item (row = (counted token, head of the group)); rows
-  // behind its last are whatever lies there, or zeros.  True: `bar` still has to
+  // behind its last are whatever lies there.  True: `bar` still has to
   // be arrived on.
   auto load_rows = [&](const Item& w, int r, uint32_t dst, uint64_t* bar) -> bool {
     if (prm.q_tma) {
@@ -282,15 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
     const int ch = lane % CPR, R = w.q.cnt * a.g;
     const int32_t* path = a.path ? a.path + (size_t)w.b * a.path_stride + w.q.first : nullptr;
-    for (int i = lane / CPR; i < BM; i += STEP) {
+#pragma unroll 4
+    for (int i = lane / CPR; i < min(BM, R - r); i += STEP) {
       const uint32_t at = dst + (ch >> 3) * (BM * 128) + i * 128 + (((ch & 7) ^ (i & 7)) << 4);
-      if (r + i < R) {
-        const int tok = (r + i) / a.g, head = (r + i) % a.g;
-        const size_t row = w.q.off + (path ? path[tok] : w.q.first + tok);
-        cp_async16(at, q + (row * a.Hq + w.kvh * a.g + head) * D + ch * 8);
-      } else {
-        *reinterpret_cast<uint4*>(smem + (at - sbase)) = make_uint4(0, 0, 0, 0);
-      }
+      const int tok = (r + i) / a.g, head = (r + i) % a.g;
+      const size_t row = w.q.off + (path ? path[tok] : w.q.first + tok);
+      cp_async16(at, q + (row * a.Hq + w.kvh * a.g + head) * D + ch * 8);
     }
     return true;
   };
@@ -301,13 +296,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(bar);
   };
 
+  auto resident = [&](const Item& w) { return MODE == kSumsFew ? w.rt : w.hi[1] > 0 ? 2 : 1; };  // tiles
   // Round k deals items k grid .. (k + 1) grid - 1 to the CTAs, every other round
   // backwards: costs fall along a request, so a CTA's sums come out alike.
   const int grid = (int)gridDim.x, me = (int)blockIdx.x;
   auto dealt = [&](int round) { return round * grid + (round & 1 ? grid - 1 - me : me); };
   auto rounds_end = [&](int n) { return (n + grid - 1) / grid * grid; };
 
-  int items = 0;                        // with steps, of this CTA so far
+  int rs = 0;                           // resident tiles so far: tile i of an item lies in slot (rs + i) & 1
   int ld = 0;                           // stream tiles so far
   int jobs[4] = {0, 0, 0, 0};           // score tiles so far: of each resident tile, or of each buffer (MMA warp)
   int c = 0;                            // the same of this warpgroup's (epilogue)
@@ -322,9 +318,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (idx >= n_items) continue;
         const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
         if (MODE == kSumsFew && w.rt == 0) continue;
-        int bad = 0, y = MODE == kSumsMany ? 0 : key_box(w, w.k0, &bad);
+        // the pages of 32 boxes at a time, one to a lane, and the next 32 ahead
+        int bad = 0, pages = -1, ahead = -1;
+        const int x0 = w.k0 / prm.box_rows + lane, boxes = w.steps * nb;
+        if (MODE != kSumsMany && lane < boxes) ahead = box_page(w, x0, &bad);
         for (int j = 0; j < w.steps; ++j, ++ld) {
-          const int st = ld % NST, next = MODE != kSumsMany && j + 1 < w.steps ? key_box(w, w.k0 + (j + 1) * BM, &bad) : 0;
+          const int st = ld % NST, at = j * nb & 31;
+          if (MODE != kSumsMany && at == 0) {
+            pages = ahead;
+            if (j * nb + 32 + lane < boxes) ahead = box_page(w, x0 + j * nb + 32, &bad);
+          }
           bool go = true;
           if (lane == 0 && ld >= NST) go = wait(&empty[st], ld / NST - 1);
           dead = !__shfl_sync(0xffffffffu, (int)go, 0);
@@ -338,9 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             if (lane == 0) mbar_expect_tx(&full[st], L::kTile);
             __syncwarp();
-            load_keys(y, dst, &full[st]);
+            load_keys(w, j, __shfl_sync(0xffffffffu, pages, (at + lane) & 31), dst, &full[st]);
           }
-          y = next;
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
       }
@@ -350,26 +352,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (idx >= n_items) continue;
         const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
         if (w.steps == 0 || (MODE == kSumsFew && w.rt == 0)) continue;
-        bool go = true;
-        if (lane == 0 && items > 0) go = wait(&res_empty, items - 1);
-        dead = !__shfl_sync(0xffffffffu, (int)go, 0);
-        if (dead) break;
-        if (lane == 0) res_issued = items;
-        ++items;
-        const int n = MODE == kSumsFew ? w.rt : w.hi[1] > 0 ? 2 : 1;
-        if (MODE == kSumsMany) {
-          int bad = 0;
-          if (lane == 0) mbar_expect_tx(&res_full, n * L::kTile);
+        const int n = resident(w);
+        int bad = 0;
+        for (int t = 0; t < n; ++t, ++rs) {
+          const int slot = rs & 1;
+          bool go = true;
+          if (lane == 0 && rs >= 2) go = wait(&res_empty[slot], (rs >> 1) - 1);
+          dead = !__shfl_sync(0xffffffffu, (int)go, 0);
+          if (dead) break;
+          if (lane == 0) res_issued[slot] = rs >> 1;
+          if (lane == 0 && (MODE == kSumsMany || prm.q_tma)) mbar_expect_tx(&res_full[slot], L::kTile);
           __syncwarp();
-          for (int t = 0; t < n; ++t) load_keys(key_box(w, w.k0 + t * BM, &bad), sbase + t * L::kTile, &res_full);
-          if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
-        } else {
-          if (lane == 0 && prm.q_tma) mbar_expect_tx(&res_full, n * L::kTile);
-          __syncwarp();
-          bool arrive = false;
-          for (int t = 0; t < n; ++t) arrive = load_rows(w, w.r0 + t * BM, sbase + t * L::kTile, &res_full);
-          if (arrive) copies_done(&res_full);
+          if (MODE == kSumsMany) {
+            const int x = w.k0 / prm.box_rows + t * nb + lane;
+            load_keys(w, t, lane < nb ? box_page(w, x, &bad) : -1, sbase + slot * L::kTile, &res_full[slot]);
+          } else if (load_rows(w, w.r0 + t * BM, sbase + slot * L::kTile, &res_full[slot])) {
+            copies_done(&res_full[slot]);
+          }
         }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA
@@ -379,9 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (idx >= n_items) continue;
         const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
         if (w.steps == 0 || (MODE == kSumsFew && w.rt == 0)) continue;
-        const int R = w.q.cnt * a.g;
-        wait(&res_full, items);
-        ++items;
+        const int R = w.q.cnt * a.g, n = resident(w);
+        for (int t = 0; t < n; ++t) wait(&res_full[(rs + t) & 1], (rs + t) >> 1);
         for (int j = 0; j < w.steps; ++j, ++ld) {
           const int st = ld % NST;
           wait(&full[st], ld / NST);
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (before > 0) wait(&s_empty[buf], before - 1);
             tc_fence_after();
-            const uint64_t rd = res + (uint64_t)(t * (L::kTile >> 4));
+            const uint64_t rd = res + (uint64_t)(((rs + t) & 1) * (L::kTile >> 4));
             const uint32_t d = tmem + buf * BM;
             // few rows: only the columns that hold some, 32 at a time
             const uint32_t n = MODE == kSumsFew ? min(BM, (R - t * BM + 31) / 32 * 32) : BM;
@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (leader) umma_commit(&empty[st]);
           __syncwarp();
         }
-        if (leader) umma_commit(&res_empty);
+        for (int t = 0; t < n; ++t, ++rs)
+          if (leader) umma_commit(&res_empty[rs & 1]);
         __syncwarp();
       }
     } else if (warp == 3 && MODE != kStats) {
@@ -651,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {  // copies in flight land before the CTA exits
       for (int st = 0; st < NST; ++st)
         if (issued[st] >= 0) mbar_drain(&full[st], (issued[st] / NST) & 1);
-      if (res_issued >= 0) mbar_drain(&res_full, res_issued & 1);
+      for (int i = 0; i < 2; ++i)
+        if (res_issued[i] >= 0) mbar_drain(&res_full[i], res_issued[i] & 1);
     }
     for (int b = threadIdx.x; b < a.B; b += kThreads) atomicOr(&a.status[b], SPEC_DEV_TIMEOUT);
   }
