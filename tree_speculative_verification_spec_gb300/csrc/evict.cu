@@ -8,11 +8,11 @@
 // draft).
 //
 // Two kernels.  The selection (a CTA for each layer, row and kv-head) finds the
-// border weight digit by digit, 11, 11 and 10 bits of an order-preserving key
-// with a histogram in shared memory each, then lists the kept slots in one
-// ordered pass; equal weights at the border are taken from the lowest slot.
-// It is bound by the latency of its four passes over the weights (from L2 but
-// for the first).  The copy moves the listed rows of every layer, 16 bytes a
+// border weight digit by digit, 8 bits of an order-preserving key with a
+// histogram in shared memory each, then lists the kept slots in one
+// ordered pass; equal weights at the border are taken from the lowest slot.  Rows
+// of up to 16384 slots are read once and kept in shared memory; longer ones are
+// read again by every pass.  The copy moves the listed rows of every layer, 16 bytes a
 // lane: HBM.
 #include <algorithm>
 
@@ -20,9 +20,12 @@
 
 namespace spectree {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBins = 2048;
+constexpr int kSelThreads = 512, kSelShort = 128;  // per row, and per row of a table of up to kSelShortSlots
+constexpr int kSelShortSlots = 2048;
+constexpr int kSelBins = 256;       // of a digit
+constexpr int kSelCopies = 4;       // of the histogram, by lane: weights crowd a few exponents
+constexpr int kSelRun = 4;          // neighbouring slots per thread of the listing
+constexpr int kSelHeld = 16384;     // most weights held in shared memory
 constexpr int kGatherThreads = 256;
 constexpr int kGatherCtas = 8;      // per SM
 constexpr int kGatherVec = 4;       // 16-byte vectors of K and V per thread and step
@@ -40,7 +43,9 @@ struct EvictArgs {
   int32_t* new_len;
   int32_t* status;
   long long stride;                 // weights of one (layer, row, kv-head)
-  int layers, B, max_blocks, bs_log2, num_blocks, N, keep_max, first, last, Hkv, vec;  // vec: 16-byte vectors of a row
+  int layers, B, max_blocks, bs_log2, num_blocks, N, keep_max, first, last, Hkv;
+  int vec;                          // 16-byte vectors of a row
+  int held;                         // weights that the selection's shared memory holds
 };
 
 // A key whose order as a whole number is the weights': NaN lowest, -0 as +0.
@@ -50,141 +55,171 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// What row i of the call keeps, or the SPEC_DEV_* bits that stop it (the same in
-// every CTA).
+// What row i of the call keeps, or the SPEC_DEV_* bits that stop it, its pages
+// apart (the same in every thread of every CTA).
 struct EvictRow {
   int src, dst, len, kept, first, last, bad;
 };
+template <int kThreads>
 __device__ __forceinline__ EvictRow evict_row(const EvictArgs& a, int i) {
   EvictRow r = {a.src[i], a.dst[i], a.len[i], 0, 0, 0, 0};
   const int keep = a.keep ? a.keep[i] : a.keep_max;
-  if (r.src < 0 || r.src >= a.B || r.dst < 0 || r.dst >= a.B || r.src == r.dst || r.len < 0 || keep < 0 || keep > a.keep_max)
-    r.bad = SPEC_DEV_BAD_ROW;
   int other = 0;
-  for (int j = threadIdx.x; j < a.N; j += kSelThreads) other |= (j != i && a.dst[j] == r.dst) || a.src[j] == r.dst;
-  if (__syncthreads_or(other)) r.bad |= SPEC_DEV_BAD_ROW;
-  if (r.bad) return r;
+  for (int j = threadIdx.x; j < a.N; j += kThreads) other |= (j != i && a.dst[j] == r.dst) || a.src[j] == r.dst;
+  other = __syncthreads_or(other);
+  if (other || r.src < 0 || r.src >= a.B || r.dst < 0 || r.dst >= a.B || r.src == r.dst || r.len < 0 || keep < 0 || keep > a.keep_max) {
+    r.bad = SPEC_DEV_BAD_ROW;
+    return r;
+  }
   r.kept = min(keep, r.len);
   r.first = min(a.first, r.kept);
   r.last = min(a.last, r.kept - r.first);
-  if (r.len > (1 << 30) || r.len > (long long)a.max_blocks << a.bs_log2 || (a.weight && r.len > a.stride)) {
-    r.bad = SPEC_DEV_CAPACITY;
-    return r;
-  }
-  int bb = 0;
-  const int32_t *from = a.table + (size_t)r.src * a.max_blocks, *to = a.table + (size_t)r.dst * a.max_blocks;
-  const long long bs = 1LL << a.bs_log2;
-  const int held = (int)((r.len + bs - 1) >> a.bs_log2), need = (int)((r.kept + bs - 1) >> a.bs_log2);
-  for (int j = threadIdx.x; j < held; j += kSelThreads) bb |= from[j] < 0 || from[j] >= a.num_blocks;
-  for (int j = threadIdx.x; j < need; j += kSelThreads) bb |= to[j] < 0 || to[j] >= a.num_blocks;
-  if (__syncthreads_or(bb)) r.bad = SPEC_DEV_BAD_BLOCK;
+  if (r.len > (1 << 30) || r.len > (long long)a.max_blocks << a.bs_log2 || (a.weight && r.len > a.stride)) r.bad = SPEC_DEV_CAPACITY;
   return r;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ uint32_t hist[kSelBins];
-  __shared__ uint32_t s_warp[kSelWarps];
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ float held[];
+  __shared__ uint32_t hist[2][kSelBins][kSelCopies];
+  __shared__ uint32_t s_warp[kWarps];
   __shared__ uint32_t s_bin, s_left;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int h = blockIdx.x % a.Hkv, i = blockIdx.x / a.Hkv % a.N, layer = blockIdx.x / a.Hkv / a.N;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const EvictRow r = evict_row(a, i);
+  EvictRow r = evict_row<kThreads>(a, i);
+  const bool cached = r.len <= a.held;
+  const float* w = nullptr;
+  if (!r.bad) {
+    // the weights (eight loads at a time) and both rows' pages in one go
+    if (a.weight) w = a.weight + (((size_t)layer * a.B + r.src) * a.Hkv + h) * a.stride;
+    if (cached) {
+      for (int s0 = t; s0 < r.len; s0 += 8 * kThreads) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = w && s0 + e * kThreads < r.len ? w[s0 + e * kThreads] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (s0 + e * kThreads < r.len) held[s0 + e * kThreads] = x[e];
+      }
+    }
+    const int32_t *from = a.table + (size_t)r.src * a.max_blocks, *into = a.table + (size_t)r.dst * a.max_blocks;
+    const long long bs = 1LL << a.bs_log2;
+    const int pages = (int)((r.len + bs - 1) >> a.bs_log2), need = (int)((r.kept + bs - 1) >> a.bs_log2);
+    int bb = 0;
+    for (int j = t; j < pages; j += kThreads) bb |= from[j] < 0 || from[j] >= a.num_blocks;
+    for (int j = t; j < need; j += kThreads) bb |= into[j] < 0 || into[j] >= a.num_blocks;
+    for (int j = t; j < kSelBins * kSelCopies; j += kThreads) (&hist[0][0][0])[j] = 0;
+    if (__syncthreads_or(bb)) r.bad = SPEC_DEV_BAD_BLOCK;
+  }
   int32_t* out = a.slots + (((size_t)layer * a.N + i) * a.Hkv + h) * a.keep_max;
   if (layer == 0 && h == 0 && t == 0) {
     a.status[i] = r.bad;
     a.new_len[i] = r.bad ? 0 : r.kept;
   }
   const int kept = r.bad ? 0 : r.kept;
-  for (int j = kept + t; j < a.keep_max; j += kSelThreads) out[j] = -1;
+  for (int j = kept + t; j < a.keep_max; j += kThreads) out[j] = -1;
   if (kept == 0) return;
-  const float* w = a.weight ? a.weight + (((size_t)layer * a.B + r.src) * a.Hkv + h) * a.stride : nullptr;
   float* to = a.weight ? a.weight + (((size_t)layer * a.B + r.dst) * a.Hkv + h) * a.stride : nullptr;
   const int begin = r.first, end = r.len - r.last;  // the slots that compete
   uint32_t want = kept - r.first - r.last;          // how many of them stay
-  auto key_at = [&](int s) -> uint32_t { return w ? weight_key(w[s]) : 0u; };
+  auto weight_at = [&](int s) -> float { return cached ? held[s] : w ? w[s] : 0.0f; };
 
   // border: every key above it stays, and `want` of those equal to it
-  uint32_t border = 0, above_all = want >= (uint32_t)(end - begin) ? 1u : 0u;
-  if (!above_all && want > 0) {
+  uint32_t border = 0;
+  const bool all = want >= (uint32_t)(end - begin);
+  if (!all && want > 0) {
     uint32_t mask = 0;
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-      for (int j = t; j < kSelBins; j += kSelThreads) hist[j] = 0;
-      __syncthreads();
-      for (int s = begin + t; s < end; s += kSelThreads) {
-        const uint32_t k = key_at(s);
-        if ((k & mask) == border) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+    for (int pass = 0, shift = 24; pass < 4; ++pass, shift -= 8) {
+      for (int s = begin + t; s < end; s += kThreads) {
+        const uint32_t k = weight_key(weight_at(s));
+        if ((k & mask) == border) atomicAdd(&hist[pass & 1][k >> shift & 255][lane % kSelCopies], 1u);
       }
       __syncthreads();
-      // the bin where the count from the top reaches `want`: thread t holds bins
-      // 4 t .. 4 t + 3 counted from the top
-      uint32_t c[4], sum = 0;
+      if (warp == 0) {
+        // the bin where the count from the top reaches `want`: eight bins a lane
+        uint32_t c[8], sum = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        c[e] = hist[kSelBins - 1 - (4 * t + e)];
-        sum += c[e];
-      }
-      uint32_t incl = sum;
+        for (int e = 0; e < 8; ++e) {
+          const uint4 x = *reinterpret_cast<const uint4*>(hist[pass & 1][255 - (8 * lane + e)]);
+          sum += c[e] = x.x + x.y + x.z + x.w;
+        }
+        uint32_t at = sum;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) s_warp[warp] = incl;
-      __syncthreads();
-      uint32_t before = incl - sum;
-      for (int k = 0; k < warp; ++k) before += s_warp[k];
-      if (before < want && want <= before + sum) {
-        uint32_t at = before;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += y;
+        }
+        at -= sum;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 8; ++e) {
           if (at < want && want <= at + c[e]) {
-            s_bin = kSelBins - 1 - (4 * t + e);
+            s_bin = 255 - (8 * lane + e);
             s_left = want - at;
           }
           at += c[e];
         }
+      } else {
+        for (int j = t - 32; j < kSelBins * kSelCopies; j += kThreads - 32) (&hist[~pass & 1][0][0])[j] = 0;
       }
       __syncthreads();
       border |= s_bin << shift;
       want = s_left;
-      mask |= (uint32_t)(bins - 1) << shift;
+      mask |= 255u << shift;
     }
   }
 
-  // the kept slots in order: counts of larger and of equal keys (the equal ones
-  // stay while there is want) go through one scan
+  // the kept slots in order, kSelRun neighbours to a thread: counts of larger and
+  // of equal keys (the equal ones stay while there is want) go through one scan
   uint32_t big = 0, equal = 0;  // of the slots before this round
-  for (int s0 = 0; s0 < r.len; s0 += kSelThreads) {
-    const int s = s0 + t;
-    uint32_t g = 0, q = 0;
-    if (s < r.len) {
-      if (s < begin || s >= end || above_all) g = 1;
+  for (int s0 = 0; s0 < r.len; s0 += kThreads * kSelRun) {
+    const int s = s0 + t * kSelRun;
+    uint32_t g = 0, q = 0;  // bit e: slot s + e
+    float x[kSelRun];
+#pragma unroll
+    for (int e = 0; e < kSelRun; ++e) x[e] = s + e < r.len ? weight_at(s + e) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < kSelRun; ++e) {
+      if (s + e >= r.len) continue;
+      if (s + e < begin || s + e >= end || all) g |= 1u << e;
       else if (want > 0) {
-        const uint32_t k = key_at(s);
-        g = k > border;
-        q = k == border;
+        const uint32_t k = weight_key(x[e]);
+        g |= (uint32_t)(k > border) << e;
+        q |= (uint32_t)(k == border) << e;
       }
     }
-    const uint32_t mg = __ballot_sync(0xffffffffu, g), mq = __ballot_sync(0xffffffffu, q);
+    const uint32_t mine = __popc(g) | (uint32_t)__popc(q) << 16;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
     __syncthreads();  // s_warp of the round before has been read
-    if (lane == 0) s_warp[warp] = __popc(mg) | (uint32_t)__popc(mq) << 16;
+    if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    uint32_t bg = big, bq = equal;
-    for (int k = 0; k < kSelWarps; ++k) {
+    uint32_t before = incl - mine, total = 0;  // 16 bits each: at most 2048 of a round
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
       const uint32_t x = s_warp[k];
-      if (k < warp) bg += x & 0xffffu, bq += x >> 16;
-      big += x & 0xffffu;
-      equal += x >> 16;
+      before += k < warp ? x : 0;
+      total += x;
     }
-    const uint32_t lower = (1u << lane) - 1;
-    bg += __popc(mg & lower);
-    bq += __popc(mq & lower);
-    if (g || (q && bq < want)) {
-      const uint32_t at = bg + min(bq, want);
-      out[at] = s;
-      if (to) to[at] = w[s];
+    uint32_t bg = big + (before & 0xffffu), bq = equal + (before >> 16);
+#pragma unroll
+    for (int e = 0; e < kSelRun; ++e) {
+      const bool heavy = g >> e & 1, even = q >> e & 1;
+      if (heavy || (even && bq < want)) {
+        const uint32_t at = bg + min(bq, want);
+        out[at] = s + e;
+        if (to) to[at] = x[e];
+      }
+      bg += heavy;
+      bq += even;
     }
+    big += total & 0xffffu;
+    equal += total >> 16;
   }
 }
 
@@ -277,7 +312,14 @@ extern "C" spec_status spec_kv_evict(void* const* k_caches, void* const* v_cache
   a.Hkv = Hkv;
   a.vec = D * (dtype == SPEC_F32 ? 4 : 2) / 16;
   cudaStream_t st = (cudaStream_t)stream;
-  evict_select_kernel<<<(unsigned)heads, kSelThreads, 0, st>>>(a);
+  // room for the weights of the longest row that the table and the weights allow
+  const long long most = std::min((long long)max_blocks << a.bs_log2, weight ? weight_stride : (1LL << 30));
+  a.held = (int)std::min<long long>(most, kSelHeld);
+  const int dyn = a.held * (int)sizeof(float);
+  const bool small = most <= kSelShortSlots;
+  const auto select = small ? evict_select_kernel<kSelShort> : evict_select_kernel<kSelThreads>;
+  if (cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess) return SPEC_ERR_CUDA;
+  select<<<(unsigned)heads, small ? kSelShort : kSelThreads, dyn, st>>>(a);
   SPEC_LAUNCH_CHECK();
   if (keep_max == 0) return SPEC_OK;
   const int rows = kGatherThreads * kGatherVec / a.vec, per_head = (keep_max + rows - 1) / rows;

@@ -45,32 +45,30 @@ struct RopeArgs {
   int max_blocks, bs_log2, num_blocks, B, T, n_max, Hq, Hkv;
 };
 
-// One 16-byte vector as fp32 values, and back (rounded to nearest).
+// One 16-byte vector as pairs of fp32 values, and back (rounded to nearest).
 template <typename T> struct Vec;
 template <> struct Vec<float> {
   static constexpr int N = 4;
-  __device__ static void open(const uint4& u, float* x) {
-    x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+  __device__ static void open(const uint4& u, float2* x) {
+    x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
   }
-  __device__ static uint4 close(const float* x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  __device__ static uint4 close(const float2* x) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
   }
 };
 template <> struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  __device__ static void open(const uint4& u, float* x) {
+  __device__ static void open(const uint4& u, float2* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  __device__ static uint4 close(const float* x) {
+  __device__ static uint4 close(const float2* x) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      const __nv_bfloat162 h = __float22bfloat162_rn(x[i]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -87,11 +85,12 @@ __device__ __forceinline__ int rope_check(const RopeArgs& a, int off, int n, int
 // Token tiles of `tt` tokens are numbered from floor(tree_off[b] / tt) + b: at
 // least ceil(n_b / tt) of them lie before the next request's first, and
 // floor(T / tt) + B cover every batch of T tokens without a prefix sum.
-template <typename T, int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs a, int tt) {
-  constexpr int VE = Vec<T>::N, LPH = D / (2 * VE), GROUPS = kRopeThreads / LPH, U = 3;
-  __shared__ float s_cos[kRopeTokens][D / 2], s_sin[kRopeTokens][D / 2];
-  __shared__ float s_row[GROUPS][D];  // a normalised row (pairs that cross lanes)
+template <typename T, int D, int MODE>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const RopeArgs a, int tt) {
+  constexpr int VE = Vec<T>::N, LPH = D / (2 * VE), GROUPS = kRopeThreads / LPH, U = 2;
+  __shared__ __align__(16) float s_cos[kRopeTokens][D / 2], s_sin[kRopeTokens][D / 2], s_norm[2][D];
+  __shared__ float s_row[MODE == kRopeShared ? GROUPS : 1][D];  // a normalised row (pairs that cross lanes)
+  __shared__ long long s_slot[kRopeTokens];  // row of the token's slot in kv-head 0 of its page
   __shared__ int s_bad[kRopeTokens];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tile = blockIdx.x, t = threadIdx.x;
@@ -117,134 +116,160 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
   if (at < 0 || at * tt >= n) return;
   const int u0 = (int)at * tt, nt = min(tt, n - u0);
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
-  // a bad page leaves the whole request untouched, so every CTA looks at all of them
-  int bb = 0;
-  for (int pg = (P >> a.bs_log2) + t; pg <= (P + n - 1) >> a.bs_log2; pg += kRopeThreads) bb |= bt[pg] < 0 || bt[pg] >= a.num_blocks;
 
-  const int heads = a.Hq + 2 * a.Hkv, units = nt * heads;
+  const int heads = a.Hq + 2 * a.Hkv;
   const int group = t / LPH, c = t % LPH;
   // lane c's vectors: the rotated ones by pairs of halves, the others by two
-  const int rv = a.mode == kRopeHalves ? a.rot / (2 * VE) : 0, half = D / (2 * VE);
+  const int rv = MODE == kRopeHalves ? a.rot / (2 * VE) : 0, half = D / (2 * VE);
   const int va = c < rv ? c : rv + c, vb = c < rv ? c + rv : half + c;
+  const char* rows = a.qkv + (long long)(off + u0) * a.row_bytes;
   uint4 lo[U] = {}, hi[U] = {};
-  auto load = [&](int first) {
+  int k = 0, h = group;  // this group's next (token, head), GROUPS heads on
+  auto load = [&]() {
+    int kk = k, hh = h;
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
-      const int unit = first + e * GROUPS;
-      if (unit < units) {
-        const char* row = a.qkv + (long long)(off + u0 + unit / heads) * a.row_bytes + (size_t)(unit % heads) * D * sizeof(T);
+    for (int e = 0; e < U; ++e, hh += GROUPS) {
+      while (hh >= heads) hh -= heads, ++kk;
+      if (kk < nt) {
+        const char* row = rows + (long long)kk * a.row_bytes + (size_t)hh * (D * sizeof(T));
         lo[e] = *reinterpret_cast<const uint4*>(row + va * 16);
         hi[e] = *reinterpret_cast<const uint4*>(row + vb * 16);
       }
     }
   };
-  load(group);
+  load();
+  // a bad page leaves the whole request untouched, so every CTA looks at all of them
+  int bb = 0;
+  for (int pg = (P >> a.bs_log2) + t; pg <= (P + n - 1) >> a.bs_log2; pg += kRopeThreads) bb |= bt[pg] < 0 || bt[pg] >= a.num_blocks;
+  if (t < nt) {
+    const int s = P + u0 + t;
+    s_slot[t] = (((long long)bt[s >> a.bs_log2] * a.Hkv) << a.bs_log2) + (s & ((1 << a.bs_log2) - 1));
+  }
+  for (int i = t; i < 2 * D; i += kRopeThreads) {
+    const T* norm = static_cast<const T*>(i < D ? a.q_norm : a.k_norm);
+    if (norm) s_norm[i / D][i % D] = to_f32(norm[i % D]);
+  }
   // the tokens' angles
   const int np = a.rot / 2;
   const int base = a.pos_base ? a.pos_base[b] : P;
   for (int i = t; i < nt * np; i += kRopeThreads) {
-    const int k = i / np, pair = i - k * np;
+    const int j = i / np, pair = i - j * np;
     const int ax = a.axis ? a.axis[pair] : 0;
     bool ok = ax >= 0 && ax < a.axes;
     long long p = base;
-    if (ok) p += a.pos ? a.pos[(size_t)ax * a.T + off + u0 + k] : u0 + k;
+    if (ok) p += a.pos ? a.pos[(size_t)ax * a.T + off + u0 + j] : u0 + j;
     ok = ok && p >= 0 && p < kRopeMaxPos;
     if (!ok) {
-      s_bad[k] = 1;
+      s_bad[j] = 1;
       continue;
     }
     const double turns = (double)p * ((double)a.inv_freq[pair] * 0.15915494309189535);  // 1 / 2pi
     float sn, cs;
     sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
-    s_cos[k][pair] = cs;
-    s_sin[k][pair] = sn;
+    s_cos[j][pair] = cs;
+    s_sin[j][pair] = sn;
   }
   bb = __syncthreads_or(bb);
   if (t == 0) {
     int bad = bb ? SPEC_DEV_BAD_BLOCK : 0;
-    for (int k = 0; k < nt; ++k) bad |= s_bad[k] ? SPEC_DEV_BAD_POSITION : 0;
+    for (int j = 0; j < nt; ++j) bad |= s_bad[j] ? SPEC_DEV_BAD_POSITION : 0;
     if (bad) atomicOr(&a.status[b], bad);
   }
   if (bb) return;
 
-  for (int first = group; first - group < units; first += U * GROUPS) {
-    if (first != group) load(first);
+  const bool norms = a.q_norm || a.k_norm;
+  for (int done = 0; done < nt * heads; done += U * GROUPS) {
+    if (done > 0) load();
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
-      const int unit = first + e * GROUPS;
-      const bool there = unit < units;  // shuffles below: every lane of the warp comes along
-      const int k = there ? unit / heads : 0, h = there ? unit - k * heads : heads;
+    for (int e = 0; e < U; ++e, h += GROUPS) {
+      while (h >= heads) h -= heads, ++k;
+      const bool there = k < nt;  // shuffles below: every lane of the warp comes along
       const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-      uint4 oa = lo[e], ob = hi[e];
       const bool turn = there && !is_v;
       if (__any_sync(0xffffffffu, turn)) {
-        float x[2 * VE];
-        Vec<T>::open(oa, x);
-        Vec<T>::open(ob, x + VE);
-        const void* norm = is_q ? a.q_norm : a.k_norm;
-        if (a.q_norm || a.k_norm) {
-          float ss = 0.0f;
+        float2 x[VE];  // the first vector's pairs, then the second's
+        Vec<T>::open(lo[e], x);
+        Vec<T>::open(hi[e], x + VE / 2);
+        if (norms) {
+          float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int i = 0; i < 2 * VE; ++i) ss = fmaf(x[i], x[i], ss);
+          for (int i = 0; i < VE; ++i) s2 = __ffma2_rn(x[i], x[i], s2);
+          float ss = s2.x + s2.y;
 #pragma unroll
           for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          if (norm && turn) {
-            const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-            float w[2 * VE];
-            Vec<T>::open(static_cast<const uint4*>(norm)[va], w);
-            Vec<T>::open(static_cast<const uint4*>(norm)[vb], w + VE);
+          if (turn && (is_q ? a.q_norm : a.k_norm)) {
+            const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+            const float2 r2 = make_float2(r, r);
+            const float* w = s_norm[is_q ? 0 : 1];
 #pragma unroll
-            for (int i = 0; i < 2 * VE; ++i) x[i] = x[i] * r * w[i];
+            for (int i = 0; i < VE; i += 2) {
+              const float4 w4 = *reinterpret_cast<const float4*>(w + (i < VE / 2 ? va * VE + 2 * i : vb * VE + 2 * i - VE));
+              x[i] = __fmul2_rn(__fmul2_rn(x[i], r2), make_float2(w4.x, w4.y));
+              x[i + 1] = __fmul2_rn(__fmul2_rn(x[i + 1], r2), make_float2(w4.z, w4.w));
+            }
           }
         }
-        if (a.mode == kRopeHalves) {
-          if (c < rv) {
+        if (turn) {
+          if (MODE == kRopeHalves) {
+            if (c < rv) {
+#pragma unroll
+              for (int i = 0; i < VE / 2; i += 2) {
+                const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[k][c * VE + 2 * i]), n4 = *reinterpret_cast<const float4*>(&s_sin[k][c * VE + 2 * i]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const float2 cs = j ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y), sn = j ? make_float2(n4.z, n4.w) : make_float2(n4.x, n4.y);
+                  const float2 y = x[i + j], z = x[VE / 2 + i + j];
+                  x[i + j] = __ffma2_rn(y, cs, __fmul2_rn(z, make_float2(-sn.x, -sn.y)));
+                  x[VE / 2 + i + j] = __ffma2_rn(z, cs, __fmul2_rn(y, sn));
+                }
+              }
+            }
+          } else if (MODE == kRopeNeighbours) {
 #pragma unroll
             for (int i = 0; i < VE; ++i) {
-              const float cs = s_cos[k][c * VE + i], sn = s_sin[k][c * VE + i], y = x[i];
-              x[i] = y * cs - x[VE + i] * sn;
-              x[VE + i] = x[VE + i] * cs + y * sn;
+              const int pair = i < VE / 2 ? va * (VE / 2) + i : vb * (VE / 2) + i - VE / 2;
+              if (pair < np) {
+                const float cs = s_cos[k][pair], sn = s_sin[k][pair];
+                x[i] = make_float2(x[i].x * cs - x[i].y * sn, x[i].y * cs + x[i].x * sn);
+              }
             }
           }
-        } else if (a.mode == kRopeNeighbours) {
-#pragma unroll
-          for (int i = 0; i < 2 * VE; i += 2) {
-            const int pair = (i < VE ? va * VE + i : vb * VE + i - VE) / 2;
-            if (pair < np) {
-              const float cs = s_cos[k][pair], sn = s_sin[k][pair], y = x[i];
-              x[i] = y * cs - x[i + 1] * sn;
-              x[i + 1] = x[i + 1] * cs + y * sn;
-            }
-          }
-        } else {  // halves whose length is no multiple of a vector: through shared memory
+        }
+        if (MODE == kRopeShared) {  // halves whose length is no multiple of a vector: through shared memory
           float* row = s_row[group];
 #pragma unroll
-          for (int i = 0; i < VE; ++i) row[va * VE + i] = x[i], row[vb * VE + i] = x[VE + i];
+          for (int i = 0; i < VE; ++i) {
+            const int el = i < VE / 2 ? va * VE + 2 * i : vb * VE + 2 * i - VE;
+            row[el] = x[i].x;
+            row[el + 1] = x[i].y;
+          }
           __syncwarp();
+          auto turned = [&](int el, float v) {
+            if (!there || el >= 2 * np) return v;
+            return el < np ? row[el] * s_cos[k][el] - row[el + np] * s_sin[k][el] : row[el] * s_cos[k][el - np] + row[el - np] * s_sin[k][el - np];
+          };
 #pragma unroll
-          for (int i = 0; i < 2 * VE; ++i) {
-            const int at = i < VE ? va * VE + i : vb * VE + i - VE;
-            if (at < np) x[i] = row[at] * s_cos[k][at] - row[at + np] * s_sin[k][at];
-            else if (at < 2 * np) x[i] = row[at] * s_cos[k][at - np] + row[at - np] * s_sin[k][at - np];
+          for (int i = 0; i < VE; ++i) {
+            const int el = i < VE / 2 ? va * VE + 2 * i : vb * VE + 2 * i - VE;
+            x[i] = make_float2(turned(el, x[i].x), turned(el + 1, x[i].y));
           }
           __syncwarp();
         }
         if (turn) {
-          oa = Vec<T>::close(x);
-          ob = Vec<T>::close(x + VE);
+          lo[e] = Vec<T>::close(x);
+          hi[e] = Vec<T>::close(x + VE / 2);
         }
       }
       if (there && !s_bad[k]) {
         char* dst;
         if (is_q) {
-          dst = a.q_out + ((size_t)(off + u0 + k) * a.Hq + h) * D * sizeof(T);
+          dst = a.q_out + ((size_t)(off + u0 + k) * a.Hq + h) * (D * sizeof(T));
         } else {
-          const int s = P + u0 + k, hk = h - a.Hq - (is_v ? a.Hkv : 0);
-          const long long slot = (((long long)bt[s >> a.bs_log2] * a.Hkv + hk) << a.bs_log2) + (s & ((1 << a.bs_log2) - 1));
-          dst = (is_v ? a.v_cache : a.k_cache) + slot * (D * (long long)sizeof(T));
+          const int hk = h - a.Hq - (is_v ? a.Hkv : 0);
+          dst = (is_v ? a.v_cache : a.k_cache) + (s_slot[k] + ((long long)hk << a.bs_log2)) * (D * (long long)sizeof(T));
         }
-        *reinterpret_cast<uint4*>(dst + va * 16) = oa;
-        *reinterpret_cast<uint4*>(dst + vb * 16) = ob;
+        *reinterpret_cast<uint4*>(dst + va * 16) = lo[e];
+        *reinterpret_cast<uint4*>(dst + vb * 16) = hi[e];
       }
     }
   }
@@ -264,7 +289,9 @@ static cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D>, a, tt);
+  const cudaError_t e = a.mode == kRopeHalves       ? cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, kRopeHalves>, a, tt)
+                        : a.mode == kRopeNeighbours ? cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, kRopeNeighbours>, a, tt)
+                                                    : cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, kRopeShared>, a, tt);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
