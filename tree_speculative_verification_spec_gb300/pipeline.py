@@ -1,14 +1,19 @@
 """A request's passes through the C ABI: buffers + the calls in order.
 
 PromptPass owns the outputs and workspace of one batch of prompts (or of their
-next chunks) and enqueues spec_kv_append -> spec_prompt_attention.
+next chunks) and enqueues spec_kv_append (or spec_rope_append, from a
+projection's output) -> spec_prompt_attention.
 
 VerifyPass owns the device outputs and workspaces of one batch shape and
 enqueues, on one stream and with no host synchronisation:
-  spec_tree_mask_build -> [spec_kv_append] -> spec_tree_attention ->
-  spec_tree_verify_{greedy, stochastic} -> [spec_path_logprobs] ->
-  spec_kv_commit.
+  spec_tree_mask_build -> [spec_kv_append or spec_rope_append] ->
+  spec_tree_attention -> spec_tree_verify_{greedy, stochastic} ->
+  [spec_path_logprobs] -> spec_kv_commit.
 Allocation happens once, in the constructor; run() only launches.
+
+CacheBudget holds the attention weight that cached slots gather over those
+passes (spec_attention_weight) and cuts rows to a budget by it
+(spec_kv_evict).
 """
 from dataclasses import dataclass
 
@@ -59,6 +64,27 @@ class DeviceBatch:
                    uniforms=d(w.uniforms), scale=w.scale)
 
 
+@dataclass
+class Rotary:
+    """How a layer's query and key heads are normalised and rotated on their way
+    from the projection (spec_rope_append)."""
+    inv_freq: torch.Tensor = None  # float32 [rot_dim / 2], radians per position
+    rot_dim: int = 0
+    axis: torch.Tensor = None      # int32 [rot_dim / 2], for axes > 1
+    axes: int = 1
+    pairing: int = S.SPEC_ROPE_HALVES
+    q_norm: torch.Tensor = None    # [D] of the caches' dtype, or None
+    k_norm: torch.Tensor = None
+    eps: float = 1e-6
+
+    def append(self, qkv, q, k_cache, v_cache, block_table, prefix_len, tree_off, n_max, status, pos_base=None, pos=None, stream=None):
+        num_blocks, Hkv, block_size, D = k_cache.shape
+        T, Hq, _ = q.shape
+        S.spec_rope_append(qkv, self.q_norm, self.k_norm, self.eps, self.inv_freq, self.axis, self.rot_dim, self.pairing, pos_base, pos, self.axes, q, k_cache,
+                           v_cache, block_table, block_table.shape[1], block_size, num_blocks, prefix_len, tree_off, tree_off.numel() - 1, T, n_max, Hq, Hkv, D,
+                           status, stream)
+
+
 def _clear(status, stream):
     with torch.cuda.stream(stream):  # None: the current one
         status.zero_()
@@ -80,12 +106,18 @@ class PromptPass:
         self.ws = torch.empty(S.spec_prompt_workspace_size(*self.size), dtype=torch.uint8, device=q.device)
         self.status = torch.zeros(max(self.size[0], 1), dtype=torch.int32, device=q.device)
 
-    def run(self, prompt_kv=None, stream=None):
+    def run(self, prompt_kv=None, stream=None, prompt_qkv=None, rotary=None, pos_base=None, pos=None):
         """prompt_kv: (k_new, v_new) rows [T][Hkv][D] put behind the prefix
-        first, or None when they are already in the cache.  status is this
-        run's: a request that an earlier one flagged is computed again."""
+        first, or None when they are already in the cache.  prompt_qkv with
+        rotary instead: a projection's rows, normalised and rotated into q and
+        the cache (pos_base int32 [B], None: the prefix; pos int32 [axes][T],
+        None: the row's index).  status is this run's: a request that an earlier
+        one flagged is computed again."""
         B, T, n_max, max_prefix, Hq, Hkv, D = self.size
         _clear(self.status, stream)
+        if prompt_qkv is not None:
+            rotary.append(prompt_qkv, self.q, self.k_cache, self.v_cache, self.block_table, self.prefix_len, self.seq_off, n_max, self.status, pos_base, pos,
+                          stream)
         if prompt_kv is not None:
             S.spec_kv_append(*prompt_kv, self.k_cache, self.v_cache, self.block_table, self.block_table.shape[1],
                              self.block_size, self.num_blocks, self.prefix_len, self.seq_off, B, n_max, Hkv, D,
@@ -143,6 +175,13 @@ class VerifyPass:
         S.spec_kv_append(k_new, v_new, b.k_cache, b.v_cache, b.block_table, b.max_blocks, b.block_size,
                          b.num_blocks, b.prefix_len, b.tree_off, b.B, b.n_max, b.Hkv, b.D, self.status, stream)
 
+    def project(self, qkv, rotary, pos_base=None, stream=None):
+        """A projection's rows of the tree, normalised and rotated into the
+        batch's q and slots prefix_len + u (before attention, after the mask
+        build): node u's position is pos_base[b] (None: the prefix) plus its depth."""
+        b = self.batch
+        rotary.append(qkv, b.q, b.k_cache, b.v_cache, b.block_table, b.prefix_len, b.tree_off, b.n_max, self.status, pos_base, self.depth, stream)
+
     def attention(self, flags=S.SPEC_ATTN_AUTO, stream=None):
         b = self.batch
         S.spec_tree_attention(b.q, b.k_cache, b.v_cache, b.block_table, b.max_blocks, b.block_size, b.num_blocks,
@@ -183,10 +222,13 @@ class VerifyPass:
                          b.prefix_len, self.path, b.n_max, self.accept_len, b.B, b.Hkv, b.D, self.new_len,
                          self.status, stream)
 
-    def run(self, mode="stochastic", attn_flags=S.SPEC_ATTN_AUTO, commit=True, stream=None, tree_kv=None):
+    def run(self, mode="stochastic", attn_flags=S.SPEC_ATTN_AUTO, commit=True, stream=None, tree_kv=None, tree_qkv=None, rotary=None, pos_base=None):
         """tree_kv: (k_new, v_new) rows appended before attention, or None when
-        the tree K/V are already in the cache."""
+        the tree K/V are already in the cache; tree_qkv with rotary instead: a
+        projection's rows (see project())."""
         self.mask_build(stream)
+        if tree_qkv is not None:
+            self.project(tree_qkv, rotary, pos_base, stream)
         if tree_kv is not None:
             self.append(*tree_kv, stream=stream)
         self.attention(attn_flags, stream)
@@ -195,3 +237,53 @@ class VerifyPass:
             self.logprobs(stream)
         if commit:
             self.commit(stream)
+
+
+class CacheBudget:
+    """What the attention of every layer gave each slot of a block table's rows,
+    and eviction by it.  weight is float32 [layers][rows][Hkv][slots], by table
+    row; a pass over part of the table says at which row its batch starts."""
+
+    def __init__(self, layers, rows, Hkv, slots, decay=1.0, device="cuda"):
+        self.weight = torch.zeros((layers, rows, Hkv, slots), dtype=torch.float32, device=device)
+        self.layers, self.rows, self.Hkv, self.slots, self.decay = layers, rows, Hkv, slots, decay
+        self._ws = torch.empty(0, dtype=torch.uint8, device=device)
+
+    def reserve(self, B, T, n_max, max_prefix, Hq, D):
+        """Workspace for passes of up to these sizes (observing a larger one
+        first makes it grow, which a captured graph must not)."""
+        need = S.spec_weight_workspace_size(B, T, n_max, max_prefix, Hq, self.Hkv, D)
+        if self._ws.numel() < need:
+            self._ws = torch.empty(need, dtype=torch.uint8, device=self._ws.device)
+
+    def _observe(self, layer, row, q, k_cache, block_table, prefix_len, off, path, accept_len, window, n_max, max_prefix, scale, status, stream):
+        num_blocks, Hkv, block_size, D = k_cache.shape
+        T, Hq, _ = q.shape
+        B = off.numel() - 1
+        if not (0 <= layer < self.layers and 0 <= row and row + B <= self.rows and Hkv == self.Hkv):
+            raise ValueError("the pass's layer, rows or heads are not the budget's")
+        self.reserve(B, T, n_max, max_prefix, Hq, D)
+        w = self.weight[layer, row:row + B]
+        S.spec_attention_weight(q, k_cache, block_table, block_table.shape[1], block_size, num_blocks, prefix_len, off, path, accept_len, window, B, T, n_max,
+                                max_prefix, Hq, Hkv, D, scale, self.decay, w, w, self.slots, self._ws, status, stream)
+
+    def observe_prompt(self, layer, p, window=0, row=0, stream=None):
+        """The rows of a PromptPass (their last `window`), after its run()."""
+        _, _, n_max, max_prefix, *_ = p.size
+        self._observe(layer, row, p.q, p.k_cache, p.block_table, p.prefix_len, p.seq_off, None, None, window, n_max, max_prefix, p.scale, p.status, stream)
+
+    def observe_path(self, layer, v, window=0, row=0, stream=None):
+        """The accepted path of a VerifyPass, after its commit()."""
+        b = v.batch
+        self._observe(layer, row, b.q, b.k_cache, b.block_table, b.prefix_len, b.tree_off, v.path, v.accept_len, window, b.n_max, b.max_prefix, b.scale, v.status,
+                      stream)
+
+    def evict(self, k_ptrs, v_ptrs, block_table, block_size, num_blocks, src, dst, length, keep_max, first, last, D, dtype, keep=None, stream=None):
+        """Rows src (int32 [N], of `length` slots) cut to rows dst, which have
+        pages for them.  Returns (slots, new_len, status) of spec_kv_evict."""
+        N, i32 = src.numel(), dict(dtype=torch.int32, device=src.device)
+        slots = torch.empty((self.layers, N, self.Hkv, keep_max), **i32)
+        new_len, status = torch.empty(N, **i32), torch.empty(N, **i32)
+        S.spec_kv_evict(k_ptrs, v_ptrs, self.layers, block_table, self.rows, block_table.shape[1], block_size, num_blocks, src, dst, length, keep, N, keep_max,
+                        first, last, self.weight, self.slots, self.Hkv, D, dtype, slots, new_len, status, stream)
+        return slots, new_len, status
