@@ -365,6 +365,84 @@ def test_weight_long_and_wide_batches(lens, prefix, dtype):
 
 
 @DTYPES
+@pytest.mark.parametrize("spread", [0.0, 6.0, 40.0])
+@pytest.mark.parametrize("lens,prefix", [([1, 2], [2000, 300]), ([3], [9000]), ([8, 1, 4], [100, 30, 20000])], ids=["short", "one", "long"])
+def test_weight_few_rows_with_steep_scores(lens, prefix, spread, dtype):
+    d = paged_batch(42, lens, prefix, 8, 2, 64, 16, dtype, spread=spread)
+    before = _before(d)
+    got, st = _weight(d, before)
+    assert not st.any()
+    _weight_holds(d, got, before)
+
+
+@DTYPES
+def test_weight_of_a_mixed_batch(dtype):
+    """Rows for every way through the kernels in one call: none, one, a few, a
+    tile, many; keys from none to more than a cluster holds."""
+    lens = [0, 1, 8, 9, 33, 64, 65, 300, 1, 0, 2]
+    prefix = [700, 0, 2500, 2500, 100, 0, 900, 50, 36000, 0, 12]
+    d = paged_batch(44, lens, prefix, 8, 2, 64, 16, dtype, extra_rows=3)
+    before = _before(d)
+    got, st = _weight(d, before)
+    assert not st.any()
+    _weight_holds(d, got, before)
+    got, st = _weight(d, before, window=5)
+    assert not st.any()
+    _weight_holds(d, got, before, window=5)
+
+
+@DTYPES
+def test_weight_at_a_scale_of_zero(dtype):
+    d = paged_batch(46, [3, 50], [20, 300], 8, 2, 64, 16, dtype)
+    d["scale"] = 0.0
+    before = _before(d)
+    got, st = _weight(d, before)
+    assert not st.any()
+    _weight_holds(d, got, before)
+
+
+@DTYPES
+@pytest.mark.parametrize("n", [1, 20], ids=["few", "rows"])
+def test_weight_bad_blocks_do_not_touch_other_requests(n, dtype):
+    """More requests than are numbered at a time, with bad pages among the last:
+    what one CTA flags, another may see before it numbers its items."""
+    B = 300
+    d = paged_batch(48, [n] * B, [(i * 37) % 900 for i in range(B)], 8, 2, 64, 16, dtype)
+    bad = [3, 255, 256, 270, 299]
+    for b in bad:
+        d["table"][b, 0] = d["nb"] + 5
+    before = _before(d)
+    for _ in range(3):
+        got, st = _weight(d, before)
+        assert st.tolist() == [S.SPEC_DEV_BAD_BLOCK if b in bad else 0 for b in range(B)]
+        table = d["table"].clone()
+        d["table"][bad, 0] = 0
+        ref, tol = weight_reference(d, before, 0.75)
+        d["table"] = table
+        for b in range(B):
+            if b not in bad:
+                mine = ~ref[b].isnan()
+                assert ((got[b].double() - ref[b]).abs()[mine] <= tol[b][mine]).all() and (got[b][~mine] == 7.0).all()
+
+
+@DTYPES
+def test_weight_two_calls_at_once(dtype):
+    """Two streams, a workspace each."""
+    ds = [paged_batch(s, [2, 40], [3000, 200], 8, 2, 64, 16, dtype) for s in (50, 51)]
+    befores, outs, streams = [_before(d) for d in ds], [], [torch.cuda.Stream() for _ in ds]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = []
+        for d, before, stream in zip(ds, befores, streams):
+            with torch.cuda.stream(stream):
+                outs.append(_weight(d, before, stream=stream))
+    torch.cuda.synchronize()
+    for d, before, (got, st) in zip(ds, befores, outs):
+        assert not st.any()
+        _weight_holds(d, got, before)
+
+
+@DTYPES
 @pytest.mark.parametrize("Hq,Hkv", [(256, 2), (96, 1), (200, 1)], ids=["128", "96", "200"])
 def test_weight_wide_groups(Hq, Hkv, dtype):
     d = paged_batch(40, [5, 1, 2], [0, 700, 33], Hq, Hkv, 64, 16, dtype)

@@ -339,7 +339,9 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
   a.g = Hq / Hkv;
   a.splits = plan.splits;
   a.chunk = plan.chunk;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  // The tensor-core kernels hide a key by -inf before the scaling, and -inf * 0 is
+  // NaN: the smallest float stands for a scale of 0.
+  a.scale_log2 = std::max(scale * 1.4426950408889634f, 0x1p-149f);
   a.decay = decay;
   cudaStream_t st = (cudaStream_t)stream;
   if (need > 0) spec_workspace_canary(workspace, need, st);

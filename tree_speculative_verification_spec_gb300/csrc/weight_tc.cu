@@ -27,6 +27,7 @@
 // the batch by a prefix sum that each CTA takes of its own, 256 requests at a
 // time, and dealt out round-robin, the longest of a request first.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "tcgen05.cuh"
@@ -44,7 +45,9 @@ constexpr uint32_t kTmemCols = 512;  // four score buffers of 128 columns
 constexpr int kLse = 4;              // row tiles whose sums are held for the epilogue
 constexpr int kGroup = 256;          // requests numbered at a time
 constexpr float kSumTop = 0x1p60f;
-enum Mode { kStats = 0, kSumsFew = 1, kSumsMany = 2 };
+enum Mode { kStats = 0, kSumsFew = 1, kSumsMany = 2, kHeld = 3 };
+constexpr int kHeldRows = 32;        // rows whose scores are held, and the columns of a key tile's
+constexpr int kHeldTiles = 512 / kHeldRows;  // key tiles of a CTA whose scores tensor memory holds
 
 template <int D> struct Layout {
   static constexpr int DH = D / 64;             // 128-byte halves of a row
@@ -63,10 +66,12 @@ struct Params {
   int bs_log2;
   int q_tma;             // Q by TMA (packed rows, g divides 128), else by cp.async
   int key_chunk;         // keys per item of the sums over few rows
+  int cluster;           // CTAs that hold one request's scores of a kv-head (0: none is held)
 };
 
 struct Request {
   int off, first, cnt, P, m;  // first counted token, counted tokens, prefix, tokens in all
+  int quiet;                  // it came in flagged: nothing of it is written
 };
 struct Table {
   Request r[kGroup];
@@ -85,6 +90,9 @@ template <int MODE>
 __device__ __forceinline__ int request_tiles(const Params& prm, const Request& r) {
   const WeightArgs& a = prm.a;
   const int R = r.cnt * a.g, total = r.P + r.m;
+  const bool held = prm.cluster > 0 && (R == 0 || (R <= kHeldRows && (total + BM - 1) / BM <= kHeldTiles * prm.cluster));
+  if (MODE == kHeld) return held;
+  if (held) return 0;
   if (MODE == kStats) return (R + 2 * BM - 1) / (2 * BM);
   const bool few = R <= 2 * BM;
   if (MODE == kSumsFew) return few ? (total + prm.key_chunk - 1) / prm.key_chunk : 0;
@@ -103,12 +111,15 @@ __device__ __forceinline__ int build_table(const Params& prm, Table& tab, int b0
     if (b < a.B) {
       WeightRequest r;
       int bad = weight_check(a, b, r);
+      // Every CTA has to number the items alike, so a status word, which a faster
+      // CTA may set meanwhile, keeps a request's weights from being written but
+      // does not take it out.
       const int came = *(const volatile int32_t*)&a.status[b];
-      if (!bad && !came && a.path)
+      if (!bad && a.path)
         for (int i = r.m - r.cnt; i < r.m; ++i) bad |= weight_path_bad(a, r, i) ? SPEC_DEV_BAD_PATH : 0;
       if (bad && blockIdx.x == 0) atomicOr(&a.status[b], bad);
-      q = {r.off, r.m - r.cnt, r.cnt, r.P, r.m};
-      if (!bad && !came) tiles = request_tiles<MODE>(prm, q);
+      q = {r.off, r.m - r.cnt, r.cnt, r.P, r.m, came};
+      if (!bad) tiles = request_tiles<MODE>(prm, q);
     }
     tab.r[c] = q;
   }
@@ -163,7 +174,7 @@ __device__ __forceinline__ Item find_item(const Params& prm, const Table& tab, i
     w.k0 = at * prm.key_chunk;
     w.steps = (min(prm.key_chunk, total - w.k0) + BM - 1) / BM;
     w.rt = (R + BM - 1) / BM;
-  } else {
+  } else if (MODE == kSumsMany) {
     w.k0 = at * (2 * BM);
     const int tok = max(0, w.k0 - w.q.P - w.q.first);  // the first counted token that sees the first key
     w.r0 = tok * a.g / BM * BM;
@@ -233,8 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  // Each kernel of a call but the first waits for the one before; each lets the
-  // next one launch as it starts.
+  // Each kernel of a call but the first waits for the one before, whose results it
+  // reads (the statistics need nothing of the held scores' kernel, and wait at
+  // their end); each lets the next one launch as it starts.
   if (MODE != kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -504,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return a.before && key < w.q.P ? a.decay * a.before[slot_at(w, key)] : 0.0f;
       };
       auto put = [&](const Item& w, int key, float sum) {
-        if (key < w.q.P + w.q.m) a.weight[slot_at(w, key)] = sum;
+        if (key < w.q.P + w.q.m && !w.q.quiet) a.weight[slot_at(w, key)] = sum;
       };
 
       for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items); ++round) {
@@ -642,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();  // the table has been read
   }
 
+  if (MODE == kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 1 && elect_one()) {  // every MMA has completed before TMEM is freed
     umma_commit(&drain);
     mbar_drain(&drain, 0);
@@ -661,6 +674,410 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
+}
+
+// ---------------------------------------------------------------------------
+// Held scores: one pass over K.  A cluster of CTAs takes one request's kv-head
+// (at most 32 rows), each CTA a run of its key tiles.  The scores of all tiles
+// stay in tensor memory (32 columns a tile, up to 16 tiles); as a tile arrives,
+// each thread adds 2^x of its key to the 32 row sums.  The CTAs exchange their
+// sums (a value per row and CTA, by st.async to every CTA of the cluster), and
+// the weights come from the scores still held: K is read once, nothing is read
+// twice.  The ring of K tiles fills with the next request's while sums travel.
+// ---------------------------------------------------------------------------
+template <int D> struct HeldLayout {
+  static constexpr int DH = D / 64;
+  static constexpr int NST = D == 128 ? 5 : 8;
+  static constexpr uint32_t kTile = BM * D * 2, kQ = kHeldRows * D * 2;
+  static constexpr uint32_t kOffQ = NST * kTile;
+  static constexpr uint32_t kBytes = kOffQ + 2 * kQ;
+  static constexpr uint32_t kDyn = kBytes + 1024 < 120 * 1024 ? 120 * 1024 : kBytes + 1024;
+  static_assert(kDyn + 16384 <= 227 * 1024, "dynamic and static shared memory within 227 KB");
+};
+
+// v[0] of lane e: the sum (or maximum) over the warp's lanes of what v[e] was.
+template <bool MAX>
+__device__ __forceinline__ float warp_columns(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      const float got = __shfl_xor_sync(0xffffffffu, give, o);
+      v[i] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  return v[0];
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 4 bytes into CTA `rank`'s copy of a shared variable, completing on its copy of `bar`.
+__device__ __forceinline__ void send_async(const float* var, uint64_t* bar, uint32_t rank, float value) {
+  uint32_t to, on;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(var)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(on) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to), "r"(__float_as_uint(value)), "r"(on)
+               : "memory");
+}
+// mbar_wait for what other CTAs of the cluster wrote.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 255u) == 255u && *abort_flag) return false;
+  }
+  *abort_flag = 1;
+  return false;
+}
+
+constexpr int kHeldClusterMax = 16;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    weight_held_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ Params prm) {
+  using L = HeldLayout<D>;
+  constexpr int NST = L::NST, N = kHeldRows, EW = 16;  // epilogue warps
+  const WeightArgs& a = prm.a;
+  extern __shared__ uint8_t dyn_raw[];
+  __shared__ uint64_t full[NST], empty[NST], q_full[2], q_empty[2], s_full[kHeldTiles], s_empty[kHeldTiles], x_full[2], drain;
+  __shared__ Table tab;
+  __shared__ float s_red[EW][N], s_in[2][kHeldClusterMax][N];
+  __shared__ __align__(16) float s_row[N];  // what the epilogue needs of each row: minus log2 of its sum, or its reference
+  __shared__ int scan[kThreads / 32], abort_flag, issued[NST], s_redo;
+  __shared__ uint32_t tmem_slot;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int C = prm.cluster, rank = (int)cluster_rank();
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+      issued[i] = -1;
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&x_full[i], 1);
+    }
+    for (int i = 0; i < kHeldTiles; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+    }
+    mbar_init(&drain, 1);
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // every CTA's barriers exist before another one's sums may arrive
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, &abort_flag); };
+
+  const int clusters = (int)gridDim.x / C, me = (int)blockIdx.x / C;
+  auto dealt = [&](int round) { return round * clusters + (round & 1 ? clusters - 1 - me : me); };
+  auto rounds_end = [&](int n) { return (n + clusters - 1) / clusters * clusters; };
+  // this CTA's key tiles of an item: [t0, t0 + nt)
+  auto share = [&](const Item& w, int& t0, int& nt) {
+    const int tiles = (w.q.P + w.q.m + BM - 1) / BM, each = (tiles + C - 1) / C;
+    t0 = rank * each;
+    nt = max(0, min(each, tiles - t0));
+  };
+
+  int ld = 0;     // key tiles of this CTA so far (stream, MMA, epilogue)
+  int units = 0;  // items with tiles here (Q, MMA); exchanges so far (epilogue)
+  bool dead = false;
+  for (int b0 = 0; b0 < a.B; b0 += kGroup) {
+    const int n_items = build_table<kHeld>(prm, tab, b0, scan) * a.Hkv;
+    if (warp == 0) {
+      // ---------------------------------------------------------- K
+      const int nb = BM / prm.box_rows;
+      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items) && !dead; ++round) {
+        if (idx >= n_items) continue;
+        const Item w = find_item<kHeld>(prm, tab, b0, idx, lane);
+        int t0, nt;
+        share(w, t0, nt);
+        if (w.q.cnt == 0 || nt == 0) continue;
+        const int32_t* bt = a.block_table + (size_t)w.b * a.max_blocks;
+        const int total = w.q.P + w.q.m, x0 = t0 * nb + lane, boxes = nt * nb;
+        int bad = 0;
+        auto page_of = [&](int x) -> int {
+          const int k = x * prm.box_rows;
+          if (k >= total) return -1;
+          const int page = __ldg(bt + (k >> prm.bs_log2));
+          if (page >= 0 && page < a.num_blocks) return page;
+          bad = 1;
+          return -1;
+        };
+        int pages = -1, ahead = lane < boxes ? page_of(x0) : -1;
+        for (int j = 0; j < nt; ++j, ++ld) {
+          const int st = ld % NST, at = j * nb & 31;
+          if (at == 0) {
+            pages = ahead;
+            if (j * nb + 32 + lane < boxes) ahead = page_of(x0 + j * nb + 32);
+          }
+          bool go = true;
+          if (lane == 0 && ld >= NST) go = wait(&empty[st], ld / NST - 1);
+          dead = !__shfl_sync(0xffffffffu, (int)go, 0);
+          if (dead) break;
+          if (lane == 0) {
+            issued[st] = ld;
+            mbar_expect_tx(&full[st], L::kTile);
+          }
+          __syncwarp();
+          const int page = __shfl_sync(0xffffffffu, pages, (at + lane) & 31);
+          if (lane < nb) {
+            const int k = (t0 + j) * BM + lane * prm.box_rows;
+            const int y = page < 0 ? (int)prm.rows_total : ((page * a.Hkv + w.kvh) << prm.bs_log2) + (k & (a.block_size - 1));
+#pragma unroll
+            for (int h = 0; h < L::DH; ++h)
+              tma_load_2d(sbase + st * L::kTile + h * (BM * 128) + lane * prm.box_rows * 128, &tmap_k, h * 64, y, &full[st]);
+          }
+        }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
+      }
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- Q: 32 rows, zeros behind the item's
+      constexpr int CPR = D / 8, STEP = 32 / CPR;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+      const int ch = lane % CPR;
+      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items) && !dead; ++round) {
+        if (idx >= n_items) continue;
+        const Item w = find_item<kHeld>(prm, tab, b0, idx, lane);
+        int t0, nt;
+        share(w, t0, nt);
+        if (w.q.cnt == 0 || nt == 0) continue;
+        const int slot = units & 1, R = w.q.cnt * a.g;
+        bool go = true;
+        if (lane == 0 && units >= 2) go = wait(&q_empty[slot], (units >> 1) - 1);
+        dead = !__shfl_sync(0xffffffffu, (int)go, 0);
+        if (dead) break;
+        const int32_t* path = a.path ? a.path + (size_t)w.b * a.path_stride + w.q.first : nullptr;
+        const uint32_t dst = L::kOffQ + slot * L::kQ + (ch >> 3) * (N * 128);
+#pragma unroll 4
+        for (int i = lane / CPR; i < N; i += STEP) {
+          const uint32_t at = dst + i * 128 + (((ch & 7) ^ (i & 7)) << 4);
+          if (i < R) {
+            const int tok = i / a.g, head = i % a.g;
+            const size_t row = w.q.off + (path ? path[tok] : w.q.first + tok);
+            cp_async16(sbase + at, q + (row * a.Hq + w.kvh * a.g + head) * D + ch * 8);
+          } else {
+            *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        cp_async_wait();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[slot]);
+        ++units;
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA: A = K tile, B = Q
+      const uint64_t ring = smem_desc_sw128(sbase, 16, 1024), qd0 = smem_desc_sw128(sbase + L::kOffQ, 16, 1024);
+      constexpr uint32_t idesc = idesc_bf16(N, 0);
+      const bool leader = elect_one();
+      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items); ++round) {
+        if (idx >= n_items) continue;
+        const Item w = find_item<kHeld>(prm, tab, b0, idx, lane);
+        int t0, nt;
+        share(w, t0, nt);
+        if (w.q.cnt == 0 || nt == 0) continue;
+        wait(&q_full[units & 1], units >> 1);
+        const uint64_t qd = qd0 + (uint64_t)((units & 1) * (L::kQ >> 4));
+        for (int j = 0; j < nt; ++j, ++ld) {
+          const int st = ld % NST, s = ld % kHeldTiles;
+          wait(&full[st], ld / NST);
+          if (ld >= kHeldTiles) wait(&s_empty[s], ld / kHeldTiles - 1);
+          tc_fence_after();
+          if (leader) {
+            const uint64_t kd = ring + (uint64_t)(st * (L::kTile >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_bf16(tmem + s * N, kd + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4), qd + (((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4), idesc,
+                        kk > 0 ? 1u : 0u);
+            umma_commit(&s_full[s]);
+            umma_commit(&empty[st]);
+          }
+          __syncwarp();
+        }
+        if (leader) umma_commit(&q_empty[units & 1]);
+        __syncwarp();
+        ++units;
+      }
+    } else if (warp >= 4) {
+      // ---------------------------------------------------------- epilogue
+      const int ew = warp - 4, wg = ew >> 2, quad = warp & 3, r = quad * 32 + lane;
+      const uint32_t tS = tmem + ((uint32_t)(quad * 32) << 16);
+      const float c2 = a.scale_log2;
+      auto all_sync = [&]() { asm volatile("bar.sync 1, 512;" ::: "memory"); };
+      // Row sums (or maxima) over the cluster, from each warp's own (row = lane):
+      // warp 4 adds the CTA's, sends them to every CTA, and adds the CTAs'.  In
+      // warp 4 the result of row `lane`, elsewhere nothing.
+      auto exchange = [&](float v, bool max) -> float {
+        s_red[ew][lane] = v;
+        all_sync();
+        if (ew != 0) return 0.0f;
+#pragma unroll
+        for (int k = 1; k < EW; ++k) v = max ? fmaxf(v, s_red[k][lane]) : v + s_red[k][lane];
+        const int buf = units & 1;
+        if (lane == 0) mbar_expect_tx(&x_full[buf], C * N * 4);
+        __syncwarp();
+        for (int k = 0; k < C; ++k) send_async(&s_in[buf][rank][lane], &x_full[buf], k, v);
+        mbar_wait_cluster(&x_full[buf], (units >> 1) & 1, &abort_flag);
+        float all = s_in[buf][0][lane];
+        for (int k = 1; k < C; ++k) all = max ? fmaxf(all, s_in[buf][k][lane]) : all + s_in[buf][k][lane];
+        __syncwarp();
+        return all;
+      };
+      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items); ++round) {
+        if (idx >= n_items) continue;
+        const Item w = find_item<kHeld>(prm, tab, b0, idx, lane);
+        int t0, nt;
+        share(w, t0, nt);
+        const int R = w.q.cnt * a.g, total = w.q.P + w.q.m;
+        const size_t base = ((size_t)w.b * a.Hkv + w.kvh) * a.stride;
+        auto old_weight = [&](int key) -> float { return a.before && key < w.q.P ? a.decay * a.before[base + key] : 0.0f; };
+        if (w.q.cnt == 0) {  // no rows: the old weights alone
+          for (int j = wg; j < nt; j += 4) {
+            const int key = (t0 + j) * BM + r;
+            if (key < total && !w.q.quiet) a.weight[base + key] = old_weight(key);
+          }
+          continue;
+        }
+        // the last slot that row `lane` sees
+        const int lim = lane < R ? w.q.P + w.q.first + lane / a.g : -1;
+        // f(e, scores of column e or -inf where the row does not see the key) over the
+        // tiles of this warpgroup
+        auto tile = [&](int j, float (&x)[N]) {  // tile j's scores, -inf where hidden
+          uint32_t u[N];
+          tmem_ld32(tS + (uint32_t)((ld + j) % kHeldTiles) * N, u);
+          tmem_wait_ld(u);
+          const int k0 = (t0 + j) * BM;
+          if (k0 + BM - 1 > w.q.P + w.q.first) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              const int last = __shfl_sync(0xffffffffu, lim, e);
+              x[e] = k0 + r <= last ? __uint_as_float(u[e]) : -INFINITY;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] = __uint_as_float(u[e]);
+          }
+        };
+        float acc[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+        for (int j = wg; j < nt; j += 4) {
+          wait(&s_full[(ld + j) % kHeldTiles], (ld + j) / kHeldTiles);
+          tc_fence_after();
+          float x[N];
+          tile(j, x);
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] += fast_exp2(x[e] * c2);
+        }
+        float old = wg < nt ? old_weight((t0 + wg) * BM + r) : 0.0f;
+        float sum = exchange(warp_columns<false>(acc, lane), false);
+        ++units;
+        if (ew == 0) {
+          const bool fits = lane >= R || (sum >= 1.0f / kSumTop && sum < kSumTop);
+          s_row[lane] = lane < R ? -log2f(sum) : -INFINITY;
+          const bool redo = !__all_sync(0xffffffffu, fits);
+          if (lane == 0) s_redo = redo;
+        }
+        all_sync();
+        if (s_redo) {  // a sum left fp32's middle: against the rows' maxima
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] = -INFINITY;
+          for (int j = wg; j < nt; j += 4) {
+            float x[N];
+            tile(j, x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[e] = fmaxf(acc[e], x[e]);
+          }
+          float top = exchange(warp_columns<true>(acc, lane), true);
+          ++units;
+          top = lane < R && top > -INFINITY ? top * c2 : 0.0f;
+          if (ew == 0) s_row[lane] = top;
+          all_sync();
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+          for (int j = wg; j < nt; j += 4) {
+            float x[N];
+            tile(j, x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[e] += fast_exp2(fmaf(x[e], c2, -s_row[e]));
+          }
+          sum = exchange(warp_columns<false>(acc, lane), false);
+          ++units;
+          if (ew == 0) s_row[lane] = lane < R ? -(top + log2f(sum)) : -INFINITY;
+          all_sync();
+        }
+        for (int j = wg; j < nt; j += 4) {
+          const int key = (t0 + j) * BM + r;
+          const float next = j + 4 < nt ? old_weight(key + 4 * BM) : 0.0f;
+          float x[N];
+          tile(j, x);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[(ld + j) % kHeldTiles]);
+          float2 p = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int e = 0; e < N; e += 4) {
+            const float4 n4 = *reinterpret_cast<const float4*>(&s_row[e]);
+            p.x += fast_exp2(fmaf(x[e], c2, n4.x)) + fast_exp2(fmaf(x[e + 1], c2, n4.y));
+            p.y += fast_exp2(fmaf(x[e + 2], c2, n4.z)) + fast_exp2(fmaf(x[e + 3], c2, n4.w));
+          }
+          if (key < total && !w.q.quiet) a.weight[base + key] = old + (p.x + p.y);
+          old = next;
+        }
+        ld += nt;
+      }
+    }
+    __syncthreads();  // the table has been read
+  }
+
+  if (warp == 1 && elect_one()) {  // every MMA has completed before TMEM is freed
+    umma_commit(&drain);
+    mbar_drain(&drain, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (abort_flag) {
+    if (threadIdx.x == 0)
+      for (int st = 0; st < NST; ++st)
+        if (issued[st] >= 0) mbar_drain(&full[st], (issued[st] / NST) & 1);
+    for (int b = threadIdx.x; b < a.B; b += kThreads) atomicOr(&a.status[b], SPEC_DEV_TIMEOUT);
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+  __syncwarp();
+  cluster_sync_all();  // no CTA's shared memory goes while another may still send to it
 }
 
 // Minus log2 of every counted row's sum, from the parts that the splits with some
@@ -741,6 +1158,51 @@ static cudaError_t launch(void (*kern)(P...), long long grid, int threads, int d
 }
 
 template <int D>
+static void held_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int c) {
+  cfg.gridDim = dim3(c, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = HeldLayout<D>::kDyn;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+}
+
+// Clusters of c CTAs that device `dev` (the current one) runs at once; asked for
+// once per device and size.
+template <int D>
+static int held_clusters(int dev, int c) {
+  static std::atomic<int> known[64][kHeldClusterMax + 1];  // number + 1
+  const bool keep = dev < 64;
+  if (keep && known[dev][c] > 0) return known[dev][c] - 1;
+  int n = 0;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  held_config<D>(cfg, attr, c);
+  if (cudaFuncSetAttribute(weight_held_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)HeldLayout<D>::kDyn) != cudaSuccess ||
+      cudaFuncSetAttribute(weight_held_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, weight_held_kernel<D>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (keep) known[dev][c] = n + 1;
+  return n;
+}
+
+template <int D>
+static cudaError_t launch_held(const CUtensorMap& mk, const Params& prm, int fit, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  held_config<D>(cfg, attr, prm.cluster);
+  cfg.gridDim = dim3((unsigned)(std::min<long long>(fit, (long long)prm.a.B * prm.a.Hkv) * prm.cluster), 1, 1);
+  cfg.stream = stream;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, weight_held_kernel<D>, mk, prm);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
 static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -770,14 +1232,31 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
     mq = mk;  // not read
   }
   const long long rows = (long long)(a.window > 0 ? std::min(a.window, a.n_max) : a.n_max) * a.g;  // the most that a request has
+  const long long longest = (long long)a.max_prefix + a.n_max;
+  // Scores are held where a request has few rows: by the fewest CTAs that can hold
+  // the longest one's, and by more while the requests and heads alone leave SMs
+  // idle.  A request with more rows or keys goes the other way, inside the kernels.
+  bool first = true;
+  if (a.g <= kHeldRows) {
+    int c = 1;
+    while (c < kHeldClusterMax && ((long long)c * kHeldTiles * BM < longest || 2LL * c * a.B * a.Hkv <= sms)) c *= 2;
+    int fit = held_clusters<D>(dev, c);
+    while (fit == 0 && c > 1) fit = held_clusters<D>(dev, c /= 2);
+    if (fit == 0) return cudaErrorInvalidConfiguration;
+    prm.cluster = c;
+    e = launch_held<D>(mk, prm, fit, stream);
+    if (e != cudaSuccess) return e;
+    if (rows <= kHeldRows && longest <= (long long)c * kHeldTiles * BM) return cudaSuccess;  // every request's are held
+    first = false;
+  }
   const int dyn = (int)Layout<D>::kDyn;
   if (rows > 0) {
     const int tiles = (int)((rows + kJoinRows - 1) / kJoinRows);
     if ((long long)tiles * a.Hkv * a.B > INT32_MAX) return cudaErrorInvalidValue;
-    e = launch(weight_tc_kernel<D, kStats>, sms, kThreads, dyn, true, stream, mk, mq, prm);
+    e = launch(weight_tc_kernel<D, kStats>, sms, kThreads, dyn, first, stream, mk, mq, prm);
     if (e == cudaSuccess) e = launch(weight_join_kernel, (long long)tiles * a.Hkv * a.B, kJoinThreads, 0, false, stream, a, tiles);
   }
-  if (e == cudaSuccess) e = launch(weight_tc_kernel<D, kSumsFew>, sms, kThreads, dyn, rows == 0, stream, mk, mq, prm);
+  if (e == cudaSuccess) e = launch(weight_tc_kernel<D, kSumsFew>, sms, kThreads, dyn, first && rows == 0, stream, mk, mq, prm);
   if (e == cudaSuccess && rows > 2 * BM) e = launch(weight_tc_kernel<D, kSumsMany>, sms, kThreads, dyn, false, stream, mk, mq, prm);
   return e;
 }
