@@ -47,6 +47,7 @@ constexpr int kGroup = 256;          // requests numbered at a time
 constexpr float kSumTop = 0x1p60f;
 enum Mode { kStats = 0, kSumsFew = 1, kSumsMany = 2, kHeld = 3 };
 constexpr int kHeldRows = 32;        // rows whose scores are held, and the columns of a key tile's
+constexpr int kHeldQ = 4;            // items whose queries are ahead in shared memory
 constexpr int kHeldTiles = 512 / kHeldRows;  // key tiles of a CTA whose scores tensor memory holds
 
 template <int D> struct Layout {
@@ -320,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int jobs[4] = {0, 0, 0, 0};           // score tiles so far: of each resident tile, or of each buffer (MMA warp)
   int c = 0;                            // the same of this warpgroup's (epilogue)
   int lt = 0;                           // row tiles of sums so far
+  int pairs = 0;                        // key tiles of two row tiles so far (epilogue)
   bool dead = false;                    // a producer that gave up
   for (int b0 = 0; b0 < a.B; b0 += kGroup) {
     const int tiles = build_table<MODE>(prm, tab, b0, scan);
@@ -609,8 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             release();
             float sum = acc.x + acc.y;
-            if (two) {  // the other row tile's share; the buffer is read before the barrier of the pair's next tile
-              float* part = s_part[wg >> 1][(j >> 1) & 1];
+            if (two) {  // the other row tile's share; a buffer is read before the barrier of the pair's next tile
+              float* part = s_part[wg >> 1][pairs++ & 1];
               if (t == 1) part[r] = sum;
               asm volatile("bar.sync %0, 256;" ::"r"(1 + (wg >> 1)) : "memory");
               if (t == 0) sum += part[r];
@@ -682,17 +684,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 // stay in tensor memory (32 columns a tile, up to 16 tiles); as a tile arrives,
 // each thread adds 2^x of its key to the 32 row sums.  The CTAs exchange their
 // sums (a value per row and CTA, by st.async to every CTA of the cluster), and
-// the weights come from the scores still held: K is read once, nothing is read
-// twice.  The ring of K tiles fills with the next request's while sums travel.
+// the weights come from the scores still held: K is read once.  While an item's
+// sums travel the next one's tiles are loaded, multiplied and summed.
 // ---------------------------------------------------------------------------
 template <int D> struct HeldLayout {
   static constexpr int DH = D / 64;
   static constexpr int NST = D == 128 ? 5 : 8;
   static constexpr uint32_t kTile = BM * D * 2, kQ = kHeldRows * D * 2;
   static constexpr uint32_t kOffQ = NST * kTile;
-  static constexpr uint32_t kBytes = kOffQ + 2 * kQ;
+  static constexpr uint32_t kBytes = kOffQ + kHeldQ * kQ;
   static constexpr uint32_t kDyn = kBytes + 1024 < 120 * 1024 ? 120 * 1024 : kBytes + 1024;
-  static_assert(kDyn + 16384 <= 227 * 1024, "dynamic and static shared memory within 227 KB");
+  static_assert(kDyn + 24576 <= 227 * 1024, "dynamic and static shared memory within 227 KB");
 };
 
 // v[0] of lane e: the sum (or maximum) over the warp's lanes of what v[e] was.
@@ -754,11 +756,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NST = L::NST, N = kHeldRows, EW = 16;  // epilogue warps
   const WeightArgs& a = prm.a;
   extern __shared__ uint8_t dyn_raw[];
-  __shared__ uint64_t full[NST], empty[NST], q_full[2], q_empty[2], s_full[kHeldTiles], s_empty[kHeldTiles], x_full[2], drain;
+  __shared__ uint64_t full[NST], empty[NST], q_full[kHeldQ], q_empty[kHeldQ], s_full[kHeldTiles], s_empty[kHeldTiles], drain;
+  __shared__ uint64_t red_full[2], x_full[2], row_full[2], redo_full[2];
   __shared__ Table tab;
-  __shared__ float s_red[EW][N], s_in[2][kHeldClusterMax][N];
-  __shared__ __align__(16) float s_row[N];  // what the epilogue needs of each row: minus log2 of its sum, or its reference
-  __shared__ int scan[kThreads / 32], abort_flag, issued[NST], s_redo;
+  // by item parity: each epilogue warp's row sums, each CTA's, and what the epilogue
+  // needs of a row (minus log2 of its sum); s_again: the same for a second look
+  __shared__ float s_red[2][EW][N], s_in[2][kHeldClusterMax][N], s_again[2][kHeldClusterMax][N], s_red2[EW][N];
+  __shared__ __align__(16) float s_row[2][N];
+  __shared__ __align__(16) int s_len[kGroup];
+  __shared__ uint8_t s_order[kGroup];  // the group's requests, the longest first
+  __shared__ int scan[kThreads / 32], abort_flag, issued[NST], s_redo[2];
   __shared__ uint32_t tmem_slot;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -771,10 +778,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[i], 1);
       issued[i] = -1;
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kHeldQ; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&red_full[i], EW);
       mbar_init(&x_full[i], 1);
+      mbar_init(&row_full[i], 1);
+      mbar_init(&redo_full[i], 1);
     }
     for (int i = 0; i < kHeldTiles; ++i) {
       mbar_init(&s_full[i], 1);
@@ -801,44 +813,90 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int clusters = (int)gridDim.x / C, me = (int)blockIdx.x / C;
   auto dealt = [&](int round) { return round * clusters + (round & 1 ? clusters - 1 - me : me); };
   auto rounds_end = [&](int n) { return (n + clusters - 1) / clusters * clusters; };
-  // this CTA's key tiles of an item: [t0, t0 + nt)
-  auto share = [&](const Item& w, int& t0, int& nt) {
-    const int tiles = (w.q.P + w.q.m + BM - 1) / BM, each = (tiles + C - 1) / C;
-    t0 = rank * each;
-    nt = max(0, min(each, tiles - t0));
+  struct HeldItem {
+    Request q;
+    int b, kvh, t0, nt;  // this CTA's key tiles: [t0, t0 + nt)
+  };
+  const int c_log2 = 31 - __clz(C);
+  auto item = [&](int b0, int idx) {
+    HeldItem w;
+    const int r = s_order[idx / a.Hkv];
+    w.kvh = idx % a.Hkv;
+    w.b = b0 + r;
+    w.q = tab.r[r];
+    const int tiles = (w.q.P + w.q.m + BM - 1) / BM, each = (tiles + C - 1) >> c_log2;
+    w.t0 = rank * each;
+    w.nt = max(0, min(each, tiles - w.t0));
+    return w;
+  };
+  // the first round from `round` on that deals this cluster an item, -1: none is left
+  auto next_item = [&](int& round, int n) -> int {
+    for (;; ++round) {
+      const int idx = dealt(round);
+      if (idx < n) return idx;
+      if (idx >= rounds_end(n)) return -1;
+    }
   };
 
   int ld = 0;     // key tiles of this CTA so far (stream, MMA, epilogue)
-  int units = 0;  // items with tiles here (Q, MMA); exchanges so far (epilogue)
+  int units = 0;  // items with tiles here (Q, MMA), items with rows (sums, epilogue)
+  int looks = 0;  // exchanges of second looks (epilogue)
   bool dead = false;
   for (int b0 = 0; b0 < a.B; b0 += kGroup) {
-    const int n_items = build_table<kHeld>(prm, tab, b0, scan) * a.Hkv;
+    const int n_requests = build_table<kHeld>(prm, tab, b0, scan), n_items = n_requests * a.Hkv;
+    {  // the longest first: the shares of the clusters come out alike
+      const int c = threadIdx.x;
+      const bool in = c < kGroup && tab.first[c + 1] > tab.first[c];
+      if (c < kGroup) s_len[c] = in ? tab.r[c].P + tab.r[c].m : -1;
+      __syncthreads();
+      if (in) {
+        const int mine = s_len[c];
+        int before = 0;
+#pragma unroll 8
+        for (int j = 0; j < kGroup; j += 4) {
+          const int4 x = *reinterpret_cast<const int4*>(&s_len[j]);
+          before += x.x > mine || (x.x == mine && j < c);
+          before += x.y > mine || (x.y == mine && j + 1 < c);
+          before += x.z > mine || (x.z == mine && j + 2 < c);
+          before += x.w > mine || (x.w == mine && j + 3 < c);
+        }
+        s_order[before] = (uint8_t)c;
+      }
+      __syncthreads();
+    }
     if (warp == 0) {
       // ---------------------------------------------------------- K
       const int nb = BM / prm.box_rows;
-      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items) && !dead; ++round) {
-        if (idx >= n_items) continue;
-        const Item w = find_item<kHeld>(prm, tab, b0, idx, lane);
-        int t0, nt;
-        share(w, t0, nt);
-        if (w.q.cnt == 0 || nt == 0) continue;
-        const int32_t* bt = a.block_table + (size_t)w.b * a.max_blocks;
-        const int total = w.q.P + w.q.m, x0 = t0 * nb + lane, boxes = nt * nb;
-        int bad = 0;
-        auto page_of = [&](int x) -> int {
-          const int k = x * prm.box_rows;
-          if (k >= total) return -1;
-          const int page = __ldg(bt + (k >> prm.bs_log2));
-          if (page >= 0 && page < a.num_blocks) return page;
-          bad = 1;
-          return -1;
-        };
-        int pages = -1, ahead = lane < boxes ? page_of(x0) : -1;
-        for (int j = 0; j < nt; ++j, ++ld) {
+      // the page of box x of an item (boxes count from the request's slot 0), -1 behind
+      // its keys, -2 at a bad id
+      auto page_of = [&](const HeldItem& w, int x) -> int {
+        const int k = x * prm.box_rows;
+        if (k >= w.q.P + w.q.m) return -1;
+        const int page = __ldg(a.block_table + (size_t)w.b * a.max_blocks + (k >> prm.bs_log2));
+        return page >= 0 && page < a.num_blocks ? page : -2;
+      };
+      // the first pages of the next item are looked up before this one's tiles go out
+      int round = 0, idx = next_item(round, n_items), first_pages = -1;
+      HeldItem w = {};
+      auto look = [&]() {
+        if (idx < 0) return;
+        w = item(b0, idx);
+        first_pages = w.q.cnt > 0 && lane < w.nt * nb ? page_of(w, w.t0 * nb + lane) : -1;
+      };
+      look();
+      while (idx >= 0 && !dead) {
+        const HeldItem v = w;
+        int ahead = first_pages, pages = -1;
+        bool bad = false;
+        ++round;
+        idx = next_item(round, n_items);
+        look();
+        for (int j = 0; j < v.nt && v.q.cnt > 0; ++j, ++ld) {
           const int st = ld % NST, at = j * nb & 31;
           if (at == 0) {
             pages = ahead;
-            if (j * nb + 32 + lane < boxes) ahead = page_of(x0 + j * nb + 32);
+            bad |= pages == -2;
+            if (j * nb + 32 + lane < v.nt * nb) ahead = page_of(v, v.t0 * nb + j * nb + 32 + lane);
           }
           bool go = true;
           if (lane == 0 && ld >= NST) go = wait(&empty[st], ld / NST - 1);
@@ -851,64 +909,77 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           const int page = __shfl_sync(0xffffffffu, pages, (at + lane) & 31);
           if (lane < nb) {
-            const int k = (t0 + j) * BM + lane * prm.box_rows;
-            const int y = page < 0 ? (int)prm.rows_total : ((page * a.Hkv + w.kvh) << prm.bs_log2) + (k & (a.block_size - 1));
+            const int k = (v.t0 + j) * BM + lane * prm.box_rows;
+            const int y = page < 0 ? (int)prm.rows_total : ((page * a.Hkv + v.kvh) << prm.bs_log2) + (k & (a.block_size - 1));
 #pragma unroll
             for (int h = 0; h < L::DH; ++h)
               tma_load_2d(sbase + st * L::kTile + h * (BM * 128) + lane * prm.box_rows * 128, &tmap_k, h * 64, y, &full[st]);
           }
         }
-        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[v.b], SPEC_DEV_BAD_BLOCK);
       }
     } else if (warp == 2) {
       // ---------------------------------------------------------- Q: 32 rows, zeros behind the item's
+      // An item is announced once the next one's copies are out.
       constexpr int CPR = D / 8, STEP = 32 / CPR;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
       const int ch = lane % CPR;
-      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items) && !dead; ++round) {
-        if (idx >= n_items) continue;
-        const Item w = find_item<kHeld>(prm, tab, b0, idx, lane);
-        int t0, nt;
-        share(w, t0, nt);
-        if (w.q.cnt == 0 || nt == 0) continue;
-        const int slot = units & 1, R = w.q.cnt * a.g;
-        bool go = true;
-        if (lane == 0 && units >= 2) go = wait(&q_empty[slot], (units >> 1) - 1);
-        dead = !__shfl_sync(0xffffffffu, (int)go, 0);
-        if (dead) break;
-        const int32_t* path = a.path ? a.path + (size_t)w.b * a.path_stride + w.q.first : nullptr;
-        const uint32_t dst = L::kOffQ + slot * L::kQ + (ch >> 3) * (N * 128);
-#pragma unroll 4
-        for (int i = lane / CPR; i < N; i += STEP) {
-          const uint32_t at = dst + i * 128 + (((ch & 7) ^ (i & 7)) << 4);
-          if (i < R) {
-            const int tok = i / a.g, head = i % a.g;
-            const size_t row = w.q.off + (path ? path[tok] : w.q.first + tok);
-            cp_async16(sbase + at, q + (row * a.Hq + w.kvh * a.g + head) * D + ch * 8);
-          } else {
-            *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        cp_async_wait();
+      int round = 0, idx = next_item(round, n_items), pending = -1;
+      HeldItem w = {};
+      int token = 0;  // row of q of counted token `lane`, looked up an item ahead
+      auto look = [&]() {
+        if (idx < 0) return;
+        w = item(b0, idx);
+        token = w.q.off + (lane >= w.q.cnt ? 0 : a.path ? a.path[(size_t)w.b * a.path_stride + w.q.first + lane] : w.q.first + lane);
+      };
+      auto announce = [&]() {
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[slot]);
+        if (lane == 0) mbar_arrive(&q_full[pending]);
+      };
+      look();
+      while (idx >= 0 && !dead) {
+        const HeldItem v = w;
+        const int tokens = token;
+        ++round;
+        idx = next_item(round, n_items);
+        look();
+        if (v.q.cnt == 0 || v.nt == 0) continue;
+        const int slot = units % kHeldQ, R = v.q.cnt * a.g;
+        bool go = true;
+        if (lane == 0 && units >= kHeldQ) go = wait(&q_empty[slot], units / kHeldQ - 1);
+        dead = !__shfl_sync(0xffffffffu, (int)go, 0);
+        if (dead) break;
+        const uint32_t dst = L::kOffQ + slot * L::kQ + (ch >> 3) * (N * 128);
+#pragma unroll
+        for (int i0 = 0; i0 < N; i0 += STEP) {
+          const int i = i0 + lane / CPR, tok = min(i / a.g, 31);
+          const size_t row = __shfl_sync(0xffffffffu, tokens, tok);
+          const uint32_t at = dst + i * 128 + (((ch & 7) ^ (i & 7)) << 4);
+          if (i < R) cp_async16(sbase + at, q + (row * a.Hq + v.kvh * a.g + i % a.g) * D + ch * 8);
+          else *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (pending >= 0) {
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          announce();
+        }
+        pending = slot;
         ++units;
       }
+      cp_async_wait();
+      if (pending >= 0) announce();
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA: A = K tile, B = Q
       const uint64_t ring = smem_desc_sw128(sbase, 16, 1024), qd0 = smem_desc_sw128(sbase + L::kOffQ, 16, 1024);
       constexpr uint32_t idesc = idesc_bf16(N, 0);
       const bool leader = elect_one();
-      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items); ++round) {
-        if (idx >= n_items) continue;
-        const Item w = find_item<kHeld>(prm, tab, b0, idx, lane);
-        int t0, nt;
-        share(w, t0, nt);
-        if (w.q.cnt == 0 || nt == 0) continue;
-        wait(&q_full[units & 1], units >> 1);
-        const uint64_t qd = qd0 + (uint64_t)((units & 1) * (L::kQ >> 4));
-        for (int j = 0; j < nt; ++j, ++ld) {
+      for (int round = 0, idx; (idx = next_item(round, n_items)) >= 0; ++round) {
+        const HeldItem w = item(b0, idx);
+        if (w.q.cnt == 0 || w.nt == 0) continue;
+        wait(&q_full[units % kHeldQ], units / kHeldQ);
+        const uint64_t qd = qd0 + (uint64_t)((units % kHeldQ) * (L::kQ >> 4));
+        for (int j = 0; j < w.nt; ++j, ++ld) {
           const int st = ld % NST, s = ld % kHeldTiles;
           wait(&full[st], ld / NST);
           if (ld >= kHeldTiles) wait(&s_empty[s], ld / kHeldTiles - 1);
@@ -924,137 +995,186 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (leader) umma_commit(&q_empty[units & 1]);
+        if (leader) umma_commit(&q_empty[units % kHeldQ]);
         __syncwarp();
+        ++units;
+      }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------- row sums over the cluster (row = lane)
+      // Item k + 1's sums leave after item k's have come in from every CTA, so two
+      // buffers do.
+      for (int round = 0, idx; (idx = next_item(round, n_items)) >= 0; ++round) {
+        const HeldItem w = item(b0, idx);
+        if (w.q.cnt == 0) continue;
+        const int buf = units & 1, phase = units >> 1;
+        wait(&red_full[buf], phase);
+        float v = s_red[buf][0][lane];
+#pragma unroll
+        for (int k = 1; k < EW; ++k) v += s_red[buf][k][lane];
+        if (lane == 0) mbar_expect_tx(&x_full[buf], C * N * 4);
+        __syncwarp();
+        for (int k = 0; k < C; ++k) send_async(&s_in[buf][rank][lane], &x_full[buf], k, v);
+        mbar_wait_cluster(&x_full[buf], phase & 1, &abort_flag);
+        float sum = s_in[buf][0][lane];
+        for (int k = 1; k < C; ++k) sum += s_in[buf][k][lane];
+        const bool there = lane < w.q.cnt * a.g, fits = !there || (sum >= 1.0f / kSumTop && sum < kSumTop);
+        s_row[buf][lane] = there ? -log2f(sum) : -INFINITY;
+        const bool redo = !__all_sync(0xffffffffu, fits);
+        if (lane == 0) s_redo[buf] = redo;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&row_full[buf]);
         ++units;
       }
     } else if (warp >= 4) {
       // ---------------------------------------------------------- epilogue
+      // Item k + 1's scores are summed while item k's sums travel, as long as tensor
+      // memory holds both.
       const int ew = warp - 4, wg = ew >> 2, quad = warp & 3, r = quad * 32 + lane;
       const uint32_t tS = tmem + ((uint32_t)(quad * 32) << 16);
       const float c2 = a.scale_log2;
       auto all_sync = [&]() { asm volatile("bar.sync 1, 512;" ::: "memory"); };
-      // Row sums (or maxima) over the cluster, from each warp's own (row = lane):
-      // warp 4 adds the CTA's, sends them to every CTA, and adds the CTAs'.  In
-      // warp 4 the result of row `lane`, elsewhere nothing.
-      auto exchange = [&](float v, bool max) -> float {
-        s_red[ew][lane] = v;
-        all_sync();
-        if (ew != 0) return 0.0f;
+      // Scores of key tile t0 + j (the CTA's tile number n), -inf where row `e`, whose
+      // last visible slot lane e holds in `lim`, does not see the key.
+      auto tile = [&](const HeldItem& w, int j, int n, float (&x)[N]) {
+        uint32_t u[N];
+        tmem_ld32(tS + (uint32_t)(n % kHeldTiles) * N, u);
+        tmem_wait_ld(u);
+        const int k0 = (w.t0 + j) * BM;
+        if (k0 + BM - 1 > w.q.P + w.q.first) {
+          const int lim = lane < w.q.cnt * a.g ? w.q.P + w.q.first + lane / a.g : -1;
 #pragma unroll
-        for (int k = 1; k < EW; ++k) v = max ? fmaxf(v, s_red[k][lane]) : v + s_red[k][lane];
-        const int buf = units & 1;
-        if (lane == 0) mbar_expect_tx(&x_full[buf], C * N * 4);
+          for (int e = 0; e < N; ++e) {
+            const int last = __shfl_sync(0xffffffffu, lim, e);
+            x[e] = k0 + r <= last ? __uint_as_float(u[e]) : -INFINITY;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e) x[e] = __uint_as_float(u[e]);
+        }
+      };
+      // A row's value over the cluster for a second look: the CTA's warps meet, warp 4
+      // does what warp 3 does for the first look.  In warp 4 the result of row `lane`.
+      auto exchange = [&](float v, bool max) -> float {
+        s_red2[ew][lane] = v;
+        all_sync();
+        const int buf = looks & 1, phase = looks >> 1;
+        ++looks;
+        if (ew != 0) return 0.0f;
+        for (int k = 1; k < EW; ++k) v = max ? fmaxf(v, s_red2[k][lane]) : v + s_red2[k][lane];
+        if (lane == 0) mbar_expect_tx(&redo_full[buf], C * N * 4);
         __syncwarp();
-        for (int k = 0; k < C; ++k) send_async(&s_in[buf][rank][lane], &x_full[buf], k, v);
-        mbar_wait_cluster(&x_full[buf], (units >> 1) & 1, &abort_flag);
-        float all = s_in[buf][0][lane];
-        for (int k = 1; k < C; ++k) all = max ? fmaxf(all, s_in[buf][k][lane]) : all + s_in[buf][k][lane];
-        __syncwarp();
+        for (int k = 0; k < C; ++k) send_async(&s_again[buf][rank][lane], &redo_full[buf], k, v);
+        mbar_wait_cluster(&redo_full[buf], phase & 1, &abort_flag);
+        float all = s_again[buf][0][lane];
+        for (int k = 1; k < C; ++k) all = max ? fmaxf(all, s_again[buf][k][lane]) : all + s_again[buf][k][lane];
         return all;
       };
-      for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items); ++round) {
-        if (idx >= n_items) continue;
-        const Item w = find_item<kHeld>(prm, tab, b0, idx, lane);
-        int t0, nt;
-        share(w, t0, nt);
-        const int R = w.q.cnt * a.g, total = w.q.P + w.q.m;
-        const size_t base = ((size_t)w.b * a.Hkv + w.kvh) * a.stride;
-        auto old_weight = [&](int key) -> float { return a.before && key < w.q.P ? a.decay * a.before[base + key] : 0.0f; };
-        if (w.q.cnt == 0) {  // no rows: the old weights alone
-          for (int j = wg; j < nt; j += 4) {
-            const int key = (t0 + j) * BM + r;
-            if (key < total && !w.q.quiet) a.weight[base + key] = old_weight(key);
-          }
-          continue;
-        }
-        // the last slot that row `lane` sees
-        const int lim = lane < R ? w.q.P + w.q.first + lane / a.g : -1;
-        // f(e, scores of column e or -inf where the row does not see the key) over the
-        // tiles of this warpgroup
-        auto tile = [&](int j, float (&x)[N]) {  // tile j's scores, -inf where hidden
-          uint32_t u[N];
-          tmem_ld32(tS + (uint32_t)((ld + j) % kHeldTiles) * N, u);
-          tmem_wait_ld(u);
-          const int k0 = (t0 + j) * BM;
-          if (k0 + BM - 1 > w.q.P + w.q.first) {
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-              const int last = __shfl_sync(0xffffffffu, lim, e);
-              x[e] = k0 + r <= last ? __uint_as_float(u[e]) : -INFINITY;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < N; ++e) x[e] = __uint_as_float(u[e]);
-          }
-        };
-        float acc[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = 0.0f;
-        for (int j = wg; j < nt; j += 4) {
-          wait(&s_full[(ld + j) % kHeldTiles], (ld + j) / kHeldTiles);
-          tc_fence_after();
-          float x[N];
-          tile(j, x);
-#pragma unroll
-          for (int e = 0; e < N; ++e) acc[e] += fast_exp2(x[e] * c2);
-        }
-        float old = wg < nt ? old_weight((t0 + wg) * BM + r) : 0.0f;
-        float sum = exchange(warp_columns<false>(acc, lane), false);
-        ++units;
-        if (ew == 0) {
-          const bool fits = lane >= R || (sum >= 1.0f / kSumTop && sum < kSumTop);
-          s_row[lane] = lane < R ? -log2f(sum) : -INFINITY;
-          const bool redo = !__all_sync(0xffffffffu, fits);
-          if (lane == 0) s_redo = redo;
-        }
-        all_sync();
-        if (s_redo) {  // a sum left fp32's middle: against the rows' maxima
+      auto old_weight = [&](const HeldItem& w, int j) -> float {
+        const int key = (w.t0 + j) * BM + r;
+        return a.before && j < w.nt && key < w.q.P ? a.decay * a.before[((size_t)w.b * a.Hkv + w.kvh) * a.stride + key] : 0.0f;
+      };
+      auto put = [&](const HeldItem& w, int j, float sum) {
+        const int key = (w.t0 + j) * BM + r;
+        if (key < w.q.P + w.q.m && !w.q.quiet) a.weight[((size_t)w.b * a.Hkv + w.kvh) * a.stride + key] = sum;
+      };
+      // the weights of item `idx`, the k-th with rows, whose first tile here was number
+      // n0; old: what its first key of this thread had
+      auto finish = [&](int idx, int k, int n0, float old) {
+        const HeldItem w = item(b0, idx);
+        const int nt = w.nt, buf = k & 1;
+        wait(&row_full[buf], k >> 1);
+        if (s_redo[buf]) {  // a sum left fp32's middle: against the rows' maxima
+          const int R = w.q.cnt * a.g;
+          float acc[N];
 #pragma unroll
           for (int e = 0; e < N; ++e) acc[e] = -INFINITY;
           for (int j = wg; j < nt; j += 4) {
             float x[N];
-            tile(j, x);
+            tile(w, j, n0 + j, x);
 #pragma unroll
             for (int e = 0; e < N; ++e) acc[e] = fmaxf(acc[e], x[e]);
           }
           float top = exchange(warp_columns<true>(acc, lane), true);
-          ++units;
           top = lane < R && top > -INFINITY ? top * c2 : 0.0f;
-          if (ew == 0) s_row[lane] = top;
+          if (ew == 0) s_row[buf][lane] = top;
           all_sync();
 #pragma unroll
           for (int e = 0; e < N; ++e) acc[e] = 0.0f;
           for (int j = wg; j < nt; j += 4) {
             float x[N];
-            tile(j, x);
+            tile(w, j, n0 + j, x);
 #pragma unroll
-            for (int e = 0; e < N; ++e) acc[e] += fast_exp2(fmaf(x[e], c2, -s_row[e]));
+            for (int e = 0; e < N; ++e) acc[e] += fast_exp2(fmaf(x[e], c2, -s_row[buf][e]));
           }
-          sum = exchange(warp_columns<false>(acc, lane), false);
-          ++units;
-          if (ew == 0) s_row[lane] = lane < R ? -(top + log2f(sum)) : -INFINITY;
+          const float sum = exchange(warp_columns<false>(acc, lane), false);
+          if (ew == 0) s_row[buf][lane] = lane < R ? -(top + log2f(sum)) : -INFINITY;
           all_sync();
         }
         for (int j = wg; j < nt; j += 4) {
-          const int key = (t0 + j) * BM + r;
-          const float next = j + 4 < nt ? old_weight(key + 4 * BM) : 0.0f;
+          const float next = old_weight(w, j + 4);
           float x[N];
-          tile(j, x);
+          tile(w, j, n0 + j, x);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[(ld + j) % kHeldTiles]);
+          if (lane == 0) mbar_arrive(&s_empty[(n0 + j) % kHeldTiles]);
           float2 p = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int e = 0; e < N; e += 4) {
-            const float4 n4 = *reinterpret_cast<const float4*>(&s_row[e]);
+            const float4 n4 = *reinterpret_cast<const float4*>(&s_row[buf][e]);
             p.x += fast_exp2(fmaf(x[e], c2, n4.x)) + fast_exp2(fmaf(x[e + 1], c2, n4.y));
             p.y += fast_exp2(fmaf(x[e + 2], c2, n4.z)) + fast_exp2(fmaf(x[e + 3], c2, n4.w));
           }
-          if (key < total && !w.q.quiet) a.weight[base + key] = old + (p.x + p.y);
+          put(w, j, old + (p.x + p.y));
           old = next;
         }
-        ld += nt;
+      };
+      // One turn: sums of the next item (if tensor memory has room beside the one
+      // whose weights are due), then the weights that are due.
+      int late = -1, late_n0 = 0;  // the item whose weights are due, and its first tile
+      float late_old = 0.0f;
+      for (int round = 0;;) {
+        const int idx = next_item(round, n_items);
+        const bool more = idx >= 0;
+        HeldItem w = {};
+        if (more) {
+          w = item(b0, idx);
+          if (w.q.cnt == 0) {  // no rows: the old weights alone
+            for (int j = wg; j < w.nt; j += 4) put(w, j, old_weight(w, j));
+            ++round;
+            continue;
+          }
+        }
+        const int nt = w.nt;
+        const float old = more ? old_weight(w, wg) : 0.0f;
+        const bool room = more && (late < 0 || ld + nt - late_n0 <= kHeldTiles);
+        if (room) {
+          float acc[N];
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+          for (int j = wg; j < nt; j += 4) {
+            wait(&s_full[(ld + j) % kHeldTiles], (ld + j) / kHeldTiles);
+            tc_fence_after();
+            float x[N];
+            tile(w, j, ld + j, x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[e] += fast_exp2(x[e] * c2);
+          }
+          s_red[units & 1][ew][lane] = warp_columns<false>(acc, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&red_full[units & 1]);
+        }
+        if (late >= 0) finish(late, units - 1, late_n0, late_old);
+        late = -1;
+        if (room) {
+          late = idx;
+          late_n0 = ld;
+          late_old = old;
+          ld += nt;
+          ++units;
+          ++round;
+        } else if (!more) {
+          break;
+        }
       }
     }
     __syncthreads();  // the table has been read
@@ -1202,6 +1322,35 @@ static cudaError_t launch_held(const CUtensorMap& mk, const Params& prm, int fit
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// CTAs per cluster, by a model of what one request's kv-head costs a cluster: some
+// 3.8 us at least (the exchange), 0.9 us a key tile where two items' scores fit
+// beside each other, else 3.3 us and 0.7 us a tile.  Measured with 512 of them of
+// 4000 keys each in clusters of 2, 4, 8 and 16 (76, 36, 15 and 7 fit on the GPU): 120, 118, 146 and
+// 271 us; of 8000 keys in 4, 8 and 16: 221, 206 and 287; 1024 of 1000 keys in 1, 2,
+// 4: 71, 80, 139.  Two passes over K (385 us for the 512 of 8000 keys) are the
+// other way.  Nodes that a path leaves out have no key, so its tree does not count
+// as keys.  Returns the clusters that fit, 0: no request is held.
+template <int D>
+static int held_plan(const WeightArgs& a, int dev, int* cluster) {
+  const long long keys = std::max(1LL, (long long)a.max_prefix + (a.path ? 0 : a.n_max));
+  const long long tiles = (keys + BM - 1) / BM, units = (long long)a.B * a.Hkv;
+  double best = 25.0 + 2.0 * units * keys * D * 2 / 5.7e6;  // us
+  int fits = 0;
+  if (a.g > kHeldRows) return 0;
+  for (int c = 1; c <= kHeldClusterMax; c *= 2) {
+    const long long nt = (tiles + c - 1) / c;
+    if (nt > kHeldTiles) continue;
+    const int fit = held_clusters<D>(dev, c);
+    if (fit == 0) continue;
+    const double cost = (double)((units + fit - 1) / fit) * std::max(3.8, nt <= kHeldTiles / 2 ? 0.9 * nt : 3.3 + 0.7 * nt);
+    if (cost >= best) continue;
+    best = cost;
+    fits = fit;
+    *cluster = c;
+  }
+  return fits;
+}
+
 template <int D>
 static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
   int dev = 0, sms = 0;
@@ -1232,21 +1381,15 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
     mq = mk;  // not read
   }
   const long long rows = (long long)(a.window > 0 ? std::min(a.window, a.n_max) : a.n_max) * a.g;  // the most that a request has
-  const long long longest = (long long)a.max_prefix + a.n_max;
-  // Scores are held where a request has few rows: by the fewest CTAs that can hold
-  // the longest one's, and by more while the requests and heads alone leave SMs
-  // idle.  A request with more rows or keys goes the other way, inside the kernels.
+  // Scores are held where a request has few rows; one with more rows, or more keys
+  // than its cluster holds, goes the other way, inside the kernels.
   bool first = true;
-  if (a.g <= kHeldRows) {
-    int c = 1;
-    while (c < kHeldClusterMax && ((long long)c * kHeldTiles * BM < longest || 2LL * c * a.B * a.Hkv <= sms)) c *= 2;
-    int fit = held_clusters<D>(dev, c);
-    while (fit == 0 && c > 1) fit = held_clusters<D>(dev, c /= 2);
-    if (fit == 0) return cudaErrorInvalidConfiguration;
-    prm.cluster = c;
+  const long long longest = (long long)a.max_prefix + a.n_max;
+  const int fit = held_plan<D>(a, dev, &prm.cluster);
+  if (fit > 0) {
     e = launch_held<D>(mk, prm, fit, stream);
     if (e != cudaSuccess) return e;
-    if (rows <= kHeldRows && longest <= (long long)c * kHeldTiles * BM) return cudaSuccess;  // every request's are held
+    if (rows <= kHeldRows && longest <= (long long)prm.cluster * kHeldTiles * BM) return cudaSuccess;  // every request's are held
     first = false;
   }
   const int dyn = (int)Layout<D>::kDyn;
