@@ -628,6 +628,15 @@ def test_evict_orders_nan_infinities_zeros_and_close_weights():
         e.run_and_check(keep_max=799)
 
 
+@pytest.mark.parametrize("n", [2047, 2048, 2049, 16385, 49152, 49153, 70000])
+def test_evict_long_rows(n):
+    """Around the sizes where the selection changes its way."""
+    e = Evict(56, [n, 100], [301, 50], 3, 5, layers=1, Hkv=1, bs=64)
+    e.run_and_check()
+    e.weight[:] = e.weight.abs() + 1.0  # one exponent and a few more
+    e.run_and_check()
+
+
 def test_evict_without_weights_is_a_window():
     e = Evict(57, [90, 400], [40, 40], 4, 36)
     e.run_and_check(weight=None)

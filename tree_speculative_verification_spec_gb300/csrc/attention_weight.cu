@@ -230,7 +230,7 @@ cudaError_t launch_weight_cc(const WeightArgs& a, const WeightPlan& p, cudaStrea
 constexpr int kWtSms = 152;  // the plan's SM count (part of the workspace query)
 
 // Row tiles of M rows, and key splits, of 512 keys at least, while the tiles alone
-// are fewer than four items per SM.  Where most requests fill no tile (single
+// are fewer than two items per SM.  Where most requests fill no tile (single
 // tokens, paths) an item is at most 2048 keys: their lengths differ, and whole
 // ones leave SMs idle at the end.
 static WeightPlan weight_plan(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int window, int M, int* per_req) {
@@ -242,7 +242,7 @@ static WeightPlan weight_plan(int B, int T, int n_max, int max_prefix, int Hq, i
   p.tiles = std::min(each * B, packed);
   const long long keys = (long long)max_prefix + n_max, work = std::max(1LL, p.tiles * Hkv);
   const bool few = p.tiles < 2LL * B;
-  long long chunk = work >= 4LL * kWtSms ? keys : std::max(512LL, keys * work / (4LL * kWtSms));
+  long long chunk = work >= 2LL * kWtSms ? keys : std::max(512LL, keys * work / (2LL * kWtSms));
   if (few) chunk = std::min(chunk, 2048LL);
   p.chunk = (int)std::max(128LL, (chunk + 127) / 128 * 128);
   p.splits = (int)std::max(1LL, (keys + p.chunk - 1) / p.chunk);

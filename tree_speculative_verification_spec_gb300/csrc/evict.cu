@@ -8,12 +8,12 @@
 // draft).
 //
 // Two kernels.  The selection (a CTA for each layer, row and kv-head) finds the
-// border weight digit by digit, 8 bits of an order-preserving key with a
-// histogram in shared memory each, then lists the kept slots in one
-// ordered pass; equal weights at the border are taken from the lowest slot.  Rows
-// of up to 16384 slots are read once and kept in shared memory; longer ones are
-// read again by every pass.  The copy moves the listed rows of every layer, 16 bytes a
-// lane: HBM.
+// border weight by histograms, 2048 equal bins between the least and the largest
+// key that compete (an order-preserving whole number), then 2048 within the bin
+// that holds the border, and so on; then it lists the kept slots in one ordered
+// pass; equal weights at the border are taken from the lowest slot.  Rows of up
+// to 49152 slots are read once and their keys kept in shared memory.  The copy
+// moves the listed rows of every layer, 16 bytes a lane: HBM.
 #include <algorithm>
 
 #include "common.cuh"
@@ -22,10 +22,9 @@ namespace spectree {
 
 constexpr int kSelThreads = 512, kSelShort = 128;  // per row, and per row of a table of up to kSelShortSlots
 constexpr int kSelShortSlots = 2048;
-constexpr int kSelBins = 256;       // of a digit
-constexpr int kSelCopies = 4;       // of the histogram, by lane: weights crowd a few exponents
+constexpr int kSelBins = 2048;
 constexpr int kSelRun = 4;          // neighbouring slots per thread of the listing
-constexpr int kSelHeld = 16384;     // most weights held in shared memory
+constexpr int kSelHeld = 49152;     // most keys held in shared memory
 constexpr int kGatherThreads = 256;
 constexpr int kGatherCtas = 8;      // per SM
 constexpr int kGatherVec = 4;       // 16-byte vectors of K and V per thread and step
@@ -45,7 +44,7 @@ struct EvictArgs {
   long long stride;                 // weights of one (layer, row, kv-head)
   int layers, B, max_blocks, bs_log2, num_blocks, N, keep_max, first, last, Hkv;
   int vec;                          // 16-byte vectors of a row
-  int held;                         // weights that the selection's shared memory holds
+  int held;                         // keys that the selection's shared memory holds
 };
 
 // A key whose order as a whole number is the weights': NaN lowest, -0 as +0.
@@ -53,6 +52,13 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   if (x != x) return 0;
   const uint32_t u = __float_as_uint(x + 0.0f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// The weight of a key, but for what a key does not tell apart (NaNs, the zeros) or
+// does not know (a slot that stays whatever it weighs).
+__device__ __forceinline__ bool key_weight(uint32_t k, float& x) {
+  x = __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+  return k != 0u && k != 0x80000000u && k != ~0u;
 }
 
 // What row i of the call keeps, or the SPEC_DEV_* bits that stop it, its pages
@@ -78,30 +84,66 @@ __device__ __forceinline__ EvictRow evict_row(const EvictArgs& a, int i) {
   return r;
 }
 
+// Kept rows j0 .. of (layer, row i, kv-head h), K and V: as many as the CTA's
+// threads hold kGatherVec vectors each.
 template <int kThreads>
+__device__ __forceinline__ void copy_rows(const EvictArgs& a, int layer, int i, int h, const int32_t* slots, int j0, int kept) {
+  const int32_t *from = a.table + (size_t)a.src[i] * a.max_blocks, *to = a.table + (size_t)a.dst[i] * a.max_blocks;
+  uint4 *kc = reinterpret_cast<uint4*>(a.k_caches[layer]), *vc = reinterpret_cast<uint4*>(a.v_caches[layer]);
+  const int within = (1 << a.bs_log2) - 1;
+  uint4 k[kGatherVec], v[kGatherVec];
+  long long put[kGatherVec];
+#pragma unroll
+  for (int e = 0; e < kGatherVec; ++e) {
+    const int x = threadIdx.x + e * kThreads, j = j0 + x / a.vec, c = x % a.vec;
+    put[e] = -1;
+    if (j < kept) {
+      const int s = slots[j];
+      const long long get = ((((long long)from[s >> a.bs_log2] * a.Hkv + h) << a.bs_log2) + (s & within)) * a.vec + c;
+      put[e] = ((((long long)to[j >> a.bs_log2] * a.Hkv + h) << a.bs_log2) + (j & within)) * a.vec + c;
+      k[e] = kc[get];
+      v[e] = vc[get];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kGatherVec; ++e)
+    if (put[e] >= 0) {
+      kc[put[e]] = k[e];
+      vc[put[e]] = v[e];
+    }
+}
+
+// COPY: the CTA moves its rows itself.
+template <int kThreads, bool COPY>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
   constexpr int kWarps = kThreads / 32;
-  extern __shared__ float held[];
-  __shared__ uint32_t hist[2][kSelBins][kSelCopies];
+  extern __shared__ uint32_t keys[];  // of the row's slots
+  __shared__ uint32_t hist[kSelBins];
   __shared__ uint32_t s_warp[kWarps];
-  __shared__ uint32_t s_bin, s_left;
+  __shared__ uint32_t s_bin, s_left, s_least, s_most;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int h = blockIdx.x % a.Hkv, i = blockIdx.x / a.Hkv % a.N, layer = blockIdx.x / a.Hkv / a.N;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   EvictRow r = evict_row<kThreads>(a, i);
   const bool cached = r.len <= a.held;
   const float* w = nullptr;
+  // the slots outside [begin, end) stay whatever they weigh: their key is the
+  // largest, which no weight has
+  const int begin = r.first, end = r.len - r.last;
+  auto key_of = [&](int s, float x) -> uint32_t { return s < begin || s >= end ? ~0u : weight_key(x); };
   if (!r.bad) {
-    // the weights (eight loads at a time) and both rows' pages in one go
+    // the weights (sixteen loads at a time) and both rows' pages in one go
     if (a.weight) w = a.weight + (((size_t)layer * a.B + r.src) * a.Hkv + h) * a.stride;
     if (cached) {
-      for (int s0 = t; s0 < r.len; s0 += 8 * kThreads) {
-        float x[8];
+      for (int s0 = t; s0 < r.len; s0 += 16 * kThreads) {
+        float x[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = w && s0 + e * kThreads < r.len ? w[s0 + e * kThreads] : 0.0f;
+        for (int e = 0; e < 16; ++e) x[e] = w && s0 + e * kThreads < r.len ? w[s0 + e * kThreads] : 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (s0 + e * kThreads < r.len) held[s0 + e * kThreads] = x[e];
+        for (int e = 0; e < 16; ++e) {
+          const int s = s0 + e * kThreads;
+          if (s < r.len) keys[s] = key_of(s, x[e]);
+        }
       }
     }
     const int32_t *from = a.table + (size_t)r.src * a.max_blocks, *into = a.table + (size_t)r.dst * a.max_blocks;
@@ -110,7 +152,10 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     int bb = 0;
     for (int j = t; j < pages; j += kThreads) bb |= from[j] < 0 || from[j] >= a.num_blocks;
     for (int j = t; j < need; j += kThreads) bb |= into[j] < 0 || into[j] >= a.num_blocks;
-    for (int j = t; j < kSelBins * kSelCopies; j += kThreads) (&hist[0][0][0])[j] = 0;
+    if (t == 0) {
+      s_least = ~0u;
+      s_most = 0;
+    }
     if (__syncthreads_or(bb)) r.bad = SPEC_DEV_BAD_BLOCK;
   }
   int32_t* out = a.slots + (((size_t)layer * a.N + i) * a.Hkv + h) * a.keep_max;
@@ -122,72 +167,86 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   for (int j = kept + t; j < a.keep_max; j += kThreads) out[j] = -1;
   if (kept == 0) return;
   float* to = a.weight ? a.weight + (((size_t)layer * a.B + r.dst) * a.Hkv + h) * a.stride : nullptr;
-  const int begin = r.first, end = r.len - r.last;  // the slots that compete
-  uint32_t want = kept - r.first - r.last;          // how many of them stay
-  auto weight_at = [&](int s) -> float { return cached ? held[s] : w ? w[s] : 0.0f; };
+  const bool all = kept == r.len;
 
-  // border: every key above it stays, and `want` of those equal to it
-  uint32_t border = 0;
-  const bool all = want >= (uint32_t)(end - begin);
-  if (!all && want > 0) {
-    uint32_t mask = 0;
-    for (int pass = 0, shift = 24; pass < 4; ++pass, shift -= 8) {
+  // border: every key above it stays, and the first `ties` of those equal to it.
+  // Of the competing keys within [low, low + 2^width) a histogram of 2048 equal bins
+  // tells the one that holds the border; the next round's range is that bin.
+  uint32_t border = 0, ties = 0;
+  if (!all) {
+    auto key_at = [&](int s) -> uint32_t { return cached ? keys[s] : w ? weight_key(w[s]) : weight_key(0.0f); };
+    uint32_t least = ~0u, most = 0;
+    for (int s = begin + t; s < end; s += kThreads) {
+      const uint32_t k = key_at(s);
+      least = min(least, k);
+      most = max(most, k);
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      atomicMin(&s_least, least);
+      atomicMax(&s_most, most);
+    }
+    __syncthreads();
+    uint32_t low = s_least, high = s_most;
+    ties = kept - r.first - r.last;  // 0: the ends alone stay, and no key is above `most`
+    if (ties == 0) border = high;
+    for (int shift = max(0, 21 - __clz(high - low)); ties > 0;) {
+      for (int j = t; j < kSelBins; j += kThreads) hist[j] = 0;
+      __syncthreads();
+#pragma unroll 4
       for (int s = begin + t; s < end; s += kThreads) {
-        const uint32_t k = weight_key(weight_at(s));
-        if ((k & mask) == border) atomicAdd(&hist[pass & 1][k >> shift & 255][lane % kSelCopies], 1u);
+        const uint32_t k = key_at(s);
+        if (k >= low && k <= high) atomicAdd(&hist[(k - low) >> shift], 1u);
       }
       __syncthreads();
-      if (warp == 0) {
-        // the bin where the count from the top reaches `want`: eight bins a lane
-        uint32_t c[8], sum = 0;
+      // the bin where the count from the top reaches `ties`: each thread holds kBins
+      // bins in a row, counted from the top
+      constexpr int kBins = kSelBins / kThreads;
+      uint32_t c[kBins], sum = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 x = *reinterpret_cast<const uint4*>(hist[pass & 1][255 - (8 * lane + e)]);
-          sum += c[e] = x.x + x.y + x.z + x.w;
-        }
-        uint32_t at = sum;
+      for (int e = 0; e < kBins; ++e) sum += c[e] = hist[kSelBins - 1 - (kBins * t + e)];
+      uint32_t at = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t y = __shfl_up_sync(0xffffffffu, at, o);
-          if (lane >= o) at += y;
-        }
-        at -= sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += y;
+      }
+      if (lane == 31) s_warp[warp] = at;
+      __syncthreads();
+      at -= sum;
+      for (int k = 0; k < warp; ++k) at += s_warp[k];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (at < want && want <= at + c[e]) {
-            s_bin = 255 - (8 * lane + e);
-            s_left = want - at;
-          }
-          at += c[e];
+      for (int e = 0; e < kBins; ++e) {
+        if (at < ties && ties <= at + c[e]) {
+          s_bin = kSelBins - 1 - (kBins * t + e);
+          s_left = ties - at;
         }
-      } else {
-        for (int j = t - 32; j < kSelBins * kSelCopies; j += kThreads - 32) (&hist[~pass & 1][0][0])[j] = 0;
+        at += c[e];
       }
       __syncthreads();
-      border |= s_bin << shift;
-      want = s_left;
-      mask |= 255u << shift;
+      low += s_bin << shift;
+      ties = s_left;
+      border = low;
+      if (shift == 0) break;
+      high = low + ((1u << shift) - 1);
+      shift = max(0, shift - 11);
     }
   }
 
   // the kept slots in order, kSelRun neighbours to a thread: counts of larger and
-  // of equal keys (the equal ones stay while there is want) go through one scan
+  // of equal keys (the first `ties` of these stay) go through one scan
   uint32_t big = 0, equal = 0;  // of the slots before this round
   for (int s0 = 0; s0 < r.len; s0 += kThreads * kSelRun) {
     const int s = s0 + t * kSelRun;
     uint32_t g = 0, q = 0;  // bit e: slot s + e
-    float x[kSelRun];
-#pragma unroll
-    for (int e = 0; e < kSelRun; ++e) x[e] = s + e < r.len ? weight_at(s + e) : 0.0f;
+    uint32_t key[kSelRun];
 #pragma unroll
     for (int e = 0; e < kSelRun; ++e) {
       if (s + e >= r.len) continue;
-      if (s + e < begin || s + e >= end || all) g |= 1u << e;
-      else if (want > 0) {
-        const uint32_t k = weight_key(x[e]);
-        g |= (uint32_t)(k > border) << e;
-        q |= (uint32_t)(k == border) << e;
-      }
+      const uint32_t k = key[e] = cached ? keys[s + e] : key_of(s + e, w ? w[s + e] : 0.0f);
+      g |= (uint32_t)(all || k > border) << e;
+      q |= (uint32_t)(!all && k == border) << e;
     }
     const uint32_t mine = __popc(g) | (uint32_t)__popc(q) << 16;
     uint32_t incl = mine;
@@ -202,18 +261,21 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     uint32_t before = incl - mine, total = 0;  // 16 bits each: at most 2048 of a round
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
-      const uint32_t x = s_warp[k];
-      before += k < warp ? x : 0;
-      total += x;
+      const uint32_t y = s_warp[k];
+      before += k < warp ? y : 0;
+      total += y;
     }
     uint32_t bg = big + (before & 0xffffu), bq = equal + (before >> 16);
 #pragma unroll
     for (int e = 0; e < kSelRun; ++e) {
       const bool heavy = g >> e & 1, even = q >> e & 1;
-      if (heavy || (even && bq < want)) {
-        const uint32_t at = bg + min(bq, want);
+      if (heavy || (even && bq < ties)) {
+        const uint32_t at = bg + min(bq, ties);
         out[at] = s + e;
-        if (to) to[at] = x[e];
+        if (to) {
+          float x;
+          to[at] = key_weight(key[e], x) ? x : w[s + e];
+        }
       }
       bg += heavy;
       bq += even;
@@ -221,10 +283,13 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     big += total & 0xffffu;
     equal += total >> 16;
   }
+  if (COPY) {
+    __syncthreads();  // the list is whole
+    const int rows = kThreads * kGatherVec / a.vec;
+    for (int j0 = 0; j0 < kept; j0 += rows) copy_rows<kThreads>(a, layer, i, h, out, j0, kept);
+  }
 }
 
-// Kept row j of (layer, row i, kv-head h), K and V: a unit is a run of rows whose
-// vectors fill the CTA's threads kGatherVec times.
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictArgs a, long long units, int per_head) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rows = kGatherThreads * kGatherVec / a.vec;  // of a unit
@@ -232,32 +297,8 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const Evic
     const int part = (int)(unit % per_head);
     const long long head = unit / per_head;
     const int h = (int)(head % a.Hkv), i = (int)(head / a.Hkv % a.N), layer = (int)(head / a.Hkv / a.N);
-    const int kept = a.new_len[i], j0 = part * rows;
-    if (j0 >= kept) continue;
-    const int32_t* slots = a.slots + (size_t)head * a.keep_max;
-    const int32_t *from = a.table + (size_t)a.src[i] * a.max_blocks, *to = a.table + (size_t)a.dst[i] * a.max_blocks;
-    uint4 *kc = reinterpret_cast<uint4*>(a.k_caches[layer]), *vc = reinterpret_cast<uint4*>(a.v_caches[layer]);
-    const int within = (1 << a.bs_log2) - 1;
-    uint4 k[kGatherVec], v[kGatherVec];
-    long long put[kGatherVec];
-#pragma unroll
-    for (int e = 0; e < kGatherVec; ++e) {
-      const int x = threadIdx.x + e * kGatherThreads, j = j0 + x / a.vec, c = x % a.vec;
-      put[e] = -1;
-      if (j < kept) {
-        const int s = slots[j];
-        const long long get = ((((long long)from[s >> a.bs_log2] * a.Hkv + h) << a.bs_log2) + (s & within)) * a.vec + c;
-        put[e] = ((((long long)to[j >> a.bs_log2] * a.Hkv + h) << a.bs_log2) + (j & within)) * a.vec + c;
-        k[e] = kc[get];
-        v[e] = vc[get];
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < kGatherVec; ++e)
-      if (put[e] >= 0) {
-        kc[put[e]] = k[e];
-        vc[put[e]] = v[e];
-      }
+    const int kept = a.new_len[i];
+    if (part * rows < kept) copy_rows<kGatherThreads>(a, layer, i, h, a.slots + (size_t)head * a.keep_max, part * rows, kept);
   }
 }
 
@@ -312,16 +353,20 @@ extern "C" spec_status spec_kv_evict(void* const* k_caches, void* const* v_cache
   a.Hkv = Hkv;
   a.vec = D * (dtype == SPEC_F32 ? 4 : 2) / 16;
   cudaStream_t st = (cudaStream_t)stream;
-  // room for the weights of the longest row that the table and the weights allow
+  // room for the keys of the longest row that the table and the weights allow
   const long long most = std::min((long long)max_blocks << a.bs_log2, weight ? weight_stride : (1LL << 30));
   a.held = (int)std::min<long long>(most, kSelHeld);
-  const int dyn = a.held * (int)sizeof(float);
+  const int dyn = a.held * (int)sizeof(uint32_t);
   const bool small = most <= kSelShortSlots;
-  const auto select = small ? evict_select_kernel<kSelShort> : evict_select_kernel<kSelThreads>;
+  // With rows enough for every SM a CTA moves what it has selected while others
+  // select; with fewer, the copy is a kernel of its own that every SM takes part in.
+  const bool copy = heads >= 2LL * sms;
+  const auto select = small ? (copy ? evict_select_kernel<kSelShort, true> : evict_select_kernel<kSelShort, false>)
+                            : (copy ? evict_select_kernel<kSelThreads, true> : evict_select_kernel<kSelThreads, false>);
   if (cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess) return SPEC_ERR_CUDA;
   select<<<(unsigned)heads, small ? kSelShort : kSelThreads, dyn, st>>>(a);
   SPEC_LAUNCH_CHECK();
-  if (keep_max == 0) return SPEC_OK;
+  if (keep_max == 0 || copy) return SPEC_OK;
   const int rows = kGatherThreads * kGatherVec / a.vec, per_head = (keep_max + rows - 1) / rows;
   const long long units = heads * per_head;
   cudaLaunchConfig_t cfg = {};

@@ -1336,7 +1336,9 @@ static int held_plan(const WeightArgs& a, int dev, int* cluster) {
   const long long tiles = (keys + BM - 1) / BM, units = (long long)a.B * a.Hkv;
   double best = 25.0 + 2.0 * units * keys * D * 2 / 5.7e6;  // us
   int fits = 0;
-  if (a.g > kHeldRows) return 0;
+  // packed rows: not for a batch whose requests have more on average
+  const long long average = a.window > 0 ? std::min<long long>(a.window, a.T / a.B) : a.T / a.B;
+  if (a.g > kHeldRows || (!a.path && average * a.g > 2 * kHeldRows)) return 0;
   for (int c = 1; c <= kHeldClusterMax; c *= 2) {
     const long long nt = (tiles + c - 1) / c;
     if (nt > kHeldTiles) continue;
@@ -1363,8 +1365,8 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
   while ((1 << prm.bs_log2) < a.block_size) ++prm.bs_log2;
   prm.rows_total = (long long)a.num_blocks * a.Hkv * a.block_size;
   prm.q_tma = !a.path && BM % a.g == 0 && a.T > 0;
-  // sums over few rows: some four items for every CTA, of 256 to 2048 keys
-  const long long keys = ((long long)a.max_prefix + a.n_max) * a.B * a.Hkv / (4LL * sms);
+  // sums over few rows: some two items for every CTA, of 256 to 2048 keys
+  const long long keys = ((long long)a.max_prefix + a.n_max) * a.B * a.Hkv / (2LL * sms);
   prm.key_chunk = (int)std::min(2048LL, std::max(256LL, (keys + 255) / 256 * 256));
   alignas(64) CUtensorMap mk, mq;
   {
