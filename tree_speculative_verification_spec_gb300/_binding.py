@@ -404,12 +404,14 @@ def spec_rope_append(qkv, q_norm, k_norm, eps, inv_freq, axis, rot_dim, pairing,
     heads and may lie apart (a slice of a wider projection); q_norm and k_norm:
     [D] of that dtype or None; inv_freq: float32; axis, pos_base and pos may be
     None."""
-    if any(t is not None and t.dtype != qkv.dtype for t in (q_norm, k_norm, q_out, k_cache, v_cache)):
+    dtype, strides = qkv.dtype, qkv.stride()
+    if q_out.dtype != dtype or k_cache.dtype != dtype or v_cache.dtype != dtype or (q_norm is not None and q_norm.dtype != dtype) or \
+            (k_norm is not None and k_norm.dtype != dtype):
         raise ValueError("qkv, q_out, the norms and the caches must have one dtype")
-    if not qkv.is_cuda or (T > 0 and not qkv[0].is_contiguous()):
+    if not qkv.is_cuda or strides[-1] != 1 or (len(strides) == 3 and strides[1] != D):
         raise ValueError("qkv must be a CUDA tensor with contiguous rows")
     _check("spec_rope_append", lib().spec_rope_append(
-        qkv.data_ptr(), qkv.stride(0) if T > 1 else (Hq + 2 * Hkv) * D, _ptr(q_norm), _ptr(k_norm), float(eps), _f32(inv_freq), _i32(axis),
+        qkv.data_ptr(), strides[0] if T > 1 else (Hq + 2 * Hkv) * D, _ptr(q_norm), _ptr(k_norm), float(eps), _f32(inv_freq), _i32(axis),
         rot_dim, pairing, _i32(pos_base), _i32(pos), axes, _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
         _i32(block_table), max_blocks, block_size, num_blocks, _i32(prefix_len), _i32(tree_off), B, T, n_max, Hq, Hkv,
         D, _dtype_code(qkv), _i32(status), _stream_of(qkv, stream)))

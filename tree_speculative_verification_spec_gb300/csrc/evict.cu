@@ -12,7 +12,7 @@
 // key that compete (an order-preserving whole number), then 2048 within the bin
 // that holds the border, and so on; then it lists the kept slots in one ordered
 // pass; equal weights at the border are taken from the lowest slot.  Rows of up
-// to 49152 slots are read once and their keys kept in shared memory.  The copy
+// to 16384 slots are read once and their keys kept in shared memory.  The copy
 // moves the listed rows of every layer, 16 bytes a lane: HBM.
 #include <algorithm>
 
@@ -24,7 +24,7 @@ constexpr int kSelThreads = 512, kSelShort = 128;  // per row, and per row of a 
 constexpr int kSelShortSlots = 2048;
 constexpr int kSelBins = 2048;
 constexpr int kSelRun = 4;          // neighbouring slots per thread of the listing
-constexpr int kSelHeld = 49152;     // most keys held in shared memory
+constexpr int kSelHeld = 16384;     // most keys held in shared memory (three CTAs an SM)
 constexpr int kGatherThreads = 256;
 constexpr int kGatherCtas = 8;      // per SM
 constexpr int kGatherVec = 4;       // 16-byte vectors of K and V per thread and step
@@ -363,7 +363,7 @@ extern "C" spec_status spec_kv_evict(void* const* k_caches, void* const* v_cache
   const bool copy = heads >= 2LL * sms;
   const auto select = small ? (copy ? evict_select_kernel<kSelShort, true> : evict_select_kernel<kSelShort, false>)
                             : (copy ? evict_select_kernel<kSelThreads, true> : evict_select_kernel<kSelThreads, false>);
-  if (cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (dyn > 32 * 1024 && cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess) return SPEC_ERR_CUDA;
   select<<<(unsigned)heads, small ? kSelShort : kSelThreads, dyn, st>>>(a);
   SPEC_LAUNCH_CHECK();
   if (keep_max == 0 || copy) return SPEC_OK;

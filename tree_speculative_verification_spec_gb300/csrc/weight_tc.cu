@@ -46,9 +46,8 @@ constexpr int kLse = 4;              // row tiles whose sums are held for the ep
 constexpr int kGroup = 256;          // requests numbered at a time
 constexpr float kSumTop = 0x1p60f;
 enum Mode { kStats = 0, kSumsFew = 1, kSumsMany = 2, kHeld = 3 };
-constexpr int kHeldRows = 32;        // rows whose scores are held, and the columns of a key tile's
+constexpr int kHeldRows = 32;        // most rows of a request whose scores are held
 constexpr int kHeldQ = 4;            // items whose queries are ahead in shared memory
-constexpr int kHeldTiles = 512 / kHeldRows;  // key tiles of a CTA whose scores tensor memory holds
 
 template <int D> struct Layout {
   static constexpr int DH = D / 64;             // 128-byte halves of a row
@@ -67,7 +66,8 @@ struct Params {
   int bs_log2;
   int q_tma;             // Q by TMA (packed rows, g divides 128), else by cp.async
   int key_chunk;         // keys per item of the sums over few rows
-  int cluster;           // CTAs that hold one request's scores of a kv-head (0: none is held)
+  int cluster;           // CTAs that hold one request's scores of a kv-head (0: none is held),
+  int held_rows;         // of at most this many rows (16 or 32: the columns of a key tile)
 };
 
 struct Request {
@@ -91,7 +91,7 @@ template <int MODE>
 __device__ __forceinline__ int request_tiles(const Params& prm, const Request& r) {
   const WeightArgs& a = prm.a;
   const int R = r.cnt * a.g, total = r.P + r.m;
-  const bool held = prm.cluster > 0 && (R == 0 || (R <= kHeldRows && (total + BM - 1) / BM <= kHeldTiles * prm.cluster));
+  const bool held = prm.cluster > 0 && (R == 0 || (R <= prm.held_rows && (total + BM - 1) / BM <= 512 / prm.held_rows * prm.cluster));
   if (MODE == kHeld) return held;
   if (held) return 0;
   if (MODE == kStats) return (R + 2 * BM - 1) / (2 * BM);
@@ -680,28 +680,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Held scores: one pass over K.  A cluster of CTAs takes one request's kv-head
-// (at most 32 rows), each CTA a run of its key tiles.  The scores of all tiles
-// stay in tensor memory (32 columns a tile, up to 16 tiles); as a tile arrives,
-// each thread adds 2^x of its key to the 32 row sums.  The CTAs exchange their
+// (N rows at most, 16 or 32), each CTA a run of its key tiles.  The scores of all
+// tiles stay in tensor memory (N columns a tile, up to 512 / N tiles); as a tile
+// arrives, each thread adds 2^x of its key to the N row sums.  The CTAs exchange their
 // sums (a value per row and CTA, by st.async to every CTA of the cluster), and
 // the weights come from the scores still held: K is read once.  While an item's
 // sums travel the next one's tiles are loaded, multiplied and summed.
 // ---------------------------------------------------------------------------
-template <int D> struct HeldLayout {
+template <int D, int N> struct HeldLayout {
   static constexpr int DH = D / 64;
   static constexpr int NST = D == 128 ? 5 : 8;
-  static constexpr uint32_t kTile = BM * D * 2, kQ = kHeldRows * D * 2;
+  static constexpr uint32_t kTile = BM * D * 2, kQ = N * D * 2;
   static constexpr uint32_t kOffQ = NST * kTile;
   static constexpr uint32_t kBytes = kOffQ + kHeldQ * kQ;
   static constexpr uint32_t kDyn = kBytes + 1024 < 120 * 1024 ? 120 * 1024 : kBytes + 1024;
   static_assert(kDyn + 24576 <= 227 * 1024, "dynamic and static shared memory within 227 KB");
 };
 
-// v[0] of lane e: the sum (or maximum) over the warp's lanes of what v[e] was.
-template <bool MAX>
-__device__ __forceinline__ float warp_columns(float (&v)[32], int lane) {
+// The sum (or maximum) over the warp's lanes of v[e], for lane e (and e + 16, with
+// 16 of them).
+template <bool MAX, int N>
+__device__ __forceinline__ float warp_columns(float (&v)[N], int lane) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
+  for (int o = N / 2; o; o >>= 1)
 #pragma unroll
     for (int i = 0; i < o; ++i) {
       const bool up = lane & o;
@@ -709,7 +710,26 @@ __device__ __forceinline__ float warp_columns(float (&v)[32], int lane) {
       const float got = __shfl_xor_sync(0xffffffffu, give, o);
       v[i] = MAX ? fmaxf(keep, got) : keep + got;
     }
+  if (N == 16) {
+    const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
+    v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
+  }
   return v[0];
+}
+
+// N consecutive TMEM columns of this thread's lane, once they have arrived.
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[32]) {
+  tmem_ld32(taddr, r);
+  tmem_wait_ld(r);
+}
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -749,14 +769,14 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 
 constexpr int kHeldClusterMax = 16;
 
-template <int D>
+template <int D, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_held_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ Params prm) {
-  using L = HeldLayout<D>;
-  constexpr int NST = L::NST, N = kHeldRows, EW = 16;  // epilogue warps
+  using L = HeldLayout<D, N>;
+  constexpr int NST = L::NST, TILES = 512 / N, EW = 16;  // EW: epilogue warps
   const WeightArgs& a = prm.a;
   extern __shared__ uint8_t dyn_raw[];
-  __shared__ uint64_t full[NST], empty[NST], q_full[kHeldQ], q_empty[kHeldQ], s_full[kHeldTiles], s_empty[kHeldTiles], drain;
+  __shared__ uint64_t full[NST], empty[NST], q_full[kHeldQ], q_empty[kHeldQ], s_full[TILES], s_empty[TILES], drain;
   __shared__ uint64_t red_full[2], x_full[2], row_full[2], redo_full[2];
   __shared__ Table tab;
   // by item parity: each epilogue warp's row sums, each CTA's, and what the epilogue
@@ -788,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&row_full[i], 1);
       mbar_init(&redo_full[i], 1);
     }
-    for (int i = 0; i < kHeldTiles; ++i) {
+    for (int i = 0; i < TILES; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4);
     }
@@ -980,9 +1000,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&q_full[units % kHeldQ], units / kHeldQ);
         const uint64_t qd = qd0 + (uint64_t)((units % kHeldQ) * (L::kQ >> 4));
         for (int j = 0; j < w.nt; ++j, ++ld) {
-          const int st = ld % NST, s = ld % kHeldTiles;
+          const int st = ld % NST, s = ld % TILES;
           wait(&full[st], ld / NST);
-          if (ld >= kHeldTiles) wait(&s_empty[s], ld / kHeldTiles - 1);
+          if (ld >= TILES) wait(&s_empty[s], ld / TILES - 1);
           tc_fence_after();
           if (leader) {
             const uint64_t kd = ring + (uint64_t)(st * (L::kTile >> 4));
@@ -1008,17 +1028,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w.q.cnt == 0) continue;
         const int buf = units & 1, phase = units >> 1;
         wait(&red_full[buf], phase);
-        float v = s_red[buf][0][lane];
+        const bool row = lane < N;
+        float v = row ? s_red[buf][0][lane] : 0.0f;
 #pragma unroll
-        for (int k = 1; k < EW; ++k) v += s_red[buf][k][lane];
+        for (int k = 1; k < EW; ++k) v += row ? s_red[buf][k][lane] : 0.0f;
         if (lane == 0) mbar_expect_tx(&x_full[buf], C * N * 4);
         __syncwarp();
-        for (int k = 0; k < C; ++k) send_async(&s_in[buf][rank][lane], &x_full[buf], k, v);
+        for (int k = 0; k < C && row; ++k) send_async(&s_in[buf][rank][lane], &x_full[buf], k, v);
+        __syncwarp();
         mbar_wait_cluster(&x_full[buf], phase & 1, &abort_flag);
-        float sum = s_in[buf][0][lane];
-        for (int k = 1; k < C; ++k) sum += s_in[buf][k][lane];
+        float sum = 0.0f;
+        for (int k = 0; k < C && row; ++k) sum += s_in[buf][k][lane];
         const bool there = lane < w.q.cnt * a.g, fits = !there || (sum >= 1.0f / kSumTop && sum < kSumTop);
-        s_row[buf][lane] = there ? -log2f(sum) : -INFINITY;
+        if (row) s_row[buf][lane] = there ? -log2f(sum) : -INFINITY;
         const bool redo = !__all_sync(0xffffffffu, fits);
         if (lane == 0) s_redo[buf] = redo;
         __syncwarp();
@@ -1037,8 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // last visible slot lane e holds in `lim`, does not see the key.
       auto tile = [&](const HeldItem& w, int j, int n, float (&x)[N]) {
         uint32_t u[N];
-        tmem_ld32(tS + (uint32_t)(n % kHeldTiles) * N, u);
-        tmem_wait_ld(u);
+        tmem_get(tS + (uint32_t)(n % TILES) * N, u);
         const int k0 = (w.t0 + j) * BM;
         if (k0 + BM - 1 > w.q.P + w.q.first) {
           const int lim = lane < w.q.cnt * a.g ? w.q.P + w.q.first + lane / a.g : -1;
@@ -1055,18 +1076,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A row's value over the cluster for a second look: the CTA's warps meet, warp 4
       // does what warp 3 does for the first look.  In warp 4 the result of row `lane`.
       auto exchange = [&](float v, bool max) -> float {
-        s_red2[ew][lane] = v;
+        if (lane < N) s_red2[ew][lane] = v;
         all_sync();
         const int buf = looks & 1, phase = looks >> 1;
         ++looks;
         if (ew != 0) return 0.0f;
-        for (int k = 1; k < EW; ++k) v = max ? fmaxf(v, s_red2[k][lane]) : v + s_red2[k][lane];
+        const bool row = lane < N;
+        for (int k = 1; k < EW && row; ++k) v = max ? fmaxf(v, s_red2[k][lane]) : v + s_red2[k][lane];
+        __syncwarp();
         if (lane == 0) mbar_expect_tx(&redo_full[buf], C * N * 4);
         __syncwarp();
-        for (int k = 0; k < C; ++k) send_async(&s_again[buf][rank][lane], &redo_full[buf], k, v);
+        for (int k = 0; k < C && row; ++k) send_async(&s_again[buf][rank][lane], &redo_full[buf], k, v);
+        __syncwarp();
         mbar_wait_cluster(&redo_full[buf], phase & 1, &abort_flag);
-        float all = s_again[buf][0][lane];
-        for (int k = 1; k < C; ++k) all = max ? fmaxf(all, s_again[buf][k][lane]) : all + s_again[buf][k][lane];
+        float all = max ? -INFINITY : 0.0f;
+        for (int k = 0; k < C && row; ++k) all = max ? fmaxf(all, s_again[buf][k][lane]) : all + s_again[buf][k][lane];
         return all;
       };
       auto old_weight = [&](const HeldItem& w, int j) -> float {
@@ -1094,9 +1118,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < N; ++e) acc[e] = fmaxf(acc[e], x[e]);
           }
-          float top = exchange(warp_columns<true>(acc, lane), true);
+          float top = exchange(warp_columns<true, N>(acc, lane), true);
           top = lane < R && top > -INFINITY ? top * c2 : 0.0f;
-          if (ew == 0) s_row[buf][lane] = top;
+          if (ew == 0 && lane < N) s_row[buf][lane] = top;
           all_sync();
 #pragma unroll
           for (int e = 0; e < N; ++e) acc[e] = 0.0f;
@@ -1106,8 +1130,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < N; ++e) acc[e] += fast_exp2(fmaf(x[e], c2, -s_row[buf][e]));
           }
-          const float sum = exchange(warp_columns<false>(acc, lane), false);
-          if (ew == 0) s_row[buf][lane] = lane < R ? -(top + log2f(sum)) : -INFINITY;
+          const float sum = exchange(warp_columns<false, N>(acc, lane), false);
+          if (ew == 0 && lane < N) s_row[buf][lane] = lane < R ? -(top + log2f(sum)) : -INFINITY;
           all_sync();
         }
         for (int j = wg; j < nt; j += 4) {
@@ -1116,7 +1140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tile(w, j, n0 + j, x);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[(n0 + j) % kHeldTiles]);
+          if (lane == 0) mbar_arrive(&s_empty[(n0 + j) % TILES]);
           float2 p = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int e = 0; e < N; e += 4) {
@@ -1146,20 +1170,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int nt = w.nt;
         const float old = more ? old_weight(w, wg) : 0.0f;
-        const bool room = more && (late < 0 || ld + nt - late_n0 <= kHeldTiles);
+        const bool room = more && (late < 0 || ld + nt - late_n0 <= TILES);
         if (room) {
           float acc[N];
 #pragma unroll
           for (int e = 0; e < N; ++e) acc[e] = 0.0f;
           for (int j = wg; j < nt; j += 4) {
-            wait(&s_full[(ld + j) % kHeldTiles], (ld + j) / kHeldTiles);
+            wait(&s_full[(ld + j) % TILES], (ld + j) / TILES);
             tc_fence_after();
             float x[N];
             tile(w, j, ld + j, x);
 #pragma unroll
             for (int e = 0; e < N; ++e) acc[e] += fast_exp2(x[e] * c2);
           }
-          s_red[units & 1][ew][lane] = warp_columns<false>(acc, lane);
+          const float mine = warp_columns<false, N>(acc, lane);
+          if (lane < N) s_red[units & 1][ew][lane] = mine;
           __syncwarp();
           if (lane == 0) mbar_arrive(&red_full[units & 1]);
         }
@@ -1277,11 +1302,11 @@ static cudaError_t launch(void (*kern)(P...), long long grid, int threads, int d
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int D>
+template <int D, int N>
 static void held_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int c) {
   cfg.gridDim = dim3(c, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = HeldLayout<D>::kDyn;
+  cfg.dynamicSmemBytes = HeldLayout<D, N>::kDyn;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;
   attr[0].val.clusterDim.y = 1;
@@ -1292,7 +1317,7 @@ static void held_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int 
 
 // Clusters of c CTAs that device `dev` (the current one) runs at once; asked for
 // once per device and size.
-template <int D>
+template <int D, int N>
 static int held_clusters(int dev, int c) {
   static std::atomic<int> known[64][kHeldClusterMax + 1];  // number + 1
   const bool keep = dev < 64;
@@ -1300,10 +1325,10 @@ static int held_clusters(int dev, int c) {
   int n = 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  held_config<D>(cfg, attr, c);
-  if (cudaFuncSetAttribute(weight_held_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)HeldLayout<D>::kDyn) != cudaSuccess ||
-      cudaFuncSetAttribute(weight_held_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, weight_held_kernel<D>, &cfg) != cudaSuccess) {
+  held_config<D, N>(cfg, attr, c);
+  if (cudaFuncSetAttribute(weight_held_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)HeldLayout<D, N>::kDyn) != cudaSuccess ||
+      cudaFuncSetAttribute(weight_held_kernel<D, N>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, weight_held_kernel<D, N>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -1311,14 +1336,14 @@ static int held_clusters(int dev, int c) {
   return n;
 }
 
-template <int D>
+template <int D, int N>
 static cudaError_t launch_held(const CUtensorMap& mk, const Params& prm, int fit, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  held_config<D>(cfg, attr, prm.cluster);
+  held_config<D, N>(cfg, attr, prm.cluster);
   cfg.gridDim = dim3((unsigned)(std::min<long long>(fit, (long long)prm.a.B * prm.a.Hkv) * prm.cluster), 1, 1);
   cfg.stream = stream;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, weight_held_kernel<D>, mk, prm);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, weight_held_kernel<D, N>, mk, prm);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -1330,21 +1355,22 @@ static cudaError_t launch_held(const CUtensorMap& mk, const Params& prm, int fit
 // 4: 71, 80, 139.  Two passes over K (385 us for the 512 of 8000 keys) are the
 // other way.  Nodes that a path leaves out have no key, so its tree does not count
 // as keys.  Returns the clusters that fit, 0: no request is held.
-template <int D>
+template <int D, int N>
 static int held_plan(const WeightArgs& a, int dev, int* cluster) {
+  constexpr int kMost = 512 / N;  // key tiles of a CTA
   const long long keys = std::max(1LL, (long long)a.max_prefix + (a.path ? 0 : a.n_max));
   const long long tiles = (keys + BM - 1) / BM, units = (long long)a.B * a.Hkv;
   double best = 25.0 + 2.0 * units * keys * D * 2 / 5.7e6;  // us
   int fits = 0;
   // packed rows: not for a batch whose requests have more on average
   const long long average = a.window > 0 ? std::min<long long>(a.window, a.T / a.B) : a.T / a.B;
-  if (a.g > kHeldRows || (!a.path && average * a.g > 2 * kHeldRows)) return 0;
+  if (a.g > N || (!a.path && average * a.g > 2 * N)) return 0;
   for (int c = 1; c <= kHeldClusterMax; c *= 2) {
     const long long nt = (tiles + c - 1) / c;
-    if (nt > kHeldTiles) continue;
-    const int fit = held_clusters<D>(dev, c);
+    if (nt > kMost) continue;
+    const int fit = held_clusters<D, N>(dev, c);
     if (fit == 0) continue;
-    const double cost = (double)((units + fit - 1) / fit) * std::max(3.8, nt <= kHeldTiles / 2 ? 0.9 * nt : 3.3 + 0.7 * nt);
+    const double cost = (double)((units + fit - 1) / fit) * std::max(3.8, nt <= kMost / 2 ? 0.9 * nt : 3.3 + 0.7 * nt);
     if (cost >= best) continue;
     best = cost;
     fits = fit;
@@ -1387,11 +1413,12 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
   // than its cluster holds, goes the other way, inside the kernels.
   bool first = true;
   const long long longest = (long long)a.max_prefix + a.n_max;
-  const int fit = held_plan<D>(a, dev, &prm.cluster);
+  prm.held_rows = rows <= 16 ? 16 : kHeldRows;
+  const int fit = prm.held_rows == 16 ? held_plan<D, 16>(a, dev, &prm.cluster) : held_plan<D, 32>(a, dev, &prm.cluster);
   if (fit > 0) {
-    e = launch_held<D>(mk, prm, fit, stream);
+    e = prm.held_rows == 16 ? launch_held<D, 16>(mk, prm, fit, stream) : launch_held<D, 32>(mk, prm, fit, stream);
     if (e != cudaSuccess) return e;
-    if (rows <= kHeldRows && longest <= (long long)prm.cluster * kHeldTiles * BM) return cudaSuccess;  // every request's are held
+    if (rows <= prm.held_rows && longest <= 512LL / prm.held_rows * prm.cluster * BM) return cudaSuccess;  // every request's are held
     first = false;
   }
   const int dyn = (int)Layout<D>::kDyn;
