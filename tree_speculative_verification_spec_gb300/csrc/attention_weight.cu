@@ -84,6 +84,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kWtThreads) weight_stats_cc_kernel(const WeightArgs a) {
   extern __shared__ float sm[];
   float *sq = sm, *sk = sm + D * (64 + kWtPad);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int kvh = blockIdx.x % a.Hkv, split = blockIdx.x / a.Hkv % a.splits;
   const long long tile = blockIdx.x / a.Hkv / a.splits;
   const int b = weight_find(a, tile, kWtRows);
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kWtThreads) weight_sums_cc_kernel(const Weight
   extern __shared__ float sm[];
   float *sq = sm, *sk = sm + D * (64 + kWtPad);
   __shared__ float s_lse[kWtRows], s_part[16][kWtKeys];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int kvh = blockIdx.x % a.Hkv;
   const int kt = (int)(blockIdx.x / a.Hkv % key_tiles), b = (int)(blockIdx.x / a.Hkv / key_tiles);
   WeightRequest r;
@@ -219,8 +221,18 @@ static cudaError_t launch_cc(const WeightArgs& a, const WeightPlan& p, cudaStrea
     if (e != cudaSuccess) return e;
   }
   const int key_tiles = (a.max_prefix + a.n_max + kWtKeys - 1) / kWtKeys;
-  weight_sums_cc_kernel<T, D><<<(unsigned)((long long)a.B * key_tiles * a.Hkv), kWtThreads, dyn, stream>>>(a, key_tiles);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)a.B * key_tiles * a.Hkv), 1, 1);
+  cfg.blockDim = dim3(kWtThreads, 1, 1);
+  cfg.dynamicSmemBytes = dyn;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];  // a programmatic dependent of the statistics
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.tiles > 0 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, weight_sums_cc_kernel<T, D>, a, key_tiles);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_weight_cc(const WeightArgs& a, const WeightPlan& p, cudaStream_t stream) {

@@ -92,6 +92,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const Rope
   __shared__ float s_row[MODE == kRopeShared ? GROUPS : 1][D];  // a normalised row (pairs that cross lanes)
   __shared__ long long s_slot[kRopeTokens];  // row of the token's slot in kv-head 0 of its page
   __shared__ int s_bad[kRopeTokens];
+  // The tables lie so that lanes that read 16 bytes each, of neighbouring vectors,
+  // read neighbouring 16 bytes: element j of vector v at ((j / 4) n + v) 4 + j % 4,
+  // n vectors in all (32 bytes apart, eight lanes' reads fell on four banks twice).
+  constexpr int PV = MODE == kRopeHalves ? VE : 4;  // pairs per vector of the angles' table
+  auto pair_at = [](int pair) { return ((pair % PV / 4) * (D / 2 / PV) + pair / PV) * 4 + pair % 4; };
+  auto norm_at = [](int el) { return ((el % VE / 4) * (D / VE) + el / VE) * 4 + el % 4; };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tile = blockIdx.x, t = threadIdx.x;
   if (t < kRopeTokens) s_bad[t] = 0;
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const Rope
   }
   for (int i = t; i < 2 * D; i += kRopeThreads) {
     const T* norm = static_cast<const T*>(i < D ? a.q_norm : a.k_norm);
-    if (norm) s_norm[i / D][i % D] = to_f32(norm[i % D]);
+    if (norm) s_norm[i / D][norm_at(i % D)] = to_f32(norm[i % D]);
   }
   // the tokens' angles
   const int np = a.rot / 2;
@@ -166,8 +172,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const Rope
     const double turns = (double)p * ((double)a.inv_freq[pair] * 0.15915494309189535);  // 1 / 2pi
     float sn, cs;
     sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
-    s_cos[j][pair] = cs;
-    s_sin[j][pair] = sn;
+    s_cos[j][pair_at(pair)] = cs;
+    s_sin[j][pair_at(pair)] = sn;
   }
   bb = __syncthreads_or(bb);
   if (t == 0) {
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const Rope
             const float* w = s_norm[is_q ? 0 : 1];
 #pragma unroll
             for (int i = 0; i < VE; i += 2) {
-              const float4 w4 = *reinterpret_cast<const float4*>(w + (i < VE / 2 ? va * VE + 2 * i : vb * VE + 2 * i - VE));
+              const float4 w4 = *reinterpret_cast<const float4*>(w + norm_at(i < VE / 2 ? va * VE + 2 * i : vb * VE + 2 * i - VE));
               x[i] = __fmul2_rn(__fmul2_rn(x[i], r2), make_float2(w4.x, w4.y));
               x[i + 1] = __fmul2_rn(__fmul2_rn(x[i + 1], r2), make_float2(w4.z, w4.w));
             }
@@ -214,7 +220,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const Rope
             if (c < rv) {
 #pragma unroll
               for (int i = 0; i < VE / 2; i += 2) {
-                const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[k][c * VE + 2 * i]), n4 = *reinterpret_cast<const float4*>(&s_sin[k][c * VE + 2 * i]);
+                const int at = pair_at(c * VE + 2 * i);
+                const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[k][at]), n4 = *reinterpret_cast<const float4*>(&s_sin[k][at]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                   const float2 cs = j ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y), sn = j ? make_float2(n4.z, n4.w) : make_float2(n4.x, n4.y);
