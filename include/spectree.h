@@ -619,7 +619,7 @@ spec_status spec_pages_compact(void* const* k_caches, void* const* v_caches, int
  *   rot_dim  even, 0 <= rot_dim <= D (0: no rotation, no position is read)
  *   pos_base int32 [B] or NULL for prefix_len;  pos int32 [axes][T] or NULL (axes = 1)
  *   axes     1 to 4
- *   q_out    [T][Hq][D] dtype out; rows outside every request are not written
+ *   q_out    [T][Hq][D] dtype out, apart from qkv; rows outside every request are not written
  *   k_cache, v_cache, block_table, max_blocks, block_size, num_blocks, prefix_len, tree_off,
  *   n_max    as for spec_kv_append (packed prompts have no limit of 1024 rows).  The rows of
  *            requests behind a tree_off that decreases are unspecified
@@ -662,7 +662,8 @@ spec_status spec_rope_append(const void* qkv, long long row_stride, const void* 
  *   before   float [B][Hkv][weight_stride], or NULL for zeros;  weight  the same shape, out;
  *            they may be one buffer.  Only slots [0, prefix_len[b] + rows) are read and
  *            written.  A request without rows has its weights decayed
- *   workspace  16-byte aligned device scratch of spec_weight_workspace_size() bytes
+ *   workspace  16-byte aligned device scratch of spec_weight_workspace_size() bytes; calls that
+ *            may run at once need one each
  *   status   int32 [B] in/out: a request that comes in non-zero is left as it was.  Or-ed with
  *            SPEC_DEV_BAD_TREE, SPEC_DEV_CAPACITY (also prefix_len + rows beyond
  *            weight_stride), SPEC_DEV_BAD_PATH (accept_len outside [0, min(path_stride, n_b)],

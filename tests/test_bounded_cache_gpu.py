@@ -724,3 +724,50 @@ def test_evict_caches_beyond_32_bit_offsets():
         got = big[0, kv, e.table[1][new // 256].long(), 1, new % 256]
         assert torch.equal(got, big[0, kv, e.table[0][old // 256].long(), 1, old % 256])
     assert small < 10
+
+
+def test_evict_right_before_tree_attention():
+    """Tree attention reads the prefix's rows before it waits for the kernel before
+    it: both ways of copying have to be done by then."""
+    for layers, N in ((1, 2), (20, 8)):  # a copy kernel of its own, and the selecting CTAs' copies
+        e = Evict(71, [900] * N, [512] * N, 4, 64, layers=layers, Hkv=2, D=128, bs=16)
+        T = N * 4
+        # each row of the short ones has a page for a tree
+        spare = torch.arange(e.nb - 3, e.nb, dtype=torch.int32, device="cuda")
+        table = e.table[N:].clone()
+        table[:, 32] = spare[torch.arange(N, device="cuda") % 3]
+        parent, off = ints([-1, 0, 1, 1] * N), ints([4 * i for i in range(N + 1)])
+        mask, depth, st = torch.zeros((T, 1), dtype=torch.int64, device="cuda"), ints([0] * T), ints([0] * N)
+        S.spec_tree_mask_build(parent, off, N, 4, mask, depth, st)
+        q = torch.randn((T, 8, 128), generator=torch.Generator("cuda").manual_seed(1), device="cuda").bfloat16()
+        ws = torch.empty(S.spec_attention_workspace_size(N, T, 4, 512, 8, 2, 128), dtype=torch.uint8, device="cuda")
+        prefix = ints([512] * N)
+        ptrs = [torch.tensor([c[i].data_ptr() for c in e.cache], dtype=torch.int64, device="cuda") for i in range(2)]
+        slots, new_len, status = torch.empty((layers, N, 2, 512), dtype=torch.int32, device="cuda"), ints([0] * N), ints([0] * N)
+        src, dst, lens = ints(e.src), ints(e.dst), ints(e.lens)
+        outs = []
+        for again in (False, True, False, True, False):
+            if not again:  # what the short rows held before
+                e.cache[:, :, e.table[N:, :32].reshape(-1).long()] = 0
+            torch.cuda.synchronize()
+            out = torch.empty_like(q)
+            if not again:
+                S.spec_kv_evict(*ptrs, layers, e.table, e.B, e.table.shape[1], 16, e.nb, src, dst, lens, None, N, 512, 4, 64, e.weight, e.stride, 2, 128,
+                                S.SPEC_BF16, slots, new_len, status)
+            S.spec_tree_attention(q, e.cache[-1, 0], e.cache[-1, 1], table, table.shape[1], 16, e.nb, prefix, off, mask, N, T, 4, 512, 8, 2, 128, 0.1, out, ws, st)
+            torch.cuda.synchronize()
+            outs.append(out)
+        assert not st.any() and all(torch.equal(o, outs[1]) for o in outs)
+
+
+@DTYPES
+def test_weight_of_requests_without_rows(dtype):
+    """No new row at all: the weights decay."""
+    d = paged_batch(72, [1, 1], [300, 5], 8, 2, 64, 16, dtype)
+    before = _before(d)
+    d.update(q=d["q"][:0], seq_off=ints([0, 0, 0]), T=0, n_max=0)
+    got, st = _weight(d, before)
+    assert not st.any()
+    _weight_holds(d, got, before)
+    got, st = _weight(d, None) if d.update(stride=before.shape[-1]) is None else None
+    assert (got[0, :, :300] == 0).all() and (got[0, :, 300:] == 7.0).all() and (got[1, :, :5] == 0).all()

@@ -13,7 +13,12 @@
 // that holds the border, and so on; then it lists the kept slots in one ordered
 // pass; equal weights at the border are taken from the lowest slot.  Rows of up
 // to 16384 slots are read once and their keys kept in shared memory.  The copy
-// moves the listed rows of every layer, 16 bytes a lane: HBM.
+// moves the listed rows, 16 bytes a lane; with rows enough for every SM the CTA
+// that selected them moves them, while others select.
+// Measured: four rows of 6000 to 8192 slots cut to 1024 in 32 layers 233 us (1.1
+// GB, 4.8 TB/s; 239 with a kernel of its own for the copy, of which the selection
+// took 63); 64 rows of up to 1024 to 256 in two layers 59 us (65).  What is lost
+// to HBM's 6.8 TB/s is a CTA's own chain: some 16 us from its row to its list.
 #include <algorithm>
 
 #include "common.cuh"
@@ -121,7 +126,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   __shared__ uint32_t hist[kSelBins];
   __shared__ uint32_t s_warp[kWarps];
   __shared__ uint32_t s_bin, s_left, s_least, s_most;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // the copy's kernel may launch early; a call's last kernel lets none, since tree
+  // attention reads cache rows before it waits for the kernel before it
+  if (!COPY) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int h = blockIdx.x % a.Hkv, i = blockIdx.x / a.Hkv % a.N, layer = blockIdx.x / a.Hkv / a.N;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   EvictRow r = evict_row<kThreads>(a, i);
