@@ -16,7 +16,8 @@
 namespace spectree {
 
 constexpr int kWtRows = 64, kWtKeys = 64, kWtThreads = 256, kWtPad = 4;
-constexpr int kWtTcRows = 256;  // rows per item of the tensor-core kernel
+// Rows per item of the tensor-core kernel: two tiles of the whole tokens of 128 rows.
+static int weight_tc_rows(int g) { return g <= 128 ? 2 * (128 / g * g) : 256; }
 constexpr int kWtParts = 2;     // partial sums it leaves of a row and split
 
 // Loads a tile of 64 vectors transposed into shared memory as fp32, [D][64 + pad];
@@ -288,7 +289,7 @@ size_t spec_weight_workspace_size(int B, int T, int n_max, int max_prefix, int H
   if (B <= 0 || T <= 0 || n_max <= 0 || weight_shape_check(B, T, n_max, max_prefix, Hq, Hkv, D, 16) != SPEC_OK) return 256;
   int per_req = 0;
   int splits = 1;
-  for (int rows : {kWtRows, kWtTcRows})
+  for (int rows : {kWtRows, weight_tc_rows(Hq / Hkv)})
     for (int window : {0, 1}) splits = std::max(splits, weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, rows, &per_req).splits);
   return std::max<size_t>(256, weight_ws_bytes(splits, T, Hq, true));
 }
@@ -317,7 +318,7 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
   const bool tc = dtype == SPEC_BF16;
   // the tensor-core path names cache rows by 32-bit coordinates
   if (tc && (long long)num_blocks * Hkv * block_size >= (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
-  const WeightPlan plan = weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, tc ? kWtTcRows : kWtRows, &a.per_req);
+  const WeightPlan plan = weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, tc ? weight_tc_rows(Hq / Hkv) : kWtRows, &a.per_req);
   const long long key_tiles = ((long long)max_prefix + n_max + kWtKeys - 1) / kWtKeys;
   if (plan.tiles * Hkv * plan.splits > (long long)INT32_MAX / 2 || key_tiles * B * Hkv > (long long)INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
   if (key_tiles == 0) return SPEC_OK;

@@ -64,7 +64,8 @@ struct Params {
   long long rows_total;  // num_blocks * Hkv * block_size: rows of the 2-D cache view
   int box_rows;          // rows per TMA box: min(block_size, 128)
   int bs_log2;
-  int q_tma;             // Q by TMA (packed rows, g divides 128), else by cp.async
+  int q_tma;             // Q by TMA (packed rows, g <= 128), else by cp.async
+  int rt;                // rows per row tile: the whole tokens of 128 rows (128 where g divides it, or is larger)
   int key_chunk;         // keys per item of the sums over few rows
   int cluster;           // CTAs that hold one request's scores of a kv-head (0: none is held),
   int held_rows;         // of at most this many rows (16 or 32: the columns of a key tile)
@@ -94,8 +95,8 @@ __device__ __forceinline__ int request_tiles(const Params& prm, const Request& r
   const bool held = prm.cluster > 0 && (R == 0 || (R <= prm.held_rows && (total + BM - 1) / BM <= 512 / prm.held_rows * prm.cluster));
   if (MODE == kHeld) return held;
   if (held) return 0;
-  if (MODE == kStats) return (R + 2 * BM - 1) / (2 * BM);
-  const bool few = R <= 2 * BM;
+  if (MODE == kStats) return (R + 2 * prm.rt - 1) / (2 * prm.rt);
+  const bool few = R <= 2 * prm.rt;
   if (MODE == kSumsFew) return few ? (total + prm.key_chunk - 1) / prm.key_chunk : 0;
   return few ? 0 : (total + 2 * BM - 1) / (2 * BM);
 }
@@ -161,30 +162,30 @@ __device__ __forceinline__ Item find_item(const Params& prm, const Table& tab, i
   w.q = tab.r[r];
   const int at = tile - tab.first[r], R = w.q.cnt * a.g, total = w.q.P + w.q.m;
   if (MODE == kStats) {
-    w.r0 = (tab.first[r + 1] - 1 - tile) * (2 * BM);  // the last rows see the most keys: first
+    w.r0 = (tab.first[r + 1] - 1 - tile) * (2 * prm.rt);  // the last rows see the most keys: first
     w.k0 = w.split * a.chunk;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int row = w.r0 + t * BM;
+      const int row = w.r0 + t * prm.rt;
       if (row >= R) continue;
-      const int end = min(w.q.P + w.q.first + (min(row + BM, R) - 1) / a.g + 1, w.k0 + a.chunk);
+      const int end = min(w.q.P + w.q.first + (min(row + prm.rt, R) - 1) / a.g + 1, w.k0 + a.chunk);
       if (end > w.k0) w.hi[t] = (end - w.k0 + BM - 1) / BM;
     }
     w.steps = max(w.hi[0], w.hi[1]);
   } else if (MODE == kSumsFew) {
     w.k0 = at * prm.key_chunk;
     w.steps = (min(prm.key_chunk, total - w.k0) + BM - 1) / BM;
-    w.rt = (R + BM - 1) / BM;
+    w.rt = (R + prm.rt - 1) / prm.rt;
   } else if (MODE == kSumsMany) {
     w.k0 = at * (2 * BM);
     const int tok = max(0, w.k0 - w.q.P - w.q.first);  // the first counted token that sees the first key
-    w.r0 = tok * a.g / BM * BM;
-    w.steps = tok < w.q.cnt ? (R - w.r0 + BM - 1) / BM : 0;
+    w.r0 = tok * a.g / prm.rt * prm.rt;
+    w.steps = tok < w.q.cnt ? (R - w.r0 + prm.rt - 1) / prm.rt : 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int need = max(0, w.k0 + t * BM - w.q.P - w.q.first);
       if (w.k0 + t * BM < total && need < w.q.cnt) {
-        w.lo[t] = (need * a.g - w.r0) / BM;
+        w.lo[t] = (need * a.g - w.r0) / prm.rt;
         w.hi[t] = w.steps;
       }
     }
@@ -241,6 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (prm.rt < BM) {  // no copy reaches the last rows of a row tile: their scores have to be numbers
+    for (uint32_t at = threadIdx.x * 16; at < L::kBytes; at += kThreads * 16) *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int h = 0; h < L::DH; ++h) tma_load_2d(dst + h * (BM * 128) + lane * prm.box_rows * 128, &tmap_k, h * 64, y, bar);
     }
   };
-  // Rows r .. r + 127 of an item (row = (counted token, head of the group)); rows
+  // The row tile from row r of an item (row = (counted token, head of the group)); rows
   // behind its last are whatever lies there.  True: `bar` still has to
   // be arrived on.
   auto load_rows = [&](const Item& w, int r, uint32_t dst, uint64_t* bar) -> bool {
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ch = lane % CPR, R = w.q.cnt * a.g;
     const int32_t* path = a.path ? a.path + (size_t)w.b * a.path_stride + w.q.first : nullptr;
 #pragma unroll 4
-    for (int i = lane / CPR; i < min(BM, R - r); i += STEP) {
+    for (int i = lane / CPR; i < min(prm.rt, R - r); i += STEP) {
       const uint32_t at = dst + (ch >> 3) * (BM * 128) + i * 128 + (((ch & 7) ^ (i & 7)) << 4);
       const int tok = (r + i) / a.g, head = (r + i) % a.g;
       const size_t row = w.q.off + (path ? path[tok] : w.q.first + tok);
@@ -349,9 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dst = sbase + L::kOffRing + st * L::kTile;
           if (lane == 0) issued[st] = ld;
           if (MODE == kSumsMany) {
-            if (lane == 0 && prm.q_tma) mbar_expect_tx(&full[st], L::kTile);
+            if (lane == 0 && prm.q_tma) mbar_expect_tx(&full[st], prm.rt * D * 2);
             __syncwarp();
-            if (load_rows(w, w.r0 + j * BM, dst, &full[st])) copies_done(&full[st]);
+            if (load_rows(w, w.r0 + j * prm.rt, dst, &full[st])) copies_done(&full[st]);
           } else {
             if (lane == 0) mbar_expect_tx(&full[st], L::kTile);
             __syncwarp();
@@ -375,12 +380,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           dead = !__shfl_sync(0xffffffffu, (int)go, 0);
           if (dead) break;
           if (lane == 0) res_issued[slot] = rs >> 1;
-          if (lane == 0 && (MODE == kSumsMany || prm.q_tma)) mbar_expect_tx(&res_full[slot], L::kTile);
+          if (lane == 0 && (MODE == kSumsMany || prm.q_tma)) mbar_expect_tx(&res_full[slot], MODE == kSumsMany ? L::kTile : prm.rt * D * 2);
           __syncwarp();
           if (MODE == kSumsMany) {
             const int x = w.k0 / prm.box_rows + t * nb + lane;
             load_keys(w, t, lane < nb ? box_page(w, x, &bad) : -1, sbase + slot * L::kTile, &res_full[slot]);
-          } else if (load_rows(w, w.r0 + t * BM, sbase + slot * L::kTile, &res_full[slot])) {
+          } else if (load_rows(w, w.r0 + t * prm.rt, sbase + slot * L::kTile, &res_full[slot])) {
             copies_done(&res_full[slot]);
           }
         }
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t rd = res + (uint64_t)(((rs + t) & 1) * (L::kTile >> 4));
             const uint32_t d = tmem + buf * BM;
             // few rows: only the columns that hold some, 32 at a time
-            const uint32_t n = MODE == kSumsFew ? min(BM, (R - t * BM + 31) / 32 * 32) : BM;
+            const uint32_t n = MODE == kSumsFew ? min(BM, (R - t * prm.rt + 31) / 32 * 32) : BM;
             const uint32_t idesc = idesc_bf16(BM, 0) & ~(0x3fu << 17) | (n >> 3) << 17;
             if (leader) {
 #pragma unroll
@@ -447,11 +452,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int at = lt % kLse;
           float nl[BM / 32];
           int lim[BM / 32];
-          const int row0 = w.r0 + t * BM + lane;
+          const int row0 = w.r0 + t * prm.rt + lane;
           const float* lse = a.ws_lse + weight_ws_row(a, w.kvh, w.q.off, w.q.first) + row0;
 #pragma unroll
           for (int e = 0; e < BM / 32; ++e) {
-            const bool there = row0 + e * 32 < R;
+            const bool there = e * 32 + lane < prm.rt && row0 + e * 32 < R;
             lim[e] = there ? w.q.P + w.q.first + (row0 + e * 32) / a.g : -1;
             nl[e] = there ? lse[e * 32] : -INFINITY;
           }
@@ -527,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int R = w.q.cnt * a.g, lo = g ? w.lo[1] : w.lo[0], hi = g ? w.hi[1] : w.hi[0];
         if (MODE == kStats) {
           if (hi == 0) continue;
-          const int row = w.r0 + g * BM + r;
-          const bool valid = row < R;
+          const int row = w.r0 + g * prm.rt + r;
+          const bool valid = r < prm.rt && row < R;
           const int tok = w.q.first + (valid ? row / a.g : w.q.cnt - 1);
           const int lim = w.q.P + tok + 1 - w.k0;  // visible keys of this range
           float m = 0.0f, l = 0.0f;
@@ -594,14 +599,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int j0 = two ? wg >> 1 : wg, dj = two ? 2 : 4, t = two ? wg & 1 : 0, at = (lt + t) % kLse;
           float old = t == 0 ? old_weight(w, w.k0 + j0 * BM + r) : 0.0f;
           wait(&lse_full[at], (lt + t) / kLse);
-          const int cols = min(BM, R - t * BM);
+          const int cols = min(prm.rt, R - t * prm.rt);
           for (int j = j0; j < w.steps; j += dj) {
             const int k0 = w.k0 + j * BM, key = k0 + r;
             const float next = t == 0 && j + dj < w.steps ? old_weight(w, key + dj * BM) : 0.0f;
             float2 acc = make_float2(0.0f, 0.0f);
             const uint32_t t0 = take();
-            // rows that do not see the tile's last key, or columns without a row
-            const bool masked = k0 + BM - 1 > w.q.P + w.q.first || (cols & 31) != 0;
+            // rows that do not see the tile's last key, or another token's rows
+            const bool masked = k0 + BM - 1 > w.q.P + w.q.first || cols < prm.rt;
 #pragma unroll 1
             for (int e = 0; e < cols; e += 32) {
               uint32_t x[32];
@@ -631,9 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int at = lt % kLse;
             wait(&lse_full[at], lt / kLse);
             if (j >= lo && j < hi) {
-              const int row0 = w.r0 + j * BM;
+              const int row0 = w.r0 + j * prm.rt;
               const uint32_t t0 = take();
-              const bool masked = k0 + BM - 1 > w.q.P + w.q.first + row0 / a.g || row0 + BM > R;
+              const bool masked = k0 + BM - 1 > w.q.P + w.q.first + row0 / a.g || row0 + prm.rt > R;
 #pragma unroll 1
               for (int e = half * 64; e < half * 64 + 64; e += 32) {
                 uint32_t x[32];
@@ -1390,7 +1395,8 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
   prm.box_rows = std::min(a.block_size, BM);
   while ((1 << prm.bs_log2) < a.block_size) ++prm.bs_log2;
   prm.rows_total = (long long)a.num_blocks * a.Hkv * a.block_size;
-  prm.q_tma = !a.path && BM % a.g == 0 && a.T > 0;
+  prm.q_tma = !a.path && a.g <= BM && a.T > 0;
+  prm.rt = a.g <= BM ? BM / a.g * a.g : BM;
   // sums over few rows: some two items for every CTA, of 256 to 2048 keys
   const long long keys = ((long long)a.max_prefix + a.n_max) * a.B * a.Hkv / (2LL * sms);
   prm.key_chunk = (int)std::min(2048LL, std::max(256LL, (keys + 255) / 256 * 256));
@@ -1429,7 +1435,7 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
     if (e == cudaSuccess) e = launch(weight_join_kernel, (long long)tiles * a.Hkv * a.B, kJoinThreads, 0, false, stream, a, tiles);
   }
   if (e == cudaSuccess) e = launch(weight_tc_kernel<D, kSumsFew>, sms, kThreads, dyn, first && rows == 0, stream, mk, mq, prm);
-  if (e == cudaSuccess && rows > 2 * BM) e = launch(weight_tc_kernel<D, kSumsMany>, sms, kThreads, dyn, false, stream, mk, mq, prm);
+  if (e == cudaSuccess && rows > 2 * prm.rt) e = launch(weight_tc_kernel<D, kSumsMany>, sms, kThreads, dyn, false, stream, mk, mq, prm);
   return e;
 }
 
