@@ -391,6 +391,20 @@ def test_weight_of_a_mixed_batch(dtype):
     _weight_holds(d, got, before, window=5)
 
 
+@pytest.mark.parametrize("lens,prefix,Hq,Hkv,window", [([3000], [0], 8, 1, 0), ([700, 64, 900], [300, 2000, 0], 6, 2, 0), ([2000, 10], [5, 90], 5, 1, 1500),
+                                                       ([600], [4000], 4, 2, 0)])
+def test_weight_in_parts_of_the_rows(lens, prefix, Hq, Hkv, window):
+    """So few key tiles that the rows of a request are summed in parts."""
+    d = paged_batch(49, lens, prefix, Hq, Hkv, 64, 16, torch.bfloat16)
+    before = _before(d)
+    got, st = _weight(d, before, window=window)
+    assert not st.any()
+    _weight_holds(d, got, before, window=window)
+    st = ints([S.SPEC_DEV_TIMEOUT] + [0] * (len(lens) - 1))
+    got, st = _weight(d, before, window=window, status=st)
+    _weight_holds(d, got, before, window=window, skip=(0,))
+
+
 @DTYPES
 def test_weight_at_a_scale_of_zero(dtype):
     d = paged_batch(46, [3, 50], [20, 300], 8, 2, 64, 16, dtype)

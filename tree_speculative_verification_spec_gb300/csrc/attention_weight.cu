@@ -276,6 +276,20 @@ static size_t weight_ws_bytes(int splits, int T, int Hq, bool tc) {
   return (size_t)T * Hq * ((size_t)splits * (tc ? kWtParts : 1) * sizeof(float2) + (tc ? sizeof(float) : 0));
 }
 
+// Parts of a request's rows whose sums are taken apart, where the items of 256 keys
+// alone leave SMs idle: for a dozen items an SM, half of which are above a prompt's
+// diagonal and fall away.  One prompt of 4000 tokens with 8, 4 and 2 kv-heads (128,
+// 64 and 32 items): 149, 192 and 144 us whole, 111, 73 and 35 us in 15 or 16 parts.
+// A prompt of 8192 (256 items) takes 311 us whole, 390 in 15 parts: an item more
+// costs a CTA some 8 us (its keys' load, the score buffers run dry).
+static int weight_parts(int B, int n_max, int max_prefix, int Hkv) {
+  const long long items = std::max(1LL, ((long long)max_prefix + n_max + 255) / 256 * B * Hkv);
+  return items >= kWtSms ? 1 : (int)std::min(16LL, (12LL * kWtSms + items - 1) / items);
+}
+static size_t weight_parts_bytes(int parts, int B, int n_max, int max_prefix, int Hkv) {
+  return parts > 1 ? (size_t)parts * B * Hkv * ((size_t)max_prefix + n_max) * sizeof(float) : 0;
+}
+
 }  // namespace spectree
 
 using namespace spectree;
@@ -291,7 +305,8 @@ size_t spec_weight_workspace_size(int B, int T, int n_max, int max_prefix, int H
   int splits = 1;
   for (int rows : {kWtRows, weight_tc_rows(Hq / Hkv)})
     for (int window : {0, 1}) splits = std::max(splits, weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, rows, &per_req).splits);
-  return std::max<size_t>(256, weight_ws_bytes(splits, T, Hq, true));
+  const size_t parts = weight_parts_bytes(weight_parts(B, n_max, max_prefix, Hkv), B, n_max, max_prefix, Hkv);
+  return std::max<size_t>(256, weight_ws_bytes(splits, T, Hq, true) + parts);
 }
 
 spec_status spec_attention_weight(const void* q, const void* k_cache, const int32_t* block_table, int max_blocks,
@@ -322,7 +337,10 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
   const long long key_tiles = ((long long)max_prefix + n_max + kWtKeys - 1) / kWtKeys;
   if (plan.tiles * Hkv * plan.splits > (long long)INT32_MAX / 2 || key_tiles * B * Hkv > (long long)INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
   if (key_tiles == 0) return SPEC_OK;
-  const size_t need = weight_ws_bytes(plan.splits, T, Hq, tc);
+  // only requests of more rows than one item's take them in parts
+  const long long rows = (long long)(window > 0 ? std::min(window, n_max) : n_max) * (Hq / Hkv);
+  a.parts = tc && rows > weight_tc_rows(Hq / Hkv) ? weight_parts(B, n_max, max_prefix, Hkv) : 1;
+  const size_t sums = weight_ws_bytes(plan.splits, T, Hq, tc), need = sums + weight_parts_bytes(a.parts, B, n_max, max_prefix, Hkv);
   if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15))) return SPEC_ERR_WORKSPACE;
   a.q = q;
   a.k_cache = k_cache;
@@ -335,6 +353,7 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
   a.weight = weight;
   a.status = status;
   a.ws_ml = static_cast<float2*>(workspace);
+  a.ws_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums);
   if (tc) a.ws_lse = static_cast<float*>(workspace) + (size_t)plan.splits * T * Hq * kWtParts * 2;
   a.stride = weight_stride;
   a.path_stride = path_stride;

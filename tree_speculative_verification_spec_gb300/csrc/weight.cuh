@@ -22,6 +22,8 @@ struct WeightArgs {
   float* weight;
   int32_t* status;
   float2* ws_ml;              // [splits][Hkv][T * g][parts] partial (reference, sum) in the log2 domain, at (off + i) g + head of token i
+  float* ws_part;             // [parts][B][Hkv][max_prefix + n_max] sums over a part of the rows (tensor cores, parts > 1)
+  int parts;                  // of a request's rows, for the sums over many of them
   float* ws_lse;              // [Hkv][T * g] minus log2 of the whole sum (tensor cores)
   long long stride;           // floats of one (request, kv-head) of before and weight
   int path_stride, window;

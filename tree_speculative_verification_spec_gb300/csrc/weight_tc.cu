@@ -58,7 +58,8 @@ constexpr uint32_t kTmemCols = 512;  // four score buffers of 128 columns
 constexpr int kLse = 4;              // row tiles whose sums are held for the epilogue
 constexpr int kGroup = 256;          // requests numbered at a time
 constexpr float kSumTop = 0x1p60f;
-enum Mode { kStats = 0, kSumsFew = 1, kSumsMany = 2, kHeld = 3 };
+enum Mode { kStats = 0, kSumsFew = 1, kSumsMany = 2, kHeld = 3, kSumsParts = 4 };  // kSumsParts: over many rows, in parts
+constexpr bool many(int mode) { return mode == kSumsMany || mode == kSumsParts; }
 constexpr int kHeldRows = 32;        // most rows of a request whose scores are held
 constexpr int kHeldQ = 4;            // items whose queries are ahead in shared memory
 
@@ -80,6 +81,7 @@ struct Params {
   int q_tma;             // Q by TMA (packed rows, g <= 128), else by cp.async
   int rt;                // rows per row tile: the whole tokens of 128 rows (128 where g divides it, or is larger)
   int key_chunk;         // keys per item of the sums over few rows
+  int part_tiles;        // row tiles per part of the sums over many rows
   int cluster;           // CTAs that hold one request's scores of a kv-head (0: none is held),
   int held_rows;         // of at most this many rows (16 or 32: the columns of a key tile)
 };
@@ -95,10 +97,21 @@ struct Table {
 
 struct Item {
   Request q;
-  int b, kvh, r0, k0, steps, split;
+  int b, kvh, r0, k0, steps;
+  int split;         // of the keys (statistics), or part of the rows (sums over many)
   int lo[2], hi[2];  // steps in which tile t has a job (statistics, sums over many rows)
   int rt;            // row tiles (sums over few rows)
 };
+
+// Pairs of key tiles (256 keys) that the last row of part p of a request's rows
+// sees some of; 0: the part has no rows.
+__device__ __forceinline__ int part_pairs(const Params& prm, const Request& r, int p) {
+  const long long begin = (long long)p * prm.part_tiles * prm.rt;
+  const int R = r.cnt * prm.a.g;
+  if (begin >= R) return 0;
+  const int last = (int)((min((long long)R, begin + prm.part_tiles * prm.rt) - 1) / prm.a.g);
+  return (r.P + r.first + last) / (2 * BM) + 1;
+}
 
 // Tiles of request r in this form of the kernel.
 template <int MODE>
@@ -111,7 +124,10 @@ __device__ __forceinline__ int request_tiles(const Params& prm, const Request& r
   if (MODE == kStats) return (R + 2 * prm.rt - 1) / (2 * prm.rt);
   const bool few = R <= 2 * prm.rt;
   if (MODE == kSumsFew) return few ? (total + prm.key_chunk - 1) / prm.key_chunk : 0;
-  return few ? 0 : (total + 2 * BM - 1) / (2 * BM);
+  if (MODE == kSumsMany) return few ? 0 : (total + 2 * BM - 1) / (2 * BM);
+  int n = 0;
+  for (int p = 0; p < a.parts && !few; ++p) n += part_pairs(prm, r, p);
+  return n;
 }
 
 // Requests b0 .. of the group with their tiles, by every thread of the CTA.
@@ -189,16 +205,24 @@ __device__ __forceinline__ Item find_item(const Params& prm, const Table& tab, i
     w.k0 = at * prm.key_chunk;
     w.steps = (min(prm.key_chunk, total - w.k0) + BM - 1) / BM;
     w.rt = (R + prm.rt - 1) / prm.rt;
-  } else if (MODE == kSumsMany) {
-    w.k0 = at * (2 * BM);
+  } else if (many(MODE)) {
+    int pair = at, begin = 0, end = R;
+    if (MODE == kSumsParts) {
+      w.split = a.parts - 1;  // the last rows see the most keys: first
+      for (int n; pair >= (n = part_pairs(prm, w.q, w.split)) && w.split > 0; --w.split) pair -= n;
+      begin = w.split * prm.part_tiles * prm.rt;
+      end = min(R, begin + prm.part_tiles * prm.rt);
+    }
+    w.k0 = pair * (2 * BM);
     const int tok = max(0, w.k0 - w.q.P - w.q.first);  // the first counted token that sees the first key
-    w.r0 = tok * a.g / prm.rt * prm.rt;
-    w.steps = tok < w.q.cnt ? (R - w.r0 + prm.rt - 1) / prm.rt : 0;
+    w.r0 = max(begin, tok * a.g / prm.rt * prm.rt);
+    w.steps = tok < w.q.cnt && w.r0 < end ? (end - w.r0 + prm.rt - 1) / prm.rt : 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int need = max(0, w.k0 + t * BM - w.q.P - w.q.first);
-      if (w.k0 + t * BM < total && need < w.q.cnt) {
-        w.lo[t] = (need * a.g - w.r0) / prm.rt;
+      const int lo = max(0, need * a.g - w.r0) / prm.rt;
+      if (w.k0 + t * BM < total && need < w.q.cnt && lo < w.steps) {
+        w.lo[t] = lo;
         w.hi[t] = w.steps;
       }
     }
@@ -353,10 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the pages of 32 boxes at a time, one to a lane, and the next 32 ahead
         int bad = 0, pages = -1, ahead = -1;
         const int x0 = w.k0 / prm.box_rows + lane, boxes = w.steps * nb;
-        if (MODE != kSumsMany && lane < boxes) ahead = box_page(w, x0, &bad);
+        if (!many(MODE) && lane < boxes) ahead = box_page(w, x0, &bad);
         for (int j = 0; j < w.steps; ++j, ++ld) {
           const int st = ld % NST, at = j * nb & 31;
-          if (MODE != kSumsMany && at == 0) {
+          if (!many(MODE) && at == 0) {
             pages = ahead;
             if (j * nb + 32 + lane < boxes) ahead = box_page(w, x0 + j * nb + 32, &bad);
           }
@@ -366,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (dead) break;
           const uint32_t dst = sbase + L::kOffRing + st * L::kTile;
           if (lane == 0) issued[st] = ld;
-          if (MODE == kSumsMany) {
+          if (many(MODE)) {
             if (lane == 0 && prm.q_tma) mbar_expect_tx(&full[st], prm.rt * D * 2);
             __syncwarp();
             if (load_rows(w, w.r0 + j * prm.rt, dst, &full[st])) copies_done(&full[st]);
@@ -393,9 +417,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           dead = !__shfl_sync(0xffffffffu, (int)go, 0);
           if (dead) break;
           if (lane == 0) res_issued[slot] = rs >> 1;
-          if (lane == 0 && (MODE == kSumsMany || prm.q_tma)) mbar_expect_tx(&res_full[slot], MODE == kSumsMany ? L::kTile : prm.rt * D * 2);
+          if (lane == 0 && (many(MODE) || prm.q_tma)) mbar_expect_tx(&res_full[slot], many(MODE) ? L::kTile : prm.rt * D * 2);
           __syncwarp();
-          if (MODE == kSumsMany) {
+          if (many(MODE)) {
             const int x = w.k0 / prm.box_rows + t * nb + lane;
             load_keys(w, t, lane < nb ? box_page(w, x, &bad) : -1, sbase + slot * L::kTile, &res_full[slot]);
           } else if (load_rows(w, w.r0 + t * prm.rt, sbase + slot * L::kTile, &res_full[slot])) {
@@ -642,8 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (two) wait(&lse_full[(lt + 1 - t) % kLse], (lt + 1 - t) / kLse);
           for (int t = 0; t < w.rt; ++t, ++lt) lse_done(lt);
         } else {
+          if (MODE == kSumsParts && w.steps == 0) continue;  // no row of the part sees a key: not added either
           const int k0 = w.k0 + g * BM, key = k0 + r;
-          const float old = half == 0 ? old_weight(w, key) : 0.0f;
+          const float old = half == 0 && MODE == kSumsMany ? old_weight(w, key) : 0.0f;
           float2 acc = make_float2(0.0f, 0.0f);
           for (int j = 0; j < w.steps; ++j, ++lt) {
             const int at = lt % kLse;
@@ -666,7 +691,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the two halves of the columns, through shared memory
           if (half == 1) s_part[g][0][r] = acc.x + acc.y;
           asm volatile("bar.sync %0, 256;" ::"r"(1 + g) : "memory");
-          if (half == 0) put(w, key, old + (acc.x + acc.y) + s_part[g][0][r]);
+          if (half == 0) {
+            const float sum = old + (acc.x + acc.y) + s_part[g][0][r];
+            if (MODE == kSumsMany) put(w, key, sum);
+            else if (key < w.q.P + w.q.m)
+              a.ws_part[(((size_t)w.split * a.B + w.b) * a.Hkv + w.kvh) * ((size_t)a.max_prefix + a.n_max) + key] = sum;
+          }
           asm volatile("bar.sync %0, 256;" ::"r"(1 + g) : "memory");
         }
       }
@@ -1277,6 +1307,26 @@ __global__ void __launch_bounds__(kJoinThreads) weight_join_kernel(const WeightA
   if (there && part == 0) a.ws_lse[at] = -(x.x + log2f(x.y));
 }
 
+// The parts of a request's rows added up, in their order: a thread a key.
+constexpr int kAddThreads = 256;
+__global__ void __launch_bounds__(kAddThreads) weight_add_kernel(const __grid_constant__ Params prm, int pairs) {
+  const WeightArgs& a = prm.a;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int kvh = blockIdx.x % a.Hkv, pair = blockIdx.x / a.Hkv % pairs, b = blockIdx.x / a.Hkv / pairs;
+  WeightRequest r;
+  if (weight_check(a, b, r) || a.status[b] != 0 || r.cnt * a.g <= 2 * prm.rt) return;
+  const int key = pair * kAddThreads + threadIdx.x;
+  if (key >= r.P + r.m) return;
+  const Request q = {r.off, r.m - r.cnt, r.cnt, r.P, r.m, 0};
+  const size_t at = ((size_t)b * a.Hkv + kvh) * a.stride + key;
+  float sum = a.before && key < r.P ? a.decay * a.before[at] : 0.0f;
+  for (int p = 0; p < a.parts; ++p) {
+    if (pair < part_pairs(prm, q, p))
+      sum += a.ws_part[(((size_t)p * a.B + b) * a.Hkv + kvh) * ((size_t)a.max_prefix + a.n_max) + key];
+  }
+  a.weight[at] = sum;
+}
+
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1432,6 +1482,7 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
     mq = mk;  // not read
   }
   const long long rows = (long long)(a.window > 0 ? std::min(a.window, a.n_max) : a.n_max) * a.g;  // the most that a request has
+  prm.part_tiles = (int)std::max(1LL, ((rows + prm.rt - 1) / prm.rt + a.parts - 1) / a.parts);
   // Scores are held where a request has few rows; one with more rows, or more keys
   // than its cluster holds, goes the other way, inside the kernels.
   bool first = true;
@@ -1452,7 +1503,14 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
     if (e == cudaSuccess) e = launch(weight_join_kernel, (long long)tiles * a.Hkv * a.B, kJoinThreads, 0, false, stream, a, tiles);
   }
   if (e == cudaSuccess) e = launch(weight_tc_kernel<D, kSumsFew>, sms, kThreads, dyn, first && rows == 0, stream, mk, mq, prm);
-  if (e == cudaSuccess && rows > 2 * prm.rt) e = launch(weight_tc_kernel<D, kSumsMany>, sms, kThreads, dyn, false, stream, mk, mq, prm);
+  if (e == cudaSuccess && rows > 2 * prm.rt) {
+    if (a.parts == 1) return launch(weight_tc_kernel<D, kSumsMany>, sms, kThreads, dyn, false, stream, mk, mq, prm);
+    e = launch(weight_tc_kernel<D, kSumsParts>, sms, kThreads, dyn, false, stream, mk, mq, prm);
+    if (e == cudaSuccess) {
+      const int pairs = (int)((longest + kAddThreads - 1) / kAddThreads);
+      e = launch(weight_add_kernel, (long long)pairs * a.Hkv * a.B, kAddThreads, 0, false, stream, prm, pairs);
+    }
+  }
   return e;
 }
 
