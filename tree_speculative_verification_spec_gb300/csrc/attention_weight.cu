@@ -15,18 +15,21 @@
 
 namespace spectree {
 
-constexpr int kWtRows = 64, kWtKeys = 64, kWtThreads = 256, kWtPad = 4;
+constexpr int kWtRows = 64, kWtFewRows = 16, kWtKeys = 64, kWtThreads = 256, kWtPad = 4;
 // Rows per item of the tensor-core kernel: two tiles of the whole tokens of 128 rows.
 static int weight_tc_rows(int g) { return g <= 128 ? 2 * (128 / g * g) : 256; }
 constexpr int kWtParts = 2;     // partial sums it leaves of a row and split
 
-// Loads a tile of 64 vectors transposed into shared memory as fp32, [D][64 + pad];
-// `row(i)` gives the address of vector i, or NULL for zeros.
-template <typename T, int D, typename F>
+// Loads a tile of N vectors transposed into shared memory as fp32, [D][64 + pad];
+// `row(i)` gives the address of vector i, or NULL for zeros.  A warp takes 64 bytes
+// of 8 vectors: whole sectors to read, two banks' conflict to write (a vector a
+// warp wrote to two banks alone).
+template <typename T, int D, int N, typename F>
 __device__ __forceinline__ void load_tile(float* dst, F row) {
   constexpr int V = 16 / sizeof(T), C = D / V;
-  for (int j = threadIdx.x; j < 64 * C; j += kWtThreads) {
-    const int i = j / C, c = j % C;
+  const int lane = threadIdx.x & 31;
+  for (int j = threadIdx.x / 32; j < N / 8 * (C / 4); j += kWtThreads / 32) {
+    const int i = j % (N / 8) * 8 + (lane & 7), c = j / (N / 8) * 4 + (lane >> 3);
     const T* p = row(i);
     uint4 u = make_uint4(0, 0, 0, 0);
     if (p) u = *reinterpret_cast<const uint4*>(p + c * V);
@@ -36,20 +39,22 @@ __device__ __forceinline__ void load_tile(float* dst, F row) {
   }
 }
 
-// 4 x 4 scores of this thread: rows 4 ty .., keys 4 tx ..
-template <int D>
-__device__ __forceinline__ void scores(const float* q, const float* k, int ty, int tx, float (&s)[4][4]) {
+// RT x 4 scores of this thread: rows RT ty .., keys 4 tx ..
+template <int D, int RT>
+__device__ __forceinline__ void scores(const float* q, const float* k, int ty, int tx, float (&s)[RT][4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
 #pragma unroll 4
   for (int d = 0; d < D; ++d) {
-    const float4 x = *reinterpret_cast<const float4*>(q + d * (64 + kWtPad) + 4 * ty);
+    float xs[RT];
+    if (RT == 4) *reinterpret_cast<float4*>(xs) = *reinterpret_cast<const float4*>(q + d * (64 + kWtPad) + 4 * ty);
+    else xs[0] = q[d * (64 + kWtPad) + ty];
     const float4 y = *reinterpret_cast<const float4*>(k + d * (64 + kWtPad) + 4 * tx);
-    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    const float ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = fmaf(xs[i], ys[j], s[i][j]);
   }
@@ -81,41 +86,43 @@ __device__ __forceinline__ const T* key_row(const WeightArgs& a, const int32_t* 
   return static_cast<const T*>(a.k_cache) + (((size_t)blk * a.Hkv + kvh) * a.block_size + s % a.block_size) * a.D;
 }
 
-template <typename T, int D>
+// RT rows a thread: 64 rows a tile, or 16 where no request has more.
+template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kWtThreads) weight_stats_cc_kernel(const WeightArgs a) {
+  constexpr int ROWS = 16 * RT;
   extern __shared__ float sm[];
   float *sq = sm, *sk = sm + D * (64 + kWtPad);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int kvh = blockIdx.x % a.Hkv, split = blockIdx.x / a.Hkv % a.splits;
   const long long tile = blockIdx.x / a.Hkv / a.splits;
-  const int b = weight_find(a, tile, kWtRows);
+  const int b = weight_find(a, tile, ROWS);
   WeightRequest r;
   if (!weight_request_cta(a, b, r, false)) return;
-  const long long at = tile - weight_first_tile(a, b, kWtRows);
+  const long long at = tile - weight_first_tile(a, b, ROWS);
   const int R = r.cnt * a.g;
-  if (at < 0 || at * kWtRows >= R) return;
-  const int r0 = (int)at * kWtRows, first = r.m - r.cnt;
+  if (at < 0 || at * ROWS >= R) return;
+  const int r0 = (int)at * ROWS, first = r.m - r.cnt;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  load_tile<T, D>(sq, [&](int i) -> const T* {
+  load_tile<T, D, ROWS>(sq, [&](int i) -> const T* {
     if (r0 + i >= R) return nullptr;
     return static_cast<const T*>(a.q) + ((size_t)weight_q_row(a, r, first + (r0 + i) / a.g) * a.Hq + kvh * a.g + (r0 + i) % a.g) * D;
   });
-  const int last = first + (min(r0 + kWtRows, R) - 1) / a.g;  // the tile's last token
+  const int last = first + (min(r0 + ROWS, R) - 1) / a.g;  // the tile's last token
   const int begin = split * a.chunk, end = min(begin + a.chunk, r.P + last + 1);
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
-  float m[4], l[4];
+  float m[RT], l[RT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.0f;
+  for (int i = 0; i < RT; ++i) m[i] = -INFINITY, l[i] = 0.0f;
   int bad = 0;
   for (int k0 = begin; k0 < end; k0 += kWtKeys) {
     __syncthreads();
-    load_tile<T, D>(sk, [&](int i) -> const T* { return k0 + i < end ? key_row<T>(a, bt, kvh, k0 + i, &bad) : nullptr; });
+    load_tile<T, D, kWtKeys>(sk, [&](int i) -> const T* { return k0 + i < end ? key_row<T>(a, bt, kvh, k0 + i, &bad) : nullptr; });
     __syncthreads();
-    float s[4][4];
-    scores<D>(sq, sk, ty, tx, s);
+    float s[RT][4];
+    scores<D, RT>(sq, sk, ty, tx, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int seen = r.P + first + (r0 + 4 * ty + i) / a.g;  // the last slot this row sees
+    for (int i = 0; i < RT; ++i) {
+      const int seen = r.P + first + (r0 + RT * ty + i) / a.g;  // the last slot this row sees
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -135,21 +142,22 @@ __global__ void __launch_bounds__(kWtThreads) weight_stats_cc_kernel(const Weigh
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RT; ++i) {
 #pragma unroll
     for (int o = 8; o; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-    const int row = r0 + 4 * ty + i;
+    const int row = r0 + RT * ty + i;
     if (tx == 0 && row < R)
       a.ws_ml[(size_t)split * a.T * a.Hq + weight_ws_row(a, kvh, r.off, first) + row] = make_float2(m[i], l[i]);
   }
   if (bad) atomicOr(&a.status[b], SPEC_DEV_BAD_BLOCK);
 }
 
-template <typename T, int D>
+template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kWtThreads) weight_sums_cc_kernel(const WeightArgs a, int key_tiles) {
+  constexpr int ROWS = 16 * RT;
   extern __shared__ float sm[];
   float *sq = sm, *sk = sm + D * (64 + kWtPad);
-  __shared__ float s_lse[kWtRows], s_part[16][kWtKeys];
+  __shared__ float s_lse[ROWS], s_part[16][kWtKeys];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int kvh = blockIdx.x % a.Hkv;
   const int kt = (int)(blockIdx.x / a.Hkv % key_tiles), b = (int)(blockIdx.x / a.Hkv / key_tiles);
@@ -165,14 +173,14 @@ __global__ void __launch_bounds__(kWtThreads) weight_sums_cc_kernel(const Weight
   float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   int bad = 0;
   if (tok0 < r.cnt) {
-    load_tile<T, D>(sk, [&](int i) -> const T* { return k0 + i < total ? key_row<T>(a, bt, kvh, k0 + i, &bad) : nullptr; });
-    for (int r0 = tok0 * a.g / kWtRows * kWtRows; r0 < R; r0 += kWtRows) {
+    load_tile<T, D, kWtKeys>(sk, [&](int i) -> const T* { return k0 + i < total ? key_row<T>(a, bt, kvh, k0 + i, &bad) : nullptr; });
+    for (int r0 = tok0 * a.g / ROWS * ROWS; r0 < R; r0 += ROWS) {
       __syncthreads();
-      load_tile<T, D>(sq, [&](int i) -> const T* {
+      load_tile<T, D, ROWS>(sq, [&](int i) -> const T* {
         if (r0 + i >= R) return nullptr;
         return static_cast<const T*>(a.q) + ((size_t)weight_q_row(a, r, first + (r0 + i) / a.g) * a.Hq + kvh * a.g + (r0 + i) % a.g) * D;
       });
-      for (int i = threadIdx.x; i < kWtRows && r0 + i < R; i += kWtThreads) {
+      for (int i = threadIdx.x; i < ROWS && r0 + i < R; i += kWtThreads) {
         // the splits that hold some of the keys this row sees
         const int splits = min(a.splits, (r.P + first + (r0 + i) / a.g) / a.chunk + 1);
         const float2* ml = a.ws_ml + weight_ws_row(a, kvh, r.off, first) + r0 + i;
@@ -181,14 +189,14 @@ __global__ void __launch_bounds__(kWtThreads) weight_sums_cc_kernel(const Weight
         s_lse[i] = x.x + log2f(x.y);
       }
       __syncthreads();
-      float s[4][4];
-      scores<D>(sq, sk, ty, tx, s);
+      float s[RT][4];
+      scores<D, RT>(sq, sk, ty, tx, s);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = r0 + 4 * ty + i;
+      for (int i = 0; i < RT; ++i) {
+        const int row = r0 + RT * ty + i;
         if (row >= R) continue;
         const int seen = r.P + first + row / a.g;
-        const float lse = s_lse[4 * ty + i];
+        const float lse = s_lse[RT * ty + i];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (k0 + 4 * tx + j <= seen) w[j] += exp2f(s[i][j] * a.scale_log2 - lse);
@@ -210,14 +218,14 @@ __global__ void __launch_bounds__(kWtThreads) weight_sums_cc_kernel(const Weight
   if (bad) atomicOr(&a.status[b], SPEC_DEV_BAD_BLOCK);
 }
 
-template <typename T, int D>
+template <typename T, int D, int RT>
 static cudaError_t launch_cc(const WeightArgs& a, const WeightPlan& p, cudaStream_t stream) {
   const int dyn = 2 * D * (64 + kWtPad) * (int)sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(weight_stats_cc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(weight_sums_cc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+  cudaError_t e = cudaFuncSetAttribute(weight_stats_cc_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(weight_sums_cc_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
   if (e != cudaSuccess) return e;
   if (p.tiles > 0) {
-    weight_stats_cc_kernel<T, D><<<(unsigned)(p.tiles * a.Hkv * p.splits), kWtThreads, dyn, stream>>>(a);
+    weight_stats_cc_kernel<T, D, RT><<<(unsigned)(p.tiles * a.Hkv * p.splits), kWtThreads, dyn, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -232,12 +240,19 @@ static cudaError_t launch_cc(const WeightArgs& a, const WeightPlan& p, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.tiles > 0 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, weight_sums_cc_kernel<T, D>, a, key_tiles);
+  e = cudaLaunchKernelEx(&cfg, weight_sums_cc_kernel<T, D, RT>, a, key_tiles);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Rows per tile of the CUDA-core kernels: the most that a request has decides.
+static int weight_cc_rows(int n_max, int window, int g) {
+  return (long long)(window > 0 ? std::min(window, n_max) : n_max) * g <= kWtFewRows ? kWtFewRows : kWtRows;
+}
+
 cudaError_t launch_weight_cc(const WeightArgs& a, const WeightPlan& p, cudaStream_t stream) {
-  return a.D == 64 ? launch_cc<float, 64>(a, p, stream) : launch_cc<float, 128>(a, p, stream);
+  if (weight_cc_rows(a.n_max, a.window, a.g) == kWtFewRows)
+    return a.D == 64 ? launch_cc<float, 64, 1>(a, p, stream) : launch_cc<float, 128, 1>(a, p, stream);
+  return a.D == 64 ? launch_cc<float, 64, 4>(a, p, stream) : launch_cc<float, 128, 4>(a, p, stream);
 }
 
 constexpr int kWtSms = 152;  // the plan's SM count (part of the workspace query)
@@ -280,8 +295,8 @@ static size_t weight_ws_bytes(int splits, int T, int Hq, bool tc) {
 // alone leave SMs idle: for a dozen items an SM, half of which are above a prompt's
 // diagonal and fall away.  One prompt of 4000 tokens with 8, 4 and 2 kv-heads (128,
 // 64 and 32 items): 149, 192 and 144 us whole, 111, 73 and 35 us in 15 or 16 parts.
-// A prompt of 8192 (256 items) takes 311 us whole, 390 in 15 parts: an item more
-// costs a CTA some 8 us (its keys' load, the score buffers run dry).
+// A prompt of 8192 (256 items) takes 300 us whole, 358 in 15 parts: an item more
+// costs a CTA some 7 us (its keys' load, the score buffers run dry).
 static int weight_parts(int B, int n_max, int max_prefix, int Hkv) {
   const long long items = std::max(1LL, ((long long)max_prefix + n_max + 255) / 256 * B * Hkv);
   return items >= kWtSms ? 1 : (int)std::min(16LL, (12LL * kWtSms + items - 1) / items);
@@ -303,7 +318,7 @@ size_t spec_weight_workspace_size(int B, int T, int n_max, int max_prefix, int H
   if (B <= 0 || T <= 0 || n_max <= 0 || weight_shape_check(B, T, n_max, max_prefix, Hq, Hkv, D, 16) != SPEC_OK) return 256;
   int per_req = 0;
   int splits = 1;
-  for (int rows : {kWtRows, weight_tc_rows(Hq / Hkv)})
+  for (int rows : {kWtRows, kWtFewRows, weight_tc_rows(Hq / Hkv)})
     for (int window : {0, 1}) splits = std::max(splits, weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, rows, &per_req).splits);
   const size_t parts = weight_parts_bytes(weight_parts(B, n_max, max_prefix, Hkv), B, n_max, max_prefix, Hkv);
   return std::max<size_t>(256, weight_ws_bytes(splits, T, Hq, true) + parts);
@@ -333,7 +348,7 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
   const bool tc = dtype == SPEC_BF16;
   // the tensor-core path names cache rows by 32-bit coordinates
   if (tc && (long long)num_blocks * Hkv * block_size >= (long long)INT32_MAX) return SPEC_ERR_UNSUPPORTED;
-  const WeightPlan plan = weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, tc ? weight_tc_rows(Hq / Hkv) : kWtRows, &a.per_req);
+  const WeightPlan plan = weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, tc ? weight_tc_rows(Hq / Hkv) : weight_cc_rows(n_max, window, Hq / Hkv), &a.per_req);
   const long long key_tiles = ((long long)max_prefix + n_max + kWtKeys - 1) / kWtKeys;
   if (plan.tiles * Hkv * plan.splits > (long long)INT32_MAX / 2 || key_tiles * B * Hkv > (long long)INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
   if (key_tiles == 0) return SPEC_OK;

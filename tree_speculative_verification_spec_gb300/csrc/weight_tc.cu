@@ -31,11 +31,11 @@
 // their own, which reads K once: see "Held scores" below.
 //
 // What bounds them, and what they measured (32/8 heads, D 128, one GB300):
-//   every row of a prompt of 8192: statistics 243 us, sums 311.  The tensor core
+//   every row of a prompt of 8192: statistics 243 us, sums 300.  The tensor core
 //   is busy for 49 % and 40 % of that, the exponentials for 50 % and 43 %, the
 //   issue slots for 54 %: the chain of a score buffer from hand to hand.  Sums
 //   have 256 items for 152 CTAs, the first keys' the longest (15 %; items of 128
-//   keys end more evenly but stream Q twice: 380 us).
+//   keys end more evenly but stream Q twice: 380 us against 311).
 //   the last 32 rows of four prompts of 8704 slots, 64/8 heads: 29 us, 37 us, and
 //   the join of the row sums between them.
 //   Two passes over K against 512 rows' of 8000 keys: 185 and 199 us, 5.8 TB/s.
@@ -669,6 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (MODE == kSumsParts && w.steps == 0) continue;  // no row of the part sees a key: not added either
           const int k0 = w.k0 + g * BM, key = k0 + r;
           const float old = half == 0 && MODE == kSumsMany ? old_weight(w, key) : 0.0f;
+          // rows before `edge` do not see the tile's last key
+          const long long edge = (long long)(k0 + BM - 1 - w.q.P - w.q.first) * a.g;
           float2 acc = make_float2(0.0f, 0.0f);
           for (int j = 0; j < w.steps; ++j, ++lt) {
             const int at = lt % kLse;
@@ -676,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j >= lo && j < hi) {
               const int row0 = w.r0 + j * prm.rt;
               const uint32_t t0 = take();
-              const bool masked = k0 + BM - 1 > w.q.P + w.q.first + row0 / a.g || row0 + prm.rt > R;
+              const bool masked = row0 < edge || row0 + prm.rt > R;
 #pragma unroll 1
               for (int e = half * 64; e < half * 64 + 64; e += 32) {
                 uint32_t x[32];
