@@ -165,3 +165,30 @@ def test_budget_refuses_what_is_not_its_own():
     for kw in (dict(layer=1), dict(layer=0, row=2), dict(layer=-1)):
         with pytest.raises(ValueError):
             budget.observe_prompt(kw.pop("layer"), p, **kw)
+
+
+def test_budget_on_a_stream_of_its_own():
+    """Observed and evicted on a side stream, with a workspace that grows between."""
+    budget = CacheBudget(1, 3, Hkv, 40 * BS)
+    pool = Pool(3, 40, 90, Hkv, BS, D, 1)
+    kc, vc = pool.caches[0]
+    pool.fork([-1, -1, -1], [0, 1, 2], [0, 0, 0], [20, 500, 64])
+    side = torch.cuda.Stream()
+    passes = []
+    for row, n in ((0, 20), (1, 500)):
+        q = torch.randn((n, Hq, D), generator=torch.Generator("cuda").manual_seed(n), device="cuda").bfloat16()
+        p = PromptPass(q, kc, vc, pool.table[row:row + 1], ints([0, n]), ints([0]), n, 0, 0.125)
+        p.run(tuple(torch.randn((n, Hkv, D), device="cuda").bfloat16() for _ in range(2)))
+        passes.append((row, p))
+    move = ints([1]), ints([2]), ints([500])  # they live as long as the call
+    side.wait_stream(torch.cuda.current_stream())
+    for row, p in passes:
+        budget.observe_prompt(0, p, row=row, stream=side)
+    slots, new_len, st = budget.evict(pool.k, pool.v, pool.table, BS, 90, *move, 64, 4, 8, D, S.SPEC_BF16, stream=side)
+    side.synchronize()
+    assert st.tolist() == [0] and new_len.tolist() == [64]
+    for row, p in passes:
+        d = dict(q=p.q, k=kc, table=pool.table[row:row + 1], seq_off=p.seq_off, prefix=p.prefix_len, Hq=Hq, Hkv=Hkv, D=D, bs=BS, scale=0.125, stride=40 * BS)
+        _weights_hold(budget, 0, row, None, d)
+    for h in range(Hkv):
+        assert slots[0, 0, h].tolist() == keep_reference(budget.weight[0, 1, h].tolist(), 500, 64, 4, 8)

@@ -679,14 +679,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int row0 = w.r0 + j * prm.rt;
               const uint32_t t0 = take();
               const bool masked = row0 < edge || row0 + prm.rt > R;
+              float2 part = make_float2(0.0f, 0.0f);  // a tile's own sum: thousands of small terms would each be rounded to acc's size
 #pragma unroll 1
               for (int e = half * 64; e < half * 64 + 64; e += 32) {
                 uint32_t x[32];
                 tmem_ld32(t0 + e, x);
                 tmem_wait_ld(x);
-                column_sum(x, &s_lse[at][e], &s_lim[at][e], masked, key, acc);
+                column_sum(x, &s_lse[at][e], &s_lim[at][e], masked, key, part);
               }
               release();
+              acc = __fadd2_rn(acc, part);
             }
             lse_done(lt);
           }

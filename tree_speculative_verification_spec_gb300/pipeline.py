@@ -242,18 +242,21 @@ class VerifyPass:
 class CacheBudget:
     """What the attention of every layer gave each slot of a block table's rows,
     and eviction by it.  weight is float32 [layers][rows][Hkv][slots], by table
-    row; a pass over part of the table says at which row its batch starts."""
+    row; a pass over part of the table says at which row its batch starts.  One
+    workspace serves every call: observe on one stream at a time."""
 
     def __init__(self, layers, rows, Hkv, slots, decay=1.0, device="cuda"):
         self.weight = torch.zeros((layers, rows, Hkv, slots), dtype=torch.float32, device=device)
         self.layers, self.rows, self.Hkv, self.slots, self.decay = layers, rows, Hkv, slots, decay
         self._ws = torch.empty(0, dtype=torch.uint8, device=device)
+        self._outgrown = []  # a call on another stream may still be using them
 
     def reserve(self, B, T, n_max, max_prefix, Hq, D):
         """Workspace for passes of up to these sizes (observing a larger one
         first makes it grow, which a captured graph must not)."""
         need = S.spec_weight_workspace_size(B, T, n_max, max_prefix, Hq, self.Hkv, D)
         if self._ws.numel() < need:
+            self._outgrown.append(self._ws)
             self._ws = torch.empty(need, dtype=torch.uint8, device=self._ws.device)
 
     def _observe(self, layer, row, q, k_cache, block_table, prefix_len, off, path, accept_len, window, n_max, max_prefix, scale, status, stream):
@@ -282,8 +285,9 @@ class CacheBudget:
         """Rows src (int32 [N], of `length` slots) cut to rows dst, which have
         pages for them.  Returns (slots, new_len, status) of spec_kv_evict."""
         N, i32 = src.numel(), dict(dtype=torch.int32, device=src.device)
-        slots = torch.empty((self.layers, N, self.Hkv, keep_max), **i32)
-        new_len, status = torch.empty(N, **i32), torch.empty(N, **i32)
+        with torch.cuda.stream(stream):  # None: the current one
+            slots = torch.empty((self.layers, N, self.Hkv, keep_max), **i32)
+            new_len, status = torch.empty(N, **i32), torch.empty(N, **i32)
         S.spec_kv_evict(k_ptrs, v_ptrs, self.layers, block_table, self.rows, block_table.shape[1], block_size, num_blocks, src, dst, length, keep, N, keep_max,
                         first, last, self.weight, self.slots, self.Hkv, D, dtype, slots, new_len, status, stream)
         return slots, new_len, status
