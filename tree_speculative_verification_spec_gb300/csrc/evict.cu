@@ -12,9 +12,10 @@
 // key that compete (an order-preserving whole number), then 2048 within the bin
 // that holds the border, and so on; then it lists the kept slots in one ordered
 // pass; equal weights at the border are taken from the lowest slot.  Rows of up
-// to 16384 slots are read once and their keys kept in shared memory.  The copy
-// moves the listed rows, 16 bytes a lane; with rows enough for every SM the CTA
-// that selected them moves them, while others select.
+// to 16384 slots (49152 where SMs are idle) are read once and their keys kept in
+// shared memory.  The copy moves the listed rows, 16 bytes a lane; with rows
+// enough for every SM, or few enough for one CTA, the CTA that selected them moves
+// them, while others select.
 // Measured: four rows of 6000 to 8192 slots cut to 1024 in 32 layers 233 us (1.1
 // GB, 4.8 TB/s; 239 with a kernel of its own for the copy, of which the selection
 // took 63); 64 rows of up to 1024 to 256 in two layers 59 us (65).  What is lost
@@ -29,7 +30,8 @@ constexpr int kSelThreads = 512, kSelShort = 128;  // per row, and per row of a 
 constexpr int kSelShortSlots = 2048;
 constexpr int kSelBins = 2048;
 constexpr int kSelRun = 4;          // neighbouring slots per thread of the listing
-constexpr int kSelHeld = 16384;     // most keys held in shared memory (three CTAs an SM)
+constexpr int kSelHeld = 16384;     // most keys held in shared memory (three CTAs an SM), and
+constexpr int kSelHeldOne = 49152;  // where there is at most one CTA for an SM
 constexpr int kGatherThreads = 256;
 constexpr int kGatherCtas = 8;      // per SM
 constexpr int kGatherVec = 4;       // 16-byte vectors of K and V per thread and step
@@ -362,12 +364,13 @@ extern "C" spec_status spec_kv_evict(void* const* k_caches, void* const* v_cache
   cudaStream_t st = (cudaStream_t)stream;
   // room for the keys of the longest row that the table and the weights allow
   const long long most = std::min((long long)max_blocks << a.bs_log2, weight ? weight_stride : (1LL << 30));
-  a.held = (int)std::min<long long>(most, kSelHeld);
+  a.held = (int)std::min<long long>(most, heads <= sms ? kSelHeldOne : kSelHeld);
   const int dyn = a.held * (int)sizeof(uint32_t);
   const bool small = most <= kSelShortSlots;
   // With rows enough for every SM a CTA moves what it has selected while others
-  // select; with fewer, the copy is a kernel of its own that every SM takes part in.
-  const bool copy = heads >= 2LL * sms;
+  // select; with fewer, the copy is a kernel of its own that every SM takes part in,
+  // unless it is so short that the launch would cost more.
+  const bool copy = heads >= 2LL * sms || (long long)keep_max * a.vec <= 8LL * (small ? kSelShort : kSelThreads) * kGatherVec;
   const auto select = small ? (copy ? evict_select_kernel<kSelShort, true> : evict_select_kernel<kSelShort, false>)
                             : (copy ? evict_select_kernel<kSelThreads, true> : evict_select_kernel<kSelThreads, false>);
   if (dyn > 32 * 1024 && cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess) return SPEC_ERR_CUDA;

@@ -927,9 +927,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncthreads();
       if (in) {
         const int mine = s_len[c];
+        const int there = min(kGroup, a.B - b0);
         int before = 0;
-#pragma unroll 8
-        for (int j = 0; j < kGroup; j += 4) {
+#pragma unroll 4
+        for (int j = 0; j < there; j += 4) {
           const int4 x = *reinterpret_cast<const int4*>(&s_len[j]);
           before += x.x > mine || (x.x == mine && j < c);
           before += x.y > mine || (x.y == mine && j + 1 < c);
