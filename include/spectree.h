@@ -655,7 +655,8 @@ spec_status spec_rope_append(const void* qkv, long long row_stride, const void* 
  * summed in a fixed order.
  *   q        [T][Hq][D] dtype, as the attention call had it; 16-byte aligned, as is k_cache
  *   k_cache, block_table, max_blocks, block_size, num_blocks, prefix_len, seq_off, B, T, n_max,
- *   max_prefix  as for spec_prompt_attention
+ *   max_prefix  as for spec_prompt_attention (slots [0, prefix_len[b] + rows) hold finite keys;
+ *            what lies in the pages behind them is never used)
  *   path     int32 [B][path_stride] and accept_len int32 [B], or both NULL: every row
  *   window   > 0: only the last `window` rows of a request count; 0: all
  *   scale, decay  finite and not negative (else SPEC_ERR_INVALID_ARG)

@@ -619,10 +619,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 64; e += 32) {
                 tmem_ld32(t0 + e, x);
                 tmem_wait_ld(x);
+                if (e == 32) release();  // as soon as it is read
                 chunk(x, vis - e);
               }
+            } else {
+              release();
             }
-            release();
           }
           if (valid)
             a.ws_ml[((size_t)w.split * a.T * a.Hq + weight_ws_row(a, w.kvh, w.q.off, w.q.first) + row) * 2 + half] = make_float2(m, l);
@@ -649,9 +651,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t x[32];
               tmem_ld32(t0 + e, x);
               tmem_wait_ld(x);
+              if (e + 32 >= cols) release();  // as soon as it is read
               column_sum(x, &s_lse[at][e], &s_lim[at][e], masked, key, acc);
             }
-            release();
             float sum = acc.x + acc.y;
             if (two) {  // the other row tile's share; a buffer is read before the barrier of the pair's next tile
               float* part = s_part[wg >> 1][pairs++ & 1];
@@ -685,9 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t x[32];
                 tmem_ld32(t0 + e, x);
                 tmem_wait_ld(x);
+                if (e == half * 64 + 32) release();  // as soon as it is read
                 column_sum(x, &s_lse[at][e], &s_lim[at][e], masked, key, part);
               }
-              release();
               acc = __fadd2_rn(acc, part);
             }
             lse_done(lt);
