@@ -53,7 +53,7 @@ namespace wtc {
 using namespace tc5;
 
 constexpr int BM = 128;
-constexpr int kThreads = 640;        // warps: 0 stream, 1 MMA, 2 resident tiles, 3 sums of the rows, 4-19 epilogue (four warpgroups)
+constexpr int kThreads = 640;        // warps: 0 stream, 1 MMA, 2 resident tiles, 3 sums of the rows (statistics: MMA of the second tile), 4-19 epilogue (four warpgroups)
 constexpr uint32_t kTmemCols = 512;  // four score buffers of 128 columns
 constexpr int kLse = 4;              // row tiles whose sums are held for the epilogue
 constexpr int kGroup = 256;          // requests numbered at a time
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NST = L::NST;
   const WeightArgs& a = prm.a;
   extern __shared__ uint8_t dyn_raw[];
-  __shared__ uint64_t full[NST], empty[NST], res_full[2], res_empty[2], s_full[4], s_empty[4], drain;
+  __shared__ uint64_t full[NST], empty[NST], res_full[2], res_empty[2], s_full[4], s_empty[4], drain[2];
   __shared__ Table tab;
   __shared__ uint64_t lse_full[kLse], lse_empty[kLse];
   __shared__ __align__(16) float s_lse[kLse][BM];  // minus log2 of the sums of a row tile's rows
@@ -253,12 +253,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], MODE == kStats ? 2 : 1);  // MMA warps
       issued[i] = -1;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&res_full[i], 1);
-      mbar_init(&res_empty[i], 1);
+      mbar_init(&res_empty[i], MODE == kStats ? 2 : 1);
       res_issued[i] = -1;
     }
     for (int i = 0; i < 4; ++i) {
@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&lse_full[i], 1);
       mbar_init(&lse_empty[i], 16);
     }
-    mbar_init(&drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -428,8 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 || (warp == 3 && MODE == kStats)) {
       // ---------------------------------------------------------- MMA
+      // statistics: a warp for each row tile, its waits (some 300 cycles each) beside
+      // the other's
+      const int own = MODE != kStats ? -1 : warp == 3 ? 1 : 0;
       const uint64_t res = smem_desc_sw128(sbase, 16, 1024), ring = smem_desc_sw128(sbase + L::kOffRing, 16, 1024);
       const bool leader = elect_one();
       for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items); ++round) {
@@ -444,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t sd = ring + (uint64_t)(st * (L::kTile >> 4));
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
+            if (own >= 0 && t != own) continue;
             if (MODE == kSumsFew ? t >= w.rt : j < w.lo[t] || j >= w.hi[t]) continue;
             // buffer, and the number of its jobs before this one
             int buf, before;
@@ -711,9 +716,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (MODE == kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == 1 && elect_one()) {  // every MMA has completed before TMEM is freed
-    umma_commit(&drain);
-    mbar_drain(&drain, 0);
+  if ((warp == 1 || warp == 3) && elect_one()) {  // every MMA has completed before TMEM is freed
+    umma_commit(&drain[warp == 3]);
+    mbar_drain(&drain[warp == 3], 0);
   }
   tc_fence_before();
   __syncthreads();
