@@ -294,8 +294,8 @@ static size_t weight_ws_bytes(int splits, int T, int Hq, bool tc) {
 // Parts of a request's rows whose sums are taken apart, where the items of 256 keys
 // alone leave SMs idle: for a dozen items an SM, half of which are above a prompt's
 // diagonal and fall away.  One prompt of 4000 tokens with 8, 4 and 2 kv-heads (128,
-// 64 and 32 items): 149, 192 and 144 us whole, 111, 73 and 35 us in 15 or 16 parts.
-// A prompt of 8192 (256 items) takes 300 us whole, 358 in 15 parts: an item more
+// 64 and 32 items): 149, 192 and 144 us whole, 98, 67 and 32 us in 15 or 16 parts.
+// A prompt of 8192 (256 items) took 300 us whole and 358 in 15 parts: an item more
 // costs a CTA some 7 us (its keys' load, the score buffers run dry).
 static int weight_parts(int B, int n_max, int max_prefix, int Hkv) {
   const long long items = std::max(1LL, ((long long)max_prefix + n_max + 255) / 256 * B * Hkv);

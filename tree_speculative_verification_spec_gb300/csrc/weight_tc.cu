@@ -31,11 +31,11 @@
 // their own, which reads K once: see "Held scores" below.
 //
 // What bounds them, and what they measured (32/8 heads, D 128, one GB300):
-//   every row of a prompt of 8192: statistics 243 us, sums 300.  The tensor core
-//   is busy for 49 % and 40 % of that, the exponentials for 50 % and 43 %, the
-//   issue slots for 54 %: the chain of a score buffer from hand to hand.  Sums
-//   have 256 items for 152 CTAs, the first keys' the longest (15 %; items of 128
-//   keys end more evenly but stream Q twice: 380 us against 311).
+//   every row of a prompt of 8192: statistics 229 us, sums 273 (241 and 298 with
+//   one MMA warp for both tiles).  No pipe is full (tensor core and exponentials
+//   some 55 %, issue slots 60 %): the chain of a score buffer from hand to hand.
+//   Sums have 256 items for 152 CTAs, the first keys' the longest (15 %; items of
+//   128 keys end more evenly but stream Q twice: 380 us against 311 at that step).
 //   the last 32 rows of four prompts of 8704 slots, 64/8 heads: 29 us, 37 us, and
 //   the join of the row sums between them.
 //   Two passes over K against 512 rows' of 8000 keys: 185 and 199 us, 5.8 TB/s.
@@ -53,7 +53,7 @@ namespace wtc {
 using namespace tc5;
 
 constexpr int BM = 128;
-constexpr int kThreads = 640;        // warps: 0 stream, 1 MMA, 2 resident tiles, 3 sums of the rows (statistics: MMA of the second tile), 4-19 epilogue (four warpgroups)
+constexpr int kThreads = 640;        // warps: 0 stream, 1 MMA, 2 resident tiles (and sums of the rows), 3 MMA of the second tile (sums over few rows: sums of the rows), 4-19 epilogue (four warpgroups)
 constexpr uint32_t kTmemCols = 512;  // four score buffers of 128 columns
 constexpr int kLse = 4;              // row tiles whose sums are held for the epilogue
 constexpr int kGroup = 256;          // requests numbered at a time
@@ -253,12 +253,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], MODE == kStats ? 2 : 1);  // MMA warps
+      mbar_init(&empty[i], MODE == kSumsFew ? 1 : 2);  // MMA warps
       issued[i] = -1;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&res_full[i], 1);
-      mbar_init(&res_empty[i], MODE == kStats ? 2 : 1);
+      mbar_init(&res_empty[i], MODE == kSumsFew ? 1 : 2);
       res_issued[i] = -1;
     }
     for (int i = 0; i < 4; ++i) {
@@ -366,6 +366,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   int lt = 0;                           // row tiles of sums so far
   int pairs = 0;                        // key tiles of two row tiles so far (epilogue)
   bool dead = false;                    // a producer that gave up
+  // The sums of an item's n row tiles for the epilogue (a whole warp).
+  auto row_sums = [&](const Item& w, int n) {
+    const int R = w.q.cnt * a.g;
+    for (int t = 0; t < n; ++t, ++lt) {
+      const int at = lt % kLse;
+      float nl[BM / 32];
+      int lim[BM / 32];
+      const int row0 = w.r0 + t * prm.rt + lane;
+      const float* lse = a.ws_lse + weight_ws_row(a, w.kvh, w.q.off, w.q.first) + row0;
+#pragma unroll
+      for (int e = 0; e < BM / 32; ++e) {
+        const bool there = e * 32 + lane < prm.rt && row0 + e * 32 < R;
+        lim[e] = there ? w.q.P + w.q.first + (row0 + e * 32) / a.g : -1;
+        nl[e] = there ? lse[e * 32] : -INFINITY;
+      }
+      bool go = true;
+      if (lane == 0 && lt >= kLse) go = wait(&lse_empty[at], lt / kLse - 1);
+      dead = !__shfl_sync(0xffffffffu, (int)go, 0);
+      if (dead) break;
+#pragma unroll
+      for (int e = 0; e < BM / 32; ++e) {
+        s_lse[at][e * 32 + lane] = nl[e];
+        s_lim[at][e * 32 + lane] = lim[e];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&lse_full[at]);
+    }
+  };
+
   for (int b0 = 0; b0 < a.B; b0 += kGroup) {
     const int tiles = build_table<MODE>(prm, tab, b0, scan);
     const int n_items = tiles * a.Hkv * (MODE == kStats ? a.splits : 1);
@@ -428,12 +457,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[w.b], SPEC_DEV_BAD_BLOCK);
+        if (many(MODE) && !dead) row_sums(w, w.steps);
       }
-    } else if (warp == 1 || (warp == 3 && MODE == kStats)) {
+    } else if (warp == 1 || (warp == 3 && MODE != kSumsFew)) {
       // ---------------------------------------------------------- MMA
-      // statistics: a warp for each row tile, its waits (some 300 cycles each) beside
-      // the other's
-      const int own = MODE != kStats ? -1 : warp == 3 ? 1 : 0;
+      // a warp for each tile that a step multiplies, its waits (some 300 cycles each)
+      // beside the other's; sums over few rows have one for both
+      const int own = MODE == kSumsFew ? -1 : warp == 3 ? 1 : 0;
       const uint64_t res = smem_desc_sw128(sbase, 16, 1024), ring = smem_desc_sw128(sbase + L::kOffRing, 16, 1024);
       const bool leader = elect_one();
       for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items); ++round) {
@@ -484,36 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (leader) umma_commit(&res_empty[rs & 1]);
         __syncwarp();
       }
-    } else if (warp == 3 && MODE != kStats) {
+    } else if (warp == 3 && MODE == kSumsFew) {
       // ---------------------------------------------------------- sums of the rows
       for (int round = 0, idx; (idx = dealt(round)) < rounds_end(n_items) && !dead; ++round) {
         if (idx >= n_items) continue;
         const Item w = find_item<MODE>(prm, tab, b0, idx, lane);
-        const int n = MODE == kSumsFew ? w.rt : w.steps, R = w.q.cnt * a.g;
-        for (int t = 0; t < n; ++t, ++lt) {
-          const int at = lt % kLse;
-          float nl[BM / 32];
-          int lim[BM / 32];
-          const int row0 = w.r0 + t * prm.rt + lane;
-          const float* lse = a.ws_lse + weight_ws_row(a, w.kvh, w.q.off, w.q.first) + row0;
-#pragma unroll
-          for (int e = 0; e < BM / 32; ++e) {
-            const bool there = e * 32 + lane < prm.rt && row0 + e * 32 < R;
-            lim[e] = there ? w.q.P + w.q.first + (row0 + e * 32) / a.g : -1;
-            nl[e] = there ? lse[e * 32] : -INFINITY;
-          }
-          bool go = true;
-          if (lane == 0 && lt >= kLse) go = wait(&lse_empty[at], lt / kLse - 1);
-          dead = !__shfl_sync(0xffffffffu, (int)go, 0);
-          if (dead) break;
-#pragma unroll
-          for (int e = 0; e < BM / 32; ++e) {
-            s_lse[at][e * 32 + lane] = nl[e];
-            s_lim[at][e * 32 + lane] = lim[e];
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&lse_full[at]);
-        }
+        row_sums(w, w.rt);
       }
     } else if (warp >= 4) {
       // ---------------------------------------------------------- epilogue
