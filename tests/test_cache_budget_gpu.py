@@ -1,0 +1,62 @@
+"""A bounded cache through the pipeline, where its parts meet: rotaries of
+several axes, streams, workspaces and table rows."""
+import math
+
+import pytest
+import torch
+
+import tree_speculative_verification_spec_gb300 as S
+from bounded_cache import ints, offsets, rope_reference
+from tree_speculative_verification_spec_gb300.pipeline import DeviceBatch, PromptPass, Rotary, VerifyPass
+
+pytestmark = pytest.mark.gpu
+Hq, Hkv, D, BS = 8, 2, 64, 16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from tree_speculative_verification_spec_gb300 import build
+    build.build()
+    S.lib()
+
+
+def _randn(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+
+
+@pytest.mark.parametrize("axes", [1, 3])
+def test_a_tree_behind_a_prompt_of_several_axes(axes):
+    """An image's prompt, then a verification of text: one rotary for both."""
+    n, parent = 40, [-1, 0, 0, 2, 1]
+    g = torch.Generator().manual_seed(3)
+    freq = (10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().cuda()
+    axis = torch.randint(0, axes, (D // 2,), generator=g).to(torch.int32).cuda() if axes > 1 else None
+    rotary = Rotary(freq, D, axis=axis, axes=axes)
+    pos = torch.randint(0, 500, (axes, n), generator=g).to(torch.int32).cuda()
+    kc, vc = (torch.zeros((6, Hkv, BS, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table, zero, scale = ints([[4, 1, 3]]), ints([0]), 1 / math.sqrt(D)
+
+    def holds(qkv, q, place, first):
+        ref, tol = rope_reference(qkv, Hq, Hkv, D, 0, freq, place, None, None, 0.0)
+        assert ((q.double() - ref[:, :Hq]).abs() <= tol[:, :Hq]).all()
+        for h in range(Hkv):
+            k = kc[table[0].long(), h].reshape(-1, D)[first:first + len(qkv)]
+            assert ((k.double() - ref[:, Hq + h]).abs() <= tol[:, Hq + h]).all()
+
+    qkv = _randn((n, Hq + 2 * Hkv, D), 1)
+    p = PromptPass(torch.empty((n, Hq, D), dtype=torch.bfloat16, device="cuda"), kc, vc, table, offsets([n]), zero, n, 0, scale)
+    p.run(prompt_qkv=qkv, rotary=rotary, pos_base=zero, pos=pos)
+    assert p.status.tolist() == [0]
+    holds(qkv, p.q, pos.t()[:, axis.long()] if axes > 1 else pos.t().expand(-1, D // 2), 0)
+
+    T, qkv = len(parent), _randn((len(parent), Hq + 2 * Hkv, D), 2)
+    v = VerifyPass(DeviceBatch(B=1, T=T, n_max=T, V=7, Hq=Hq, Hkv=Hkv, D=D, block_size=BS, num_blocks=6, max_prefix=n, parent=ints(parent),
+                               tree_off=offsets([T]), tokens=ints([0] * T), prefix_len=ints([n]), block_table=table,
+                               q=torch.empty((T, Hq, D), dtype=torch.bfloat16, device="cuda"), k_cache=kc, v_cache=vc,
+                               p_logits=torch.zeros((T, 7), device="cuda"), q_probs=None, uniforms=None, scale=scale))
+    v.run("greedy", commit=False, tree_qkv=qkv, rotary=rotary, pos_base=ints([700]))
+    assert v.status.tolist() == [0]
+    depth = torch.tensor([0, 1, 1, 2, 2], device="cuda")
+    holds(qkv, v.batch.q, (700 + depth)[:, None].expand(-1, D // 2), n)

@@ -15,7 +15,7 @@ CacheBudget holds the attention weight that cached slots gather over those
 passes (spec_attention_weight) and cuts rows to a budget by it
 (spec_kv_evict).
 """
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 
 import torch
 
@@ -178,8 +178,11 @@ class VerifyPass:
     def project(self, qkv, rotary, pos_base=None, stream=None):
         """A projection's rows of the tree, normalised and rotated into the
         batch's q and slots prefix_len + u (before attention, after the mask
-        build): node u's position is pos_base[b] (None: the prefix) plus its depth."""
+        build): node u's position is pos_base[b] (None: the prefix) plus its depth,
+        on every axis that the rotary has (nodes are text)."""
         b = self.batch
+        # one axis stands for all: depth holds no more
+        rotary = replace(rotary, axis=None, axes=1)
         rotary.append(qkv, b.q, b.k_cache, b.v_cache, b.block_table, b.prefix_len, b.tree_off, b.n_max, self.status, pos_base, self.depth, stream)
 
     def attention(self, flags=S.SPEC_ATTN_AUTO, stream=None):
