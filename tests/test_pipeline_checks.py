@@ -61,3 +61,37 @@ def test_project_names_a_position_for_every_axis_it_asks_for(calls, axes):
         assert 0 <= a < args[AXES]
         assert pos[a * T:(a + 1) * T].tolist() == [0, 1, 2, 0, 1]
     assert args[POS_BASE] is base and rotary.axes == axes and rotary.axis is axis
+
+
+def _append(calls, T=5, B=2, rot=D, **change):
+    """Rotary.append over T rows, with one buffer changed."""
+    kw = dict(qkv=torch.zeros((T, Hq + 2 * Hkv, D)), inv_freq=torch.ones(rot // 2), axis=None, axes=1, pos_base=None, pos=None, q_norm=None, k_norm=None)
+    kw.update(change)
+    cache = torch.zeros((8, Hkv, BS, D))
+    rotary = Rotary(kw["inv_freq"], rot, axis=kw["axis"], axes=kw["axes"], q_norm=kw["q_norm"], k_norm=kw["k_norm"])
+    rotary.append(kw["qkv"], torch.zeros((T, Hq, D)), cache, cache, ints([[0, 1]] * B), ints([0] * B), ints([0] * (B + 1)), T, ints([0] * B), kw["pos_base"],
+                  kw["pos"])
+    return calls[-1][1]
+
+
+AXIS3 = dict(axis=ints([0, 1, 2] * 10 + [0, 1]), axes=3)
+
+
+@pytest.mark.parametrize("change", [
+    dict(pos=ints([0] * 4)), dict(pos=ints([[0] * 5] * 2), **AXIS3), dict(pos=ints([0] * 14), **AXIS3), dict(pos=ints([[0] * 6] * 3), **AXIS3),
+    dict(pos=ints([[0] * 5] * 3), axis=ints([0] * 31), axes=3), dict(pos_base=ints([0])), dict(qkv=torch.zeros((4, Hq + 2 * Hkv, D))),
+    dict(qkv=torch.zeros((5, Hq + Hkv, D))), dict(qkv=torch.zeros((5, 511))), dict(inv_freq=torch.ones(31)), dict(q_norm=torch.ones(63)), dict(k_norm=torch.ones(32))],
+    ids=["pos", "pos of two axes", "flat pos", "pos of other rows", "axis", "pos_base", "qkv", "heads", "width", "inv_freq", "q_norm", "k_norm"])
+def test_append_refuses_buffers_that_end_early(calls, change):
+    with pytest.raises(ValueError):
+        _append(calls, **change)
+    assert not calls
+
+
+@pytest.mark.parametrize("change", [
+    dict(), dict(pos=ints([0] * 5)), dict(pos=ints([[0] * 5])), dict(pos=ints([0] * 9)), dict(pos=ints([[0] * 5] * 3), **AXIS3), dict(pos=ints([0] * 15), **AXIS3),
+    dict(pos=ints([[0] * 5] * 4), **AXIS3), dict(pos_base=ints([0, 0])), dict(pos_base=ints([0] * 9)), dict(qkv=torch.zeros((9, (Hq + 2 * Hkv) * D))),
+    dict(inv_freq=None, rot=0), dict(inv_freq=torch.ones(40)), dict(q_norm=torch.ones(64), k_norm=torch.ones(64))])
+def test_append_takes_buffers_that_are_long_enough(calls, change):
+    args = _append(calls, **change)
+    assert args[POS] is change.get("pos") and args[POS_BASE] is change.get("pos_base")
