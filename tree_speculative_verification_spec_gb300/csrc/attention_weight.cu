@@ -354,8 +354,9 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
   if (key_tiles == 0) return SPEC_OK;
   // only requests of more rows than one item's take them in parts
   const long long rows = (long long)(window > 0 ? std::min(window, n_max) : n_max) * (Hq / Hkv);
-  a.parts = tc && rows > weight_tc_rows(Hq / Hkv) ? weight_parts(B, n_max, max_prefix, Hkv) : 1;
-  const size_t sums = weight_ws_bytes(plan.splits, T, Hq, tc), need = sums + weight_parts_bytes(a.parts, B, n_max, max_prefix, Hkv);
+  const bool rowless = T == 0 || n_max == 0;  // no request can have a row: nothing goes through the workspace
+  a.parts = tc && !rowless && rows > weight_tc_rows(Hq / Hkv) ? weight_parts(B, n_max, max_prefix, Hkv) : 1;
+  const size_t sums = rowless ? 0 : weight_ws_bytes(plan.splits, T, Hq, tc), need = sums + weight_parts_bytes(a.parts, B, n_max, max_prefix, Hkv);
   if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15))) return SPEC_ERR_WORKSPACE;
   a.q = q;
   a.k_cache = k_cache;
@@ -368,8 +369,8 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
   a.weight = weight;
   a.status = status;
   a.ws_ml = static_cast<float2*>(workspace);
-  a.ws_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums);
-  if (tc) a.ws_lse = static_cast<float*>(workspace) + (size_t)plan.splits * T * Hq * kWtParts * 2;
+  if (a.parts > 1) a.ws_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums);
+  if (tc && sums > 0) a.ws_lse = static_cast<float*>(workspace) + (size_t)plan.splits * T * Hq * kWtParts * 2;
   a.stride = weight_stride;
   a.path_stride = path_stride;
   a.window = window;
