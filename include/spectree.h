@@ -663,8 +663,9 @@ spec_status spec_rope_append(const void* qkv, long long row_stride, const void* 
  *   before   float [B][Hkv][weight_stride], or NULL for zeros;  weight  the same shape, out;
  *            they may be one buffer.  Only slots [0, prefix_len[b] + rows) are read and
  *            written.  A request without rows has its weights decayed
- *   workspace  16-byte aligned device scratch of spec_weight_workspace_size() bytes; calls that
- *            may run at once need one each
+ *   workspace  16-byte aligned device scratch of spec_weight_workspace_size() bytes, which are
+ *            enough for every batch of no larger sizes too, whatever its window and type; calls
+ *            that may run at once need one each
  *   status   int32 [B] in/out: a request that comes in non-zero is left as it was.  Or-ed with
  *            SPEC_DEV_BAD_TREE, SPEC_DEV_CAPACITY (also prefix_len + rows beyond
  *            weight_stride), SPEC_DEV_BAD_PATH (accept_len outside [0, min(path_stride, n_b)],

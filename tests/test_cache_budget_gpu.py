@@ -7,7 +7,7 @@ import torch
 
 import tree_speculative_verification_spec_gb300 as S
 from bounded_cache import ints, offsets, rope_reference
-from tree_speculative_verification_spec_gb300.pipeline import DeviceBatch, PromptPass, Rotary, VerifyPass
+from tree_speculative_verification_spec_gb300.pipeline import CacheBudget, DeviceBatch, PromptPass, Rotary, VerifyPass
 
 pytestmark = pytest.mark.gpu
 Hq, Hkv, D, BS = 8, 2, 64, 16
@@ -60,3 +60,25 @@ def test_a_tree_behind_a_prompt_of_several_axes(axes):
     assert v.status.tolist() == [0]
     depth = torch.tensor([0, 1, 1, 2, 2], device="cuda")
     holds(qkv, v.batch.q, (700 + depth)[:, None].expand(-1, D // 2), n)
+
+
+def _observed(budget, lens, prefix, **kw):
+    """A pass of rows in an empty cache, observed."""
+    n = sum(lens)
+    pages = -(-(max(lens) + max(prefix)) // BS)
+    kc = torch.zeros((pages * len(lens), budget.Hkv, BS, D), dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(pages * len(lens), dtype=torch.int32, device="cuda").view(len(lens), pages)
+    p = PromptPass(torch.ones((n, Hq, D), dtype=torch.bfloat16, device="cuda"), kc, kc, table, offsets(lens), ints(prefix), max(lens), max(prefix), 0.125)
+    budget.observe_prompt(0, p, **kw)
+    return p
+
+
+def test_a_reserved_workspace_serves_smaller_passes():
+    """Captured with less rows and keys than were reserved: nothing is allocated."""
+    budget = CacheBudget(1, 64, Hkv, 8192)
+    budget.reserve(64, 512, 300, 4096, Hq, D)
+    ws = budget._ws.data_ptr()
+    for lens, prefix in (([1], [4096]), ([1] * 8, [4000] * 8), ([300], [0]), ([300], [4096]), ([8] * 64, [100] * 64), ([300, 200], [5, 3000])):
+        p = _observed(budget, lens, prefix)
+        _observed(budget, lens, prefix, window=1)
+        assert budget._ws.data_ptr() == ws and not p.status.any()

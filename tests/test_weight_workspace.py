@@ -41,3 +41,35 @@ def test_batches_without_rows_need_no_more_than_the_query_says(size, dtype):
     """No request can have a row: nothing is put into the workspace."""
     assert _suffices(size, S.spec_weight_workspace_size(*size), dtype=dtype)
     assert _suffices(size, 0, dtype=dtype)
+
+
+def _sizes(rng):
+    Hq, Hkv = rng.choice([(32, 8), (64, 8), (8, 2), (4, 4), (6, 2), (5, 1), (96, 1), (200, 1), (8, 1)])
+
+    def log(lo, hi):
+        return int(lo * (hi / lo) ** rng.random())
+    return (log(1, 400), log(1, 40000), log(1, 20000), rng.choice((0, log(1, 200000))), Hq, Hkv, rng.choice((64, 128)))
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_a_workspace_serves_every_call_of_no_larger_sizes(seed):
+    """Whatever the batch, its window and its type: smaller ones split further."""
+    rng = random.Random(seed)
+    for _ in range(400):
+        size = _sizes(rng)
+        have = S.spec_weight_workspace_size(*size)
+        for _ in range(6):
+            less = tuple(rng.choice((x, rng.randint(0, x), min(x, 1))) for x in size[:4])
+            less = (max(less[0], 1),) + less[1:] + size[4:]
+            if less[2] + less[3] == 0:
+                continue
+            assert S.spec_weight_workspace_size(*less) <= have, (size, less)
+            kw = dict(dtype=rng.choice((S.SPEC_BF16, S.SPEC_F32)), window=rng.choice((0, 0, 1, rng.randint(1, 300))), path=less[2] > 0 and rng.random() < 0.3)
+            assert _suffices(less, have, **kw), (size, less, kw)
+
+
+def test_a_small_tree_after_a_wide_batch():
+    """32/8 heads, D 128, prefix 4096: four trees of 8 nodes, and one of 8."""
+    have = S.spec_weight_workspace_size(4, 32, 8, 4096, 32, 8, 128)
+    assert S.spec_weight_workspace_size(1, 8, 8, 4096, 32, 8, 128) <= have
+    assert have <= 1 << 20

@@ -311,17 +311,20 @@ using namespace spectree;
 
 extern "C" {
 
-// (reference, sum) for every row of q and split, and for the tensor cores two of
-// them and the row's whole; a window only lowers the number of splits that are
-// wanted without one, or raises it to what one row tile wants.
+// What no call of these sizes or smaller ones exceeds, whatever its window and
+// type: fewer rows and keys split further, so the need itself does not grow with
+// the sizes (32/8 heads, D 128, prefix 4096: 38 KB for one request of 8 rows, 21 for
+// 8 requests of one).  Splits: weight_plan's chunk is at least 512 keys,
+// and, but for the 2048 of few rows, the keys that 2 kWtSms items of one row tile
+// have (rounded down once: one split more).  Parts: fewer than kWtSms items of 256
+// keys, in at most 12 kWtSms parts of items in all and one more each.
 size_t spec_weight_workspace_size(int B, int T, int n_max, int max_prefix, int Hq, int Hkv, int D) {
   if (B <= 0 || T <= 0 || n_max <= 0 || weight_shape_check(B, T, n_max, max_prefix, Hq, Hkv, D, 16) != SPEC_OK) return 256;
-  int per_req = 0;
-  int splits = 1;
-  for (int rows : {kWtRows, kWtFewRows, weight_tc_rows(Hq / Hkv)})
-    for (int window : {0, 1}) splits = std::max(splits, weight_plan(B, T, n_max, max_prefix, Hq, Hkv, window, rows, &per_req).splits);
-  const size_t parts = weight_parts_bytes(weight_parts(B, n_max, max_prefix, Hkv), B, n_max, max_prefix, Hkv);
-  return std::max<size_t>(256, weight_ws_bytes(splits, T, Hq, true) + parts);
+  const long long keys = (long long)max_prefix + n_max;
+  const int splits = (int)std::max(std::min((keys + 511) / 512, 2LL * kWtSms / Hkv + 2), (keys + 2047) / 2048);
+  const bool parts = (long long)n_max * (Hq / Hkv) > weight_tc_rows(Hq / Hkv);
+  const long long part_sums = parts ? 16 * std::min(B * keys * Hkv, 13LL * kWtSms * 16) : 0;
+  return std::max<size_t>(256, weight_ws_bytes(splits, T, Hq, true) + part_sums * sizeof(float));
 }
 
 spec_status spec_attention_weight(const void* q, const void* k_cache, const int32_t* block_table, int max_blocks,
