@@ -1,5 +1,7 @@
 """Calls of a bounded cache at the edges of what their arguments may say:
 against plain implementations in 64 bits."""
+import threading
+
 import pytest
 import torch
 
@@ -42,3 +44,35 @@ def test_weight_flags_rows_that_the_batch_cannot_have(dtype):
         got, st = _weight(d, before, n_max=n_max)
         assert st.tolist() == [S.SPEC_DEV_BAD_TREE if b in bad else 0 for b in range(3)]
         _weight_holds({**d, "seq_off": ints([0, 0, 0, 0])}, got, before, skip=bad)
+
+
+def test_evict_from_two_threads():
+    """Tables of different widths want different amounts of shared memory: neither
+    thread's may be taken for the other's."""
+    def work(width, out):
+        try:
+            torch.cuda.set_device(0)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                cache = torch.zeros((2, 4, 1, 16, 64), dtype=torch.bfloat16, device="cuda")
+                k, v = (torch.tensor([c.data_ptr()], dtype=torch.int64, device="cuda") for c in cache)
+                table = torch.full((2, width), -1, dtype=torch.int32, device="cuda")
+                table[0, :2], table[1, 0] = ints([0, 1]), 2
+                weight = torch.rand((1, 2, 1, width * 16), device="cuda")
+                src, dst, length = ints([0]), ints([1]), ints([20])
+                slots, new_len, status = torch.empty((1, 1, 1, 8), dtype=torch.int32, device="cuda"), ints([0]), ints([0])
+                stream.synchronize()
+                for _ in range(4000):
+                    S.spec_kv_evict(k, v, 1, table, 2, width, 16, 4, src, dst, length, None, 1, 8, 1, 2, weight, width * 16, 1, 64, S.SPEC_BF16, slots, new_len,
+                                    status)
+                stream.synchronize()
+                out.append((new_len.tolist(), status.tolist()))
+        except Exception as e:
+            out.append(repr(e))
+    outs = [[], []]
+    threads = [threading.Thread(target=work, args=a) for a in zip((3000, 600), outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert outs == [[([8], [0])]] * 2

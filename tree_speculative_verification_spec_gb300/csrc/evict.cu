@@ -373,7 +373,10 @@ extern "C" spec_status spec_kv_evict(void* const* k_caches, void* const* v_cache
   const bool copy = heads >= 2LL * sms || (long long)keep_max * a.vec <= 8LL * (small ? kSelShort : kSelThreads) * kGatherVec;
   const auto select = small ? (copy ? evict_select_kernel<kSelShort, true> : evict_select_kernel<kSelShort, false>)
                             : (copy ? evict_select_kernel<kSelThreads, true> : evict_select_kernel<kSelThreads, false>);
-  if (dyn > 32 * 1024 && cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess) return SPEC_ERR_CUDA;
+  // the limit belongs to the function, not to this call: one value for every call, as
+  // another thread's may set it between this one's set and its launch
+  constexpr int kDynMax = kSelHeldOne * (int)sizeof(uint32_t);
+  if (dyn > 32 * 1024 && cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynMax) != cudaSuccess) return SPEC_ERR_CUDA;
   select<<<(unsigned)heads, small ? kSelShort : kSelThreads, dyn, st>>>(a);
   SPEC_LAUNCH_CHECK();
   if (keep_max == 0 || copy) return SPEC_OK;
