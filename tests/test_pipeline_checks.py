@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tree_speculative_verification_spec_gb300 import pipeline
-from tree_speculative_verification_spec_gb300.pipeline import DeviceBatch, Rotary, VerifyPass
+from tree_speculative_verification_spec_gb300.pipeline import CacheBudget, DeviceBatch, Rotary, VerifyPass
 
 Hq, Hkv, D, BS = 4, 2, 64, 16
 
@@ -95,3 +95,26 @@ def test_append_refuses_buffers_that_end_early(calls, change):
 def test_append_takes_buffers_that_are_long_enough(calls, change):
     args = _append(calls, **change)
     assert args[POS] is change.get("pos") and args[POS_BASE] is change.get("pos_base")
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_evict_refuses_a_part_of_the_table(calls, rows):
+    """Rows are checked against the budget's number of them: a slice of the table
+    would be read behind its end."""
+    budget = CacheBudget(1, 4, Hkv, 64, device="cpu")
+    with pytest.raises(ValueError, match="rows"):
+        budget.evict(None, None, ints([[0, 1]] * rows), BS, 8, ints([0]), ints([3]), ints([20]), 8, 0, 0, D, 0)
+    assert not calls
+    for whole in (4, 5):  # the rows behind the budget's are not named
+        budget.evict(None, None, ints([[0, 1]] * whole), BS, 8, ints([0]), ints([3]), ints([20]), 8, 0, 0, D, 0)
+    assert [n for n, _, _ in calls] == ["spec_kv_evict"] * 2
+
+
+@pytest.mark.parametrize("change", [dict(dst=ints([3])), dict(length=ints([20])), dict(keep=ints([8]))])
+def test_evict_refuses_lists_that_end_early(calls, change):
+    budget = CacheBudget(1, 4, Hkv, 64, device="cpu")
+    kw = dict(src=ints([0, 1]), dst=ints([2, 3]), length=ints([20, 20]), keep=None)
+    kw.update(change)
+    with pytest.raises(ValueError):
+        budget.evict(None, None, ints([[0, 1]] * 4), BS, 8, kw["src"], kw["dst"], kw["length"], 8, 0, 0, D, 0, keep=kw["keep"])
+    assert not calls

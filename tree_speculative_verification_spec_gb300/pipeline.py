@@ -303,8 +303,13 @@ class CacheBudget:
 
     def evict(self, k_ptrs, v_ptrs, block_table, block_size, num_blocks, src, dst, length, keep_max, first, last, D, dtype, keep=None, stream=None):
         """Rows src (int32 [N], of `length` slots) cut to rows dst, which have
-        pages for them.  Returns (slots, new_len, status) of spec_kv_evict."""
+        pages for them; block_table is the whole table, not a pass's rows of it.
+        Returns (slots, new_len, status) of spec_kv_evict."""
         N, i32 = src.numel(), dict(dtype=torch.int32, device=src.device)
+        if block_table.shape[0] < self.rows:
+            raise ValueError("the block table has fewer rows than the budget")
+        if dst.numel() < N or length.numel() < N or (keep is not None and keep.numel() < N):
+            raise ValueError("dst, length and keep must hold an entry for each of src")
         with torch.cuda.stream(stream):  # None: the current one
             slots = torch.empty((self.layers, N, self.Hkv, keep_max), **i32)
             new_len, status = torch.empty(N, **i32), torch.empty(N, **i32)
