@@ -69,6 +69,8 @@ def _observed(budget, lens, prefix, **kw):
     kc = torch.zeros((pages * len(lens), budget.Hkv, BS, D), dtype=torch.bfloat16, device="cuda")
     table = torch.arange(pages * len(lens), dtype=torch.int32, device="cuda").view(len(lens), pages)
     p = PromptPass(torch.ones((n, Hq, D), dtype=torch.bfloat16, device="cuda"), kc, kc, table, offsets(lens), ints(prefix), max(lens), max(prefix), 0.125)
+    if kw.get("stream") is not None:
+        kw["stream"].wait_stream(torch.cuda.current_stream())
     budget.observe_prompt(0, p, **kw)
     return p
 
@@ -82,3 +84,26 @@ def test_a_reserved_workspace_serves_smaller_passes():
         p = _observed(budget, lens, prefix)
         _observed(budget, lens, prefix, window=1)
         assert budget._ws.data_ptr() == ws and not p.status.any()
+
+
+def _stream_of_memory(t):
+    """The stream whose pool a tensor's memory is from."""
+    at = t.data_ptr()
+    return [s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"]]
+
+
+def test_a_workspace_is_the_observing_streams_own():
+    """Memory of another stream may still be written by what was queued there."""
+    budget, side = CacheBudget(1, 64, Hkv, 8192), torch.cuda.Stream()
+    for lens, prefix in (([5], [0]), ([300], [4000])):
+        p = _observed(budget, lens, prefix, stream=side)
+        side.synchronize()
+        assert not p.status.any()
+        assert _stream_of_memory(budget._ws) == [side.cuda_stream]
+    budget.reserve(64, 4096, 4000, 8000, Hq, D, stream=side)
+    assert _stream_of_memory(budget._ws) == [side.cuda_stream]
+    with torch.cuda.stream(side):
+        again = CacheBudget(1, 64, Hkv, 8192)
+        _observed(again, [5], [0])
+        assert _stream_of_memory(again._ws) == [side.cuda_stream]
+    side.synchronize()

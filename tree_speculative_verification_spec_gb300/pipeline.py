@@ -263,7 +263,8 @@ class CacheBudget:
     """What the attention of every layer gave each slot of a block table's rows,
     and eviction by it.  weight is float32 [layers][rows][Hkv][slots], by table
     row; a pass over part of the table says at which row its batch starts.  One
-    workspace serves every call: observe on one stream at a time."""
+    workspace serves every call: observe on one stream at a time, and let another
+    one wait for it first."""
 
     def __init__(self, layers, rows, Hkv, slots, decay=1.0, device="cuda"):
         self.weight = torch.zeros((layers, rows, Hkv, slots), dtype=torch.float32, device=device)
@@ -271,13 +272,15 @@ class CacheBudget:
         self._ws = torch.empty(0, dtype=torch.uint8, device=device)
         self._outgrown = []  # a call on another stream may still be using them
 
-    def reserve(self, B, T, n_max, max_prefix, Hq, D):
-        """Workspace for passes of up to these sizes (observing a larger one
-        first makes it grow, which a captured graph must not)."""
+    def reserve(self, B, T, n_max, max_prefix, Hq, D, stream=None):
+        """Workspace for passes of up to these sizes, observed on `stream`
+        (observing a larger one first makes it grow, which a captured graph must
+        not)."""
         need = S.spec_weight_workspace_size(B, T, n_max, max_prefix, Hq, self.Hkv, D)
         if self._ws.numel() < need:
             self._outgrown.append(self._ws)
-            self._ws = torch.empty(need, dtype=torch.uint8, device=self._ws.device)
+            with torch.cuda.stream(stream):  # another stream's free memory may still be in use there
+                self._ws = torch.empty(need, dtype=torch.uint8, device=self._ws.device)
 
     def _observe(self, layer, row, q, k_cache, block_table, prefix_len, off, path, accept_len, window, n_max, max_prefix, scale, status, stream):
         num_blocks, Hkv, block_size, D = k_cache.shape
@@ -285,7 +288,7 @@ class CacheBudget:
         B = off.numel() - 1
         if not (0 <= layer < self.layers and 0 <= row and row + B <= self.rows and Hkv == self.Hkv):
             raise ValueError("the pass's layer, rows or heads are not the budget's")
-        self.reserve(B, T, n_max, max_prefix, Hq, D)
+        self.reserve(B, T, n_max, max_prefix, Hq, D, stream)
         w = self.weight[layer, row:row + B]
         S.spec_attention_weight(q, k_cache, block_table, block_table.shape[1], block_size, num_blocks, prefix_len, off, path, accept_len, window, B, T, n_max,
                                 max_prefix, Hq, Hkv, D, scale, self.decay, w, w, self.slots, self._ws, status, stream)
