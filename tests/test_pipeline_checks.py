@@ -118,3 +118,24 @@ def test_evict_refuses_lists_that_end_early(calls, change):
     with pytest.raises(ValueError):
         budget.evict(None, None, ints([[0, 1]] * 4), BS, 8, kw["src"], kw["dst"], kw["length"], 8, 0, 0, D, 0, keep=kw["keep"])
     assert not calls
+
+
+def test_a_budget_that_grows_slot_by_slot_keeps_little(calls):
+    """Outgrown workspaces stay (a captured graph may still use them), so their sum
+    has to stay near the last one's size."""
+    budget, need = CacheBudget(1, 1, Hkv, 64, device="cpu"), 0
+    for step in range(4800):
+        need = calls.RETURNS = 512 * (step + 1)
+        budget.reserve(1, 1, 1, step, Hq, D)
+        assert budget._ws.numel() >= need
+    assert budget._ws.numel() + sum(t.numel() for t in budget._outgrown) <= 4 * need
+    kept = [t.data_ptr() for t in budget._outgrown] + [budget._ws.data_ptr()]
+    budget.reserve(1, 1, 1, 0, Hq, D)
+    assert [t.data_ptr() for t in budget._outgrown] + [budget._ws.data_ptr()] == kept
+
+
+def test_a_first_reservation_is_exact(calls):
+    calls.RETURNS = 1000
+    budget = CacheBudget(1, 1, Hkv, 64, device="cpu")
+    budget.reserve(1, 1, 1, 0, Hq, D)
+    assert budget._ws.numel() == 1000

@@ -270,7 +270,9 @@ class CacheBudget:
         self.weight = torch.zeros((layers, rows, Hkv, slots), dtype=torch.float32, device=device)
         self.layers, self.rows, self.Hkv, self.slots, self.decay = layers, rows, Hkv, slots, decay
         self._ws = torch.empty(0, dtype=torch.uint8, device=device)
-        self._outgrown = []  # a call on another stream may still be using them
+        # calls in flight and captured graphs may still be using them; each is half of
+        # the next at most, so together they are no larger than the last
+        self._outgrown = []
 
     def reserve(self, B, T, n_max, max_prefix, Hq, D, stream=None):
         """Workspace for passes of up to these sizes, observed on `stream`
@@ -280,7 +282,7 @@ class CacheBudget:
         if self._ws.numel() < need:
             self._outgrown.append(self._ws)
             with torch.cuda.stream(stream):  # another stream's free memory may still be in use there
-                self._ws = torch.empty(need, dtype=torch.uint8, device=self._ws.device)
+                self._ws = torch.empty(max(need, 2 * self._ws.numel()), dtype=torch.uint8, device=self._ws.device)
 
     def _observe(self, layer, row, q, k_cache, block_table, prefix_len, off, path, accept_len, window, n_max, max_prefix, scale, status, stream):
         num_blocks, Hkv, block_size, D = k_cache.shape
