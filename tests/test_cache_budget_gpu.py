@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import tree_speculative_verification_spec_gb300 as S
-from bounded_cache import ints, offsets, rope_reference
+from bounded_cache import ints, offsets, rope_reference, weight_reference
+from test_request_life_gpu import Pool
 from tree_speculative_verification_spec_gb300.pipeline import CacheBudget, DeviceBatch, PromptPass, Rotary, VerifyPass
 
 pytestmark = pytest.mark.gpu
@@ -107,3 +108,39 @@ def test_a_workspace_is_the_observing_streams_own():
         _observed(again, [5], [0])
         assert _stream_of_memory(again._ws) == [side.cuda_stream]
     side.synchronize()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_forked_rows_go_on_from_their_weights(captured):
+    """A prompt, two forks of it and a flagged one, a chunk on both: what they
+    gather decays what the prompt gave, not what the rows held before."""
+    n, chunk = 50, [3, 7]
+    budget = CacheBudget(1, 4, Hkv, 6 * BS, decay=0.5)
+    pool = Pool(4, 6, 30, Hkv, BS, D, 1)
+    kc, vc = pool.caches[0]
+    pool.fork([-1], [0], [0], [n])
+    p = PromptPass(_randn((n, Hq, D), 1), kc, vc, pool.table[:1], offsets([n]), ints([0]), n, 0, 0.125)
+    p.run((_randn((n, Hkv, D), 2), _randn((n, Hkv, D), 3)))
+    budget.weight.fill_(5.0)
+    budget.observe_prompt(0, p)
+    src, dst, length, room, st = ints([0, 0, 9]), ints([1, 2, 3]), ints([n, n, 0]), ints(chunk + [0]), ints([77] * 3)
+    S.spec_pages_fork(pool.k, pool.v, 1, pool.table, *pool.shape, src, dst, length, room, 3, Hkv, D, S.SPEC_BF16, pool.pool, pool.count, pool.ws, st)
+    if captured:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            budget.fork(src, dst, st)
+        graph.replay()
+    else:
+        budget.fork(src, dst, st)
+    assert st.tolist() == [0, 0, S.SPEC_DEV_BAD_ROW]
+    before = budget.weight[0, 0].clone()
+    assert torch.equal(budget.weight[0, 1], before) and torch.equal(budget.weight[0, 2], before) and (budget.weight[0, 3] == 5.0).all()
+    c = PromptPass(_randn((sum(chunk), Hq, D), 4), kc, vc, pool.table[1:3], offsets(chunk), ints([n, n]), max(chunk), n, 0.125)
+    c.run((_randn((sum(chunk), Hkv, D), 5), _randn((sum(chunk), Hkv, D), 6)))
+    budget.observe_prompt(0, c, row=1)
+    assert c.status.tolist() == [0, 0] and torch.equal(budget.weight[0, 0], before)
+    d = dict(q=c.q, k=kc, table=pool.table[1:3], seq_off=c.seq_off, prefix=c.prefix_len, Hq=Hq, Hkv=Hkv, D=D, bs=BS, scale=0.125)
+    ref, tol = weight_reference(d, torch.stack([before] * 2), 0.5)
+    mine = ~ref.isnan()
+    assert ((budget.weight[0, 1:3].double() - ref).abs()[mine] <= tol[mine]).all()

@@ -139,3 +139,18 @@ def test_a_first_reservation_is_exact(calls):
     budget = CacheBudget(1, 1, Hkv, 64, device="cpu")
     budget.reserve(1, 1, 1, 0, Hq, D)
     assert budget._ws.numel() == 1000
+
+
+@pytest.mark.parametrize("src,dst,status,moved", [
+    ([0], [3], None, {3: 0}), ([0, 0, 1], [2, 3, 4], None, {2: 0, 3: 0, 4: 1}), ([-1, 2], [0, 1], None, {1: 2}), ([1, 1], [1, 4], None, {4: 1}),
+    ([0, 1, 2], [3, 4, 5], [0, 128, 0], {3: 0, 5: 2}), ([6, -2, 0, 1], [3, 4, 6, -1], None, {}), ([0, 7, 5], [9, 2, 0], None, {0: 5}), ([], [], None, {}),
+    ([0, 1], [4, 5], [4, 4], {})])
+def test_a_fork_takes_its_weights_along(src, dst, status, moved):
+    """Rows that are no fork's, or a flagged one's, stay as they were."""
+    budget = CacheBudget(2, 6, Hkv, 8, device="cpu")
+    budget.weight.copy_(torch.rand(budget.weight.shape, generator=torch.Generator().manual_seed(1)))
+    want = budget.weight.clone()
+    for d, s in moved.items():
+        want[:, d] = budget.weight[:, s]
+    budget.fork(ints(src), ints(dst), None if status is None else ints(status))
+    assert torch.equal(budget.weight, want)

@@ -262,9 +262,10 @@ class VerifyPass:
 class CacheBudget:
     """What the attention of every layer gave each slot of a block table's rows,
     and eviction by it.  weight is float32 [layers][rows][Hkv][slots], by table
-    row; a pass over part of the table says at which row its batch starts.  One
-    workspace serves every call: observe on one stream at a time, and let another
-    one wait for it first."""
+    row; a pass over part of the table says at which row its batch starts, and
+    rows forked from others take their weights along by fork().  One workspace
+    serves every call: observe on one stream at a time, and let another one wait
+    for it first."""
 
     def __init__(self, layers, rows, Hkv, slots, decay=1.0, device="cuda"):
         self.weight = torch.zeros((layers, rows, Hkv, slots), dtype=torch.float32, device=device)
@@ -305,6 +306,23 @@ class CacheBudget:
         b = v.batch
         self._observe(layer, row, b.q, b.k_cache, b.block_table, b.prefix_len, b.tree_off, v.path, v.accept_len, window, b.n_max, b.max_prefix, b.scale, v.status,
                       stream)
+
+    def fork(self, src, dst, status=None, stream=None):
+        """Rows dst take the weights of rows src along (int32 [N], after
+        spec_pages_fork of them, with its status: a flagged fork changes nothing).
+        Empty rows (src -1) and rows out of range are left as they were."""
+        if src.numel() == 0:
+            return
+        with torch.cuda.stream(stream):  # None: the current one
+            done = (src >= 0) & (src < self.rows) & (dst >= 0) & (dst < self.rows)
+            if status is not None:
+                done &= status == 0
+            # the others write what one that is done writes (or row 0 to itself), so that
+            # nothing has to be counted on the host
+            one = done.int().argmax().view(1)
+            s, d = (torch.where(done, x, x.index_select(0, one)).long() for x in (src.masked_fill(~done, 0), dst.masked_fill(~done, 0)))
+            for w in self.weight:
+                w.index_copy_(0, d, w.index_select(0, s))
 
     def evict(self, k_ptrs, v_ptrs, block_table, block_size, num_blocks, src, dst, length, keep_max, first, last, D, dtype, keep=None, stream=None):
         """Rows src (int32 [N], of `length` slots) cut to rows dst, which have
