@@ -154,3 +154,30 @@ def test_a_fork_takes_its_weights_along(src, dst, status, moved):
         want[:, d] = budget.weight[:, s]
     budget.fork(ints(src), ints(dst), None if status is None else ints(status))
     assert torch.equal(budget.weight, want)
+
+
+def _prompt_pass():
+    cache = torch.zeros((8, Hkv, BS, D))
+    return pipeline.PromptPass(torch.zeros((5, Hq, D)), cache, cache, ints([[0, 1]]), ints([0, 5]), ints([0]), 5, 0, 0.1)
+
+
+@pytest.mark.parametrize("kind", ["prompt", "tree"])
+def test_a_pass_takes_rows_once(calls, kind):
+    """Ready rows or a projection's: never both, and a projection with its rotary."""
+    kv, qkv, rotary = (torch.zeros((5, Hkv, D)),) * 2, torch.zeros((5, Hq + 2 * Hkv, D)), Rotary()
+    p, first = (_prompt_pass(), ()) if kind == "prompt" else (_verify_pass(), ("greedy",))
+    calls.clear()
+    for kw in ({f"{kind}_kv": kv, f"{kind}_qkv": qkv, "rotary": rotary}, {f"{kind}_qkv": qkv}, {f"{kind}_kv": kv, f"{kind}_qkv": qkv}):
+        with pytest.raises(ValueError, match="qkv"):
+            p.run(*first, **kw)
+        assert not calls
+    p.run(*first, **{f"{kind}_kv": kv})
+    assert "spec_kv_append" in [n for n, _, _ in calls]
+    calls.clear()
+    p.run(*first, **{f"{kind}_qkv": qkv, "rotary": rotary})
+    names = [n for n, _, _ in calls]
+    assert "spec_rope_append" in names and "spec_kv_append" not in names
+    calls.clear()
+    p.run(*first, rotary=rotary)  # rows that are in the cache already
+    names = [n for n, _, _ in calls]
+    assert "spec_rope_append" not in names and "spec_kv_append" not in names

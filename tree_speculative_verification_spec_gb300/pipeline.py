@@ -107,6 +107,11 @@ def _clear(status, stream):
         status.zero_()
 
 
+def _one_source(kv, qkv, rotary):
+    if qkv is not None and (kv is not None or rotary is None):
+        raise ValueError("a projection's rows (qkv) come with their rotary, and not beside ready K/V rows")
+
+
 class PromptPass:
     """Causal attention of packed prompts (or chunks) over the paged cache.
 
@@ -131,6 +136,7 @@ class PromptPass:
         None: the row's index).  status is this run's: a request that an earlier
         one flagged is computed again."""
         B, T, n_max, max_prefix, Hq, Hkv, D = self.size
+        _one_source(prompt_kv, prompt_qkv, rotary)
         _clear(self.status, stream)
         if prompt_qkv is not None:
             rotary.append(prompt_qkv, self.q, self.k_cache, self.v_cache, self.block_table, self.prefix_len, self.seq_off, n_max, self.status, pos_base, pos,
@@ -246,6 +252,7 @@ class VerifyPass:
         """tree_kv: (k_new, v_new) rows appended before attention, or None when
         the tree K/V are already in the cache; tree_qkv with rotary instead: a
         projection's rows (see project())."""
+        _one_source(tree_kv, tree_qkv, rotary)
         self.mask_build(stream)
         if tree_qkv is not None:
             self.project(tree_qkv, rotary, pos_base, stream)
