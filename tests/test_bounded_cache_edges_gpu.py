@@ -76,3 +76,15 @@ def test_evict_from_two_threads():
     for t in threads:
         t.join()
     assert outs == [[([8], [0])]] * 2
+
+
+@pytest.mark.parametrize("window", [0, 40])
+def test_weight_under_a_wide_bound_of_rows(window):
+    """n_max says what a request may have at most, not what a batch of a thousand has."""
+    lens = [(i * 7) % 3 for i in range(1200)]
+    lens[700], lens[1199] = 300, 41
+    d = paged_batch(82, lens, [(i * 5) % 40 for i in range(1200)], 64, 8, 64, 16, torch.bfloat16, extra_rows=1)
+    before = _before(d)
+    got, st = _weight(d, before, n_max=1 << 20, window=window)
+    assert not st.any()
+    _weight_holds(d, got, before, window=window)

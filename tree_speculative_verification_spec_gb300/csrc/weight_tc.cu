@@ -1296,16 +1296,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Minus log2 of every counted row's sum, from the parts that the splits with some
-// of its keys left: 8 lanes a row, 32 rows a CTA.
+// of its keys left: 8 lanes a row, 32 rows a CTA.  a.per_req counts these tiles.
 constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 8;
 __global__ void __launch_bounds__(kJoinThreads) weight_join_kernel(const WeightArgs a, int tiles) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tile = blockIdx.x % tiles, kvh = blockIdx.x / tiles % a.Hkv, b = blockIdx.x / tiles / a.Hkv;
+  const int tile = blockIdx.x % tiles, kvh = blockIdx.x / tiles;
+  int b, at_tile;  // the division in 32 bits: 8192 CTAs of a prompt's rows pay for it
+  if (a.per_req > 0) {
+    b = tile / a.per_req;
+    at_tile = tile - b * a.per_req;
+  } else {
+    b = weight_find(a, tile, kJoinRows);
+    at_tile = (int)max(-1LL, tile - weight_first_tile(a, b, kJoinRows));
+  }
   WeightRequest r;
-  const bool bad = weight_check(a, b, r) != 0;
-  const int row = tile * kJoinRows + threadIdx.x / 8, part = threadIdx.x % 8;
+  const bool bad = weight_check(a, b, r) != 0 || at_tile < 0 || at_tile > (r.cnt * a.g - 1) / kJoinRows || r.cnt == 0;
+  const int row = at_tile * kJoinRows + threadIdx.x / 8, part = threadIdx.x % 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (bad || tile * kJoinRows >= r.cnt * a.g) return;
+  if (bad) return;
   const bool there = row < r.cnt * a.g;
   const int first = r.m - r.cnt;
   const int splits = there ? min(a.splits, (r.P + first + row / a.g) / a.chunk + 1) : 0;
@@ -1515,10 +1523,14 @@ static cudaError_t launch_d(const WeightArgs& a, cudaStream_t stream) {
   }
   const int dyn = (int)Layout<D>::kDyn;
   if (rows > 0) {
-    const int tiles = (int)((rows + kJoinRows - 1) / kJoinRows);
-    if ((long long)tiles * a.Hkv * a.B > INT32_MAX) return cudaErrorInvalidValue;
+    // n_max may be far above what a batch has: the fewer of each request's most and
+    // the packing's tiles (as the row tiles of the fp32 kernels)
+    WeightArgs join = a;
+    const long long each = (rows + kJoinRows - 1) / kJoinRows, packed = (long long)a.T * a.g / kJoinRows + a.B;
+    join.per_req = each * a.B < packed ? (int)each : 0;
+    const int tiles = (int)std::min(each * a.B, packed);
     e = launch(weight_tc_kernel<D, kStats>, sms, kThreads, dyn, first, stream, mk, mq, prm);
-    if (e == cudaSuccess) e = launch(weight_join_kernel, (long long)tiles * a.Hkv * a.B, kJoinThreads, 0, false, stream, a, tiles);
+    if (e == cudaSuccess) e = launch(weight_join_kernel, (long long)tiles * a.Hkv, kJoinThreads, 0, false, stream, join, tiles);
   }
   if (e == cudaSuccess) e = launch(weight_tc_kernel<D, kSumsFew>, sms, kThreads, dyn, first && rows == 0, stream, mk, mq, prm);
   if (e == cudaSuccess && rows > 2 * prm.rt) {
