@@ -88,3 +88,43 @@ def test_weight_under_a_wide_bound_of_rows(window):
     got, st = _weight(d, before, n_max=1 << 20, window=window)
     assert not st.any()
     _weight_holds(d, got, before, window=window)
+
+
+@DTYPES
+@pytest.mark.parametrize("spread", [6.0, 40.0])
+@pytest.mark.parametrize("Hq,lens,prefix", [(32, [1, 2], [2000, 300]), (16, [3, 8], [900, 3000]), (32, [8, 1, 4], [100, 30, 20000])], ids=["short", "rows", "long"])
+def test_weight_few_wide_rows_with_steep_scores(Hq, lens, prefix, spread, dtype):
+    """Heads of 128, sums that leave the middle of 32 bits: a second look at the rows."""
+    d = paged_batch(83, lens, prefix, Hq, 4, 128, 16, dtype, spread=spread)
+    before = _before(d)
+    got, st = _weight(d, before)
+    assert not st.any()
+    _weight_holds(d, got, before)
+
+
+def test_weight_two_graphs_with_a_workspace_each():
+    """Captured passes of two streams replayed at once."""
+    ds = [paged_batch(s, lens, prefix, 8, 2, 64, 16, torch.bfloat16) for s, lens, prefix in ((84, [2, 40], [3000, 200]), (85, [300], [50]))]
+    befores, outs, graphs, keep = [_before(d) for d in ds], [], [], []
+    for d, before in zip(ds, befores):
+        size = (d["B"], d["T"], d["n_max"], d["max_prefix"], 8, 2, 64)
+        ws = torch.empty(S.spec_weight_workspace_size(*size), dtype=torch.uint8, device="cuda")
+        out, st = torch.full_like(before, 7.0), ints([0] * d["B"])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            S.spec_attention_weight(d["q"], d["k"], d["table"], d["table"].shape[1], 16, d["nb"], d["prefix"], d["seq_off"], None, None, 0, *size, d["scale"], 0.75,
+                                    before, out, out.shape[-1], ws, st)
+        outs.append((out, st))
+        graphs.append(graph)
+        keep.append(ws)
+    streams = [torch.cuda.Stream() for _ in ds]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for d, before, (out, st) in zip(ds, befores, outs):
+        assert not st.any()
+        _weight_holds(d, out, before)
