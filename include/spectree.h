@@ -705,7 +705,8 @@ spec_status spec_attention_weight(const void* q, const void* k_cache, const int3
  *            SPEC_DEV_CAPACITY (len beyond the table, weight_stride or 2^30);
  *            SPEC_DEV_BAD_BLOCK (a page of either row outside [0, num_blocks)).  A flagged
  *            eviction copies nothing
- * Two launches, no workspace.
+ * No workspace.  One launch where the CTAs that select also copy (layers * N * Hkv of two
+ * or more per SM, or little to copy), else two.
  */
 spec_status spec_kv_evict(void* const* k_caches, void* const* v_caches, int layers, const int32_t* block_table, int B,
                           int max_blocks, int block_size, int num_blocks, const int32_t* src, const int32_t* dst,

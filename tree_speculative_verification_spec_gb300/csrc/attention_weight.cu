@@ -292,11 +292,15 @@ static size_t weight_ws_bytes(int splits, int T, int Hq, bool tc) {
 }
 
 // Parts of a request's rows whose sums are taken apart, where the items of 256 keys
-// alone leave SMs idle: for a dozen items an SM, half of which are above a prompt's
-// diagonal and fall away.  One prompt of 4000 tokens with 8, 4 and 2 kv-heads (128,
-// 64 and 32 items): 149, 192 and 144 us whole, 98, 67 and 32 us in 15 or 16 parts.
-// A prompt of 8192 (256 items) took 300 us whole and 358 in 15 parts: an item more
-// costs a CTA some 7 us (its keys' load, the score buffers run dry).
+// alone do not reach every SM: for a dozen items an SM, half of which are above a
+// prompt's diagonal and fall away.  One prompt of 4000 tokens with 8, 4 and 2 kv-heads
+// (128, 64 and 32 items): 149, 192 and 144 us whole, 98, 67 and 32 us in 15 or 16 parts.
+// An item more costs a CTA some 7 us (its keys' load, the score buffers run dry).  Whole
+// calls (statistics too, 8 kv-heads, L2 flushed), whole rows, the best number of parts,
+// and 12 parts: 144 items 259, 222 (3 parts), 230 us; 160 items 280, 231 (2), 247; 176
+// items 323, 289 (6), 298; 208 items 395, 384 (6), 384; 240 items 477, 479 (8), 500; 256
+// items 532, 558 (6), 569.  So from 152 to some 200 items two to six parts would be
+// faster than the whole rows that the rule takes (up to 18 %).
 static int weight_parts(int B, int n_max, int max_prefix, int Hkv) {
   const long long items = std::max(1LL, ((long long)max_prefix + n_max + 255) / 256 * B * Hkv);
   return items >= kWtSms ? 1 : (int)std::min(16LL, (12LL * kWtSms + items - 1) / items);

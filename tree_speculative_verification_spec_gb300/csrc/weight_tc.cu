@@ -33,7 +33,7 @@
 // What bounds them, and what they measured (32/8 heads, D 128, one GB300):
 //   every row of a prompt of 8192: statistics 229 us, sums 273 (241 and 298 with
 //   one MMA warp for both tiles).  No pipe is full (tensor core and exponentials
-//   some 55 %, issue slots 60 %): the chain of a score buffer from hand to hand.
+//   some 50 %, issue slots 60 %): the chain of a score buffer from hand to hand.
 //   Sums have 256 items for 152 CTAs, the first keys' the longest (15 %; items of
 //   128 keys end more evenly but stream Q twice: 380 us against 311 at that step).
 //   the last 32 rows of four prompts of 8704 slots, 64/8 heads: 29 us, 37 us, and
@@ -1451,8 +1451,14 @@ static cudaError_t launch_held(const CUtensorMap& mk, const Params& prm, int fit
 // 4000 keys each in clusters of 2, 4, 8 and 16 (76, 36, 15 and 7 fit on the GPU): 120, 118, 146 and
 // 271 us; of 8000 keys in 4, 8 and 16: 221, 206 and 287; 1024 of 1000 keys in 1, 2,
 // 4: 71, 80, 139.  Two passes over K (385 us for the 512 of 8000 keys) are the
-// other way.  Nodes that a path leaves out have no key, so its tree does not count
-// as keys.  Returns the clusters that fit, 0: no request is held.
+// other way.  The costs are those of D 128; D 64 is charged the same, and its two
+// passes by their bytes, less than they take.  At D 64, 32/8 heads, L2 flushed, two
+// passes and clusters of 2, 4, 8 (* the choice): 64 requests of 4 rows over 4000 slots
+// 188, 91*, 97, 122 us, over 8000 355, 171*, 175, 205; of 32 rows over 4000 186, 95*,
+// 103, 136, but over 8000 350*, -, 181, 217 and over 16000 663*, -, -, 396: there the
+// held form would take little more than half.
+// Nodes that a path leaves out have no key, so its tree does not count as keys.
+// Returns the clusters that fit, 0: no request is held.
 template <int D, int N>
 static int held_plan(const WeightArgs& a, int dev, int* cluster) {
   constexpr int kMost = 512 / N;  // key tiles of a CTA
