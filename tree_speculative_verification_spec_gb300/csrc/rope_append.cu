@@ -14,10 +14,10 @@
 // each (VE elements a vector).  Lane c's vectors are the two halves of the same
 // pairs, so that a rotation needs no other lane.
 //
-// What bounds it, and what it measured (one GB300): HBM and the issue slots (57 %
+// What bounds it, and what it measured (one GB300): HBM and the issue slots (62 %
 // used; 100 us for a prompt of 16384 tokens, 32/8 heads, D 128, bf16, before the
 // arithmetic was paired, 81 before the tables lost their bank conflicts).  That
-// prompt 76 us, 5.3 TB/s; four prompts of 1500 to 2048 tokens with 64/8 heads and
+// prompt 77 us, 5.2 TB/s; four prompts of 1500 to 2048 tokens with 64/8 heads and
 // three axes 57 us; trees of 64 requests 19 us, of which a CTA's own chain (packing,
 // table, rows, angles) is most; a few tokens 5 us on the GPU.
 #include <algorithm>
