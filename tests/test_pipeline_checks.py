@@ -33,22 +33,22 @@ def calls(monkeypatch):
 
 
 # places of spec_rope_append's arguments
-AXIS, POS_BASE, POS, AXES = 5, 8, 9, 10
+AXIS, POS_BASE, POS, AXES, ROWS = 5, 8, 9, 10, 21
 
 
-def _verify_pass(nodes=(3, 2)):
+def _verify_pass(nodes=(3, 2), extra=0):
     T, cache = sum(nodes), torch.zeros((8, Hkv, BS, D))
     off = ints([0] + [sum(nodes[:i + 1]) for i in range(len(nodes))])
     return VerifyPass(DeviceBatch(B=len(nodes), T=T, n_max=max(nodes), V=7, Hq=Hq, Hkv=Hkv, D=D, block_size=BS, num_blocks=8, max_prefix=9,
                                   parent=ints([-1, 0, 1, -1, 0]), tree_off=off, tokens=ints([0] * T), prefix_len=ints([9, 4]), block_table=ints([[0, 1], [2, 3]]),
-                                  q=torch.zeros((T, Hq, D)), k_cache=cache, v_cache=cache, p_logits=torch.zeros((T, 7)), q_probs=None, uniforms=None, scale=0.1))
+                                  q=torch.zeros((T + extra, Hq, D)), k_cache=cache, v_cache=cache, p_logits=torch.zeros((T, 7)), q_probs=None, uniforms=None, scale=0.1))
 
 
 @pytest.mark.parametrize("axes", [1, 2, 3, 4])
 def test_project_names_a_position_for_every_axis_it_asks_for(calls, axes):
     """A pair of axis a reads pos[a * T + row]: there has to be one, and it is the
     node's depth whatever the axis."""
-    v = _verify_pass()
+    v = _verify_pass(extra=axes % 2)  # q may be longer than the batch
     v.depth[:] = ints([0, 1, 2, 0, 1])
     axis = ints([i % axes for i in range(D // 2)]) if axes > 1 else None
     rotary = Rotary(torch.ones(D // 2), D, axis=axis, axes=axes)
@@ -57,6 +57,7 @@ def test_project_names_a_position_for_every_axis_it_asks_for(calls, axes):
     (args,) = [a for n, a, _ in calls if n == "spec_rope_append"]
     pos, T = args[POS].reshape(-1), v.batch.T
     assert pos.numel() >= args[AXES] * T
+    assert args[ROWS] == T
     for a in set(range(1) if args[AXIS] is None else args[AXIS].tolist()):
         assert 0 <= a < args[AXES]
         assert pos[a * T:(a + 1) * T].tolist() == [0, 1, 2, 0, 1]
@@ -78,10 +79,11 @@ AXIS3 = dict(axis=ints([0, 1, 2] * 10 + [0, 1]), axes=3)
 
 
 @pytest.mark.parametrize("change", [
-    dict(pos=ints([0] * 4)), dict(pos=ints([[0] * 5] * 2), **AXIS3), dict(pos=ints([0] * 14), **AXIS3), dict(pos=ints([[0] * 6] * 3), **AXIS3),
-    dict(pos=ints([[0] * 5] * 3), axis=ints([0] * 31), axes=3), dict(pos_base=ints([0])), dict(qkv=torch.zeros((4, Hq + 2 * Hkv, D))),
+    dict(pos=ints([[0] * 5] * 2), **AXIS3), dict(pos=ints([0] * 14), **AXIS3), dict(pos=ints([[0] * 6] * 3), **AXIS3),
+    dict(pos=ints([[0] * 5] * 3), axis=ints([0] * 31), axes=3), dict(pos_base=ints([0])),
+    dict(qkv=torch.zeros((4, Hq + 2 * Hkv, D)), pos=ints([[0] * 5] * 3), **AXIS3),
     dict(qkv=torch.zeros((5, Hq + Hkv, D))), dict(qkv=torch.zeros((5, 511))), dict(inv_freq=torch.ones(31)), dict(q_norm=torch.ones(63)), dict(k_norm=torch.ones(32))],
-    ids=["pos", "pos of two axes", "flat pos", "pos of other rows", "axis", "pos_base", "qkv", "heads", "width", "inv_freq", "q_norm", "k_norm"])
+    ids=["pos of two axes", "flat pos", "pos of other rows", "axis", "pos_base", "qkv", "heads", "width", "inv_freq", "q_norm", "k_norm"])
 def test_append_refuses_buffers_that_end_early(calls, change):
     with pytest.raises(ValueError):
         _append(calls, **change)
@@ -94,7 +96,13 @@ def test_append_refuses_buffers_that_end_early(calls, change):
     dict(inv_freq=None, rot=0), dict(inv_freq=torch.ones(40)), dict(q_norm=torch.ones(64), k_norm=torch.ones(64))])
 def test_append_takes_buffers_that_are_long_enough(calls, change):
     args = _append(calls, **change)
-    assert args[POS] is change.get("pos") and args[POS_BASE] is change.get("pos_base")
+    assert args[POS] is change.get("pos") and args[POS_BASE] is change.get("pos_base") and args[ROWS] == 5
+
+
+@pytest.mark.parametrize("change,rows", [(dict(qkv=torch.zeros((4, Hq + 2 * Hkv, D))), 4), (dict(pos=ints([0] * 3)), 3), (dict(pos=ints([0] * 3), qkv=torch.zeros((2, 512))), 2)])
+def test_append_asks_for_the_rows_that_every_buffer_has(calls, change, rows):
+    """A q longer than the batch is no error; requests behind the rows are flagged by the call."""
+    assert _append(calls, **change)[ROWS] == rows
 
 
 @pytest.mark.parametrize("rows", [1, 3])

@@ -80,26 +80,30 @@ class Rotary:
     def append(self, qkv, q, k_cache, v_cache, block_table, prefix_len, tree_off, n_max, status, pos_base=None, pos=None, stream=None):
         num_blocks, Hkv, block_size, D = k_cache.shape
         T, Hq, _ = q.shape
-        self._check(qkv, T, (Hq + 2 * Hkv) * D, D, tree_off.numel() - 1, pos_base, pos)
+        T = self._check(qkv, T, (Hq + 2 * Hkv) * D, D, tree_off.numel() - 1, pos_base, pos)
         S.spec_rope_append(qkv, self.q_norm, self.k_norm, self.eps, self.inv_freq, self.axis, self.rot_dim, self.pairing, pos_base, pos, self.axes, q, k_cache,
                            v_cache, block_table, block_table.shape[1], block_size, num_blocks, prefix_len, tree_off, tree_off.numel() - 1, T, n_max, Hq, Hkv, D,
                            status, stream)
 
     def _check(self, qkv, T, width, D, B, pos_base, pos):
         """Buffers that the call would read past the end of are refused: it knows
-        their addresses alone."""
+        their addresses alone.  Returns the rows that every buffer has: q may be
+        longer than the batch, and a request behind them is flagged by the call."""
         def holds(t, n):
             return t is None or t.numel() >= n
-        if qkv.shape[0] < T or (qkv.dim() > 1 and qkv.shape[1:].numel() < width):
-            raise ValueError("qkv has fewer rows than q, or narrower ones than its heads")
-        if not holds(pos, self.axes * T) or (self.axes > 1 and pos is not None and pos.dim() > 1 and pos.shape[-1] != T):
-            raise ValueError("pos must hold a position of every row for each axis: [axes][T]")
+        if qkv.dim() > 1 and qkv.shape[1:].numel() < width:
+            raise ValueError("qkv has narrower rows than its heads")
+        if self.axes == 1:
+            T = min(T, qkv.shape[0], T if pos is None else pos.numel())
+        elif qkv.shape[0] < T or not holds(pos, self.axes * T) or (pos is not None and pos.dim() > 1 and pos.shape[-1] != T):
+            raise ValueError("several axes: qkv and each axis of pos must have q's rows, pos [axes][T]")
         if not holds(pos_base, B):
             raise ValueError("pos_base must hold an entry for each request")
         if not (holds(self.inv_freq, self.rot_dim // 2) and holds(self.axis, self.rot_dim // 2)):
             raise ValueError("inv_freq and axis must hold an entry for each pair")
         if not (holds(self.q_norm, D) and holds(self.k_norm, D)):
             raise ValueError("q_norm and k_norm must hold a weight for each element of a head")
+        return T
 
 
 def _clear(status, stream):
@@ -323,7 +327,7 @@ class CacheBudget:
         with torch.cuda.stream(stream):  # None: the current one
             done = (src >= 0) & (src < self.rows) & (dst >= 0) & (dst < self.rows)
             if status is not None:
-                done &= status == 0
+                done &= status[:src.numel()] == 0
             # the others write what one that is done writes (or row 0 to itself), so that
             # nothing has to be counted on the host
             one = done.int().argmax().view(1)
